@@ -26,13 +26,37 @@ EXPORTS = ("attn_prefill_causal", "attn_decode_contig", "attn_decode_paged", "kv
            "attn_prefill_causal_ex", "attn_decode_contig_ex", "attn_decode_paged_ex", "attn_prefill_paged",
            "attn_prefill_paged_ex", "mla_absorb_q", "attn_decode_mla_absorbed",
            "attn_decode_mla_absorbed_workspace_bytes", "mla_unabsorb_out", "attn_decode_mla_absorbed_paged",
-           "attn_rope_interleaved_qk")
+           "attn_rope_interleaved_qk", "gqa_rope_frequencies", "attn_qk_norm_rope", "kv_append_paged_rows")
 
 
 class GqaArms(ctypes.Structure):
     """`gqa_arms` (include/gqa_attn.h): window, softcap, sinks, ALiBi slopes."""
     _fields_ = [("window", ctypes.c_int), ("softcap", ctypes.c_float), ("sinks", ctypes.c_void_p),
                 ("alibi_slopes", ctypes.c_void_p)]
+
+
+class GqaHeads(ctypes.Structure):
+    """`gqa_heads` (include/gqa_attn.h): a strided tensor [batch, tokens, heads, d]."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class GqaRopeScaling(ctypes.Structure):
+    """`gqa_rope_scaling` (include/gqa_attn.h)."""
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("original_max", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("magnitude", ctypes.c_double),
+                ("divisors", ctypes.c_void_p)]
+
+
+class GqaRope(ctypes.Structure):
+    """`gqa_rope` (include/gqa_attn.h); made by rope_init, which keeps the device
+    copy of the frequencies in `table`."""
+    _fields_ = [("layout", ctypes.c_int), ("rot_offset", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("magnitude", ctypes.c_float), ("freqs", ctypes.c_void_p)]
+
+
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "turns": 2, "index": 3}
 
 STATIC_WORKSPACE_BYTES = 16 << 20  # GQA_STATIC_WORKSPACE_BYTES
 
@@ -74,6 +98,9 @@ def load(path: str = None):
         "attn_decode_mla_absorbed": [P, P, P, P, I, I, I, I, I, F, I, P, S, P],
         "mla_unabsorb_out": [P, P, P, I, I, I, I, I, P],
         "attn_decode_mla_absorbed_paged": [P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, S, P],
+        "gqa_rope_frequencies": [P, P, I, D, P],
+        "attn_qk_norm_rope": [P, P, P, P, P, P, F, P, I, I, I, I, I, P, I, P],
+        "kv_append_paged_rows": [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P, F, P, I, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -327,6 +354,127 @@ def attn_rope_interleaved_qk(q, k, positions, theta, rot_offset=0, rot_dim=None,
                                            int(bool(k_heads_outer)), rot_offset, rot_dim, float(theta), _dtype(q),
                                            _stream(stream)), "attn_rope_interleaved_qk")
     return q, k
+
+
+def _here(*ts):
+    """Check that the tensors live on the current CUDA device (calls launch there)."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError("tensors must live on the current CUDA device")
+
+
+def _heads(t, ndim):
+    """`gqa_heads` of a [B, T, heads, d] (ndim 4) or [N, heads, d] (ndim 3) tensor
+    with a dense last axis and any other strides (an axis of one element has none)."""
+    if t is None:
+        return None
+    if t.dim() != ndim:
+        raise ValueError(f"expected {ndim} axes, got shape {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("the last axis must be dense")
+    st = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
+    return GqaHeads(t.data_ptr(), st[0] if ndim == 4 else 0, st[-3], st[-2])
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def _writes_once(*ts):
+    for t in ts:
+        if t is not None and any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
+            raise ValueError("an output must not be broadcast")
+
+
+def _weight(w, d):
+    if w is not None and tuple(w.shape) != (d,):
+        raise ValueError(f"a norm weight must be [{d}], got {tuple(w.shape)}")
+    return _p(w)
+
+
+def rope_frequencies(rot_dim, theta, scaling="none", factor=1.0, original_max=0.0, low=1.0, high=4.0, magnitude=0.0,
+                     divisors=None):
+    """The frequencies of a rotation as (host float32 tensor [rot_dim / 2, 2], magnitude);
+    include/gqa_attn.h, `gqa_rope_scaling`, has the formulas. divisors: rot_dim / 2 numbers or None."""
+    div = None
+    if divisors is not None:
+        div = (ctypes.c_double * len(divisors))(*[float(x) for x in divisors])
+        if len(divisors) != rot_dim // 2:
+            raise ValueError(f"divisors must have {rot_dim // 2} entries")
+    sc = GqaRopeScaling(ROPE_SCALINGS[scaling], float(factor), float(original_max), float(low), float(high),
+                        float(magnitude), ctypes.cast(div, ctypes.c_void_p) if div is not None else None)
+    out = (ctypes.c_float * max(2, int(rot_dim)))()
+    mag = ctypes.c_float()
+    _check(load().gqa_rope_frequencies(out, ctypes.byref(mag), int(rot_dim), float(theta), ctypes.byref(sc)),
+           "gqa_rope_frequencies")
+    return torch.tensor(list(out), dtype=torch.float32).view(-1, 2), mag.value
+
+
+def rope_init(rot_dim, theta, layout="interleaved", rot_offset=0, device="cuda", **scaling):
+    """A rotation for attn_qk_norm_rope and kv_append_paged_rows, made once for a
+    model: layout "interleaved" (adjacent pairs) or "half"; **scaling as for
+    rope_frequencies. The frequencies go to `device`."""
+    freqs, mag = rope_frequencies(rot_dim, theta, **scaling)
+    table = freqs.to(device)
+    r = GqaRope(ROPE_LAYOUTS[layout], int(rot_offset), int(rot_dim), mag, table.data_ptr())
+    r.table = table
+    return r
+
+
+def attn_qk_norm_rope(q, k, q_out, k_out, positions, rope=None, q_weight=None, k_weight=None, eps=1e-6, stream=None):
+    """RMS norm per head (a weight of None: no norm), then the rotation (rope of None:
+    none). q, q_out [B, T, H, d] and k, k_out [B, T, Hkv, d], of any strides with a dense
+    last axis (a head-major cache [B, Hkv, T, d] goes in as k_out.transpose(1, 2)); q with
+    q_out, or k with k_out, may be None. positions int32 [B, T]. Outputs may be the inputs."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("neither queries nor keys given")
+    B, T, _, d = x.shape
+    for y, o in ((q, q_out), (k, k_out)):
+        if (y is None) != (o is None):
+            raise ValueError("an input and its output go together")
+        if y is not None and (y.shape != o.shape or y.shape[:2] != x.shape[:2] or y.shape[-1] != d):
+            raise ValueError("q, k and their outputs must agree in batch, tokens and width")
+    _here(q, k, q_out, k_out, positions, q_weight, k_weight, rope.table if rope is not None else None)
+    _writes_once(q_out, k_out)
+    if positions is not None and positions.numel() != B * T:
+        raise ValueError("positions must be [B, T]")
+    _check(load().attn_qk_norm_rope(
+        _ref(_heads(q, 4)), _ref(_heads(k, 4)), _ref(_heads(q_out, 4)), _ref(_heads(k_out, 4)), _weight(q_weight, d),
+        _weight(k_weight, d), float(eps), _i32(positions), B, T, 0 if q is None else q.shape[2],
+        0 if k is None else k.shape[2], d, _ref(rope), _dtype(q, k, q_out, k_out, q_weight, k_weight),
+        _stream(stream)), "attn_qk_norm_rope")
+    return q_out, k_out
+
+
+def kv_append_paged_rows(q, k_new, v_new, q_out, k_pool, v_pool, block_tables, row_starts, seq_lens_in, seq_lens_out,
+                         rope=None, q_weight=None, k_weight=None, eps=1e-6, stream=None):
+    """Norm and rotate the packed new rows q [N, H, dk] (into q_out; both may be None) and
+    k_new [N, Hkv, dk], and write k_new and v_new [N, Hkv, dv] to the pools: rows
+    row_starts[b] .. row_starts[b + 1] - 1 (int32 [B + 1]) go behind the seq_lens_in[b]
+    rows of sequence b; seq_lens_out[b] = seq_lens_in[b] + their number (may be the same
+    tensor). Inputs of any strides with a dense last axis."""
+    N, Hkv, dk = k_new.shape
+    nb, _, bs, dv = v_pool.shape
+    B = seq_lens_in.shape[0]
+    if tuple(v_new.shape) != (N, Hkv, dv) or tuple(k_pool.shape) != (nb, Hkv, bs, dk) or v_pool.shape[1] != Hkv:
+        raise ValueError("k_new, v_new and the pools do not agree")
+    if (q is None) != (q_out is None) or (q is not None and (q.shape != q_out.shape or q.shape[0] != N or
+                                                             q.shape[-1] != dk)):
+        raise ValueError("q and q_out must both be [N, H, dk]")
+    if row_starts.numel() != B + 1 or seq_lens_out.numel() != B or block_tables.shape[0] != B:
+        raise ValueError("row_starts, the lengths and block_tables do not agree in the number of sequences")
+    _here(q, k_new, v_new, q_out, k_pool, v_pool, block_tables, row_starts, seq_lens_in, seq_lens_out, q_weight,
+          k_weight, rope.table if rope is not None else None)
+    _writes_once(q_out)
+    _check(load().kv_append_paged_rows(
+        _ref(_heads(q, 3)), _ref(_heads(k_new, 3)), _ref(_heads(v_new, 3)), _ref(_heads(q_out, 3)), _p(k_pool),
+        _p(v_pool), _i32(block_tables), _i32(row_starts), _i32(seq_lens_in), _i32(seq_lens_out), N, B,
+        block_tables.shape[1], nb, bs, 0 if q is None else q.shape[1], Hkv, dk, dv, _weight(q_weight, dk),
+        _weight(k_weight, dk), float(eps), _ref(rope),
+        _dtype(q, k_new, v_new, q_out, k_pool, v_pool, q_weight, k_weight), _stream(stream)), "kv_append_paged_rows")
+    return q_out
 
 
 def attn_get_device_error(stream=None):

@@ -369,6 +369,185 @@ gqa_status attn_rope_interleaved_qk(void* q, void* k, const int32_t* positions, 
                                     static_cast<cudaStream_t>(stream), k, heads_k, k_heads_outer));
 }
 
+gqa_status gqa_rope_frequencies(float* freqs_host, float* magnitude, int rot_dim, double theta,
+                                const gqa_rope_scaling* scaling) {
+  if (!freqs_host || !magnitude || rot_dim <= 0 || rot_dim % 2 || rot_dim > 256 || !(theta > 0.0) ||
+      !std::isfinite(theta))
+    return GQA_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586;
+  const int kind = scaling ? scaling->kind : GQA_ROPE_SCALING_NONE;
+  if (kind < GQA_ROPE_SCALING_NONE || kind > GQA_ROPE_SCALING_INDEX) return GQA_ERR_INVALID_ARG;
+  if (kind != GQA_ROPE_SCALING_NONE && !(scaling->factor > 0.0 && std::isfinite(scaling->factor)))
+    return GQA_ERR_INVALID_ARG;
+  const bool blend = kind == GQA_ROPE_SCALING_TURNS || kind == GQA_ROPE_SCALING_INDEX;
+  if (blend && !(scaling->original_max > 0.0 && std::isfinite(scaling->original_max) && scaling->low > 0.0 &&
+                 scaling->high > scaling->low && std::isfinite(scaling->high)))
+    return GQA_ERR_INVALID_ARG;
+  if (scaling && !(scaling->magnitude >= 0.0 && std::isfinite(scaling->magnitude))) return GQA_ERR_INVALID_ARG;
+  double first = 0.0, last = 0.0;
+  if (kind == GQA_ROPE_SCALING_INDEX) {
+    if (!(theta > 1.0)) return GQA_ERR_INVALID_ARG;  // the index of a pair needs falling frequencies
+    const auto index = [&](double turns) {
+      return rot_dim * std::log(scaling->original_max / (two_pi * turns)) / (2.0 * std::log(theta));
+    };
+    first = std::fmax(0.0, std::floor(index(scaling->high)));
+    last = std::fmin(rot_dim - 1.0, std::ceil(index(scaling->low)));
+  }
+  for (int t = 0; t < rot_dim / 2; ++t) {
+    double w = std::pow(theta, -2.0 * t / rot_dim);
+    if (scaling && scaling->divisors) {
+      if (!(scaling->divisors[t] > 0.0)) return GQA_ERR_INVALID_ARG;
+      w /= scaling->divisors[t];
+    }
+    double keep = 1.0;
+    if (kind == GQA_ROPE_SCALING_LINEAR) keep = 0.0;
+    if (kind == GQA_ROPE_SCALING_TURNS)
+      keep = (scaling->original_max * w / two_pi - scaling->low) / (scaling->high - scaling->low);
+    if (kind == GQA_ROPE_SCALING_INDEX) keep = 1.0 - (t - first) / std::fmax(last - first, 0.001);
+    keep = std::fmin(1.0, std::fmax(0.0, keep));
+    if (kind != GQA_ROPE_SCALING_NONE) w = keep * w + (1.0 - keep) * w / scaling->factor;
+    const float hi = (float)w;
+    freqs_host[2 * t] = hi;
+    freqs_host[2 * t + 1] = (float)(w - (double)hi);
+  }
+  double m = scaling ? scaling->magnitude : 1.0;
+  if (m == 0.0) m = kind == GQA_ROPE_SCALING_INDEX ? 0.1 * std::log(scaling->factor) + 1.0 : 1.0;
+  *magnitude = (float)m;
+  return GQA_OK;
+}
+
+// The checks that attn_qk_norm_rope and kv_append_paged_rows share, and the norm
+// and the rotation into the kernel's parameters.
+static bool heads_view_ok(const gqa_heads* x, int bf16, bool batched) {
+  const int v = bf16 ? 8 : 4;  // elements of 16 bytes
+  return x->data && aligned16(x->data) && x->token_stride % v == 0 && x->head_stride % v == 0 &&
+         (!batched || x->batch_stride % v == 0);
+}
+
+static gqa::HeadsView heads_view(const gqa_heads* x, bool batched) {
+  return {x->data, batched ? x->batch_stride : 0, x->token_stride, x->head_stride};
+}
+
+// An output that starts where its input does has to be the same view.
+static bool in_place_ok(const gqa_heads* x, const gqa_heads* y, bool batched) {
+  return x->data != y->data || (x->token_stride == y->token_stride && x->head_stride == y->head_stride &&
+                                (!batched || x->batch_stride == y->batch_stride));
+}
+
+static gqa_status qk_norm_and_rope(gqa::QkParams& p, const void* q_weight, const void* k_weight, float eps,
+                                   const gqa_rope* rope, int d) {
+  if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight))) return GQA_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return GQA_ERR_INVALID_ARG;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.eps = eps;
+  p.d = d;
+  if (!rope) return GQA_OK;
+  if ((rope->layout != GQA_ROPE_ADJACENT && rope->layout != GQA_ROPE_HALF) || rope->rot_dim <= 0 ||
+      rope->rot_dim % 2 || rope->rot_dim > 256 || rope->rot_offset < 0 || rope->rot_offset > d - rope->rot_dim ||
+      !rope->freqs || reinterpret_cast<uintptr_t>(rope->freqs) % 8 || !std::isfinite(rope->magnitude))
+    return GQA_ERR_INVALID_ARG;
+  p.layout = rope->layout;
+  p.rot_offset = rope->rot_offset;
+  p.rot_dim = rope->rot_dim;
+  p.magnitude = rope->magnitude;
+  p.freqs = rope->freqs;
+  return GQA_OK;
+}
+
+gqa_status attn_qk_norm_rope(const gqa_heads* q, const gqa_heads* k, const gqa_heads* q_out, const gqa_heads* k_out,
+                             const void* q_weight, const void* k_weight, float eps, const int32_t* positions, int B,
+                             int T, int H, int Hkv, int d, const gqa_rope* rope, gqa_dtype dt, void* stream) {
+  const int bf16 = dtype_flag(dt);
+  if (bf16 < 0 || B < 0 || T < 0 || H < 0 || Hkv < 0 || !width_ok(d) || (long long)B * T > INT_MAX ||
+      (long long)H + Hkv > INT_MAX / 2)
+    return GQA_ERR_INVALID_ARG;
+  if ((q == nullptr) != (H == 0) || (k == nullptr) != (Hkv == 0) || (q == nullptr) != (q_out == nullptr) ||
+      (k == nullptr) != (k_out == nullptr))
+    return GQA_ERR_INVALID_ARG;
+  gqa::QkParams p{};
+  const gqa_status s = qk_norm_and_rope(p, q_weight, k_weight, eps, rope, d);
+  if (s != GQA_OK) return s;
+  if (B == 0 || T == 0 || H + Hkv == 0) return GQA_OK;
+  if ((q && (!heads_view_ok(q, bf16, true) || !heads_view_ok(q_out, bf16, true) || !in_place_ok(q, q_out, true))) ||
+      (k && (!heads_view_ok(k, bf16, true) || !heads_view_ok(k_out, bf16, true) || !in_place_ok(k, k_out, true))))
+    return GQA_ERR_INVALID_ARG;
+  if (rope && !positions) return GQA_ERR_INVALID_ARG;
+  if (q) {
+    p.q = heads_view(q, true);
+    p.q_out = heads_view(q_out, true);
+  }
+  if (k) {
+    p.k = heads_view(k, true);
+    p.k_out = heads_view(k_out, true);
+  }
+  p.positions = positions;
+  p.N = B * T;
+  p.T = T;
+  p.B = B;
+  p.H = H;
+  p.Hk = p.Hkv = Hkv;
+  p.run_rows = 1;
+  return from_cuda(gqa::launch_qk_rows(p, bf16, 0, static_cast<cudaStream_t>(stream)));
+}
+
+gqa_status kv_append_paged_rows(const gqa_heads* q, const gqa_heads* k_new, const gqa_heads* v_new,
+                                const gqa_heads* q_out, void* k_pool, void* v_pool, const int32_t* block_tables,
+                                const int32_t* row_starts, const int32_t* seq_lens_in, int32_t* seq_lens_out, int N,
+                                int B, int max_blocks_per_seq, int num_blocks, int block_size, int H, int Hkv, int d_k,
+                                int d_v, const void* q_weight, const void* k_weight, float eps, const gqa_rope* rope,
+                                gqa_dtype dt, void* stream) {
+  const int bf16 = dtype_flag(dt);
+  if (bf16 < 0 || N < 0 || B < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || block_size <= 0 || H < 0 ||
+      Hkv <= 0 || !width_ok(d_k) || !width_ok(d_v) || (long long)H + Hkv > INT_MAX / 2)
+    return GQA_ERR_INVALID_ARG;
+  if ((long long)max_blocks_per_seq * block_size > INT_MAX / 2) return GQA_ERR_INVALID_ARG;
+  if ((q == nullptr) != (H == 0) || (q == nullptr) != (q_out == nullptr)) return GQA_ERR_INVALID_ARG;
+  gqa::QkParams p{};
+  const gqa_status s = qk_norm_and_rope(p, q_weight, k_weight, eps, rope, d_k);
+  if (s != GQA_OK) return s;
+  if (B == 0) return GQA_OK;
+  if (!k_new || !v_new || !k_pool || !v_pool || !block_tables || !row_starts || !seq_lens_in || !seq_lens_out)
+    return GQA_ERR_INVALID_ARG;
+  if (N > 0 && (!heads_view_ok(k_new, bf16, false) || !heads_view_ok(v_new, bf16, false) ||
+                (q && (!heads_view_ok(q, bf16, false) || !heads_view_ok(q_out, bf16, false) ||
+                       !in_place_ok(q, q_out, false)))))
+    return GQA_ERR_INVALID_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return GQA_ERR_INVALID_ARG;
+  const bool same_lens = seq_lens_in == seq_lens_out;
+  if (!same_lens && seq_lens_in < seq_lens_out + B && seq_lens_out < seq_lens_in + B) return GQA_ERR_INVALID_ARG;
+  if (q) {
+    p.q = heads_view(q, false);
+    p.q_out = heads_view(q_out, false);
+  }
+  p.k = heads_view(k_new, false);
+  p.v = heads_view(v_new, false);
+  p.k_out.data = k_pool;
+  p.v_pool = v_pool;
+  p.tables = block_tables;
+  p.row_starts = row_starts;
+  p.lens_in = seq_lens_in;
+  p.lens_out = seq_lens_out;
+  p.err = error_word();
+  if (!p.err) return GQA_ERR_CUDA;
+  p.N = N;
+  p.B = B;
+  p.H = H;
+  p.Hk = p.Hkv = Hkv;
+  p.dv = d_v;
+  p.mbps = max_blocks_per_seq;
+  p.bs = block_size;
+  p.num_blocks = num_blocks;
+  p.run_rows = 1;
+  // the lengths are read by every row: written in the same launch only to another array
+  p.lens_items = same_lens ? 0 : B;
+  const cudaError_t e = gqa::launch_qk_rows(p, bf16, 1, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess || !same_lens) return from_cuda(e);
+  p.run_rows = 0;
+  p.lens_items = B;
+  return from_cuda(gqa::launch_qk_rows(p, bf16, 1, static_cast<cudaStream_t>(stream)));
+}
+
 size_t attn_decode_mla_absorbed_workspace_bytes(int B, int H, int d_c, int max_len) {
   if (B <= 0 || H <= 0 || d_c <= 0 || max_len <= 0) return 0;
   const int chunk = gqa::mla_chunk_rows(B, H, max_len);

@@ -90,6 +90,38 @@ cudaError_t launch_append(void* q, const void* k_new, const void* v_new, void* k
                           int num_blocks, int bs, int H, int Hkv, int dk, int dv, double theta, int rot_offset,
                           int rot_dim, int bf16, unsigned* err, cudaStream_t st);
 
+// A tensor [batch, tokens, heads, d] with its last axis dense; strides in elements.
+struct HeadsView {
+  void* data;
+  int64_t batch_stride, token_stride, head_stride;
+};
+
+// Parameters of the q/k row kernel (norm, rotation, paged write).
+struct QkParams {
+  HeadsView q, k, q_out, k_out;  // PAGED: k_out.data is the key pool, no batch axis
+  HeadsView v;                   // PAGED
+  void* v_pool;
+  const void* q_weight;          // [d] of the element type, or NULL: no norm
+  const void* k_weight;
+  const int32_t* positions;      // [B, T] (not PAGED)
+  const float* freqs;            // [rot_dim / 2] float pairs (high, low part) of the frequencies
+  const int32_t* tables;         // PAGED, from here on: as kv_append_paged_rows
+  const int32_t* row_starts;
+  const int32_t* lens_in;
+  int32_t* lens_out;
+  unsigned* err;
+  int N, T, B;                   // N token rows (= B * T when not PAGED)
+  int H, Hk, Hkv;                // query heads, key heads turned (0 without keys), KV heads of the pool
+  int d, dv;
+  int layout, rot_offset, rot_dim;  // layout 1: half pairs; rot_dim 0: no rotation
+  float magnitude, eps;
+  int parts;                     // items per token (set by the launcher)
+  int mbps, bs, num_blocks;
+  int run_rows;                  // 0: only the lengths
+  int lens_items;                // sequences whose length this launch advances (0 or B)
+};
+cudaError_t launch_qk_rows(const QkParams& p, int bf16, int paged, cudaStream_t st);
+
 // The arms for the tensor-core prefill: window (<= 0: none), softcap * log2 e
 // (0: none), sink logits and ALiBi slopes ([H] fp32 on the device, natural
 // units, or NULL).

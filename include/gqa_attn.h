@@ -293,6 +293,125 @@ gqa_status attn_rope_interleaved_qk(void* q, void* k, const int32_t* positions, 
                                     int heads_k, int d, int q_heads_outer, int k_heads_outer, int rot_offset,
                                     int rot_dim, double theta, gqa_dtype dt, void* stream);
 
+/* ---- query and key rows: norm, rotation, paged append of many rows ----------
+ * What decoder layers do to the query and key rows before the cache (frink-models
+ * src/decoder/attn_block.rs, `attn_block_tail`: per-head norm and per-head RoPE at
+ * the row's position, then the push), for both pair layouts and scaled
+ * frequencies. These calls take strided tensors, so that they read the slices of
+ * a fused q/k/v projection where they lie.
+ */
+
+/* A tensor [batch, tokens, heads, d]: element (b, t, h, e) at
+ * data + b * batch_stride + t * token_stride + h * head_stride + e; strides in
+ * elements. data 16-byte aligned, every stride a multiple of 16 bytes. */
+typedef struct gqa_heads {
+  void* data;
+  int64_t batch_stride, token_stride, head_stride;
+} gqa_heads;
+
+typedef enum {
+  GQA_ROPE_ADJACENT = 0, /* pair t: columns rot_offset + 2t and rot_offset + 2t + 1 */
+  GQA_ROPE_HALF = 1      /* pair t: columns rot_offset + t and rot_offset + t + rot_dim / 2 */
+} gqa_rope_layout;
+
+/* How frequencies theta^(-2t / rot_dim) are lowered for contexts beyond the one a
+ * model was trained on (`original_max` positions). With w the unscaled frequency
+ * of pair t:
+ *   NONE    w
+ *   LINEAR  w / factor (position interpolation)
+ *   TURNS   keep * w + (1 - keep) * w / factor, keep = (n - low) / (high - low)
+ *           clamped to [0, 1], n = original_max * w / (2 pi) the turns that the pair
+ *           makes in the original context: pairs that turn at least `high` times
+ *           keep their frequency, those that turn at most `low` times are interpolated
+ *   INDEX   the same two ends, blended linearly in the pair's index: with
+ *           t(n) = rot_dim * ln(original_max / (2 pi n)) / (2 ln theta) the index of
+ *           a pair that turns n times, first = max(0, floor(t(high))), last =
+ *           min(rot_dim - 1, ceil(t(low))): keep = 1 - (t - first) / max(last - first,
+ *           0.001), clamped to [0, 1]. `magnitude` 0 stands for 0.1 ln(factor) + 1.
+ *           (Peng et al. 2023, YaRN.)
+ * A frequency is first divided by divisors[t] (host, rot_dim / 2 doubles, or NULL). */
+typedef enum {
+  GQA_ROPE_SCALING_NONE = 0,
+  GQA_ROPE_SCALING_LINEAR = 1,
+  GQA_ROPE_SCALING_TURNS = 2,
+  GQA_ROPE_SCALING_INDEX = 3
+} gqa_rope_scaling_kind;
+
+typedef struct gqa_rope_scaling {
+  int kind;              /* gqa_rope_scaling_kind */
+  double factor;         /* > 0 (kinds other than NONE) */
+  double original_max;   /* > 0 (TURNS, INDEX) */
+  double low, high;      /* turns, 0 < low < high (TURNS, INDEX) */
+  double magnitude;      /* factor on cos and sin; 0: the kind's own (1, or INDEX's) */
+  const double* divisors;
+} gqa_rope_scaling;
+
+/* The rotation of a call. freqs: DEVICE array of rot_dim / 2 float pairs (high part,
+ * remainder) of the frequencies, 8-byte aligned, as gqa_rope_frequencies writes
+ * them; a program copies them to the device once for a model. rot_dim even, at
+ * most 256; rot_offset + rot_dim <= d. */
+typedef struct gqa_rope {
+  int layout; /* gqa_rope_layout */
+  int rot_offset, rot_dim;
+  float magnitude; /* factor on cos and sin, applied to the rotated columns only */
+  const float* freqs;
+} gqa_rope;
+
+/* Host only: writes the rot_dim floats (rot_dim / 2 pairs) that gqa_rope.freqs
+ * points to a device copy of, and the magnitude. scaling NULL: NONE. */
+gqa_status gqa_rope_frequencies(float* freqs_host, float* magnitude, int rot_dim, double theta,
+                                const gqa_rope_scaling* scaling);
+
+/*
+ * RMS norm of every query and key head, then the rotation, in one pass:
+ *   y_e = x_e / sqrt(mean_e(x_e^2) + eps) * weight_e
+ *   pair (a, b) of y turns by angle = positions[b, t] * w:  a' = m (a cos - b sin), b' = m (a sin + b cos)
+ * in fp32, rounded once on the store (m: rope->magnitude).
+ *
+ *   q, q_out   [B, T, H, d]; k, k_out [B, T, Hkv, d] as gqa_heads. k (with k_out)
+ *              or q (with q_out) may be NULL, with its head count 0: keys or queries
+ *              alone. An output may be its input with the same strides (in place);
+ *              otherwise outputs overlap nothing.
+ *   q_weight, k_weight  [d] of the element type, 16-byte aligned; NULL: no norm
+ *   eps        >= 0
+ *   positions  int32 [B, T] on the device (NULL without a rotation)
+ *   rope       on the host, read during the call; NULL: no rotation
+ * d a multiple of 8, at most 256. No workspace.
+ */
+gqa_status attn_qk_norm_rope(const gqa_heads* q, const gqa_heads* k, const gqa_heads* q_out, const gqa_heads* k_out,
+                             const void* q_weight, const void* k_weight, float eps, const int32_t* positions, int B,
+                             int T, int H, int Hkv, int d, const gqa_rope* rope, gqa_dtype dt, void* stream);
+
+/*
+ * Append of any number of new rows per sequence to the paged pool, with
+ * attn_qk_norm_rope's norm and rotation on the way (kv_append_paged is the case of
+ * one row per sequence, adjacent pairs, no norm). The rows of all sequences lie
+ * packed, sequence after sequence:
+ *
+ *   q, q_out    [N, H, d_k]   (gqa_heads, batch_stride unused); NULL with H = 0
+ *   k_new       [N, Hkv, d_k], v_new [N, Hkv, d_v]
+ *   row_starts  int32 [B + 1], ascending: rows row_starts[b] .. row_starts[b + 1] - 1
+ *               belong to sequence b, which may have none; rows outside every
+ *               sequence (padding) are neither read nor written
+ *   seq_lens_in int32 [B]: rows present before the call; row i of sequence b sits at
+ *               position p = seq_lens_in[b] + i, in block block_tables[b][p / block_size],
+ *               slot p % block_size
+ *   seq_lens_out[b] = seq_lens_in[b] + its rows (may be the array seq_lens_in, at the
+ *               cost of a second launch, but not overlap it otherwise)
+ *   k_pool [num_blocks, Hkv, block_size, d_k], v_pool [.., d_v], block_tables as for kv_append_paged
+ * A row whose position or block entry is out of range is skipped, and the length of
+ * a sequence with such a row (or with row_starts out of order or past N) is left at
+ * seq_lens_in[b]; both set the device error word. q_out rows of such a sequence are
+ * unspecified. Two rows must not fall on one slot of the pool.
+ * d_k, d_v multiples of 8, at most 256. No workspace.
+ */
+gqa_status kv_append_paged_rows(const gqa_heads* q, const gqa_heads* k_new, const gqa_heads* v_new,
+                                const gqa_heads* q_out, void* k_pool, void* v_pool, const int32_t* block_tables,
+                                const int32_t* row_starts, const int32_t* seq_lens_in, int32_t* seq_lens_out, int N,
+                                int B, int max_blocks_per_seq, int num_blocks, int block_size, int H, int Hkv, int d_k,
+                                int d_v, const void* q_weight, const void* k_weight, float eps, const gqa_rope* rope,
+                                gqa_dtype dt, void* stream);
+
 /* Bytes of workspace attn_decode_contig / attn_decode_paged need for B
  * sequences of at most max_len_upper_bound rows (0 when no sequence that long
  * is split). With S = ceil(max_len_upper_bound / 2048) splits and U = B*H*S:
