@@ -26,7 +26,9 @@ EXPORTS = ("attn_prefill_causal", "attn_decode_contig", "attn_decode_paged", "kv
            "attn_prefill_causal_ex", "attn_decode_contig_ex", "attn_decode_paged_ex", "attn_prefill_paged",
            "attn_prefill_paged_ex", "mla_absorb_q", "attn_decode_mla_absorbed",
            "attn_decode_mla_absorbed_workspace_bytes", "mla_unabsorb_out", "attn_decode_mla_absorbed_paged",
-           "attn_rope_interleaved_qk", "gqa_rope_frequencies", "attn_qk_norm_rope", "kv_append_paged_rows")
+           "attn_rope_interleaved_qk", "gqa_rope_frequencies", "attn_qk_norm_rope", "kv_append_paged_rows",
+           "attn_decode_shared_prefix", "attn_decode_shared_prefix_workspace_bytes", "attn_cross",
+           "attn_cross_workspace_bytes")
 
 
 class GqaArms(ctypes.Structure):
@@ -98,6 +100,8 @@ def load(path: str = None):
         "attn_decode_mla_absorbed": [P, P, P, P, I, I, I, I, I, F, I, P, S, P],
         "mla_unabsorb_out": [P, P, P, I, I, I, I, I, P],
         "attn_decode_mla_absorbed_paged": [P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, S, P],
+        "attn_decode_shared_prefix": [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, P, S, P, P],
+        "attn_cross": [P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, S, P],
         "gqa_rope_frequencies": [P, P, I, D, P],
         "attn_qk_norm_rope": [P, P, P, P, P, P, F, P, I, I, I, I, I, P, I, P],
         "kv_append_paged_rows": [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P, F, P, I, P],
@@ -110,6 +114,10 @@ def load(path: str = None):
     lib.attn_decode_workspace_bytes.restype = S
     lib.attn_decode_mla_absorbed_workspace_bytes.argtypes = [I, I, I, I]
     lib.attn_decode_mla_absorbed_workspace_bytes.restype = S
+    lib.attn_decode_shared_prefix_workspace_bytes.argtypes = [I] * 6
+    lib.attn_decode_shared_prefix_workspace_bytes.restype = S
+    lib.attn_cross_workspace_bytes.argtypes = [I] * 8
+    lib.attn_cross_workspace_bytes.restype = S
     lib.gqa_status_string.argtypes = [I]
     lib.gqa_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -391,6 +399,69 @@ def _weight(w, d):
     if w is not None and tuple(w.shape) != (d,):
         raise ValueError(f"a norm weight must be [{d}], got {tuple(w.shape)}")
     return _p(w)
+
+
+def attn_decode_shared_prefix_workspace_bytes(B, H, Hkv, d_v, max_len, n_groups):
+    return int(load().attn_decode_shared_prefix_workspace_bytes(B, H, Hkv, d_v, max_len, n_groups))
+
+
+def shared_prefix_workspace(B, H, Hkv, d_v, max_len, n_groups, device="cuda"):
+    """A workspace tensor of the size attn_decode_shared_prefix needs (max_len: rows a table row can name)."""
+    n = attn_decode_shared_prefix_workspace_bytes(B, H, Hkv, d_v, max_len, n_groups)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def attn_decode_shared_prefix(q, k_pool, v_pool, block_tables, seq_lens, group_starts, shared_blocks, out,
+                              attention_scale, workspace, stream=None, window=0, softcap=0.0, sinks=None,
+                              alibi_slopes=None):
+    """attn_decode_paged for a batch in groups: sequences group_starts[g] .. group_starts[g + 1] - 1
+    (int32 [n_groups + 1]) share their tables' first shared_blocks[g] (int32 [n_groups]) blocks, whose
+    rows are read once a group. q [B, H, dk]; pools [num_blocks, Hkv, bs, d]; block_tables int32
+    [B, mbps]; workspace from shared_prefix_workspace; window / softcap / sinks / alibi_slopes: the arms."""
+    B, H, dk = q.shape
+    nb, Hkv, bs, dv = v_pool.shape
+    n = shared_blocks.shape[0]
+    if (tuple(k_pool.shape) != (nb, Hkv, bs, dk) or tuple(out.shape) != (B, H, dv) or block_tables.shape[0] != B or
+            seq_lens.numel() != B or group_starts.numel() != n + 1):
+        raise ValueError("q, the pools, the tables, the lengths, the groups and out do not agree")
+    _here(q, k_pool, v_pool, block_tables, seq_lens, group_starts, shared_blocks, out, workspace, sinks, alibi_slopes)
+    if any(x is not None and x.numel() != H for x in (sinks, alibi_slopes)):
+        raise ValueError("sinks and alibi_slopes must be float32 [H]")
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().attn_decode_shared_prefix(
+        _p(q), _p(k_pool), _p(v_pool), _i32(block_tables), _i32(seq_lens), _i32(group_starts), _i32(shared_blocks),
+        _p(out), B, n, block_tables.shape[1], nb, bs, H, Hkv, dk, dv, float(attention_scale),
+        _dtype(q, k_pool, v_pool, out), _p(workspace), ws, _arms(window, softcap, sinks, alibi_slopes),
+        _stream(stream)), "attn_decode_shared_prefix")
+    return out
+
+
+def attn_cross_workspace_bytes(B, seq_q, seq_kv_max, H, Hkv, d_k, d_v, dtype=torch.bfloat16):
+    return int(load().attn_cross_workspace_bytes(B, seq_q, seq_kv_max, H, Hkv, d_k, d_v,
+                                                 BF16 if dtype == torch.bfloat16 else F32))
+
+
+def cross_workspace(B, seq_q, H, Hkv, d_k, d_v, seq_kv_max, dtype=torch.bfloat16, device="cuda"):
+    """A workspace tensor of the size attn_cross needs (None when none)."""
+    n = attn_cross_workspace_bytes(B, seq_q, seq_kv_max, H, Hkv, d_k, d_v, dtype)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def attn_cross(q, k, v, out, attention_scale, kv_lens=None, workspace=None, stream=None):
+    """Every row sees all keys of its sequence: q [B, S, H, dk], k [B, Hkv, L, dk], v [B, Hkv, L, dv],
+    out [B, S, H, dv]; kv_lens int32 [B] (None: L; a sequence of 0 keys gets zeros); workspace from
+    cross_workspace."""
+    B, S, H, dk = q.shape
+    _, Hkv, L, dv = v.shape
+    if (tuple(k.shape) != (B, Hkv, L, dk) or v.shape[0] != B or tuple(out.shape) != (B, S, H, dv) or
+            (kv_lens is not None and kv_lens.numel() != B)):
+        raise ValueError("q, k, v, kv_lens and out do not agree")
+    _here(q, k, v, out, kv_lens, workspace)
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().attn_cross(_p(q), _p(k), _p(v), _i32(kv_lens), _p(out), B, S, L, H, Hkv, dk, dv,
+                             float(attention_scale), _dtype(q, k, v, out), _p(workspace), ws, _stream(stream)),
+           "attn_cross")
+    return out
 
 
 def rope_frequencies(rot_dim, theta, scaling="none", factor=1.0, original_max=0.0, low=1.0, high=4.0, magnitude=0.0,

@@ -320,6 +320,360 @@ gqa_status attn_prefill_paged(const void* q, const void* k_pool, const void* v_p
                                num_blocks, block_size, H, Hkv, d_k, d_v, attention_scale, dt, nullptr, stream);
 }
 
+// ---- attn_decode_shared_prefix ------------------------------------------------
+namespace {
+
+// The workspace of a shared-prefix step: header, the plan's arrays, the units of the
+// prefixes with their partial results, then the own rows' split-K plan and results.
+struct SharedLayout {
+  int GH, RPT, n_hchunks, max_units, max_splits;
+  size_t groups, group_of, kv_lo, units, partial, rows, rows_partial, bytes;
+};
+
+SharedLayout shared_layout(int B, int H, int Hkv, int d_v, int capacity, int n_groups) {
+  SharedLayout s{};
+  const int G = H / Hkv;
+  gqa::dense_rows(G, &s.GH, &s.RPT);
+  s.n_hchunks = G / s.GH;
+  s.max_splits = ceil_div(capacity, gqa::kSplitRows);
+  // row tiles of the groups that count (two members or more), then as many key ranges
+  // more as two waves of the SMs take, or as the longest unit makes necessary
+  const int counted = n_groups < B / 2 ? n_groups : B / 2;
+  const long long tiles = (long long)Hkv * s.n_hchunks * (B / s.RPT + counted);
+  const long long longest = (long long)gqa::kDenseMaxUnitTiles * 128;
+  const long long units = counted ? tiles * ((capacity + longest - 1) / longest) + 2 * gqa::kDenseSms : 0;
+  s.max_units = units > INT_MAX ? INT_MAX : (int)units;
+  size_t at = 256;  // [0]: units listed
+  const auto take = [&](size_t n) {
+    const size_t a = at;
+    at += gqa::round_up256(n);
+    return a;
+  };
+  s.groups = take((size_t)n_groups * sizeof(gqa::DenseGroup));
+  s.group_of = take((size_t)B * 4);
+  s.kv_lo = take((size_t)B * 4);
+  s.units = take((size_t)s.max_units * sizeof(gqa::DenseUnit));
+  s.partial = take((size_t)s.max_units * 128 * (size_t)(d_v + 2) * 4);
+  const size_t row_units = (size_t)B * (size_t)H * (size_t)s.max_splits;
+  s.rows = take(gqa::plan_bytes(row_units));
+  s.rows_partial = take(row_units * (size_t)(d_v + 2) * 4);
+  s.bytes = at;
+  return s;
+}
+
+}  // namespace
+
+size_t attn_decode_shared_prefix_workspace_bytes(int B, int H, int Hkv, int d_v, int max_len, int n_groups) {
+  if (B <= 0 || !heads_ok(H, Hkv) || d_v <= 0 || max_len <= 0 || n_groups < 0) return 0;
+  return shared_layout(B, H, Hkv, d_v, max_len, n_groups).bytes;
+}
+
+gqa_status attn_decode_shared_prefix(const void* q, const void* k_pool, const void* v_pool,
+                                     const int32_t* block_tables, const int32_t* seq_lens,
+                                     const int32_t* group_starts, const int32_t* shared_blocks, void* out, int B,
+                                     int n_groups, int max_blocks_per_seq, int num_blocks, int block_size, int H,
+                                     int Hkv, int d_k, int d_v, float attention_scale, gqa_dtype dt, void* workspace,
+                                     size_t workspace_bytes, const gqa_arms* arms, void* stream) {
+  const int bf16 = dtype_flag(dt);
+  if (bf16 < 0 || B < 0 || n_groups < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || block_size <= 0 ||
+      !heads_ok(H, Hkv) || !width_ok(d_k) || !width_ok(d_v))
+    return GQA_ERR_INVALID_ARG;
+  if ((long long)max_blocks_per_seq * block_size > INT_MAX / 2) return GQA_ERR_INVALID_ARG;
+  if (B == 0) return GQA_OK;
+  if (!q || !k_pool || !v_pool || !block_tables || !seq_lens || !out) return GQA_ERR_INVALID_ARG;
+  if (n_groups > 0 && (!group_starts || !shared_blocks)) return GQA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return GQA_ERR_INVALID_ARG;
+  const int capacity = max_blocks_per_seq * block_size;
+  const SharedLayout s = shared_layout(B, H, Hkv, d_v, capacity, n_groups);
+  if (!workspace || workspace_bytes < s.bytes) return GQA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return GQA_ERR_INVALID_ARG;
+  gqa::RowsParams p{};
+  bool arms_on;
+  const gqa_status sa = apply_arms(p, arms, &arms_on);
+  if (sa != GQA_OK) return sa;
+  // Nothing to share, or a shape that the tensor-core kernel does not take: every
+  // sequence reads its whole history, as attn_decode_paged.
+  if (n_groups == 0 || !gqa::dense_tc_supported(bf16, d_k, d_v, block_size) || !(attention_scale > 0.f))
+    return attn_decode_paged_ex(q, k_pool, v_pool, block_tables, seq_lens, out, B, max_blocks_per_seq, num_blocks,
+                                block_size, H, Hkv, d_k, d_v, attention_scale, dt,
+                                static_cast<char*>(workspace) + s.rows, workspace_bytes - s.rows, arms, stream);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  p.q = q;
+  p.k = k_pool;
+  p.v = v_pool;
+  p.out = out;
+  p.kv_len = seq_lens;
+  p.tables = block_tables;
+  p.paged = 1;
+  p.B = B;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.capacity = capacity;
+  p.mbps = max_blocks_per_seq;
+  p.bs = block_size;
+  p.num_blocks = num_blocks;
+  p.qscale = attention_scale * gqa::kLog2e;
+  const int nvmax = gqa::rows_max_nv(bf16, d_k, d_v, 0);
+  p.G = H / Hkv;
+  p.GH = pow2_divisor(p.G, nvmax);
+  p.QR = 1;
+  p.n_hchunks = p.G / p.GH;
+  p.n_rblocks = 1;
+  p.seq_q = 1;
+  p.split_rows = gqa::kSplitRows;
+  p.max_splits = s.max_splits;
+  const size_t row_units = (size_t)B * (size_t)H * (size_t)s.max_splits;
+  p.sched = reinterpret_cast<int*>(ws + s.rows);
+  p.units = reinterpret_cast<int2*>(ws + s.rows + gqa::kPlanHeaderBytes);
+  p.partial = reinterpret_cast<float*>(ws + s.rows_partial);
+  p.kv_lo = reinterpret_cast<int32_t*>(ws + s.kv_lo);
+  if (row_units > (size_t)INT_MAX) return GQA_ERR_INVALID_ARG;
+  p.err = error_word();
+  if (!p.err) return GQA_ERR_CUDA;
+  p.debug_withhold = g_withhold_first_tile;
+
+  gqa::SharedPlan plan{};
+  plan.group_starts = group_starts;
+  plan.shared_blocks = shared_blocks;
+  plan.n_groups = n_groups;
+  plan.max_units = s.max_units;
+  plan.GH = s.GH;
+  plan.RPT = s.RPT;
+  plan.n_hchunks = s.n_hchunks;
+  plan.groups = reinterpret_cast<gqa::DenseGroup*>(ws + s.groups);
+  plan.group_of = reinterpret_cast<int32_t*>(ws + s.group_of);
+  plan.kv_lo = reinterpret_cast<int32_t*>(ws + s.kv_lo);
+  plan.units = reinterpret_cast<gqa::DenseUnit*>(ws + s.units);
+  plan.n_units = reinterpret_cast<int*>(ws);
+  cudaError_t e = gqa::launch_shared_plan(p, plan, st);
+  if (e != cudaSuccess) return from_cuda(e);
+
+  gqa::DenseParams d{};
+  d.H = H;
+  d.Hkv = Hkv;
+  d.G = p.G;
+  d.GH = s.GH;
+  d.RPT = s.RPT;
+  d.n_hchunks = s.n_hchunks;
+  d.n_i = B;
+  d.S_kv = capacity;
+  d.units = plan.units;
+  d.n_units = plan.n_units;
+  d.seq_lens = seq_lens;
+  d.tables = block_tables;
+  d.mbps = max_blocks_per_seq;
+  d.bs = block_size;
+  d.num_blocks = num_blocks;
+  d.partial = reinterpret_cast<float*>(ws + s.partial);
+  d.out = static_cast<__nv_bfloat16*>(out);
+  d.qscale = p.qscale;
+  d.err = p.err;
+  d.debug_withhold = g_withhold_first_tile;
+  d.window = p.window;
+  d.cap_out = p.softcap2;
+  d.cap_in = p.softcap2 > 0.f ? p.qscale / p.softcap2 : 0.f;
+  d.alibi = p.alibi;
+  const bool score_arms = p.window > 0 || p.softcap2 > 0.f || p.alibi;  // sinks join in the combine
+  e = gqa::launch_dense_tc(q, k_pool, v_pool, d, 1, d_k, d_v, s.max_units, score_arms, st);
+  if (e != cudaSuccess) return from_cuda(e);
+  e = gqa::launch_attn_rows_bf16(p, d_k, d_v, 0, p.GH, st);
+  if (e != cudaSuccess) return from_cuda(e);
+
+  gqa::DenseCombine c{};
+  c.n_rows = (long long)B * H;
+  c.H = H;
+  c.Hkv = Hkv;
+  c.G = p.G;
+  c.GH = s.GH;
+  c.RPT = s.RPT;
+  c.n_hchunks = s.n_hchunks;
+  c.n_i = B;
+  c.dv = d_v;
+  c.partial = d.partial;
+  c.groups = plan.groups;
+  c.group_of = plan.group_of;
+  c.kv_lo = plan.kv_lo;
+  c.seq_lens = seq_lens;
+  c.rows_partial = p.partial;
+  c.max_splits = p.max_splits;
+  c.split_rows = p.split_rows;
+  c.capacity = capacity;
+  c.window = p.window;
+  c.sinks = p.sinks;
+  c.out = d.out;
+  return from_cuda(gqa::launch_dense_combine(c, st));
+}
+
+// ---- attn_cross ----------------------------------------------------------------
+namespace {
+
+// How a cross attention runs: on the tensor cores (row tiles and key ranges), or on
+// the SIMT kernel (splits of one query row's keys), with the workspace of each.
+struct CrossPlan {
+  bool tc;
+  int GH, RPT, n_hchunks, n_tiles, n_splits, split_tiles;
+  long long units;
+  int simt_GH, simt_QR, split_rows, max_splits;
+  size_t bytes;
+};
+
+// Rows of a KV head (query rows times heads of its group) from which the tensor cores
+// are taken.
+constexpr int kCrossTcRows = 16;
+
+bool cross_plan(int B, int S, int L, int H, int Hkv, int d_k, int d_v, int bf16, bool scale_ok, CrossPlan* c) {
+  *c = CrossPlan{};
+  const int G = H / Hkv;
+  c->tc = scale_ok && gqa::dense_tc_supported(bf16, d_k, d_v) && (long long)S * G >= kCrossTcRows;
+  if (c->tc) {
+    gqa::dense_rows(G, &c->GH, &c->RPT);
+    c->n_hchunks = G / c->GH;
+    c->n_tiles = ceil_div(S, c->RPT);
+    const long long tiles = (long long)B * Hkv * c->n_hchunks * c->n_tiles;
+    const int nt = ceil_div(L, 128);
+    // key ranges of st tiles: the fewest waves * (st + a unit's own cost); one range
+    // writes the result itself, more leave partial results to join (a further cost)
+    long long best = -1;
+    for (int ns = 1; ns <= nt && (ns == 1 || tiles * ns <= 4 * gqa::kDenseSms); ++ns) {
+      const int st = ceil_div(nt, ns), n = ceil_div(nt, st);
+      const long long waves = (tiles * n + gqa::kDenseSms - 1) / gqa::kDenseSms;
+      const long long cost = waves * (st + gqa::kDenseUnitTiles) + (n > 1 ? 2 : 0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        c->n_splits = n;
+        c->split_tiles = st;
+      }
+    }
+    c->units = tiles * c->n_splits;
+    c->bytes = c->n_splits > 1 ? (size_t)c->units * 128 * (size_t)(d_v + 2) * 4 : 0;
+    return true;
+  }
+  const int nvmax = gqa::rows_max_nv(bf16, d_k, d_v, 0);
+  if (nvmax == 0) return false;
+  c->simt_GH = pow2_divisor(G, nvmax);
+  c->simt_QR = 1;
+  while (c->simt_GH * c->simt_QR * 2 <= nvmax && c->simt_QR < S) c->simt_QR *= 2;
+  c->split_rows = L;
+  c->max_splits = 1;
+  if (S == 1) {
+    // splits of 2048 keys, halved down to 256 while they would leave SMs without work
+    const long long items = (long long)B * Hkv * (G / c->simt_GH);
+    int r = gqa::kSplitRows;
+    while (r > 256 && items * ceil_div(L, r) < 2 * gqa::kDenseSms) r /= 2;
+    c->max_splits = ceil_div(L, r);
+    if (c->max_splits > 1) {
+      c->split_rows = r;
+      const size_t units = (size_t)B * (size_t)H * (size_t)c->max_splits;
+      c->bytes = gqa::plan_bytes(units) + units * (size_t)(d_v + 2) * 4;
+    }
+  }
+  return true;
+}
+
+}  // namespace
+
+size_t attn_cross_workspace_bytes(int B, int seq_q, int seq_kv_max, int H, int Hkv, int d_k, int d_v, gqa_dtype dt) {
+  const int bf16 = dtype_flag(dt);
+  if (bf16 < 0 || B <= 0 || seq_q <= 0 || seq_kv_max <= 0 || !heads_ok(H, Hkv) || !width_ok(d_k) || !width_ok(d_v))
+    return 0;
+  size_t n = 0;
+  for (int scale_ok = 0; scale_ok < 2; ++scale_ok) {  // (a scale that is not positive takes the SIMT kernel)
+    CrossPlan c;
+    if (cross_plan(B, seq_q, seq_kv_max, H, Hkv, d_k, d_v, bf16, scale_ok, &c) && c.bytes > n) n = c.bytes;
+  }
+  return n;
+}
+
+gqa_status attn_cross(const void* q, const void* k, const void* v, const int32_t* kv_lens, void* out, int B, int seq_q,
+                      int seq_kv_max, int H, int Hkv, int d_k, int d_v, float attention_scale, gqa_dtype dt,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  const int bf16 = dtype_flag(dt);
+  if (bf16 < 0 || B < 0 || seq_q < 0 || seq_kv_max <= 0 || seq_kv_max > INT_MAX / 2 || !heads_ok(H, Hkv) ||
+      !width_ok(d_k) || !width_ok(d_v) || (long long)B * seq_q > INT_MAX || !std::isfinite(attention_scale))
+    return GQA_ERR_INVALID_ARG;
+  if (B == 0 || seq_q == 0) return GQA_OK;
+  if (!q || !k || !v || !out) return GQA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return GQA_ERR_INVALID_ARG;
+  CrossPlan c;
+  if (!cross_plan(B, seq_q, seq_kv_max, H, Hkv, d_k, d_v, bf16, attention_scale > 0.f, &c)) return GQA_ERR_UNSUPPORTED;
+  if (c.bytes > 0) {
+    if (!workspace || workspace_bytes < c.bytes) return GQA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return GQA_ERR_INVALID_ARG;
+  }
+  unsigned* err = error_word();
+  if (!err) return GQA_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const float qscale = attention_scale * gqa::kLog2e;
+  if (c.tc) {
+    gqa::DenseParams d{};
+    d.H = H;
+    d.Hkv = Hkv;
+    d.G = H / Hkv;
+    d.GH = c.GH;
+    d.RPT = c.RPT;
+    d.n_hchunks = c.n_hchunks;
+    d.n_i = seq_q;
+    d.S_kv = seq_kv_max;
+    d.kv_lens = kv_lens;
+    d.n_tiles = c.n_tiles;
+    d.n_splits = c.n_splits;
+    d.split_tiles = c.split_tiles;
+    d.partial = c.n_splits > 1 ? static_cast<float*>(workspace) : nullptr;
+    d.out = static_cast<__nv_bfloat16*>(out);
+    d.qscale = qscale;
+    d.err = err;
+    d.debug_withhold = g_withhold_first_tile;
+    const cudaError_t e = gqa::launch_dense_tc(q, k, v, d, B, d_k, d_v, c.units, false, st);
+    if (e != cudaSuccess || c.n_splits == 1) return from_cuda(e);
+    gqa::DenseCombine m{};
+    m.n_rows = (long long)B * seq_q * H;
+    m.H = H;
+    m.Hkv = Hkv;
+    m.G = d.G;
+    m.GH = c.GH;
+    m.RPT = c.RPT;
+    m.n_hchunks = c.n_hchunks;
+    m.n_i = seq_q;
+    m.dv = d_v;
+    m.n_tiles = c.n_tiles;
+    m.n_splits = c.n_splits;
+    m.partial = d.partial;
+    m.out = d.out;
+    return from_cuda(gqa::launch_dense_combine(m, st));
+  }
+  gqa::RowsParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.out = out;
+  p.kv_len = kv_lens;
+  p.full = 1;
+  p.B = B;
+  p.seq_q = seq_q;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.max_len = seq_kv_max;
+  p.capacity = seq_kv_max;
+  p.G = H / Hkv;
+  p.GH = c.simt_GH;
+  p.QR = c.simt_QR;
+  p.n_hchunks = p.G / p.GH;
+  p.n_rblocks = ceil_div(seq_q, p.QR);
+  p.split_rows = c.split_rows;
+  p.max_splits = c.max_splits;
+  p.qscale = qscale;
+  p.err = err;
+  p.debug_withhold = g_withhold_first_tile;
+  if (c.max_splits > 1) {
+    const size_t units = (size_t)B * (size_t)H * (size_t)c.max_splits;
+    p.sched = static_cast<int*>(workspace);
+    p.units = reinterpret_cast<int2*>(static_cast<char*>(workspace) + gqa::kPlanHeaderBytes);
+    p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + gqa::plan_bytes(units));
+  }
+  return launch_rows(p, bf16, d_k, d_v, 0, p.GH * p.QR, st);
+}
+
 gqa_status kv_append_paged(void* q, const void* k_new, const void* v_new, void* k_pool, void* v_pool,
                            const int32_t* block_tables, const int32_t* seq_lens_in, int32_t* seq_lens_out, int B,
                            int max_blocks_per_seq, int num_blocks, int block_size, int H, int Hkv, int d_k, int d_v,

@@ -240,7 +240,8 @@ struct Unit {
   int b, kvh, hc, split;
   int kv_len, i0, i_last;
   int r0, r1;   // key rows [r0, r1) of this split
-  int lo;       // first key the unit's first row sees (the window's lower end)
+  int lo;       // first key the unit's first row sees (the window's lower end) and this call reads
+  int own_lo;   // first key of the sequence that this call reads (RowsParams::kv_lo)
   int nsplit;   // splits of the item that hold a visible key
   bool len_ok;
 };
@@ -254,13 +255,15 @@ __device__ __forceinline__ Unit decode_unit(const RowsParams& p, int item, int s
   item /= p.n_hchunks;
   u.kvh = item % p.Hkv;
   u.b = item / p.Hkv;
-  u.kv_len = p.kv_len ? __ldg(p.kv_len + u.b) : (p.offsets ? __ldg(p.offsets + u.b) : 0) + p.seq_q;
+  u.kv_len = rows_kv_len(p, u.b);
   u.i0 = rb * p.QR;
   u.i_last = min(u.i0 + p.QR, p.seq_q) - 1;
-  u.len_ok = u.kv_len >= p.seq_q && u.kv_len >= 1 && u.kv_len <= p.capacity;
-  const int kv_hi = u.len_ok ? u.kv_len - p.seq_q + u.i_last + 1 : 0;  // keys the last row sees
-  u.lo = u.len_ok ? first_visible_key(u.kv_len - p.seq_q + u.i0, p.window) : 0;
+  u.len_ok = rows_len_ok(p, u.kv_len);
+  const int kv_hi = u.len_ok ? rows_limit(p, u.kv_len, u.i_last) : 0;  // keys the last row sees
+  u.own_lo = p.kv_lo ? __ldg(p.kv_lo + u.b) : 0;
+  u.lo = u.len_ok ? max(first_visible_key(u.kv_len - p.seq_q + u.i0, p.window), u.own_lo) : 0;
   u.nsplit = (kv_hi + p.split_rows - 1) / p.split_rows - u.lo / p.split_rows;
+  if (u.own_lo > 0) u.nsplit = max(u.nsplit, 2);  // never the whole result: always a partial one
   u.r0 = split * p.split_rows;
   u.r1 = min(u.r0 + p.split_rows, kv_hi);
   return u;
@@ -348,8 +351,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
       }
       const Unit u = decode_unit(p, item, split);
       if (!u.len_ok) {
-        // Length out of range: record it, write zeros, touch no K/V.
-        if (lane == 0 && split == 0 && item % (p.Hkv * p.n_hchunks * p.n_rblocks) == 0)
+        // Length out of range: record it, write zeros, touch no K/V (no keys at all,
+        // where the call allows that: zeros are the result).
+        if (lane == 0 && split == 0 && item % (p.Hkv * p.n_hchunks * p.n_rblocks) == 0 && !(p.full && u.kv_len == 0))
           raise_error(p.err, kErrBounds);
         for (int idx = lane; idx < NV * DV; idx += 32) {
           const int vh = idx / DV;
@@ -534,9 +538,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
         for (int e = 0; e < H2V; ++e) o2[vh][e] = make_float2(0.f, 0.f);
         const int iq = u.i0 + vh / p.GH;
         if (vh == own) {
-          lim_own = iq <= u.i_last ? u.kv_len - p.seq_q + iq + 1 : 0;
+          lim_own = iq <= u.i_last ? rows_limit(p, u.kv_len, iq) : 0;
           if (ARMS) {
-            lo_own = first_visible_key(lim_own - 1, p.window);
+            lo_own = max(first_visible_key(lim_own - 1, p.window), u.own_lo);
             slope2 = p.alibi ? __ldg(p.alibi + u.kvh * p.G + u.hc * p.GH + vh % p.GH) * kLog2e : 0.f;
           }
         }
@@ -719,7 +723,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
       }
       const size_t row = unit_out_row(p, u, vh);
       if (u.nsplit == 1) {
-        float res = ls > 0.f ? os / ls : 0.f;
+        // (without a causal rule a NaN among a row's scores reaches its output)
+        float res = (p.full ? ls != 0.f : ls > 0.f) ? os / ls : 0.f;
         if (ARMS && p.sinks) {  // the sink logit joins the denominator (once per row and head)
           const float z2 = __ldg(p.sinks + u.kvh * p.G + u.hc * p.GH + vh % p.GH) * kLog2e;
           const float Mx = fmaxf(M, z2);
@@ -781,7 +786,7 @@ cudaError_t launch_rows_inst_arms(const RowsParams& p, cudaStream_t st) {
 
 template <typename ET, int DK, int DV, int DROT, int NV>
 cudaError_t launch_rows_inst(const RowsParams& p, cudaStream_t st) {
-  const bool arms = p.window > 0 || p.softcap2 > 0.f || p.sinks || p.alibi;
+  const bool arms = p.window > 0 || p.softcap2 > 0.f || p.sinks || p.alibi || p.kv_lo;  // kv_lo masks as a window does
   return arms ? launch_rows_inst_arms<ET, DK, DV, DROT, NV, true>(p, st)
               : launch_rows_inst_arms<ET, DK, DV, DROT, NV, false>(p, st);
 }

@@ -2,6 +2,7 @@
 // libgqa_attn.so (not part of the public ABI; see include/gqa_attn.h).
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -50,7 +51,25 @@ struct RowsParams {
   float softcap2;           // softcap * log2(e) (the kernels score in the log2 domain); 0: none
   const float* sinks;       // [H] device, natural units, or NULL
   const float* alibi;       // [H] device, natural units, or NULL
+  // Shared-prefix step: the keys of sequence b below kv_lo[b] are another kernel's;
+  // a sequence with kv_lo[b] > 0 always leaves partial results (NULL: all zero).
+  const int32_t* kv_lo;
+  // No causal rule (attn_cross): every row sees all keys of its sequence, which may
+  // hold none (its rows are zeros); kv_len NULL stands for `capacity` keys.
+  int full;
 };
+
+// Keys present in sequence b, and whether the call takes that many.
+__host__ __device__ inline int rows_kv_len(const RowsParams& p, int b) {
+  return p.kv_len ? p.kv_len[b] : p.full ? p.capacity : (p.offsets ? p.offsets[b] : 0) + p.seq_q;
+}
+__host__ __device__ inline bool rows_len_ok(const RowsParams& p, int kv_len) {
+  return (p.full || kv_len >= p.seq_q) && kv_len >= 1 && kv_len <= p.capacity;
+}
+// Keys that query row i sees (the row's own limit; window apart).
+__host__ __device__ inline int rows_limit(const RowsParams& p, int kv_len, int i) {
+  return p.full ? kv_len : kv_len - p.seq_q + i + 1;
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -143,6 +162,91 @@ cudaError_t launch_prefill_tc(const void* q, const void* k, const void* v, void*
                               int debug_withhold = 0);
 // bs = 0: contiguous K/V; else the pool's block size and max blocks per sequence.
 bool prefill_tc_supported(int bf16, int dk, int dv, int bs = 0, int mbps = 0);
+
+// ---- attention without a causal rule on tcgen05 (dense_tc.cu) -----------------
+// One unit of work: rows i0 .. i0 + n_i - 1 of heads head0 .. head0 + GH - 1 against
+// key tiles t0 .. t1 - 1 of 128 keys, keys below kv_hi; seq is the sequence whose
+// keys (table row) are read.
+struct alignas(16) DenseUnit {
+  int i0, n_i, head0, seq;
+  int t0, t1, kv_hi, kvh;
+};
+
+// A group of sequences with a shared prefix: its members from `first` on, its units
+// (KV head, head chunk, row tile, key range, ranges fastest) from unit0 on.
+struct alignas(16) DenseGroup {
+  int first, members, tiles, n_splits;
+  int unit0, kv_hi, t_lo, pad;
+};
+
+struct DenseParams {
+  int H, Hkv, G;
+  int GH, RPT, n_hchunks;  // rows of a tile: RPT rows i x GH heads (dense_rows)
+  int n_i;                 // rows i of a sequence (attn_cross: seq_q; shared prefix: B)
+  int S_kv;                // keys a sequence can hold
+  // attn_cross: units from the block index, key ranges of split_tiles tiles
+  const int32_t* kv_lens;  // [B] or NULL: S_kv
+  int n_tiles, n_splits, split_tiles;
+  // shared prefix: units from the plan, a length per row
+  const DenseUnit* units;
+  const int* n_units;
+  const int32_t* seq_lens;
+  const int32_t* tables;   // paged pools (NULL: contiguous)
+  int mbps, bs, num_blocks;
+  float* partial;          // per unit 128 * (d_v + 2) floats, or NULL: final results to out
+  __nv_bfloat16* out;
+  float qscale;
+  unsigned* err;
+  int debug_withhold;
+  int window;              // the arms, as for the tensor-core prefill
+  float cap_in, cap_out;
+  const float* alibi;
+};
+
+// Heads of a group per row tile (the largest divisor of G that is at most 128) and
+// rows i per tile.
+void dense_rows(int G, int* GH, int* RPT);
+bool dense_tc_supported(int bf16, int dk, int dv, int bs = 0);
+cudaError_t launch_dense_tc(const void* q, const void* k, const void* v, const DenseParams& p, int n_b, int dk, int dv,
+                            long long units, bool arms, cudaStream_t st);
+
+struct DenseCombine {
+  long long n_rows;        // B * n_i * H output rows
+  int H, Hkv, G, GH, RPT, n_hchunks, n_i, dv;
+  int n_tiles, n_splits;   // attn_cross
+  const float* partial;
+  // shared prefix
+  const DenseGroup* groups;
+  const int32_t* group_of;
+  const int32_t* kv_lo;
+  const int32_t* seq_lens;
+  const float* rows_partial;  // the own rows' partial results, as RowsParams
+  int max_splits, split_rows, capacity, window;
+  const float* sinks;
+  __nv_bfloat16* out;
+};
+cudaError_t launch_dense_combine(const DenseCombine& p, cudaStream_t st);
+
+// A plan's cost is counted in key tiles: what a unit takes beside its tiles (set-up,
+// the first tiles' latency, the epilogue and its share of the join).
+constexpr int kDenseUnitTiles = 3;
+constexpr int kDenseSms = 152;
+constexpr int kDenseMaxUnitTiles = 256;  // a unit's table entries fit the kernel's copy at every block size
+
+// The plan of a shared-prefix step: groups and first own keys, the units of the
+// prefixes, then the plan of the own rows (launch_plan_units).
+struct SharedPlan {
+  const int32_t* group_starts;   // [n_groups + 1]
+  const int32_t* shared_blocks;  // [n_groups]
+  int n_groups, max_units;
+  int GH, RPT, n_hchunks;
+  DenseGroup* groups;
+  int32_t* group_of;             // [B]: -1 without a prefix
+  int32_t* kv_lo;                // [B]
+  DenseUnit* units;
+  int* n_units;
+};
+cudaError_t launch_shared_plan(const RowsParams& p, const SharedPlan& s, cudaStream_t st);
 
 // Absorbed MLA decode on tcgen05 (bf16, d_c = 512, d_r = 64): attention of
 // q_abs [B, H, d_c + d_r] over the latent rows [B, max_len, d_c + d_r] (value =

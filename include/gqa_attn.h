@@ -205,6 +205,63 @@ gqa_status attn_prefill_paged_ex(const void* q, const void* k_pool, const void* 
                                  int num_blocks, int block_size, int H, int Hkv, int d_k, int d_v,
                                  float attention_scale, gqa_dtype dt, const gqa_arms* arms, void* stream);
 
+/*
+ * attn_decode_paged for a batch whose sequences share prefixes (one system prompt or
+ * document behind many requests): the result is that of attn_decode_paged_ex on the
+ * same arguments, up to the order of its sums, but the rows of a shared prefix are
+ * read once for a whole group of sequences instead of once for each.
+ *
+ *   q, k_pool, v_pool, block_tables, seq_lens, out, arms  as for attn_decode_paged_ex
+ *   group_starts   int32 [n_groups + 1], ascending, within 0..B: sequences
+ *                  group_starts[g] .. group_starts[g + 1] - 1 form group g; sequences
+ *                  before the first and behind the last group share nothing
+ *   shared_blocks  int32 [n_groups]: the first shared_blocks[g] entries of every member's
+ *                  table row name the same blocks (0 .. max_blocks_per_seq). The entries
+ *                  are read from the first member's row; the caller answers for the rest.
+ * A member may be shorter than the prefix: it sees the rows below its own length. A
+ * group of one member reads its rows itself. Groups out of order, or a prefix longer
+ * than a table row, share nothing and set the device error word.
+ * bf16 with (d_k, d_v) = (64, 64), (128, 128) or (192, 128), block_size a multiple of
+ * 8 dividing 128 and attention_scale > 0 runs the prefixes on the tcgen05 tensor-core
+ * kernel (the probabilities rounded to bf16 for the product with V); every other
+ * case reads every history whole, as attn_decode_paged does. How a prefix is split
+ * depends on the batch, so the last bits of a sequence's result do too; repeated
+ * calls give the same bits.
+ * workspace: at least attn_decode_shared_prefix_workspace_bytes(B, H, Hkv, d_v,
+ * max_blocks_per_seq * block_size, n_groups) bytes, 16-byte aligned, always needed;
+ * calls whose kernels may overlap must not share one.
+ */
+gqa_status attn_decode_shared_prefix(const void* q, const void* k_pool, const void* v_pool,
+                                     const int32_t* block_tables, const int32_t* seq_lens,
+                                     const int32_t* group_starts, const int32_t* shared_blocks, void* out, int B,
+                                     int n_groups, int max_blocks_per_seq, int num_blocks, int block_size, int H,
+                                     int Hkv, int d_k, int d_v, float attention_scale, gqa_dtype dt, void* workspace,
+                                     size_t workspace_bytes, const gqa_arms* arms, void* stream);
+/* Host only; launches nothing. */
+size_t attn_decode_shared_prefix_workspace_bytes(int B, int H, int Hkv, int d_v, int max_len, int n_groups);
+
+/*
+ * Cross attention: decoder rows against an encoder's keys and values of another
+ * length. No causal rule: every row of a sequence sees all of its keys.
+ *
+ *   q    [B, seq_q, H, d_k]; out [B, seq_q, H, d_v]
+ *   k    [B, Hkv, seq_kv_max, d_k], v [B, Hkv, seq_kv_max, d_v]; rows at or past a
+ *        sequence's length may hold anything
+ *   kv_lens  int32 [B] on the device, 0..seq_kv_max, or NULL for seq_kv_max; a sequence
+ *        without keys gets zeros. A length outside that range gives zeros and sets the
+ *        device error word.
+ * bf16 with (d_k, d_v) = (64, 64), (128, 128) or (192, 128), attention_scale > 0 and
+ * seq_q * H / Hkv >= 16 runs on the tcgen05 tensor-core kernel (the probabilities
+ * rounded to bf16 for the product with V), everything else on the SIMT kernel.
+ * workspace: at least attn_cross_workspace_bytes(..) bytes, 16-byte aligned (NULL
+ * allowed when that is 0); calls whose kernels may overlap must not share one.
+ */
+gqa_status attn_cross(const void* q, const void* k, const void* v, const int32_t* kv_lens, void* out, int B, int seq_q,
+                      int seq_kv_max, int H, int Hkv, int d_k, int d_v, float attention_scale, gqa_dtype dt,
+                      void* workspace, size_t workspace_bytes, void* stream);
+/* Host only; launches nothing. */
+size_t attn_cross_workspace_bytes(int B, int seq_q, int seq_kv_max, int H, int Hkv, int d_k, int d_v, gqa_dtype dt);
+
 /* Size of the fixed device scratch behind attn_decode_paged_static_workspace. */
 #define GQA_STATIC_WORKSPACE_BYTES ((size_t)16 << 20)
 

@@ -57,25 +57,31 @@ def rotate(x, positions, freqs, layout, rot_offset=0, magnitude=1.0):
 
 def attend(q, k, v, scale, window=0, softcap=0.0, sinks=None, slopes=None, position=None):
     """q [S, H, dk], k [Hkv, n, dk], v [Hkv, n, dv] of one sequence, every row seeing every
-    key (with a window or ALiBi slopes: all rows at `position`). No keys: zeros."""
+    key (with a window or ALiBi slopes: all rows at `position`). No keys: zeros. Returns
+    the output, and sum_j w_j |v_j| and the largest scale * sum_i |q_i k_ji| of each row:
+    the sizes that the arithmetic's errors go by."""
     S, H, _ = q.shape
     n, dv = v.shape[1], v.shape[2]
-    out = np.zeros((S, H, dv))
+    out, size, reach = np.zeros((S, H, dv)), np.zeros((S, H, dv)), np.zeros((S, H, 1))
+    if n == 0:
+        return out, size, reach
     G = H // k.shape[0]
     j = np.arange(n)
     for h in range(H):
-        s = scale * (q[:, h] @ k[h // G].T)
+        kh, vh = k[h // G], v[h // G]
+        s = scale * (q[:, h] @ kh.T)
+        reach[:, h, 0] = scale * (np.abs(q[:, h]) @ np.abs(kh).T).max(-1)
         if softcap > 0:
             s = softcap * np.tanh(s / softcap)
         if slopes is not None:
             s = s + slopes[h] * (j - position)
         if window > 0:
             s = np.where(j > position - window, s, -np.inf)
-        for i in range(S):
-            m = max(s[i].max() if n else -np.inf, -np.inf if sinks is None else sinks[h])
-            if m == -np.inf:
-                continue
-            w = np.exp(s[i] - m)
-            den = w.sum() + (0.0 if sinks is None else math.exp(sinks[h] - m))
-            out[i, h] = (w @ v[h // G]) / den
-    return out
+        m = s.max(-1, keepdims=True)
+        if sinks is not None:
+            m = np.maximum(m, sinks[h])
+        w = np.exp(s - m)
+        den = w.sum(-1, keepdims=True) + (0.0 if sinks is None else np.exp(sinks[h] - m))
+        out[:, h] = w @ vh / den
+        size[:, h] = w @ np.abs(vh) / den
+    return out, size, reach
