@@ -317,7 +317,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         alive = false;
         break;
       }
-      if (!warp_live) {  // padding rows: P may hold anything, only the barriers matter
+      if (!warp_live) {
+        // padding rows: P may hold anything, only the barriers matter. At d_v = 64 S_{j+2}
+        // is issued before PV_j, so this warp has to be held back here as the others are
+        // by P_w, or its second arrival on p_full would stand in for another warp's first.
+        if (!C::kAlias && k >= 1 && !warp_wait_tc(&bars->o_done[wg], (k - 1) & 1, bars, p.err)) {
+          alive = false;
+          break;
+        }
         if (lane == 0) {
           mbar_arrive(&bars->s_free[wg]);
           if (C::kAlias) mbar_arrive(&bars->p_half[wg]);

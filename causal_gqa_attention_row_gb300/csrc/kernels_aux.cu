@@ -339,7 +339,7 @@ cudaError_t launch_shared_plan(const RowsParams& p, const SharedPlan& s, cudaStr
 // ---------------------------------------------------------------------------
 // Split combine: out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the
 // splits of one (sequence, head), M = max_s m_s, in split order. Empty splits
-// (m = -inf) weigh zero. One warp per output row and group of up to 256
+// (m = -inf; without a causal rule l = 0, so that NaN goes through) weigh zero. One warp per output row and group of up to 256
 // columns (a 512-wide row takes two warps, which read the same (m, l) pairs).
 
 constexpr int kCombineCols = 256;  // output columns per warp
@@ -396,10 +396,10 @@ __global__ void __launch_bounds__(256) split_combine_kernel(const RowsParams p, 
 #pragma unroll
     for (int e = 0; e < kMaxE / 2; ++e) acc[e] = make_float2(0.f, 0.f);
     float dsum = 0.f;
-    if (M != -INFINITY) {
+    if (M != -INFINITY || p.full) {
 #pragma unroll
       for (int j = 0; j < kFast; ++j) {
-        const float w = (mk[j] == -INFINITY) ? 0.f : exp2f(mk[j] - M);
+        const float w = (p.full ? lk[j] == 0.f : mk[j] == -INFINITY) ? 0.f : exp2f(mk[j] - M);
         dsum = fmaf(w, lk[j], dsum);
 #pragma unroll
         for (int e = 0; e < kMaxE / 2; ++e) {
@@ -408,12 +408,13 @@ __global__ void __launch_bounds__(256) split_combine_kernel(const RowsParams p, 
         }
       }
     }
-    const float den = M == -INFINITY ? 0.f : (p.sinks ? exp2f(z2 - M) : 0.f) + dsum;
+    const float den = M == -INFINITY && !p.full ? 0.f : (p.sinks ? exp2f(z2 - M) : 0.f) + dsum;
 #pragma unroll
     for (int e = 0; e < kMaxE / 2; ++e) {
       const int d = 2 * lane + 64 * e;
       if (d >= DW) continue;
-      const float a = den > 0.f ? acc[e].x / den : 0.f, c = den > 0.f ? acc[e].y / den : 0.f;
+      const bool some = p.full ? den != 0.f : den > 0.f;
+      const float a = some ? acc[e].x / den : 0.f, c = some ? acc[e].y / den : 0.f;
       if constexpr (sizeof(ET) == 2)
         *reinterpret_cast<__nv_bfloat162*>(out + d) = __floats2bfloat162_rn(a, c);
       else
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(256) split_combine_kernel(const RowsParams p, 
   for (int s = s_lo + lane; s < n; s += 32) M = fmaxf(M, P[(size_t)s * stride]);
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if (M == -INFINITY) {
+  if (M == -INFINITY && !p.full) {
     for (int d = lane; d < DW; d += 32) out[d] = Elem<ET>::from_f32(0.f);
     return;
   }
@@ -441,8 +442,9 @@ __global__ void __launch_bounds__(256) split_combine_kernel(const RowsParams p, 
     float w = 0.f;
     if (s < n) {
       const float ms = P[(size_t)s * stride];
-      w = (ms == -INFINITY) ? 0.f : exp2f(ms - M);
-      den_part = fmaf(w, P[(size_t)s * stride + 1], den_part);
+      const float ls = P[(size_t)s * stride + 1];
+      w = (p.full ? ls == 0.f : ms == -INFINITY) ? 0.f : exp2f(ms - M);
+      den_part = fmaf(w, ls, den_part);
     }
     // The rows of up to kBatch splits are loaded before any of them is
     // accumulated, so that many loads are in flight per lane; the sum still
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(256) split_combine_kernel(const RowsParams p, 
   const float den = (p.sinks ? exp2f(z2 - M) : 0.f) + den_part;
 #pragma unroll
   for (int e = 0; e < kMaxE; ++e)
-    if (lane + 32 * e < DW) out[lane + 32 * e] = Elem<ET>::from_f32(den > 0.f ? acc[e] / den : 0.f);
+    if (lane + 32 * e < DW) out[lane + 32 * e] = Elem<ET>::from_f32((p.full ? den != 0.f : den > 0.f) ? acc[e] / den : 0.f);
 }
 
 cudaError_t launch_split_combine(const RowsParams& p, int dv, int bf16, cudaStream_t st) {

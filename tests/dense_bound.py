@@ -22,4 +22,5 @@ def excess(got, oracle, bf16, tensor_cores, dk, n, softcap=0.0):
         p = p + 2.0 ** -8
     store = 2.0 ** -8 if bf16 else 2.0 ** -24
     tol = store * np.abs(out) + (1 + store) * p * size
-    return float((err / (tol + 1e-37)).max())
+    worst = (err / (tol + 1e-37)).max()
+    return float("inf") if np.isnan(worst) else float(worst)
