@@ -8,6 +8,7 @@ If the shared library is missing, ``load()`` raises.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -151,8 +152,11 @@ def _i32(t):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # the handle of torch.cuda.current_stream() without building a Stream object for
+    # it, which took 3 us of a call's 14 on a Grace core
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _check(status, what):
@@ -368,21 +372,24 @@ def _here(*ts):
     """Check that the tensors live on the current CUDA device (calls launch there)."""
     dev = torch.cuda.current_device()
     for t in ts:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors must live on the current CUDA device")
 
 
-def _heads(t, ndim):
-    """`gqa_heads` of a [B, T, heads, d] (ndim 4) or [N, heads, d] (ndim 3) tensor
-    with a dense last axis and any other strides (an axis of one element has none)."""
+_pack_view = struct.Struct("4q").pack  # `gqa_heads`, which a call only reads
+
+
+def _view(t, ndim):
+    """The bytes of `gqa_heads` of a [B, T, heads, d] (ndim 4) or [N, heads, d] (ndim 3)
+    tensor with a dense last axis and any other strides; None stays None."""
     if t is None:
         return None
-    if t.dim() != ndim:
+    st = t.stride()
+    if len(st) != ndim:
         raise ValueError(f"expected {ndim} axes, got shape {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if st[-1] != 1:
         raise ValueError("the last axis must be dense")
-    st = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
-    return GqaHeads(t.data_ptr(), st[0] if ndim == 4 else 0, st[-3], st[-2])
+    return _pack_view(t.data_ptr(), *st[:3]) if ndim == 4 else _pack_view(t.data_ptr(), 0, st[0], st[1])
 
 
 def _ref(x):
@@ -391,12 +398,12 @@ def _ref(x):
 
 def _writes_once(*ts):
     for t in ts:
-        if t is not None and any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
+        if t is not None and 0 in t.stride() and any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
             raise ValueError("an output must not be broadcast")
 
 
 def _weight(w, d):
-    if w is not None and tuple(w.shape) != (d,):
+    if w is not None and w.shape != (d,):
         raise ValueError(f"a norm weight must be [{d}], got {tuple(w.shape)}")
     return _p(w)
 
@@ -421,7 +428,7 @@ def attn_decode_shared_prefix(q, k_pool, v_pool, block_tables, seq_lens, group_s
     B, H, dk = q.shape
     nb, Hkv, bs, dv = v_pool.shape
     n = shared_blocks.shape[0]
-    if (tuple(k_pool.shape) != (nb, Hkv, bs, dk) or tuple(out.shape) != (B, H, dv) or block_tables.shape[0] != B or
+    if (k_pool.shape != (nb, Hkv, bs, dk) or out.shape != (B, H, dv) or block_tables.shape[0] != B or
             seq_lens.numel() != B or group_starts.numel() != n + 1):
         raise ValueError("q, the pools, the tables, the lengths, the groups and out do not agree")
     _here(q, k_pool, v_pool, block_tables, seq_lens, group_starts, shared_blocks, out, workspace, sinks, alibi_slopes)
@@ -453,7 +460,7 @@ def attn_cross(q, k, v, out, attention_scale, kv_lens=None, workspace=None, stre
     cross_workspace."""
     B, S, H, dk = q.shape
     _, Hkv, L, dv = v.shape
-    if (tuple(k.shape) != (B, Hkv, L, dk) or v.shape[0] != B or tuple(out.shape) != (B, S, H, dv) or
+    if (k.shape != (B, Hkv, L, dk) or v.shape[0] != B or out.shape != (B, S, H, dv) or
             (kv_lens is not None and kv_lens.numel() != B)):
         raise ValueError("q, k, v, kv_lens and out do not agree")
     _here(q, k, v, out, kv_lens, workspace)
@@ -498,23 +505,28 @@ def attn_qk_norm_rope(q, k, q_out, k_out, positions, rope=None, q_weight=None, k
     none). q, q_out [B, T, H, d] and k, k_out [B, T, Hkv, d], of any strides with a dense
     last axis (a head-major cache [B, Hkv, T, d] goes in as k_out.transpose(1, 2)); q with
     q_out, or k with k_out, may be None. positions int32 [B, T]. Outputs may be the inputs."""
-    x = q if q is not None else k
-    if x is None:
+    if q is None and k is None:
         raise ValueError("neither queries nor keys given")
-    B, T, _, d = x.shape
-    for y, o in ((q, q_out), (k, k_out)):
-        if (y is None) != (o is None):
-            raise ValueError("an input and its output go together")
-        if y is not None and (y.shape != o.shape or y.shape[:2] != x.shape[:2] or y.shape[-1] != d):
-            raise ValueError("q, k and their outputs must agree in batch, tokens and width")
+    H = Hkv = 0
+    if q is not None:
+        B, T, H, d = q.shape
+    if k is not None:
+        kB, kT, Hkv, kd = k.shape
+        if q is None:
+            B, T, d = kB, kT, kd
+        elif (kB, kT, kd) != (B, T, d):
+            raise ValueError("q and k must agree in batch, tokens and width")
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("an input and its output go together")
+    if (q is not None and q_out.shape != q.shape) or (k is not None and k_out.shape != k.shape):
+        raise ValueError("an output must have its input's shape")
     _here(q, k, q_out, k_out, positions, q_weight, k_weight, rope.table if rope is not None else None)
     _writes_once(q_out, k_out)
     if positions is not None and positions.numel() != B * T:
         raise ValueError("positions must be [B, T]")
     _check(load().attn_qk_norm_rope(
-        _ref(_heads(q, 4)), _ref(_heads(k, 4)), _ref(_heads(q_out, 4)), _ref(_heads(k_out, 4)), _weight(q_weight, d),
-        _weight(k_weight, d), float(eps), _i32(positions), B, T, 0 if q is None else q.shape[2],
-        0 if k is None else k.shape[2], d, _ref(rope), _dtype(q, k, q_out, k_out, q_weight, k_weight),
+        _view(q, 4), _view(k, 4), _view(q_out, 4), _view(k_out, 4), _weight(q_weight, d),
+        _weight(k_weight, d), float(eps), _i32(positions), B, T, H, Hkv, d, _ref(rope), _dtype(q, k, q_out, k_out, q_weight, k_weight),
         _stream(stream)), "attn_qk_norm_rope")
     return q_out, k_out
 
@@ -528,21 +540,24 @@ def kv_append_paged_rows(q, k_new, v_new, q_out, k_pool, v_pool, block_tables, r
     tensor). Inputs of any strides with a dense last axis."""
     N, Hkv, dk = k_new.shape
     nb, _, bs, dv = v_pool.shape
-    B = seq_lens_in.shape[0]
-    if tuple(v_new.shape) != (N, Hkv, dv) or tuple(k_pool.shape) != (nb, Hkv, bs, dk) or v_pool.shape[1] != Hkv:
+    B, mbps = block_tables.shape
+    H = 0
+    if v_new.shape != (N, Hkv, dv) or k_pool.shape != (nb, Hkv, bs, dk) or v_pool.shape[1] != Hkv:
         raise ValueError("k_new, v_new and the pools do not agree")
-    if (q is None) != (q_out is None) or (q is not None and (q.shape != q_out.shape or q.shape[0] != N or
-                                                             q.shape[-1] != dk)):
-        raise ValueError("q and q_out must both be [N, H, dk]")
-    if row_starts.numel() != B + 1 or seq_lens_out.numel() != B or block_tables.shape[0] != B:
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        H = q.shape[1]
+        if q.shape != (N, H, dk) or q_out.shape != (N, H, dk):
+            raise ValueError("q and q_out must both be [N, H, dk]")
+    if row_starts.numel() != B + 1 or seq_lens_in.numel() != B or seq_lens_out.numel() != B:
         raise ValueError("row_starts, the lengths and block_tables do not agree in the number of sequences")
     _here(q, k_new, v_new, q_out, k_pool, v_pool, block_tables, row_starts, seq_lens_in, seq_lens_out, q_weight,
           k_weight, rope.table if rope is not None else None)
     _writes_once(q_out)
     _check(load().kv_append_paged_rows(
-        _ref(_heads(q, 3)), _ref(_heads(k_new, 3)), _ref(_heads(v_new, 3)), _ref(_heads(q_out, 3)), _p(k_pool),
-        _p(v_pool), _i32(block_tables), _i32(row_starts), _i32(seq_lens_in), _i32(seq_lens_out), N, B,
-        block_tables.shape[1], nb, bs, 0 if q is None else q.shape[1], Hkv, dk, dv, _weight(q_weight, dk),
+        _view(q, 3), _view(k_new, 3), _view(v_new, 3), _view(q_out, 3), _p(k_pool), _p(v_pool), _i32(block_tables), _i32(row_starts), _i32(seq_lens_in), _i32(seq_lens_out), N, B,
+        mbps, nb, bs, H, Hkv, dk, dv, _weight(q_weight, dk),
         _weight(k_weight, dk), float(eps), _ref(rope),
         _dtype(q, k_new, v_new, q_out, k_pool, v_pool, q_weight, k_weight), _stream(stream)), "kv_append_paged_rows")
     return q_out

@@ -772,20 +772,22 @@ gqa_status gqa_rope_frequencies(float* freqs_host, float* magnitude, int rot_dim
 
 // The checks that attn_qk_norm_rope and kv_append_paged_rows share, and the norm
 // and the rotation into the kernel's parameters.
-static bool heads_view_ok(const gqa_heads* x, int bf16, bool batched) {
-  const int v = bf16 ? 8 : 4;  // elements of 16 bytes
-  return x->data && aligned16(x->data) && x->token_stride % v == 0 && x->head_stride % v == 0 &&
-         (!batched || x->batch_stride % v == 0);
+// A call's view of a tensor of B sequences (0: no batch axis), T tokens, heads heads:
+// an axis of one element has no stride.
+static gqa::HeadsView heads_view(const gqa_heads* x, int B, int T, int heads) {
+  if (!x) return {};
+  return {x->data, B > 1 ? x->batch_stride : 0, T > 1 ? x->token_stride : 0, heads > 1 ? x->head_stride : 0};
 }
 
-static gqa::HeadsView heads_view(const gqa_heads* x, bool batched) {
-  return {x->data, batched ? x->batch_stride : 0, x->token_stride, x->head_stride};
+static bool heads_view_ok(const gqa::HeadsView& x, int bf16) {
+  const int v = bf16 ? 8 : 4;  // elements of 16 bytes
+  return x.data && aligned16(x.data) && x.batch_stride % v == 0 && x.token_stride % v == 0 && x.head_stride % v == 0;
 }
 
 // An output that starts where its input does has to be the same view.
-static bool in_place_ok(const gqa_heads* x, const gqa_heads* y, bool batched) {
-  return x->data != y->data || (x->token_stride == y->token_stride && x->head_stride == y->head_stride &&
-                                (!batched || x->batch_stride == y->batch_stride));
+static bool in_place_ok(const gqa::HeadsView& x, const gqa::HeadsView& y) {
+  return x.data != y.data ||
+         (x.batch_stride == y.batch_stride && x.token_stride == y.token_stride && x.head_stride == y.head_stride);
 }
 
 static gqa_status qk_norm_and_rope(gqa::QkParams& p, const void* q_weight, const void* k_weight, float eps,
@@ -823,18 +825,14 @@ gqa_status attn_qk_norm_rope(const gqa_heads* q, const gqa_heads* k, const gqa_h
   const gqa_status s = qk_norm_and_rope(p, q_weight, k_weight, eps, rope, d);
   if (s != GQA_OK) return s;
   if (B == 0 || T == 0 || H + Hkv == 0) return GQA_OK;
-  if ((q && (!heads_view_ok(q, bf16, true) || !heads_view_ok(q_out, bf16, true) || !in_place_ok(q, q_out, true))) ||
-      (k && (!heads_view_ok(k, bf16, true) || !heads_view_ok(k_out, bf16, true) || !in_place_ok(k, k_out, true))))
+  p.q = heads_view(q, B, T, H);
+  p.q_out = heads_view(q_out, B, T, H);
+  p.k = heads_view(k, B, T, Hkv);
+  p.k_out = heads_view(k_out, B, T, Hkv);
+  if ((q && (!heads_view_ok(p.q, bf16) || !heads_view_ok(p.q_out, bf16) || !in_place_ok(p.q, p.q_out))) ||
+      (k && (!heads_view_ok(p.k, bf16) || !heads_view_ok(p.k_out, bf16) || !in_place_ok(p.k, p.k_out))))
     return GQA_ERR_INVALID_ARG;
   if (rope && !positions) return GQA_ERR_INVALID_ARG;
-  if (q) {
-    p.q = heads_view(q, true);
-    p.q_out = heads_view(q_out, true);
-  }
-  if (k) {
-    p.k = heads_view(k, true);
-    p.k_out = heads_view(k_out, true);
-  }
   p.positions = positions;
   p.N = B * T;
   p.T = T;
@@ -863,19 +861,16 @@ gqa_status kv_append_paged_rows(const gqa_heads* q, const gqa_heads* k_new, cons
   if (B == 0) return GQA_OK;
   if (!k_new || !v_new || !k_pool || !v_pool || !block_tables || !row_starts || !seq_lens_in || !seq_lens_out)
     return GQA_ERR_INVALID_ARG;
-  if (N > 0 && (!heads_view_ok(k_new, bf16, false) || !heads_view_ok(v_new, bf16, false) ||
-                (q && (!heads_view_ok(q, bf16, false) || !heads_view_ok(q_out, bf16, false) ||
-                       !in_place_ok(q, q_out, false)))))
+  p.q = heads_view(q, 0, N, H);
+  p.q_out = heads_view(q_out, 0, N, H);
+  p.k = heads_view(k_new, 0, N, Hkv);
+  p.v = heads_view(v_new, 0, N, Hkv);
+  if (N > 0 && (!heads_view_ok(p.k, bf16) || !heads_view_ok(p.v, bf16) ||
+                (q && (!heads_view_ok(p.q, bf16) || !heads_view_ok(p.q_out, bf16) || !in_place_ok(p.q, p.q_out)))))
     return GQA_ERR_INVALID_ARG;
   if (!aligned16(k_pool) || !aligned16(v_pool)) return GQA_ERR_INVALID_ARG;
   const bool same_lens = seq_lens_in == seq_lens_out;
   if (!same_lens && seq_lens_in < seq_lens_out + B && seq_lens_out < seq_lens_in + B) return GQA_ERR_INVALID_ARG;
-  if (q) {
-    p.q = heads_view(q, false);
-    p.q_out = heads_view(q_out, false);
-  }
-  p.k = heads_view(k_new, false);
-  p.v = heads_view(v_new, false);
   p.k_out.data = k_pool;
   p.v_pool = v_pool;
   p.tables = block_tables;

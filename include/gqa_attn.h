@@ -360,7 +360,8 @@ gqa_status attn_rope_interleaved_qk(void* q, void* k, const int32_t* positions, 
 
 /* A tensor [batch, tokens, heads, d]: element (b, t, h, e) at
  * data + b * batch_stride + t * token_stride + h * head_stride + e; strides in
- * elements. data 16-byte aligned, every stride a multiple of 16 bytes. */
+ * elements. data 16-byte aligned, every stride a multiple of 16 bytes (that of an
+ * axis of one element is ignored). */
 typedef struct gqa_heads {
   void* data;
   int64_t batch_stride, token_stride, head_stride;

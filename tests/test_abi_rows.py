@@ -73,9 +73,9 @@ def test_binding_checks(g):
     """Shapes and layouts that the binding turns down, with tensors that live on the CPU."""
     x = torch.zeros(2, 3, 4, 64)
     with pytest.raises(ValueError):
-        g._heads(x.transpose(-1, -2), 4)      # last axis not dense
+        g._view(x.transpose(-1, -2), 4)      # last axis not dense
     with pytest.raises(ValueError):
-        g._heads(x, 3)
+        g._view(x, 3)
     with pytest.raises(ValueError):
         g._writes_once(x[:, :, :1].expand(2, 3, 4, 64))
     with pytest.raises(ValueError):
@@ -84,5 +84,16 @@ def test_binding_checks(g):
         g.attn_qk_norm_rope(x, None, None, None, None)
     with pytest.raises(ValueError):
         g.rope_frequencies(8, 1e4, divisors=[1.0])
-    h = g._heads(x[:1, :, :1], 4)             # axes of one element have no stride
-    assert (h.batch_stride, h.token_stride, h.head_stride) == (0, 256, 0)
+    assert g._view(None, 4) is None
+    for y in (x, x.transpose(1, 2)):
+        h = g.GqaHeads.from_buffer_copy(g._view(y, 4))
+        assert (h.data, h.batch_stride, h.token_stride, h.head_stride) == (y.data_ptr(), *y.stride()[:3])
+    h = g.GqaHeads.from_buffer_copy(g._view(x[0], 3))
+    assert (h.data, h.batch_stride, h.token_stride, h.head_stride) == (x.data_ptr(), 0, 256, 64)
+
+
+def test_an_axis_of_one_element_has_no_stride(g):
+    # B = T = Hkv = 1: any strides go; refused for another reason (no positions), not for them
+    odd = dict(q=(P, 3, 5, 64), qo=(48, 7, 1, 64), k=(32, 1, 1, 1), ko=(64, 9, 9, 9), B=1, T=1, Hkv=1)
+    assert norm_rope(g, **odd, pos=N) == INV
+    assert norm_rope(g, **{**odd, "q": (P, 3, 5, 60)}, pos=P) == INV      # the heads' own stride counts
