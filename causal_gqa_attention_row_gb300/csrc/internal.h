@@ -134,7 +134,7 @@ struct QkParams {
   int d, dv;
   int layout, rot_offset, rot_dim;  // layout 1: half pairs; rot_dim 0: no rotation
   float magnitude, eps;
-  int parts;                     // items per token (set by the launcher)
+  int parts, part_rows, first_part, lens_part;  // items per token, rows of one (set by the launcher)
   int mbps, bs, num_blocks;
   int run_rows;                  // 0: only the lengths
   int lens_items;                // sequences whose length this launch advances (0 or B)

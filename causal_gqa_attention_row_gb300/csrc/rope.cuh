@@ -47,4 +47,12 @@ __device__ __forceinline__ void rope_cos_sin_f(int pos, float w_hi, float w_lo, 
   sincosf(r + a_lo, s, c);
 }
 
+// The same with the frequency given as the float pair alone.
+__device__ __forceinline__ void rope_cos_sin_pair(int pos, float w_hi, float w_lo, float* c, float* s) {
+  if (pos >= (1 << 24) || pos <= -(1 << 24))
+    rope_cos_sin((double)pos, (double)w_hi + (double)w_lo, c, s);
+  else
+    rope_cos_sin_f(pos, w_hi, w_lo, 0.0, c, s);
+}
+
 }  // namespace gqa
