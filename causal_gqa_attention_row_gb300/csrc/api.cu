@@ -323,11 +323,11 @@ gqa_status attn_prefill_paged(const void* q, const void* k_pool, const void* v_p
 // ---- attn_decode_shared_prefix ------------------------------------------------
 namespace {
 
-// The workspace of a shared-prefix step: header, the plan's arrays, the units of the
-// prefixes with their partial results, then the own rows' split-K plan and results.
+// The workspace of a shared-prefix step: header, the plan's records, the list of units,
+// the partial results of the prefixes' units and of the own parts.
 struct SharedLayout {
-  int GH, RPT, n_hchunks, max_units, max_splits;
-  size_t groups, group_of, kv_lo, units, partial, rows, rows_partial, bytes;
+  int GH, RPT, n_hchunks, own_rows, max_prefix_units;
+  size_t groups, seq, units, partial, own, bytes;
 };
 
 SharedLayout shared_layout(int B, int H, int Hkv, int d_v, int capacity, int n_groups) {
@@ -335,14 +335,16 @@ SharedLayout shared_layout(int B, int H, int Hkv, int d_v, int capacity, int n_g
   const int G = H / Hkv;
   gqa::dense_rows(G, &s.GH, &s.RPT);
   s.n_hchunks = G / s.GH;
-  s.max_splits = ceil_div(capacity, gqa::kSplitRows);
-  // row tiles of the groups that count (two members or more), then as many key ranges
-  // more as two waves of the SMs take, or as the longest unit makes necessary
+  s.own_rows = (s.GH + 3) / 4 * 4;  // a whole number of 16-byte steps per part
+  // row tiles of the groups that count (two members or more), each with one key range or
+  // more: as many more as two rounds of the SMs' two slots take, at most one per key tile
   const int counted = n_groups < B / 2 ? n_groups : B / 2;
-  const long long tiles = (long long)Hkv * s.n_hchunks * (B / s.RPT + counted);
-  const long long longest = (long long)gqa::kDenseMaxUnitTiles * 128;
-  const long long units = counted ? tiles * ((capacity + longest - 1) / longest) + 2 * gqa::kDenseSms : 0;
-  s.max_units = units > INT_MAX ? INT_MAX : (int)units;
+  const long long heads = (long long)Hkv * s.n_hchunks;
+  const long long tiles = counted ? heads * (B / s.RPT + counted) : 0;
+  const long long each = tiles * ((capacity + 127) / 128), some = tiles ? tiles + 4 * gqa::kDenseSms : 0;
+  const long long units = each < some ? each : some;
+  s.max_prefix_units = units > INT_MAX ? INT_MAX : (int)units;
+  const size_t parts = (size_t)B * (size_t)heads + gqa::kOwnExtra;
   size_t at = 256;  // [0]: units listed
   const auto take = [&](size_t n) {
     const size_t a = at;
@@ -350,13 +352,10 @@ SharedLayout shared_layout(int B, int H, int Hkv, int d_v, int capacity, int n_g
     return a;
   };
   s.groups = take((size_t)n_groups * sizeof(gqa::DenseGroup));
-  s.group_of = take((size_t)B * 4);
-  s.kv_lo = take((size_t)B * 4);
-  s.units = take((size_t)s.max_units * sizeof(gqa::DenseUnit));
-  s.partial = take((size_t)s.max_units * 128 * (size_t)(d_v + 2) * 4);
-  const size_t row_units = (size_t)B * (size_t)H * (size_t)s.max_splits;
-  s.rows = take(gqa::plan_bytes(row_units));
-  s.rows_partial = take(row_units * (size_t)(d_v + 2) * 4);
+  s.seq = take((size_t)B * sizeof(gqa::SeqPlan));
+  s.units = take(((size_t)s.max_prefix_units + parts) * sizeof(gqa::DenseUnit));
+  s.partial = take((size_t)s.max_prefix_units * gqa::dense_part_floats(128, d_v) * 4);
+  s.own = take(parts * gqa::dense_part_floats(s.own_rows, d_v) * 4);
   s.bytes = at;
   return s;
 }
@@ -365,7 +364,10 @@ SharedLayout shared_layout(int B, int H, int Hkv, int d_v, int capacity, int n_g
 
 size_t attn_decode_shared_prefix_workspace_bytes(int B, int H, int Hkv, int d_v, int max_len, int n_groups) {
   if (B <= 0 || !heads_ok(H, Hkv) || d_v <= 0 || max_len <= 0 || n_groups < 0) return 0;
-  return shared_layout(B, H, Hkv, d_v, max_len, n_groups).bytes;
+  // (a shape that the tensor-core kernel does not take needs attn_decode_paged's workspace)
+  const size_t shared = shared_layout(B, H, Hkv, d_v, max_len, n_groups).bytes;
+  const size_t paged = attn_decode_workspace_bytes(B, H, d_v, max_len);
+  return shared > paged ? shared : paged;
 }
 
 gqa_status attn_decode_shared_prefix(const void* q, const void* k_pool, const void* v_pool,
@@ -384,123 +386,101 @@ gqa_status attn_decode_shared_prefix(const void* q, const void* k_pool, const vo
   if (n_groups > 0 && (!group_starts || !shared_blocks)) return GQA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return GQA_ERR_INVALID_ARG;
   const int capacity = max_blocks_per_seq * block_size;
-  const SharedLayout s = shared_layout(B, H, Hkv, d_v, capacity, n_groups);
-  if (!workspace || workspace_bytes < s.bytes) return GQA_ERR_WORKSPACE;
+  if (!workspace ||
+      workspace_bytes < attn_decode_shared_prefix_workspace_bytes(B, H, Hkv, d_v, capacity, n_groups))
+    return GQA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return GQA_ERR_INVALID_ARG;
-  gqa::RowsParams p{};
+  gqa::RowsParams arm{};  // (the arms in the kernels' units)
   bool arms_on;
-  const gqa_status sa = apply_arms(p, arms, &arms_on);
+  const gqa_status sa = apply_arms(arm, arms, &arms_on);
   if (sa != GQA_OK) return sa;
-  // Nothing to share, or a shape that the tensor-core kernel does not take: every
-  // sequence reads its whole history, as attn_decode_paged.
-  if (n_groups == 0 || !gqa::dense_tc_supported(bf16, d_k, d_v, block_size) || !(attention_scale > 0.f))
+  if (!gqa::dense_tc_supported(bf16, d_k, d_v, block_size) || !(attention_scale > 0.f))
     return attn_decode_paged_ex(q, k_pool, v_pool, block_tables, seq_lens, out, B, max_blocks_per_seq, num_blocks,
-                                block_size, H, Hkv, d_k, d_v, attention_scale, dt,
-                                static_cast<char*>(workspace) + s.rows, workspace_bytes - s.rows, arms, stream);
+                                block_size, H, Hkv, d_k, d_v, attention_scale, dt, workspace, workspace_bytes, arms,
+                                stream);
+  const SharedLayout s = shared_layout(B, H, Hkv, d_v, capacity, n_groups);
+  // offsets of partial results are 32-bit counts of 16 bytes, units 32-bit
+  if ((s.bytes - s.partial) / 16 > (size_t)INT_MAX || (s.own - s.partial) % 16 ||
+      (long long)B * H > INT_MAX / 2)
+    return GQA_ERR_INVALID_ARG;
+  unsigned* err = error_word();
+  if (!err) return GQA_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  p.q = q;
-  p.k = k_pool;
-  p.v = v_pool;
-  p.out = out;
-  p.kv_len = seq_lens;
-  p.tables = block_tables;
-  p.paged = 1;
-  p.B = B;
-  p.H = H;
-  p.Hkv = Hkv;
-  p.capacity = capacity;
-  p.mbps = max_blocks_per_seq;
-  p.bs = block_size;
-  p.num_blocks = num_blocks;
-  p.qscale = attention_scale * gqa::kLog2e;
-  const int nvmax = gqa::rows_max_nv(bf16, d_k, d_v, 0);
-  p.G = H / Hkv;
-  p.GH = pow2_divisor(p.G, nvmax);
-  p.QR = 1;
-  p.n_hchunks = p.G / p.GH;
-  p.n_rblocks = 1;
-  p.seq_q = 1;
-  p.split_rows = gqa::kSplitRows;
-  p.max_splits = s.max_splits;
-  const size_t row_units = (size_t)B * (size_t)H * (size_t)s.max_splits;
-  p.sched = reinterpret_cast<int*>(ws + s.rows);
-  p.units = reinterpret_cast<int2*>(ws + s.rows + gqa::kPlanHeaderBytes);
-  p.partial = reinterpret_cast<float*>(ws + s.rows_partial);
-  p.kv_lo = reinterpret_cast<int32_t*>(ws + s.kv_lo);
-  if (row_units > (size_t)INT_MAX) return GQA_ERR_INVALID_ARG;
-  p.err = error_word();
-  if (!p.err) return GQA_ERR_CUDA;
-  p.debug_withhold = g_withhold_first_tile;
 
   gqa::SharedPlan plan{};
+  plan.seq_lens = seq_lens;
   plan.group_starts = group_starts;
   plan.shared_blocks = shared_blocks;
+  plan.B = B;
+  plan.Hkv = Hkv;
+  plan.G = H / Hkv;
+  plan.capacity = capacity;
+  plan.bs = block_size;
+  plan.mbps = max_blocks_per_seq;
+  plan.window = arm.window;
+  plan.dv = d_v;
   plan.n_groups = n_groups;
-  plan.max_units = s.max_units;
+  plan.max_prefix_units = s.max_prefix_units;
+  plan.slots = gqa::dense_tc_slots(d_k);
   plan.GH = s.GH;
   plan.RPT = s.RPT;
   plan.n_hchunks = s.n_hchunks;
+  plan.own_rows = s.own_rows;
+  plan.own_part_at = (int)((s.own - s.partial) / 16);
   plan.groups = reinterpret_cast<gqa::DenseGroup*>(ws + s.groups);
-  plan.group_of = reinterpret_cast<int32_t*>(ws + s.group_of);
-  plan.kv_lo = reinterpret_cast<int32_t*>(ws + s.kv_lo);
+  plan.seq = reinterpret_cast<gqa::SeqPlan*>(ws + s.seq);
   plan.units = reinterpret_cast<gqa::DenseUnit*>(ws + s.units);
-  plan.n_units = reinterpret_cast<int*>(ws);
-  cudaError_t e = gqa::launch_shared_plan(p, plan, st);
+  plan.units_listed = reinterpret_cast<int*>(ws);
+  plan.err = err;
+  cudaError_t e = gqa::launch_shared_plan(plan, st);
   if (e != cudaSuccess) return from_cuda(e);
 
   gqa::DenseParams d{};
   d.H = H;
   d.Hkv = Hkv;
-  d.G = p.G;
+  d.G = plan.G;
   d.GH = s.GH;
   d.RPT = s.RPT;
   d.n_hchunks = s.n_hchunks;
   d.n_i = B;
   d.S_kv = capacity;
   d.units = plan.units;
-  d.n_units = plan.n_units;
+  d.units_listed = plan.units_listed;
   d.seq_lens = seq_lens;
+  d.own_rows = s.own_rows;
   d.tables = block_tables;
   d.mbps = max_blocks_per_seq;
   d.bs = block_size;
   d.num_blocks = num_blocks;
   d.partial = reinterpret_cast<float*>(ws + s.partial);
   d.out = static_cast<__nv_bfloat16*>(out);
-  d.qscale = p.qscale;
-  d.err = p.err;
+  d.qscale = attention_scale * gqa::kLog2e;
+  d.err = err;
   d.debug_withhold = g_withhold_first_tile;
-  d.window = p.window;
-  d.cap_out = p.softcap2;
-  d.cap_in = p.softcap2 > 0.f ? p.qscale / p.softcap2 : 0.f;
-  d.alibi = p.alibi;
-  const bool score_arms = p.window > 0 || p.softcap2 > 0.f || p.alibi;  // sinks join in the combine
-  e = gqa::launch_dense_tc(q, k_pool, v_pool, d, 1, d_k, d_v, s.max_units, score_arms, st);
-  if (e != cudaSuccess) return from_cuda(e);
-  e = gqa::launch_attn_rows_bf16(p, d_k, d_v, 0, p.GH, st);
+  d.window = arm.window;
+  d.cap_out = arm.softcap2;
+  d.cap_in = arm.softcap2 > 0.f ? d.qscale / arm.softcap2 : 0.f;
+  d.alibi = arm.alibi;
+  const bool score_arms = arm.window > 0 || arm.softcap2 > 0.f || arm.alibi;  // sinks join in the combine
+  e = gqa::launch_dense_tc(q, k_pool, v_pool, d, 1, d_k, d_v, score_arms, st);
   if (e != cudaSuccess) return from_cuda(e);
 
   gqa::DenseCombine c{};
   c.n_rows = (long long)B * H;
   c.H = H;
   c.Hkv = Hkv;
-  c.G = p.G;
+  c.G = plan.G;
   c.GH = s.GH;
   c.RPT = s.RPT;
   c.n_hchunks = s.n_hchunks;
   c.n_i = B;
   c.dv = d_v;
   c.partial = d.partial;
-  c.groups = plan.groups;
-  c.group_of = plan.group_of;
-  c.kv_lo = plan.kv_lo;
-  c.seq_lens = seq_lens;
-  c.rows_partial = p.partial;
-  c.max_splits = p.max_splits;
-  c.split_rows = p.split_rows;
-  c.capacity = capacity;
-  c.window = p.window;
-  c.sinks = p.sinks;
+  c.seq = plan.seq;
+  c.own_partial = reinterpret_cast<const float*>(ws + s.own);
+  c.own_rows = s.own_rows;
+  c.sinks = arm.sinks;
   c.out = d.out;
   return from_cuda(gqa::launch_dense_combine(c, st));
 }
@@ -528,17 +508,18 @@ bool cross_plan(int B, int S, int L, int H, int Hkv, int d_k, int d_v, int bf16,
   c->tc = scale_ok && gqa::dense_tc_supported(bf16, d_k, d_v) && (long long)S * G >= kCrossTcRows;
   if (c->tc) {
     gqa::dense_rows(G, &c->GH, &c->RPT);
+    if (c->RPT > S) c->RPT = S;
     c->n_hchunks = G / c->GH;
     c->n_tiles = ceil_div(S, c->RPT);
     const long long tiles = (long long)B * Hkv * c->n_hchunks * c->n_tiles;
-    const int nt = ceil_div(L, 128);
-    // key ranges of st tiles: the fewest waves * (st + a unit's own cost); one range
+    const int nt = ceil_div(L, 128), slots = gqa::dense_tc_slots(d_k);
+    // key ranges of st tiles: the fewest rounds * (st + a unit's own cost); one range
     // writes the result itself, more leave partial results to join (a further cost)
     long long best = -1;
-    for (int ns = 1; ns <= nt && (ns == 1 || tiles * ns <= 4 * gqa::kDenseSms); ++ns) {
+    for (int ns = 1; ns <= nt && (ns == 1 || tiles * ns <= 4 * slots); ++ns) {
       const int st = ceil_div(nt, ns), n = ceil_div(nt, st);
-      const long long waves = (tiles * n + gqa::kDenseSms - 1) / gqa::kDenseSms;
-      const long long cost = waves * (st + gqa::kDenseUnitTiles) + (n > 1 ? 2 : 0);
+      const long long rounds = (tiles * n + slots - 1) / slots;
+      const long long cost = rounds * (st + gqa::kDenseUnitTiles) + (n > 1 ? 2 : 0);
       if (best < 0 || cost < best) {
         best = cost;
         c->n_splits = n;
@@ -546,7 +527,7 @@ bool cross_plan(int B, int S, int L, int H, int Hkv, int d_k, int d_v, int bf16,
       }
     }
     c->units = tiles * c->n_splits;
-    c->bytes = c->n_splits > 1 ? (size_t)c->units * 128 * (size_t)(d_v + 2) * 4 : 0;
+    c->bytes = c->n_splits > 1 ? (size_t)c->units * gqa::dense_part_floats(128, d_v) * 4 : 0;
     return true;
   }
   const int nvmax = gqa::rows_max_nv(bf16, d_k, d_v, 0);
@@ -616,6 +597,7 @@ gqa_status attn_cross(const void* q, const void* k, const void* v, const int32_t
     d.n_i = seq_q;
     d.S_kv = seq_kv_max;
     d.kv_lens = kv_lens;
+    d.n_units = (int)c.units;
     d.n_tiles = c.n_tiles;
     d.n_splits = c.n_splits;
     d.split_tiles = c.split_tiles;
@@ -624,7 +606,8 @@ gqa_status attn_cross(const void* q, const void* k, const void* v, const int32_t
     d.qscale = qscale;
     d.err = err;
     d.debug_withhold = g_withhold_first_tile;
-    const cudaError_t e = gqa::launch_dense_tc(q, k, v, d, B, d_k, d_v, c.units, false, st);
+    if (c.units > INT_MAX / 2 || c.bytes / 16 > (size_t)INT_MAX) return GQA_ERR_INVALID_ARG;
+    const cudaError_t e = gqa::launch_dense_tc(q, k, v, d, B, d_k, d_v, false, st);
     if (e != cudaSuccess || c.n_splits == 1) return from_cuda(e);
     gqa::DenseCombine m{};
     m.n_rows = (long long)B * seq_q * H;

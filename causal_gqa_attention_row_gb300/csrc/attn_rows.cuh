@@ -241,13 +241,12 @@ struct Unit {
   int kv_len, i0, i_last;
   int r0, r1;   // key rows [r0, r1) of this split
   int lo;       // first key the unit's first row sees (the window's lower end) and this call reads
-  int own_lo;   // first key of the sequence that this call reads (RowsParams::kv_lo)
   int nsplit;   // splits of the item that hold a visible key
   bool len_ok;
 };
 
-// EXT: the call may have own first keys (kv_lo) or no causal rule (full).
-template <bool EXT>
+// FULL: no causal rule.
+template <bool FULL>
 __device__ __forceinline__ Unit decode_unit(const RowsParams& p, int item, int split) {
   Unit u;
   u.split = split;
@@ -257,17 +256,14 @@ __device__ __forceinline__ Unit decode_unit(const RowsParams& p, int item, int s
   item /= p.n_hchunks;
   u.kvh = item % p.Hkv;
   u.b = item / p.Hkv;
-  u.kv_len = EXT ? rows_kv_len(p, u.b)
-                 : p.kv_len ? __ldg(p.kv_len + u.b) : (p.offsets ? __ldg(p.offsets + u.b) : 0) + p.seq_q;
+  u.kv_len = FULL ? rows_kv_len(p, u.b)
+                  : p.kv_len ? __ldg(p.kv_len + u.b) : (p.offsets ? __ldg(p.offsets + u.b) : 0) + p.seq_q;
   u.i0 = rb * p.QR;
   u.i_last = min(u.i0 + p.QR, p.seq_q) - 1;
-  u.len_ok = EXT ? rows_len_ok(p, u.kv_len) : u.kv_len >= p.seq_q && u.kv_len >= 1 && u.kv_len <= p.capacity;
-  const int kv_hi =
-      u.len_ok ? (EXT ? rows_limit(p, u.kv_len, u.i_last) : u.kv_len - p.seq_q + u.i_last + 1) : 0;  // keys the last row sees
-  u.own_lo = EXT && p.kv_lo ? __ldg(p.kv_lo + u.b) : 0;
-  u.lo = u.len_ok ? max(first_visible_key(u.kv_len - p.seq_q + u.i0, p.window), u.own_lo) : 0;
+  u.len_ok = (FULL || u.kv_len >= p.seq_q) && u.kv_len >= 1 && u.kv_len <= p.capacity;
+  const int kv_hi = u.len_ok ? (FULL ? u.kv_len : u.kv_len - p.seq_q + u.i_last + 1) : 0;  // keys the last row sees
+  u.lo = u.len_ok ? first_visible_key(u.kv_len - p.seq_q + u.i0, p.window) : 0;
   u.nsplit = (kv_hi + p.split_rows - 1) / p.split_rows - u.lo / p.split_rows;
-  if (EXT && u.own_lo > 0) u.nsplit = max(u.nsplit, 2);  // never the whole result: always a partial one
   u.r0 = split * p.split_rows;
   u.r1 = min(u.r0 + p.split_rows, kv_hi);
   return u;
@@ -290,10 +286,9 @@ __device__ __forceinline__ bool compute_sync(uint64_t* bar, uint32_t parity, vol
   return warp_wait(bar, parity, abort_flag, err);
 }
 
-// ARMS: the window / softcap / sink / ALiBi code is compiled in, and that of the calls
-// with a shared prefix or without a causal rule (a plain call runs the instantiation
-// without it, at the plain kernel's register count).
-template <typename ET, int DK, int DV, int DROT, int NV, bool ARMS>
+// ARMS: the window / softcap / sink / ALiBi code is compiled in; FULL: no causal rule (a
+// plain call runs the instantiation without either, at the plain kernel's register count).
+template <typename ET, int DK, int DV, int DROT, int NV, bool ARMS, bool FULL>
 __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::MIN_CTAS)
     attn_rows_kernel(const RowsParams p) {
   using C = RowsCfg<ET, DK, DV, DROT, NV>;
@@ -354,11 +349,11 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
         split = 0;
         next_static += gridDim.x;
       }
-      const Unit u = decode_unit<ARMS>(p, item, split);
+      const Unit u = decode_unit<FULL>(p, item, split);
       if (!u.len_ok) {
         // Length out of range: record it, write zeros, touch no K/V (no keys at all,
         // where the call allows that: zeros are the result).
-        if (lane == 0 && split == 0 && item % (p.Hkv * p.n_hchunks * p.n_rblocks) == 0 && !(ARMS && p.full && u.kv_len == 0))
+        if (lane == 0 && split == 0 && item % (p.Hkv * p.n_hchunks * p.n_rblocks) == 0 && !(FULL && u.kv_len == 0))
           raise_error(p.err, kErrBounds);
         for (int idx = lane; idx < NV * DV; idx += 32) {
           const int vh = idx / DV;
@@ -521,10 +516,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
   int lo_own = 0;     // ... and keys >= lo_own inside its window
   int lo_unit = 0;    // first key the unit reads; rows below it in its first tile may hold anything
   float slope2 = 0.f; // the owned head's ALiBi slope in the log2 domain
-  // Calls without a causal rule and the shared-prefix step let a NaN among a row's scores
-  // through to its output: a row group is empty when its sum is zero, not when its
-  // reference max is still -infinity (which a row of NaN alone leaves it at).
-  const bool nan_through = ARMS && (p.full || p.kv_lo);
+  // Without a causal rule a NaN among a row's scores goes through to its output: a row
+  // group is empty when its sum is zero, not when its reference max is still -infinity
+  // (which a row of NaN alone leaves it at).
   const float cap_k = ARMS && p.softcap2 > 0.f ? 2.8853900817779268f / p.softcap2 : 0.f;  // 2 log2(e) / cap
   int merges = 0;
   for (int gt = 0;; ++gt) {
@@ -536,7 +530,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
     const unsigned char* st = data + s * C::stage_bytes;
     if (dsc.w & (1 << 16)) {
       // first tile of a unit: fresh state, queries from the stage into qw
-      const Unit u = decode_unit<ARMS>(p, dsc.x, dsc.y);
+      const Unit u = decode_unit<FULL>(p, dsc.x, dsc.y);
       const ET* sQ = reinterpret_cast<const ET*>(st + C::kN + C::kR + C::kV);
       for (int idx = lane; idx < NV * DK; idx += 32) {
         const bool active = u.i0 + (idx / DK) / p.GH <= u.i_last;
@@ -548,10 +542,10 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
         for (int e = 0; e < H2V; ++e) o2[vh][e] = make_float2(0.f, 0.f);
         const int iq = u.i0 + vh / p.GH;
         if (vh == own) {
-          lim_own = iq <= u.i_last ? (ARMS ? rows_limit(p, u.kv_len, iq) : u.kv_len - p.seq_q + iq + 1) : 0;
+          lim_own = iq <= u.i_last ? (FULL ? u.kv_len : u.kv_len - p.seq_q + iq + 1) : 0;
           if (ARMS) {
             lo_unit = u.lo;
-            lo_own = max(first_visible_key(lim_own - 1, p.window), u.own_lo);
+            lo_own = first_visible_key(lim_own - 1, p.window);
             slope2 = p.alibi ? __ldg(p.alibi + u.kvh * p.G + u.hc * p.GH + vh % p.GH) * kLog2e : 0.f;
           }
         }
@@ -678,7 +672,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
       float M = mg;
 #pragma unroll
       for (int off = L; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      const float w = (nan_through ? lg == 0.f : mg == -INFINITY) ? 0.f : ex2(mg - M);
+      const float w = (FULL ? lg == 0.f : mg == -INFINITY) ? 0.f : ex2(mg - M);
       float lsum = w * lg;
 #pragma unroll
       for (int off = L; off < 32; off <<= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
@@ -719,24 +713,24 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
                             o2[vh][qv * (CH / 2) + e + 1].x, o2[vh][qv * (CH / 2) + e + 1].y);
     }
     if (!compute_sync(&hdr->merge[1], par, abort_flag, p.err)) break;
-    const Unit u = decode_unit<ARMS>(p, dsc.x, dsc.y);
+    const Unit u = decode_unit<FULL>(p, dsc.x, dsc.y);
     for (int idx = ctid; idx < NV * DV; idx += kRowsWarps * 32) {
       const int vh = idx / DV, d = idx % DV;
       if (u.i0 + vh / p.GH > u.i_last) continue;
       float M = -INFINITY;
       for (int g = 0; g < kRowsWarps; ++g) M = fmaxf(M, mm[g * NV + vh]);
       float ls = 0.f, os = 0.f;
-      if (M != -INFINITY || nan_through) {
+      if (M != -INFINITY || FULL) {
         for (int g = 0; g < kRowsWarps; ++g) {
           const float mg = mm[g * NV + vh];
-          const float wg = (nan_through ? ml[g * NV + vh] == 0.f : mg == -INFINITY) ? 0.f : ex2(mg - M);
+          const float wg = (FULL ? ml[g * NV + vh] == 0.f : mg == -INFINITY) ? 0.f : ex2(mg - M);
           ls = fmaf(wg, ml[g * NV + vh], ls);
           os = fmaf(wg, mo[(g * NV + vh) * DV + d], os);
         }
       }
       const size_t row = unit_out_row(p, u, vh);
       if (u.nsplit == 1) {
-        float res = (nan_through ? ls != 0.f : ls > 0.f) ? os / ls : 0.f;
+        float res = (FULL ? ls != 0.f : ls > 0.f) ? os / ls : 0.f;
         if (ARMS && p.sinks) {  // the sink logit joins the denominator (once per row and head)
           const float z2 = __ldg(p.sinks + u.kvh * p.G + u.hc * p.GH + vh % p.GH) * kLog2e;
           const float Mx = fmaxf(M, z2);
@@ -759,10 +753,10 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
 
 // Host launcher of one instantiation: a persistent grid of one CTA per
 // resident slot (SMs x CTAs per SM), capped at the number of units.
-template <typename ET, int DK, int DV, int DROT, int NV, bool ARMS>
+template <typename ET, int DK, int DV, int DROT, int NV, bool ARMS, bool FULL>
 cudaError_t launch_rows_inst_arms(const RowsParams& p, cudaStream_t st) {
   using C = RowsCfg<ET, DK, DV, DROT, NV>;
-  auto kern = attn_rows_kernel<ET, DK, DV, DROT, NV, ARMS>;
+  auto kern = attn_rows_kernel<ET, DK, DV, DROT, NV, ARMS, FULL>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -798,9 +792,12 @@ cudaError_t launch_rows_inst_arms(const RowsParams& p, cudaStream_t st) {
 
 template <typename ET, int DK, int DV, int DROT, int NV>
 cudaError_t launch_rows_inst(const RowsParams& p, cudaStream_t st) {
-  const bool arms = p.window > 0 || p.softcap2 > 0.f || p.sinks || p.alibi || p.kv_lo || p.full;
-  return arms ? launch_rows_inst_arms<ET, DK, DV, DROT, NV, true>(p, st)
-              : launch_rows_inst_arms<ET, DK, DV, DROT, NV, false>(p, st);
+  const bool arms = p.window > 0 || p.softcap2 > 0.f || p.sinks || p.alibi;
+  if constexpr (DROT == 0) {
+    if (p.full) return launch_rows_inst_arms<ET, DK, DV, DROT, NV, false, true>(p, st);  // (has no arms)
+  }
+  return arms ? launch_rows_inst_arms<ET, DK, DV, DROT, NV, true, false>(p, st)
+              : launch_rows_inst_arms<ET, DK, DV, DROT, NV, false, false>(p, st);
 }
 
 }  // namespace gqa

@@ -51,9 +51,6 @@ struct RowsParams {
   float softcap2;           // softcap * log2(e) (the kernels score in the log2 domain); 0: none
   const float* sinks;       // [H] device, natural units, or NULL
   const float* alibi;       // [H] device, natural units, or NULL
-  // Shared-prefix step: the keys of sequence b below kv_lo[b] are another kernel's;
-  // a sequence with kv_lo[b] > 0 always leaves partial results (NULL: all zero).
-  const int32_t* kv_lo;
   // No causal rule (attn_cross): every row sees all keys of its sequence, which may
   // hold none (its rows are zeros); kv_len NULL stands for `capacity` keys.
   int full;
@@ -164,36 +161,36 @@ cudaError_t launch_prefill_tc(const void* q, const void* k, const void* v, void*
 bool prefill_tc_supported(int bf16, int dk, int dv, int bs = 0, int mbps = 0);
 
 // ---- attention without a causal rule on tcgen05 (dense_tc.cu) -----------------
-// One unit of work: rows i0 .. i0 + n_i - 1 of heads head0 .. head0 + GH - 1 against
-// key tiles t0 .. t1 - 1 of 128 keys, keys below kv_hi; seq is the sequence whose
-// keys (table row) are read.
+// One unit of work: rows i0 .. i0 + n_i - 1 of heads head0 .. head0 + GH - 1 against keys
+// key0 .. key1 - 1 of sequence seq (key0 a multiple of the pool's block size). part: where
+// the partial result goes, in 16-byte steps from DenseParams::partial (-1: final results);
+// batch: attn_cross, the sequence's place in q and out; own: shared prefix, a unit of one
+// sequence's own keys, with a partial result of own_rows rows instead of 128.
 struct alignas(16) DenseUnit {
   int i0, n_i, head0, seq;
-  int t0, t1, kv_hi, kvh;
+  int key0, key1, part, batch_or_own;
 };
 
-// A group of sequences with a shared prefix: its members from `first` on, its units
-// (KV head, head chunk, row tile, key range, ranges fastest) from unit0 on.
-struct alignas(16) DenseGroup {
-  int first, members, tiles, n_splits;
-  int unit0, kv_hi, t_lo, pad;
-};
+// A partial result of R rows: o [d_v / 4][R][4], then m [R] (log2 units) and l [R].
+__host__ __device__ inline size_t dense_part_floats(int R, int dv) { return (size_t)R * (size_t)(dv + 2); }
 
 struct DenseParams {
-  int H, Hkv, G;
+  int H, G;
   int GH, RPT, n_hchunks;  // rows of a tile: RPT rows i x GH heads (dense_rows)
   int n_i;                 // rows i of a sequence (attn_cross: seq_q; shared prefix: B)
   int S_kv;                // keys a sequence can hold
-  // attn_cross: units from the block index, key ranges of split_tiles tiles
+  // attn_cross: units from their index, key ranges of split_tiles tiles
+  int Hkv, n_units;
   const int32_t* kv_lens;  // [B] or NULL: S_kv
   int n_tiles, n_splits, split_tiles;
   // shared prefix: units from the plan, a length per row
   const DenseUnit* units;
-  const int* n_units;
+  const int* units_listed;
   const int32_t* seq_lens;
+  int own_rows;
   const int32_t* tables;   // paged pools (NULL: contiguous)
   int mbps, bs, num_blocks;
-  float* partial;          // per unit 128 * (d_v + 2) floats, or NULL: final results to out
+  float* partial;
   __nv_bfloat16* out;
   float qscale;
   unsigned* err;
@@ -207,46 +204,63 @@ struct DenseParams {
 // rows i per tile.
 void dense_rows(int G, int* GH, int* RPT);
 bool dense_tc_supported(int bf16, int dk, int dv, int bs = 0);
+// Units that the SMs work on at a time.
+int dense_tc_slots(int dk);
 cudaError_t launch_dense_tc(const void* q, const void* k, const void* v, const DenseParams& p, int n_b, int dk, int dv,
-                            long long units, bool arms, cudaStream_t st);
+                            bool arms, cudaStream_t st);
+
+// A group of sequences with a shared prefix (the planner's record).
+struct alignas(16) DenseGroup {
+  int first, members, tiles, n_splits;  // row tiles, key ranges (key tiles until they are chosen)
+  int unit0, kv_hi, key_lo, prefix;     // its first unit, the keys [key_lo, kv_hi) that members see, all its rows
+};
+
+// One sequence of a shared-prefix step, for the combine: n_pre key ranges, for head chunk c
+// in units pre_unit0 + c * pre_stride on, its row row0 + (head within the chunk); n_own
+// parts of its own keys, for head chunk c in own parts own_part0 + c * n_own on.
+struct alignas(16) SeqPlan {
+  int n_pre, pre_unit0, pre_stride, row0;
+  int n_own, own_part0, pad[2];
+};
 
 struct DenseCombine {
   long long n_rows;        // B * n_i * H output rows
   int H, Hkv, G, GH, RPT, n_hchunks, n_i, dv;
   int n_tiles, n_splits;   // attn_cross
   const float* partial;
-  // shared prefix
-  const DenseGroup* groups;
-  const int32_t* group_of;
-  const int32_t* kv_lo;
-  const int32_t* seq_lens;
-  const float* rows_partial;  // the own rows' partial results, as RowsParams
-  int max_splits, split_rows, capacity, window;
+  const SeqPlan* seq;      // shared prefix
+  const float* own_partial;
+  int own_rows;
   const float* sinks;
   __nv_bfloat16* out;
 };
 cudaError_t launch_dense_combine(const DenseCombine& p, cudaStream_t st);
 
-// A plan's cost is counted in key tiles: what a unit takes beside its tiles (set-up,
-// the first tiles' latency, the epilogue and its share of the join).
-constexpr int kDenseUnitTiles = 3;
+// A plan's cost is counted in key tiles: what a unit takes beside its tiles (the first
+// tile's latency, the epilogue and its share of the join).
+constexpr int kDenseUnitTiles = 1;
 constexpr int kDenseSms = 152;
-constexpr int kDenseMaxUnitTiles = 256;  // a unit's table entries fit the kernel's copy at every block size
 
-// The plan of a shared-prefix step: groups and first own keys, the units of the
-// prefixes, then the plan of the own rows (launch_plan_units).
+// Parts of own keys beyond one per item (sequence, KV head, head chunk) that a plan may make.
+constexpr int kOwnExtra = 4 * kDenseSms;
+
+// The plan of a shared-prefix step: the units of the prefixes and of the own keys, and what
+// each sequence has.
 struct SharedPlan {
+  const int32_t* seq_lens;
   const int32_t* group_starts;   // [n_groups + 1]
   const int32_t* shared_blocks;  // [n_groups]
-  int n_groups, max_units;
-  int GH, RPT, n_hchunks;
-  DenseGroup* groups;
-  int32_t* group_of;             // [B]: -1 without a prefix
-  int32_t* kv_lo;                // [B]
+  int B, Hkv, G, capacity, bs, mbps, window, dv;
+  int n_groups, max_prefix_units, slots;
+  int GH, RPT, n_hchunks, own_rows;
+  int own_part_at;               // where the own parts begin, in 16-byte steps from the partial results
+  DenseGroup* groups;            // scratch [n_groups], used where they do not fit shared memory
+  SeqPlan* seq;                  // [B]
   DenseUnit* units;
-  int* n_units;
+  int* units_listed;
+  unsigned* err;
 };
-cudaError_t launch_shared_plan(const RowsParams& p, const SharedPlan& s, cudaStream_t st);
+cudaError_t launch_shared_plan(const SharedPlan& s, cudaStream_t st);
 
 // Absorbed MLA decode on tcgen05 (bf16, d_c = 512, d_r = 64): attention of
 // q_abs [B, H, d_c + d_r] over the latent rows [B, max_len, d_c + d_r] (value =

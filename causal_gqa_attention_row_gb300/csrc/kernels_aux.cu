@@ -91,11 +91,9 @@ __device__ __forceinline__ void item_split_counts(const RowsParams& p, int item,
   }
   const int i_last = min(rb * p.QR + p.QR, p.seq_q) - 1;
   const int kv_hi = rows_limit(p, kv_len, i_last);
-  const int own_lo = p.kv_lo ? p.kv_lo[b] : 0;
-  s_first = max(first_visible_key(kv_len - p.seq_q + rb * p.QR, p.window), own_lo) / p.split_rows;
+  s_first = first_visible_key(kv_len - p.seq_q + rb * p.QR, p.window) / p.split_rows;
   full = max(0, kv_hi / p.split_rows - s_first);
   part = (kv_hi % p.split_rows) != 0;
-  if (own_lo >= kv_hi) full = part = 0;  // no key of its own
 }
 
 // Partial units are listed longest first, in buckets of kPartBucketRows rows
@@ -104,8 +102,14 @@ __device__ __forceinline__ void item_split_counts(const RowsParams& p, int item,
 // arbitrary; it only decides which CTA takes a unit, never what a unit computes.
 constexpr int kPartBuckets = 64;
 
-// The plan by one CTA of kPlanThreads.
-__device__ void plan_units(const RowsParams& p, int* warp_sums, int* bucket_at) {
+__global__ void __launch_bounds__(kPlanThreads) plan_units_kernel(const RowsParams p) {
+  __shared__ int warp_sums[32];
+  __shared__ int bucket_at[kPartBuckets];
+  // The lengths may come from the kernel before this one (the append). The
+  // attention kernel after this one may launch at once: it waits for this
+  // kernel's completion before it reads the plan.
+  grid_dep_wait();
+  grid_dep_launch();
   const int n_items = p.B * p.Hkv * p.n_hchunks * p.n_rblocks;
   for (int i = threadIdx.x; i < kPartBuckets; i += blockDim.x) bucket_at[i] = 0;
   // thread t owns the contiguous items [lo, hi): one scan for the full units (in
@@ -150,17 +154,6 @@ __device__ void plan_units(const RowsParams& p, int* warp_sums, int* bucket_at) 
   }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_units_kernel(const RowsParams p) {
-  __shared__ int warp_sums[32];
-  __shared__ int bucket_at[kPartBuckets];
-  // The lengths may come from the kernel before this one (the append). The
-  // attention kernel after this one may launch at once: it waits for this
-  // kernel's completion before it reads the plan.
-  grid_dep_wait();
-  grid_dep_launch();
-  plan_units(p, warp_sums, bucket_at);
-}
-
 cudaError_t launch_plan_units(const RowsParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
@@ -170,170 +163,6 @@ cudaError_t launch_plan_units(const RowsParams& p, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, plan_units_kernel, p);
-}
-
-// ---------------------------------------------------------------------------
-// The plan of a shared-prefix decode step, by one CTA: which sequences have a prefix
-// to share (groups of two members or more), the units of the prefixes, then the plan
-// of the own rows.
-//
-// The prefix of group g is tiles_g row tiles per KV head (and head chunk) times n_g
-// key tiles. Its units take c key tiles each, c the same for all groups and chosen to
-// minimise waves * (c + kDenseUnitTiles): the time of the whole in key tiles when
-// `waves` = ceil(units / SMs) units follow one another on an SM. All candidates c are
-// tried, a thread each.
-
-// Units of all groups at c key tiles each.
-__device__ __forceinline__ long long shared_units(const SharedPlan& s, int heads, int c) {
-  long long n = 0;
-  for (int g = 0; g < s.n_groups; ++g) {
-    const int nt = s.groups[g].n_splits;  // key tiles, until the plan replaces them
-    if (nt > 0) n += (long long)heads * s.groups[g].tiles * ((nt + c - 1) / c);
-  }
-  return n;
-}
-
-__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const RowsParams p, const SharedPlan s) {
-  __shared__ int warp_sums[32];
-  __shared__ int bucket_at[kPartBuckets];
-  __shared__ int bad, max_tiles;
-  __shared__ unsigned long long best;
-  grid_dep_wait();
-  grid_dep_launch();
-  const int tid = threadIdx.x;
-  if (tid == 0) {
-    bad = 0;
-    max_tiles = 1;
-    best = ~0ull;
-  }
-  __syncthreads();
-  // ---- groups: ascending starts within the batch, prefixes within the tables; with
-  // anything else no prefix is shared (every sequence reads its own rows) and the
-  // error word says so
-  for (int g = tid; g < s.n_groups; g += kPlanThreads) {
-    const int a = s.group_starts[g], z = s.group_starts[g + 1], nb = s.shared_blocks[g];
-    if (a < 0 || z < a || z > p.B || nb < 0 || nb > p.mbps) bad = 1;
-    DenseGroup d = {};
-    d.first = a;
-    d.members = z - a;
-    d.kv_hi = 0;          // largest length of a member ...
-    d.t_lo = p.capacity;  // ... and the smallest
-    s.groups[g] = d;
-  }
-  for (int b = tid; b < p.B; b += kPlanThreads) {
-    s.kv_lo[b] = 0;
-    s.group_of[b] = -1;
-  }
-  __syncthreads();
-  const bool ok = !bad;
-  if (!ok && tid == 0) raise_error(p.err, kErrBounds);
-  auto find = [&](int b) {  // the group of sequence b, -1 without one
-    if (!ok || s.n_groups == 0 || b < s.group_starts[0] || b >= s.group_starts[s.n_groups]) return -1;
-    int lo = 0, hi = s.n_groups;  // starts[lo] <= b < starts[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (s.group_starts[mid] <= b) lo = mid;
-      else hi = mid;
-    }
-    return lo;
-  };
-  for (int b = tid; b < p.B; b += kPlanThreads) {
-    const int g = find(b), len = p.kv_len[b];
-    if (g < 0 || !rows_len_ok(p, len)) continue;
-    atomicMax(&s.groups[g].kv_hi, len);
-    atomicMin(&s.groups[g].t_lo, len);
-  }
-  __syncthreads();
-  for (int g = tid; g < s.n_groups; g += kPlanThreads) {
-    DenseGroup d = s.groups[g];
-    const int prefix = ok && d.members >= 2 ? s.shared_blocks[g] * p.bs : 0;
-    d.kv_hi = min(prefix, d.kv_hi);
-    // tiles that every member's window hides are left out
-    d.t_lo = first_visible_key(d.t_lo - 1, p.window) / 128;
-    const int nt = d.kv_hi > 0 ? (d.kv_hi + 127) / 128 - d.t_lo : 0;
-    if (nt <= 0) d.kv_hi = 0;
-    d.n_splits = max(nt, 0);
-    d.tiles = nt > 0 ? (d.members + s.RPT - 1) / s.RPT : 0;
-    s.groups[g] = d;
-    if (nt > 0) atomicMax(&max_tiles, nt);
-  }
-  __syncthreads();
-  const int heads = p.Hkv * s.n_hchunks;
-  const int c_most = min(max_tiles, kDenseMaxUnitTiles);
-  for (int c = 1 + tid; c <= c_most; c += kPlanThreads) {
-    const long long n = shared_units(s, heads, c);
-    if (n > s.max_units) continue;
-    const long long waves = (n + kDenseSms - 1) / kDenseSms;
-    const unsigned long long cost = (unsigned long long)waves * (unsigned)(c + kDenseUnitTiles);
-    atomicMin(&best, cost << 16 | (unsigned)c);
-  }
-  __syncthreads();
-  // (the largest c always fits: the caller sized max_units for it)
-  const int c = best == ~0ull ? c_most : (int)(best & 0xffff);
-  // ---- key ranges per group and where its units start
-  const int per = (s.n_groups + kPlanThreads - 1) / kPlanThreads;
-  const int lo = min(s.n_groups, tid * per), hi = min(s.n_groups, lo + per);
-  int mine = 0;
-  for (int g = lo; g < hi; ++g) {
-    DenseGroup& d = s.groups[g];
-    d.n_splits = (d.n_splits + c - 1) / c;
-    mine += heads * d.tiles * d.n_splits;
-  }
-  int n_units;
-  int at = block_exclusive_scan(mine, warp_sums, n_units);
-  for (int g = lo; g < hi; ++g) {
-    DenseGroup& d = s.groups[g];
-    d.unit0 = at;
-    at += heads * d.tiles * d.n_splits;
-  }
-  __syncthreads();
-  if (n_units > s.max_units) n_units = 0;  // cannot happen; no unit past the list
-  if (tid == 0) *s.n_units = n_units;
-  for (int x = tid; x < n_units; x += kPlanThreads) {
-    int a = 0, z = s.n_groups;  // the last group that starts at or below x
-    while (z - a > 1) {
-      const int mid = (a + z) / 2;
-      if (s.groups[mid].unit0 <= x) a = mid;
-      else z = mid;
-    }
-    const DenseGroup d = s.groups[a];
-    int y = x - d.unit0;
-    const int split = y % d.n_splits;
-    y /= d.n_splits;
-    const int tile = y % d.tiles;
-    y /= d.tiles;
-    const int hc = y % s.n_hchunks, kvh = y / s.n_hchunks;
-    DenseUnit u;
-    u.i0 = d.first + tile * s.RPT;
-    u.n_i = min(s.RPT, d.members - tile * s.RPT);
-    u.head0 = kvh * p.G + hc * s.GH;
-    u.seq = d.first;
-    u.t0 = d.t_lo + split * c;
-    u.t1 = min(u.t0 + c, (d.kv_hi + 127) / 128);
-    u.kv_hi = d.kv_hi;
-    u.kvh = kvh;
-    s.units[x] = u;
-  }
-  // ---- the first own key of every sequence
-  for (int b = tid; b < p.B; b += kPlanThreads) {
-    const int g = find(b);
-    if (g < 0 || n_units == 0 || s.groups[g].kv_hi == 0) continue;
-    s.group_of[b] = g;
-    s.kv_lo[b] = s.shared_blocks[g] * p.bs;
-  }
-  __syncthreads();
-  plan_units(p, warp_sums, bucket_at);
-}
-
-cudaError_t launch_shared_plan(const RowsParams& p, const SharedPlan& s, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_plan_kernel, p, s);
 }
 
 // ---------------------------------------------------------------------------

@@ -131,31 +131,43 @@ def test_arms(gpu_lib, d, arms):
     verify(c, 0.11, out, **a)
 
 
-@pytest.mark.parametrize("how", ["f32", "odd block", "width"])
+@pytest.mark.parametrize("how", ["f32", "odd block", "width", "wide", "narrow"])
 def test_shapes_without_the_tensor_cores(gpu_lib, how):
-    """Every history read whole: attn_decode_paged's bits."""
+    """Every sequence reads all of its rows."""
     g = gpu_lib
-    dt = torch.float32 if how == "f32" else torch.bfloat16
-    d = 32 if how == "width" else 64
-    c = case([3, 2], [4, 2], [1, 20, 7, 9, 3], 4, 2, d, d, bs=12 if how == "odd block" else 16, dt=dt)
-    out = run(g, c, 0.125)
-    verify(c, 0.125, out, tc=False)
-    want = torch.empty_like(out)
-    B, H, dv = out.shape
-    ws = g.decode_workspace(B, H, dv, c["tables"].shape[1] * c["bs"])
-    g.attn_decode_paged(c["q"], c["k"], c["v"], c["tables"], c["lens"], want, 0.125, workspace=ws)
-    assert torch.equal(out, want)
+    dt = torch.float32 if how in ("f32", "narrow") else torch.bfloat16
+    d = {"width": 32, "wide": 256, "narrow": 16}.get(how, 64)
+    c = case([3, 2], [4, 2], [1, 20, 700, 9, 3], 4, 2, d, d, bs=12 if how == "odd block" else 16, dt=dt)
+    for arms in ({}, dict(window=30, softcap=9.0)):
+        out = run(g, c, 0.125, **arms)
+        assert g.attn_get_device_error() == g.OK
+        verify(c, 0.125, out, tc=False, **arms)
 
 
 def test_no_groups_is_the_paged_decode(gpu_lib):
     g = gpu_lib
     c = case([3], [0], [40, 5, 2100], 4, 2, 64, 64)
-    want = torch.empty(3, 4, 64, dtype=torch.bfloat16, device=DEV)
+    out = run(g, c, 0.125)  # a group without a prefix
+    verify(c, 0.125, out)
+    c["starts"], c["shared"] = c["starts"][:1], c["shared"][:0]
+    assert torch.equal(run(g, c, 0.125), out)  # no group at all
+    want = torch.empty_like(out)
     ws = g.decode_workspace(3, 4, 64, c["tables"].shape[1] * c["bs"])
     g.attn_decode_paged(c["q"], c["k"], c["v"], c["tables"], c["lens"], want, 0.125, workspace=ws)
-    assert torch.equal(run(g, c, 0.125), want)  # a group without a prefix
-    c["starts"], c["shared"] = c["starts"][:1], c["shared"][:0]
-    assert torch.equal(run(g, c, 0.125), want)  # no group at all
+    verify(c, 0.125, want, tc=False)
+
+
+def test_many_groups_and_sequences(gpu_lib):
+    """More groups than the planner keeps in shared memory, more sequences than its threads."""
+    g = gpu_lib
+    n = 150
+    members = [(i % 4) * 3 for i in range(n)]
+    B = sum(members)
+    c = case(members, [i % 5 for i in range(n)], [1 + (i * 7) % 40 for i in range(B)] + [3] * 400, 2, 1, 64, 64, bs=8,
+             alone=400, seed=9)
+    out = run(g, c, 0.125)
+    assert g.attn_get_device_error() == g.OK
+    verify(c, 0.125, out)
 
 
 def test_bad_groups_lengths_and_entries(gpu_lib):
