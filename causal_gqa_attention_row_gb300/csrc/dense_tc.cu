@@ -195,15 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // boxes of a lane, one for each 32 columns' blocks, lie in one pool block)
         const int per = p.tables ? kBN / p.bs : 1;
         const int my_block = lane % per;
-        const auto entry = [&](int j) {  // pool block of this lane's rows of tile j; num_blocks: zeros
+        const auto entry = [&](int j) {  // table entry of this lane's rows of tile j (-1 where it holds no key)
           const int t = (u.key0 + j * kBN) / p.bs + my_block;
-          if (j >= tiles || t >= p.mbps || t * p.bs >= u.key1) return p.num_blocks;
-          const int e = __ldg(p.tables + (size_t)u.seq * p.mbps + t);
-          if (e >= 0 && e < p.num_blocks) return e;
-          raise_error(p.err, kErrBounds);
-          return p.num_blocks;
+          return p.tables && j < tiles && t < p.mbps && t * p.bs < u.key1
+                     ? __ldg(p.tables + (size_t)u.seq * p.mbps + t)
+                     : p.num_blocks;
         };
-        int blk = p.tables ? entry(0) : 0;
+        int next_e = entry(0);  // (checked when it is used, a tile later)
         // the record's slot is free once the unit before last has been taken; Q once the
         // last S of the previous unit is done
         bool ok = true;
@@ -231,7 +229,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                           p.units ? 0 : u.batch_or_own, &hb.q_full[us]);
         for (int j = 0; j < tiles; ++j, ++t_all) {
           const int st = t_all % kStages;
-          const int next_blk = p.tables ? entry(j + 1) : 0;
+          // a block that holds no key, or whose entry is out of range (flagged), loads from
+          // past the end of the pool: the TMA engine fills it with zeros
+          int blk = next_e;
+          if (p.tables && (blk < 0 || blk > p.num_blocks)) blk = -1;
+          if (blk < 0 || (blk == p.num_blocks && (u.key0 + j * kBN) + my_block * p.bs < u.key1)) {
+            if (p.tables) raise_error(p.err, kErrBounds);
+            blk = p.num_blocks;
+          }
+          next_e = entry(j + 1);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {  // the K tile, then the V tile
             uint64_t* full = kv ? &hb.v_full[st] : &hb.k_full[st];
@@ -262,7 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             alive = false;
             break;
           }
-          blk = next_blk;
         }
       }
       if (lane == 0) {
@@ -602,11 +607,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float scale = part ? 1.f : (some ? 1.f / l_run : 0.f);
 #pragma unroll 1
       for (int cc = 0; cc < DV / 32; ++cc) {
+        // (a unit without keys reads whatever O holds, and writes zeros)
         uint32_t o[32];
-        if (tiles > 0) {
-          tc::tmem_ld_32x32b_x32(tO + cc * 32, o);
-          tc::tmem_ld_wait();
-        }
+        tc::tmem_ld_32x32b_x32(tO + cc * 32, o);
+        tc::tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = some ? __float_as_uint(__uint_as_float(o[e]) * scale) : 0u;
         if (r >= rows) {
