@@ -345,7 +345,7 @@ SharedLayout shared_layout(int B, int H, int Hkv, int d_v, int capacity, int n_g
   const long long units = each < some ? each : some;
   s.max_prefix_units = units > INT_MAX ? INT_MAX : (int)units;
   const size_t parts = (size_t)B * (size_t)heads + gqa::kOwnExtra;
-  size_t at = 256;  // [0]: units listed
+  size_t at = 256;  // [0]: units listed, [1]: ticket counter
   const auto take = [&](size_t n) {
     const size_t a = at;
     at += gqa::round_up256(n);
@@ -447,6 +447,7 @@ gqa_status attn_decode_shared_prefix(const void* q, const void* k_pool, const vo
   d.S_kv = capacity;
   d.units = plan.units;
   d.units_listed = plan.units_listed;
+  d.ticket = plan.units_listed + 1;
   d.seq_lens = seq_lens;
   d.own_rows = s.own_rows;
   d.tables = block_tables;

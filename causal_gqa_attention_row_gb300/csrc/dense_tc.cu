@@ -44,6 +44,7 @@
 // be 0. Warps whose rows are all padding only keep the barriers going.
 
 #include <atomic>
+#include <climits>
 
 #include "attn_tc.cuh"
 #include "tmap.h"
@@ -177,31 +178,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       int k_sent = 0, v_sent = 0;        // K and V tiles requested
       int last_q[2] = {-1, -1};          // the last unit of each parity, if a Q copy was requested for it
       bool alive = true;
-      for (int x = (int)blockIdx.x + (int)gridDim.x * w; alive; x += slots, ++n) {
-        const int us = n & 1;
-        DenseUnit u = {};
-        if (x < n_units) {
+      // The units of a plan differ in length: the first of each half is its slot, the others
+      // come by ticket. A unit's ticket, record and first table entry are three round trips
+      // to memory, so they are fetched step by step while the unit before sends its tiles.
+      int next_x = (int)blockIdx.x + (int)gridDim.x * w, ahead = 1;  // steps done: 1 number, 2 record, 3 entry
+      DenseUnit next_u = {};
+      int next_e = 0;
+      // boxes of a paged tile: this lane's lie in block my_block of its `per` (both powers of
+      // two or less than the warp: y and y + 32 fall on one block)
+      const int per = p.tables ? kBN / p.bs : 1;
+      const int my_block = lane % per;
+      // table entry of this lane's rows of tile j (num_blocks where it holds no key); checked
+      // where it is used
+      const auto entry = [&](const DenseUnit& u, int j) {
+        const int t = (u.key0 + j * kBN) / p.bs + my_block;
+        return t < p.mbps && t * p.bs < u.key1 ? __ldg(p.tables + (size_t)u.seq * p.mbps + t) : p.num_blocks;
+      };
+      const auto fetch_ahead = [&](int steps) {
+        if (ahead == 0) {
           if (p.units) {
-            const int4 a = __ldcg(reinterpret_cast<const int4*>(p.units + x));
-            const int4 c = __ldcg(reinterpret_cast<const int4*>(p.units + x) + 1);
-            u = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+            if (lane == 0) next_x = slots + atomicAdd(p.ticket, 1);
           } else {
-            u = cross_unit(p, x, DV);
+            next_x += slots;
           }
+          ahead = 1;
+        } else if (ahead == 1 && steps >= 2) {
+          if (p.units) next_x = __shfl_sync(0xffffffffu, next_x, 0);
+          next_u = DenseUnit{};
+          if (next_x < n_units) {
+            if (p.units) {
+              const int4 a = __ldcg(reinterpret_cast<const int4*>(p.units + next_x));
+              const int4 c = __ldcg(reinterpret_cast<const int4*>(p.units + next_x) + 1);
+              next_u = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+            } else {
+              next_u = cross_unit(p, next_x, DV);
+            }
+          }
+          ahead = 2;
+        } else if (ahead == 2 && steps >= 3) {
+          if (p.tables) next_e = entry(next_u, 0);
+          ahead = 3;
         }
+      };
+      for (; alive; ++n) {
+        const int us = n & 1;
+        while (ahead < 3) fetch_ahead(3);
+        const DenseUnit u = next_u;
+        int e = next_e;
+        ahead = 0;
         const int tiles = u.n_i ? unit_tiles(u) : 0;
         const int kvh = u.head0 / p.G;
-        // this lane's box of a paged tile (per and the lane count are powers of two: the
-        // boxes of a lane, one for each 32 columns' blocks, lie in one pool block)
-        const int per = p.tables ? kBN / p.bs : 1;
-        const int my_block = lane % per;
-        const auto entry = [&](int j) {  // table entry of this lane's rows of tile j (-1 where it holds no key)
-          const int t = (u.key0 + j * kBN) / p.bs + my_block;
-          return p.tables && j < tiles && t < p.mbps && t * p.bs < u.key1
-                     ? __ldg(p.tables + (size_t)u.seq * p.mbps + t)
-                     : p.num_blocks;
-        };
-        int next_e = entry(0);  // (checked when it is used, a tile later)
         // the record's slot is free once the unit before last has been taken; Q once the
         // last S of the previous unit is done
         bool ok = true;
@@ -231,13 +257,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = t_all % kStages;
           // a block that holds no key, or whose entry is out of range (flagged), loads from
           // past the end of the pool: the TMA engine fills it with zeros
-          int blk = next_e;
-          if (p.tables && (blk < 0 || blk > p.num_blocks)) blk = -1;
-          if (blk < 0 || (blk == p.num_blocks && (u.key0 + j * kBN) + my_block * p.bs < u.key1)) {
-            if (p.tables) raise_error(p.err, kErrBounds);
-            blk = p.num_blocks;
+          int blk = e;
+          if (p.tables) {
+            if ((blk < 0 || blk >= p.num_blocks) && u.key0 + j * kBN + my_block * p.bs < u.key1) {
+              raise_error(p.err, kErrBounds);
+              blk = p.num_blocks;
+            }
+            if (j + 1 < tiles) e = entry(u, j + 1);
           }
-          next_e = entry(j + 1);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {  // the K tile, then the V tile
             uint64_t* full = kv ? &hb.v_full[st] : &hb.k_full[st];
@@ -268,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             alive = false;
             break;
           }
+          fetch_ahead(3);  // one step a tile
         }
       }
       if (lane == 0) {
@@ -396,7 +424,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // With the arms the scores are moved into log2 units before the max, so the
     // exponent's multiplier is 1; plain: the raw q.k and the scale folded into it.
     const float qs = ARMS ? 1.f : p.qscale;
-    const float th = kRescaleLog2 / qs;
     const uint32_t tS = tmem + lane_addr + C::col_s(wg);
     const uint32_t tO = tmem + lane_addr + C::col_o(wg);
     const uint32_t tP = tmem + lane_addr + C::col_p(wg);
@@ -413,18 +440,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int key0 = u.key0, tiles = (u.key1 - key0 + kBN - 1) / kBN;
       // keys of this row: [lo_key, lim)
       int lim, lo_key = 0, pos = 0;
+      float th;  // the reference max moves when a score passes it by this much
       float alibi2 = 0.f;
       bool warp_live;
       {
         const int rows = u.n_i * p.GH;  // rows of the tile in use
         warp_live = quarter * 32 < rows;
-        lim = r < rows ? u.key1 : 0;
+        lim = u.key1;
         if (p.seq_lens) {  // a row is a sequence of its own length; its position is its last key's
           const int len = __ldg(p.seq_lens + u.i0 + min(r, rows - 1) / p.GH);
           pos = len - 1;
           lim = len >= 1 && len <= p.S_kv ? min(lim, len) : 0;
           if (ARMS) lo_key = first_visible_key(pos, p.window);
         }
+        // a padding row beside live ones needs no mask and never moves its reference: whatever
+        // it holds stays in its own row
+        if (r >= rows) lim = INT_MAX;
+        th = r < rows ? kRescaleLog2 / qs : INFINITY;
         if (ARMS && p.alibi) alibi2 = __ldg(p.alibi + u.head0 + min(r, rows - 1) % p.GH) * kLog2e;
       }
       float m_ref = -INFINITY;
@@ -497,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // keys that some row of the warp does not see weigh zero for it
-        if (__any_sync(0xffffffffu, j0 + kBN > lim || (ARMS && j0 < lo_key))) {
+        if (__any_sync(0xffffffffu, j0 > lim - kBN || (ARMS && j0 < lo_key))) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll

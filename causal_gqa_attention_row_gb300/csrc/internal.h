@@ -186,6 +186,7 @@ struct DenseParams {
   // shared prefix: units from the plan, a length per row
   const DenseUnit* units;
   const int* units_listed;
+  int* ticket;             // 0 at the launch
   const int32_t* seq_lens;
   int own_rows;
   const int32_t* tables;   // paged pools (NULL: contiguous)

@@ -5,9 +5,10 @@
 // The prefix of group g is tiles_g row tiles per KV head (and head chunk) times n_g key
 // tiles; the own keys of a sequence are one row tile per KV head (and head chunk). Units
 // take c key tiles each, c the same for all and chosen to minimise
-//   max(ceil(prefix units / slots) * (c + kDenseUnitTiles), (all tiles + units * kDenseUnitTiles) / slots),
+//   max(ceil(prefix units / slots) * (c + kDenseUnitTiles), (all tiles + units * kDenseUnitTiles) / slots) + c / 4,
 // in key tiles: the rounds that the prefixes' equal units take on the slots (units worked on
-// at a time), in whose last round own units fill the rest, or all work spread evenly.
+// at a time), in whose last round own units fill the rest, or all work spread evenly; and
+// something for the longest unit, which the rest may have to wait for.
 // Every candidate c is tried, a thread each. Own units are listed longest first.
 //
 // The other kernels wait for this one, so its round trips to memory count: groups, their
@@ -46,11 +47,42 @@ __device__ __forceinline__ int exclusive_scan(int v, int* warp_sums, int& total)
   return before + x - v;
 }
 
+// CTA-wide minimum and sum of 64-bit values (shuffles, then one value a warp: 64-bit
+// atomics on one shared word by every thread took the kernel 10 us). Ends with a barrier.
+__device__ __forceinline__ unsigned long long block_min(unsigned long long v, unsigned long long* warps) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) {
+    const unsigned long long o = __shfl_xor_sync(0xffffffffu, v, off);
+    v = o < v ? o : v;
+  }
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = warps[threadIdx.x & 31];
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) {
+    const unsigned long long o = __shfl_xor_sync(0xffffffffu, v, off);
+    v = o < v ? o : v;
+  }
+  __syncthreads();
+  return v;
+}
+__device__ __forceinline__ unsigned long long block_sum(unsigned long long v, unsigned long long* warps) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = warps[threadIdx.x & 31];
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  __syncthreads();
+  return v;
+}
+
 __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlan s) {
   __shared__ int warp_sums[32];
   __shared__ int bucket_at[kBuckets];
   __shared__ int bad, bad_len, max_tiles;
-  __shared__ unsigned long long best, own_total;
+  __shared__ unsigned long long warp_values[32];
   __shared__ DenseGroup group_s[kPlanGroups];
   grid_dep_wait();
   grid_dep_launch();
@@ -59,8 +91,6 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlan 
   if (tid == 0) {
     bad = bad_len = 0;
     max_tiles = 1;
-    best = ~0ull;
-    own_total = 0;
   }
   if (tid < kBuckets) bucket_at[tid] = 0;
   __syncthreads();
@@ -99,11 +129,19 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlan 
     }
     return b < groups[lo].first + groups[lo].members ? lo : -1;
   };
-  for (int b = tid; b < s.B; b += kThreads) {
-    const int g = find(b), len = length(b);
-    if (g < 0 || len == 0) continue;
-    atomicMax(&groups[g].kv_hi, len);
-    atomicMin(&groups[g].key_lo, len);
+  for (int b0 = 0; b0 < s.B; b0 += kThreads) {
+    const int b = b0 + tid, len = b < s.B ? length(b) : 0, g = len ? find(b) : -1;
+    // (most warps hold members of one group: one atomic a warp then)
+    if (__all_sync(0xffffffffu, g == __shfl_sync(0xffffffffu, g, 0))) {
+      const int most = __reduce_max_sync(0xffffffffu, len), least = __reduce_min_sync(0xffffffffu, len);
+      if (g >= 0 && (tid & 31) == 0) {
+        atomicMax(&groups[g].kv_hi, most);
+        atomicMin(&groups[g].key_lo, least);
+      }
+    } else if (g >= 0) {
+      atomicMax(&groups[g].kv_hi, len);
+      atomicMin(&groups[g].key_lo, len);
+    }
   }
   __syncthreads();
   for (int g = tid; g < s.n_groups; g += kThreads) {
@@ -135,13 +173,13 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlan 
     mine_own += (unsigned long long)nt * heads;
     longest = max(longest, nt);
   }
-  if (mine_own) atomicAdd(&own_total, mine_own);
-  if (longest > 1) atomicMax(&max_tiles, longest);
-  __syncthreads();
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (longest > 1 && (tid & 31) == 0) atomicMax(&max_tiles, longest);
   // ---- c
-  const long long own_tiles = (long long)own_total, own_items = (long long)s.B * heads;
+  const long long own_tiles = (long long)block_sum(mine_own, warp_values), own_items = (long long)s.B * heads;
   const long long c_own_least = (own_tiles + kOwnExtra - 1) / kOwnExtra;  // own parts <= items + kOwnExtra
   const int c_most = min(max_tiles, kMostTiles);
+  unsigned long long mine_best = ~0ull;
   for (int c = 1 + tid; c <= c_most; c += kThreads) {
     long long units = 0, tiles = 0;
     for (int g = 0; g < s.n_groups; ++g) {
@@ -154,10 +192,12 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlan 
     const long long even =
         (tiles + own_tiles + (units + own_tiles / max((long long)c, c_own_least) + own_items / 2) * kDenseUnitTiles) /
         s.slots;
-    // ties go to the longer units: fewer partial results
-    atomicMin(&best, (unsigned long long)max(max(rounds, even), (long long)c) << 24 | (unsigned)(kMostTiles - c));
+    // a quarter of a unit for the tail that one leaves behind; ties go to the longer units
+    const long long cost = 4 * max(rounds, even) + c;
+    const unsigned long long key = (unsigned long long)cost << 24 | (unsigned)(kMostTiles - c);
+    mine_best = key < mine_best ? key : mine_best;
   }
-  __syncthreads();
+  const unsigned long long best = block_min(mine_best, warp_values);
   // (the largest c always fits: the caller sized max_prefix_units for it)
   const int c = best == ~0ull ? c_most : kMostTiles - (int)(best & 0xffffff);
   const int c_own = (int)max((long long)c, max(c_own_least, 1ll));
@@ -209,7 +249,10 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlan 
     }
     bucket_at[2 * tid] = n_prefix + n_full + sum - x - y;
     bucket_at[2 * tid + 1] = n_prefix + n_full + sum - y;
-    if (tid == 31) *s.units_listed = n_prefix + n_full + sum;
+    if (tid == 31) {
+      s.units_listed[0] = n_prefix + n_full + sum;
+      s.units_listed[1] = 0;  // the ticket counter
+    }
   }
   __syncthreads();
   const int part_step = (int)(dense_part_floats(s.own_rows, s.dv) / 4);
