@@ -468,14 +468,11 @@ gqa_status attn_decode_shared_prefix(const void* q, const void* k_pool, const vo
   if (e != cudaSuccess) return from_cuda(e);
 
   gqa::DenseCombine c{};
-  c.n_rows = (long long)B * H;
+  c.n_b = 1;
+  c.n_i = B;
   c.H = H;
-  c.Hkv = Hkv;
-  c.G = plan.G;
   c.GH = s.GH;
   c.RPT = s.RPT;
-  c.n_hchunks = s.n_hchunks;
-  c.n_i = B;
   c.dv = d_v;
   c.partial = d.partial;
   c.seq = plan.seq;
@@ -500,8 +497,11 @@ struct CrossPlan {
 };
 
 // Rows of a KV head (query rows times heads of its group) from which the tensor cores
-// are taken.
-constexpr int kCrossTcRows = 16;
+// are taken: the SIMT kernel reads the keys once for up to NV rows (a power of two), the
+// tensor-core kernel once for 128. Measured at 64 sequences of up to 1500 keys: one row of 16
+// KV heads of 64 40.9 us on the SIMT kernel and 65 us on the tensor cores, two rows 58 and 66,
+// four 89 and 66, eight 147 and 66; one row of 8 groups of four, d = 128, 56 and 55.
+constexpr int kCrossTcRows = 3;
 
 bool cross_plan(int B, int S, int L, int H, int Hkv, int d_k, int d_v, int bf16, bool scale_ok, CrossPlan* c) {
   *c = CrossPlan{};
@@ -539,10 +539,14 @@ bool cross_plan(int B, int S, int L, int H, int Hkv, int d_k, int d_v, int bf16,
   c->split_rows = L;
   c->max_splits = 1;
   if (S == 1) {
-    // splits of 2048 keys, halved down to 256 while they would leave SMs without work
+    // splits of 2048 keys, halved to 512 until there are several units for each of the
+    // kernel's 456 resident CTAs, and to 256 while SMs would go without work. Measured: 1024
+    // items of up to 1500 keys 51.6 us whole, 42.2 / 40.9 / 43.2 us in splits of 1024 / 512 /
+    // 256; 16 items of 4000 keys 40.2, 24.9, 17.4, 15.1 us.
     const long long items = (long long)B * Hkv * (G / c->simt_GH);
     int r = gqa::kSplitRows;
-    while (r > 256 && items * ceil_div(L, r) < 2 * gqa::kDenseSms) r /= 2;
+    while ((r > 512 && items * ceil_div(L, r) < 3 * 1024) || (r > 256 && items * ceil_div(L, r) < 2 * gqa::kDenseSms))
+      r /= 2;
     c->max_splits = ceil_div(L, r);
     if (c->max_splits > 1) {
       c->split_rows = r;
@@ -611,14 +615,11 @@ gqa_status attn_cross(const void* q, const void* k, const void* v, const int32_t
     const cudaError_t e = gqa::launch_dense_tc(q, k, v, d, B, d_k, d_v, false, st);
     if (e != cudaSuccess || c.n_splits == 1) return from_cuda(e);
     gqa::DenseCombine m{};
-    m.n_rows = (long long)B * seq_q * H;
+    m.n_b = B;
+    m.n_i = seq_q;
     m.H = H;
-    m.Hkv = Hkv;
-    m.G = d.G;
     m.GH = c.GH;
     m.RPT = c.RPT;
-    m.n_hchunks = c.n_hchunks;
-    m.n_i = seq_q;
     m.dv = d_v;
     m.n_tiles = c.n_tiles;
     m.n_splits = c.n_splits;

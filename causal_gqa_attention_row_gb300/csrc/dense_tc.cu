@@ -15,10 +15,10 @@
 // keys; where a row has more than one range, each leaves (m, l, o) in fp32 and
 // dense_combine_kernel joins them in a fixed order.
 //
-// A tile of 128 keys (64 KB of K and V at d = 128) takes a CTA about 1.1 us, more than the
-// 57 GB/s an SM that HBM can deliver, even for a single row: so rows that stream their own
-// keys (M = 4 of 128 rows in use) run here too, in the same list as the prefixes, and the
-// two share the GPU without a boundary between them.
+// A tile of 128 keys (64 KB of K and V at d = 128) takes a CTA about 1.1 us whatever rows it
+// has: 58 GB/s, above the 45 GB/s that is an SM's share of HBM. So rows that stream their
+// own keys (M = 4 of 128 rows in use) run here too, in the same list as the prefixes, and
+// the two share the GPU without a boundary between them.
 //
 // The kernel is persistent: a CTA per SM with two independent halves, each a softmax
 // warpgroup with a producer warp and an MMA warp of its own, its own Q buffer, K and V
@@ -26,8 +26,18 @@
 // half, so that a list shorter than the slots spreads over the SMs first). While one half
 // is in its softmax the other's products run. The producer runs ahead into the next unit
 // as stages come free, so a unit costs its tiles plus one epilogue, not a launch, a set-up
-// and a first load (one CTA per unit, with two warpgroups that shared a unit and merged at
-// its end: shared document 62 -> see DESIGN, cross long 357 us).
+// and a first load. Units of unequal length (the shared prefixes) are drawn from a ticket
+// counter; those of attn_cross are alike and go round by slot.
+//
+// Measured at 32 heads on 8 KV heads of 128, combine included: 64 sequences behind a prefix
+// of 8,192 keys with up to 512 of their own 48 us with their plan; 256 sequences behind four
+// prefixes of 16,384 keys 202 us (0.59 of the measured bf16 rate); attn_cross of 8 x 1,024 rows
+// on 2,048 to 4,096 keys 385 us, 1.07 PFLOP/s (0.57). What bounds the long cases is the time
+// between a half's tiles, about 2.1 us for 1,024 cycles of products: S, softmax and PV of a
+// half follow one another, and the K and V tiles, which the halves do not share, come from
+// L2 at 8.4 TB/s. (One CTA per unit, with two warpgroups that shared a unit and merged at its
+// end: 357 us for that attn_cross call, but 62 us for the first, whose units are many and
+// short.)
 //
 //   warps 0-3, 4-7   softmax of half 0, 1: thread t owns row t of the tile (TMEM lane t)
 //   warps 8, 11      TMA producer of half 0, 1 (Q once a unit, then K and V tiles; paged:
@@ -36,7 +46,7 @@
 //
 // Per tile and half, as in the causal prefill (see prefill_tc.cu): S into registers, row
 // max, lazily moved reference max, fp32 exponentials, P in bf16 for the second product
-// (rounded once, a relative 2^-9 that averages over the keys; the row sum keeps the fp32
+// (rounded once, a relative 2^-8 at most that averages over the keys; the row sum keeps the fp32
 // p). At d_v = 64 S_{j+1} is issued as soon as S_j is in registers; at d_v = 128 P lies over
 // S, so S_{j+1} waits for PV_j, of which half is issued at half of P. A row's keys end at its
 // own limit, and in the tile that holds the last key the V rows behind it are zeroed in
@@ -59,14 +69,15 @@ struct DenseCfg {
   static constexpr int kTileK = kCBK * kBlk, kTileV = kCBV * kBlk;
   static constexpr bool kAlias = DV > 64;  // P over the first 64 columns of S
   static constexpr int kHalves = DK > 128 ? 1 : 2;
-  static constexpr int kStages = DK > 128 ? 2 : DK > 64 ? 1 : 3;  // K and V stages of a half
+  static constexpr int kStages = DK > 128 ? 2 : DK > 64 ? 1 : 2;  // K and V stages of a half
   __host__ __device__ static constexpr uint32_t col_s(int w) { return kAlias ? (128 + DV) * w : 128 * w; }
   __host__ __device__ static constexpr uint32_t col_o(int w) { return kAlias ? (128 + DV) * w + 128 : 256 + 64 * w; }
   __host__ __device__ static constexpr uint32_t col_p(int w) { return kAlias ? (128 + DV) * w : 384 + 64 * w; }
   // shared memory of a half: Q, K stages, V stages
   static constexpr int kOffK = kTileK, kOffV = kOffK + kStages * kTileK;
   static constexpr int kHalfBytes = kOffV + kStages * kTileV;
-  static constexpr int kOffBar = kHalves * kHalfBytes;
+  static constexpr int kOffOut = kHalves * kHalfBytes;  // 64 columns of a half's output tile
+  static constexpr int kOffBar = kOffOut + kHalves * kBlk;
   static constexpr int kSmemBytes = kOffBar + 1024 + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 232448, "over the 227 KiB a CTA may use");
 };
@@ -87,6 +98,12 @@ struct DenseBars {
   int abort_flag;
 };
 static_assert(sizeof(DenseBars) <= 1024, "barrier block");
+
+// A value that the compiler takes for a new one.
+__device__ __forceinline__ uint32_t fresh(uint32_t x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
 
 // Unit x of an attn_cross call.
 __device__ __forceinline__ DenseUnit cross_unit(const DenseParams& p, int x, int dv) {
@@ -117,7 +134,7 @@ template <int DK, int DV, bool ARMS>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const DenseParams p) {
+                    const __grid_constant__ CUtensorMap tm_o, const DenseParams p) {
   using C = DenseCfg<DK, DV>;
   constexpr int kTileK = C::kTileK, kTileV = C::kTileV, kStages = C::kStages;
   extern __shared__ unsigned char smem_raw[];
@@ -217,6 +234,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           ahead = 2;
         } else if (ahead == 2 && steps >= 3) {
           if (p.tables) next_e = entry(next_u, 0);
+          // its Q and (contiguous) first K and V tiles on their way to L2: units that end
+          // together would all wait for HBM at their next one's start
+          if (next_u.n_i && next_u.key1 > next_u.key0) {
+            const int own = p.units && next_u.batch_or_own, seq = p.units ? 0 : next_u.batch_or_own;
+            if (lane < C::kCBK)
+              tc::tma_prefetch_4d(own ? &tm_q1 : &tm_q, lane * 64, next_u.head0, next_u.i0, seq);
+            if (!p.tables && lane < C::kCBK)
+              tc::tma_prefetch_4d(&tm_k, lane * 64, next_u.key0, next_u.head0 / p.G, next_u.seq);
+            if (!p.tables && lane < C::kCBV)
+              tc::tma_prefetch_4d(&tm_v, lane * 64, next_u.key0, next_u.head0 / p.G, next_u.seq);
+          }
           ahead = 3;
         }
       };
@@ -315,96 +343,87 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The whole warp walks the loop (it zeroes V rows together); lane 0 waits and issues.
       const uint32_t idS = tc::idesc_bf16_f32(kBM, kBN, false);
       const uint32_t idO = tc::idesc_bf16_f32(kBM, DV, true);
-      constexpr uint64_t kHi = tc::desc_sw128_hi(0, 1024);
-      const uint64_t dQ = kHi | (smem_u32(sm) >> 4);
-      const uint64_t dK0 = kHi | (smem_u32(sm + C::kOffK) >> 4);
-      const uint64_t dV0 = tc::desc_sw128_hi(C::kCBV > 1 ? kBlk : 0, 1024) | (smem_u32(sm + C::kOffV) >> 4);
+      constexpr uint64_t kHi = tc::desc_sw128_hi(0, 1024), kHiV = tc::desc_sw128_hi(C::kCBV > 1 ? kBlk : 0, 1024);
       const uint32_t dS = tmem + C::col_s(w), dO = tmem + C::col_o(w), tP = tmem + C::col_p(w);
-      const auto issue_s = [&](int t) -> bool {  // S = Q K_t^T (lane 0)
-        const int st = t % kStages;
-        if (!wait_or_abort(&hb.k_full[st], (t / kStages) & 1, bars, p.err)) return false;
-        tc::fence_after_sync();
-        const uint64_t dK = dK0 + (uint64_t)((st * kTileK) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) {
-          const uint32_t at = (kk / 4) * kBlk + (kk % 4) * 32;
-          tc::mma_f16_ss(dS, dQ + (at >> 4), dK + (at >> 4), idS, kk > 0);
-        }
-        tc::mma_commit(&hb.s_full);
-        tc::mma_commit(&hb.k_empty[st]);  // the K stage is free once S is done
-        return true;
-      };
+      // One place that issues S and one that issues PV, whatever tile or unit they are for: a
+      // second copy of either, run once a unit, was fetched from L2 instruction by instruction
+      // (2,000 cycles for eight MMAs). At d_v = 64 PV runs a tile behind S.
+      constexpr int kLag = C::kAlias ? 0 : 1;
       bool ok = true;
-      int t_all = 0;
+      int t_all = 0;  // tiles before this unit
       for (int n = 0; ok; ++n) {
         const int us = n & 1;
         ok = warp_wait_tc(&hb.q_full[us], (n >> 1) & 1, bars, p.err);
         if (!ok) break;
-        const int n_i = hb.unit[us].n_i, key0 = hb.unit[us].key0, key1 = hb.unit[us].key1;
+        const int n_i = hb.unit[us].n_i, keys = hb.unit[us].key1 - hb.unit[us].key0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&hb.unit_free[us]);
         if (n_i == 0) break;
-        const int tiles = (key1 - key0 + kBN - 1) / kBN;
-        if (tiles == 0) continue;
-        if (lane == 0) {
-          // S's columns: free once the previous tile's S is in registers (d_v = 64), or its PV
-          // has read the P that lies over them (d_v = 128)
-          if (t_all > 0) ok = wait_or_abort(C::kAlias ? &hb.o_done : &hb.s_free, (t_all - 1) & 1, bars, p.err);
-          if (ok) {
-            tc::fence_after_sync();
-            ok = issue_s(t_all);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        for (int k = 0; ok && k < tiles; ++k, ++t_all) {
-          const int st = t_all % kStages;
-          if (lane == 0) {
-            if (!C::kAlias && k + 1 < tiles)
-              ok = wait_or_abort(&hb.s_free, t_all & 1, bars, p.err) && issue_s(t_all + 1);
-            ok = ok && wait_or_abort(&hb.v_full[st], (t_all / kStages) & 1, bars, p.err);
-          }
-          const int valid = key1 - key0 - k * kBN;  // keys of the tile
-          if (valid < kBN) {  // (uniform) the rows behind the last key; the swizzle moves chunks within a row only
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-            __syncwarp();
-            unsigned char* dst = sm + C::kOffV + st * kTileV;
-            for (int i = lane; i < (kBN - valid) * 8 * C::kCBV; i += 32) {
-              const int chunk = i % 8, cb = (i / 8) % C::kCBV, row = valid + i / (8 * C::kCBV);
-              *reinterpret_cast<uint4*>(dst + cb * kBlk + row * 128 + chunk * 16) = make_uint4(0, 0, 0, 0);
-            }
-            tc::fence_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) {
-            ok = ok && wait_or_abort(C::kAlias ? &hb.p_half : &hb.p_full, t_all & 1, bars, p.err);
+        const int tiles = (keys + kBN - 1) / kBN;
+#pragma unroll 1
+        for (int i = 0; ok && i < tiles + kLag && tiles > 0; ++i) {
+          if (lane == 0 && i < tiles) {  // S = Q K^T of tile i
+            const int t = t_all + i, st = t % kStages;
+            // its columns are free once the previous tile's S is in registers (d_v = 64), or its
+            // PV has read the P that lies over them (d_v = 128)
+            if (t > 0) ok = wait_or_abort(C::kAlias ? &hb.o_done : &hb.s_free, (t - 1) & 1, bars, p.err);
+            ok = ok && wait_or_abort(&hb.k_full[st], (t / kStages) & 1, bars, p.err);
             if (ok) {
               tc::fence_after_sync();
-              const uint64_t dV = dV0 + (uint64_t)((st * kTileV) >> 4);
+              // (the descriptors are built here from the buffers' addresses: as loop invariants
+              // all of them were kept, in more registers than the control warps have)
+              const uint64_t dQ = kHi | fresh(smem_u32(sm) >> 4);
+              const uint64_t dK = kHi | fresh(smem_u32(sm + C::kOffK + st * kTileK) >> 4);
 #pragma unroll
-              for (int kk = 0; kk < kBN / 16; ++kk) {
-                if (C::kAlias && kk == kBN / 32) {
-                  ok = wait_or_abort(&hb.p_full, t_all & 1, bars, p.err);
-                  if (!ok) break;
-                  tc::fence_after_sync();
-                }
-                tc::mma_f16_ts(dO, tP + kk * 8, dV + kk * (2048 >> 4), idO, (k > 0 || kk > 0));
+              for (int kk = 0; kk < DK / 16; ++kk) {
+                const uint32_t at = (kk / 4) * kBlk + (kk % 4) * 32;
+                tc::mma_f16_ss(dS, dQ + (at >> 4), dK + (at >> 4), idS, kk > 0);
               }
+              tc::mma_commit(&hb.s_full);
+              tc::mma_commit(&hb.k_empty[st]);  // the K stage is free once S is done
             }
-            if (ok) {
-              tc::mma_commit(&hb.o_done);
-              tc::mma_commit(&hb.v_empty[st]);
-              if (C::kAlias && k + 1 < tiles) {
-                ok = wait_or_abort(&hb.o_done, t_all & 1, bars, p.err);
-                if (ok) {
-                  tc::fence_after_sync();
-                  ok = issue_s(t_all + 1);
+          }
+          const int k = i - kLag;
+          if (k >= 0) {  // O += P V of tile k
+            const int t = t_all + k, st = t % kStages;
+            if (lane == 0) ok = ok && wait_or_abort(&hb.v_full[st], (t / kStages) & 1, bars, p.err);
+            const int valid = keys - k * kBN;  // keys of the tile
+            if (valid < kBN) {  // (uniform) the rows behind the last key; the swizzle moves chunks within a row only
+              ok = __shfl_sync(0xffffffffu, ok, 0);
+              if (!ok) break;
+              __syncwarp();
+              unsigned char* dst = sm + C::kOffV + st * kTileV;
+              dst += lane / 8 % C::kCBV * kBlk + lane % 8 * 16;
+#pragma unroll 4
+              for (int row = valid + lane / (8 * C::kCBV); row < kBN; row += 4 / C::kCBV)
+                *reinterpret_cast<uint4*>(dst + row * 128) = make_uint4(0, 0, 0, 0);
+              tc::fence_async_smem();
+              __syncwarp();
+            }
+            if (lane == 0) {
+              ok = ok && wait_or_abort(C::kAlias ? &hb.p_half : &hb.p_full, t & 1, bars, p.err);
+              if (ok) {
+                tc::fence_after_sync();
+                const uint64_t dV = kHiV | fresh(smem_u32(sm + C::kOffV + st * kTileV) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kBN / 16; ++kk) {
+                  if (C::kAlias && kk == kBN / 32) {
+                    ok = wait_or_abort(&hb.p_full, t & 1, bars, p.err);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                  }
+                  tc::mma_f16_ts(dO, tP + kk * 8, dV + kk * (2048 >> 4), idO, (k > 0 || kk > 0));
                 }
+              }
+              if (ok) {
+                tc::mma_commit(&hb.o_done);
+                tc::mma_commit(&hb.v_empty[st]);
               }
             }
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
         }
+        t_all += tiles;
       }
       // every MMA issued above has completed before TMEM is released
       if (lane == 0) {
@@ -530,13 +549,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // keys that some row of the warp does not see weigh zero for it
         if (__any_sync(0xffffffffu, j0 > lim - kBN || (ARMS && j0 < lo_key))) {
+          const int end = lim - j0, begin = ARMS ? lo_key - j0 : 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int key = j0 + c * 32 + e;
-              if (key >= lim || key < lo_key) sv[c][e] = __float_as_uint(-INFINITY);
-            }
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e >= end || (ARMS && c * 32 + e < begin)) sv[c][e] = __float_as_uint(-INFINITY);
         }
         // ---- the tile's row max; the reference moves only past the threshold
         float mx8[8];
@@ -565,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::fence_after_sync();
             uint32_t o[32];
-#pragma unroll
+#pragma unroll 1  // (rare, and the tile loop's code has to stay in the instruction cache)
             for (int c = 0; c < DV / 32; ++c) {
               tc::tmem_ld_32x32b_x32(tO + c * 32, o);
               tc::tmem_ld_wait();
@@ -623,55 +641,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait_tc(&hb.o_done, (t_all - 1) & 1, bars, p.err)) break;
         tc::fence_after_sync();
       }
-      if (!warp_live) {
-        if (lane == 0) mbar_arrive(&hb.unit_free[us]);
-        continue;
-      }
-      const int rows = u.n_i * p.GH, at = u.part, batch_or_own = u.batch_or_own;
-      const int R = p.units && batch_or_own ? p.own_rows : kBM;
-      float* part = at >= 0 ? p.partial + (size_t)at * 4 : nullptr;
-      __nv_bfloat16* out = nullptr;
-      if (!part)
-        out = p.out + (((size_t)batch_or_own * p.n_i + u.i0 + min(r, rows - 1) / p.GH) * p.H + u.head0 +
-                       min(r, rows - 1) % p.GH) * DV;
       // (a NaN among a row's scores makes its l NaN, and has to reach the output)
       const bool some = l_run != 0.f;
-      const float scale = part ? 1.f : (some ? 1.f / l_run : 0.f);
+      const int at = u.part;
+      if (at >= 0) {
+        if (warp_live) {
+          const int rows = u.n_i * p.GH, R = p.units && u.batch_or_own ? p.own_rows : kBM;
+          float* part = p.partial + (size_t)at * 4;
 #pragma unroll 1
-      for (int cc = 0; cc < DV / 32; ++cc) {
-        // (a unit without keys reads whatever O holds, and writes zeros)
-        uint32_t o[32];
-        tc::tmem_ld_32x32b_x32(tO + cc * 32, o);
-        tc::tmem_ld_wait();
+          for (int cc = 0; cc < DV / 32; ++cc) {
+            // (a unit without keys reads whatever O holds, and writes zeros)
+            uint32_t o[32];
+            tc::tmem_ld_32x32b_x32(tO + cc * 32, o);
+            tc::tmem_ld_wait();
+            if (r < rows) {
+              // [column / 4][row][4]: the rows of a warp write contiguous bytes
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = some ? __float_as_uint(__uint_as_float(o[e]) * scale) : 0u;
-        if (r >= rows) {
-          // a padding row beside live ones: nothing to write
-        } else if (part) {
-          // [column / 4][row][4]: the rows of a warp write contiguous bytes
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-            *reinterpret_cast<uint4*>(part + ((size_t)(cc * 8 + t) * R + r) * 4) =
-                make_uint4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
-        } else {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            uint32_t w4[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              w4[v] = pack_bf16(__uint_as_float(o[t * 8 + 2 * v]), __uint_as_float(o[t * 8 + 2 * v + 1]));
-            *reinterpret_cast<uint4*>(out + cc * 32 + t * 8) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              for (int t = 0; t < 8; ++t)
+                *reinterpret_cast<uint4*>(part + ((size_t)(cc * 8 + t) * R + r) * 4) =
+                    some ? make_uint4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]) : make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();  // the next columns are loaded by the whole warp
+          }
+          if (r < rows) {
+            part[(size_t)R * DV + r] = m_ref * qs;
+            part[(size_t)R * DV + R + r] = l_run;
           }
         }
-        __syncwarp();  // the next columns are loaded by the whole warp
-      }
-      if (part && r < rows) {
-        part[(size_t)R * DV + r] = m_ref * qs;
-        part[(size_t)R * DV + R + r] = l_run;
+      } else {
+        // 64 columns at a time through shared memory (the output map's 128-byte swizzle) and
+        // out by TMA: stored from the registers, each row's 16 bytes on a line of its own, a
+        // tile held the load/store unit for 8,000 cycles, the other half's barriers with it
+        const float inv = some ? 1.f / l_run : 0.f;
+        unsigned char* so = smem + C::kOffOut + wg * kBlk;
+#pragma unroll 1
+        for (int cb = 0; cb < C::kCBV; ++cb) {
+          if ((threadIdx.x & 127) == 0) tc::bulk_wait_group_read0();  // the last store has read the buffer
+          named_bar_sync(1 + wg, 128);
+          if (warp_live) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t o[32];
+              tc::tmem_ld_32x32b_x32(tO + cb * 64 + hf * 32, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                uint32_t w4[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                  const float x0 = __uint_as_float(o[t * 8 + 2 * v]) * inv, x1 = __uint_as_float(o[t * 8 + 2 * v + 1]) * inv;
+                  w4[v] = some ? pack_bf16(x0, x1) : 0u;
+                }
+                *reinterpret_cast<uint4*>(so + r * 128 + (((hf * 4 + t) ^ (r & 7)) * 16)) =
+                    make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              }
+            }
+          }
+          tc::fence_async_smem();
+          named_bar_sync(1 + wg, 128);
+          if ((threadIdx.x & 127) == 0) {
+            // rows past the end of the sequence fall outside the tensor and are not written
+            tc::tma_store_4d(&tm_o, so, cb * 64, u.head0, u.i0, u.batch_or_own);
+            tc::bulk_commit_group();
+          }
+        }
       }
       tc::fence_before_sync();  // O is read: the next unit's first PV may overwrite it
+      __syncwarp();
       if (lane == 0) mbar_arrive(&hb.unit_free[us]);
     }
+    if ((threadIdx.x & 127) == 0) tc::bulk_wait_group_read0();  // shared memory stays valid until then
   }
 
   tc::fence_before_sync();
@@ -684,74 +723,72 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the partial results of a row, in a fixed order (key ranges of the row's tile,
 // then, for the shared-prefix step, the parts of the sequence's own keys):
 //   M = max m_s (and the sink logit),  out = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s
-// A warp per row; lane c takes columns 4c .. 4c + 3. Latency bounds it, so a row costs
-// two round trips: its plan, then the loads of up to kFlight parts at once; M moves from
-// round to round as the sums are rescaled.
+// A CTA takes rows (i, head) of one head chunk, next to one another in the parts: 256 / (d_v /
+// 4) rows by d_v / 4 threads of four columns, rows along the lanes, so that a warp's loads of
+// a part fall on few lines. Latency bounds it: four parts are in flight a thread, M moves from
+// round to round as the sums are rescaled. (A row per warp touched 32 lines a part; on an SM
+// whose shared memory the kernel above had just used, with 28 KB left for L1, each round of
+// loads took 3 us. The L1 is asked for in full at the launch.)
 __global__ void __launch_bounds__(256) dense_combine_kernel(const DenseCombine p) {
-  constexpr int kFlight = 8;
   grid_dep_wait();
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (row >= p.n_rows) return;
-  const int h = (int)(row % p.H);
-  const int i = (int)(row / p.H % p.n_i);  // shared prefix: the sequence
-  const int chunk = h / p.GH;              // (KV head, head chunk)
+  const int dv = p.dv, rows_here = 1024 / dv;  // a power of two, as dv is
+  const int r = threadIdx.x & (rows_here - 1), c = threadIdx.x / rows_here;
+  const int chunks = p.H / p.GH, per_chunk = (p.n_i * p.GH + rows_here - 1) / rows_here;
+  int x = blockIdx.x;
+  const int at_row = x % per_chunk * rows_here + r;  // i * GH + head within the chunk
+  x /= per_chunk;
+  const int chunk = x % chunks, b = x / chunks;  // chunk: (KV head, head chunk)
+  if (at_row >= p.n_i * p.GH) return;
+  const int i = at_row / p.GH, g = at_row - i * p.GH;  // shared prefix: i is the sequence
   // ---- the row's parts: n units of 128 rows, then n_own of own_rows
-  long long unit0;
-  int n, in_tile, n_own = 0;
-  const float* R = nullptr;
-  const int dv = p.dv;
-  if (p.seq) {
-    const int4* sp = reinterpret_cast<const int4*>(p.seq + i);
-    const int4 s0 = __ldcg(sp), s1 = __ldcg(sp + 1);
-    n = s0.x;
-    unit0 = s0.y + (long long)chunk * s0.z;
-    in_tile = s0.w + h % p.GH;
-    n_own = s1.x;
-    R = p.own_partial + (size_t)(s1.y + chunk * n_own) * dense_part_floats(p.own_rows, dv);
-  } else {
-    n = p.n_splits;
-    unit0 = ((row / p.H / p.n_i * (p.H / p.GH) + chunk) * p.n_tiles + i / p.RPT) * n;
-    in_tile = i % p.RPT * p.GH + h % p.GH;
-  }
   const size_t unit_floats = dense_part_floats(kBM, dv), own_floats = dense_part_floats(p.own_rows, dv);
-  const float* U = p.partial + (size_t)unit0 * unit_floats;
-  const float z2 = p.sinks ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
+  int n = p.n_splits, n_own = 0, in_tile;
+  const float *U, *R = nullptr;
+  if (p.seq) {
+    const int4 s0 = __ldcg(reinterpret_cast<const int4*>(p.seq + i));
+    const int4 s1 = __ldcg(reinterpret_cast<const int4*>(p.seq + i) + 1);
+    n = s0.x;
+    U = p.partial + (size_t)(s0.y + chunk * s0.z) * unit_floats;
+    in_tile = s0.w + g;
+    n_own = s1.x;
+    R = p.own_partial + (size_t)(s1.y + chunk * n_own) * own_floats;
+  } else {
+    const int tile = i / p.RPT;
+    U = p.partial + (size_t)((b * chunks + chunk) * p.n_tiles + tile) * n * unit_floats;
+    in_tile = at_row - tile * p.RPT * p.GH;
+  }
   const int total = n + n_own;
-  const int c = lane;
-  if (4 * c >= dv) return;
+  const float z2 = p.sinks ? __ldg(p.sinks + chunk * p.GH + g) * kLog2e : -INFINITY;
   float M = z2, den = z2 != -INFINITY ? 1.f : 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < total; s0 += kFlight) {
-    float4 o[kFlight];
-    float m[kFlight], l[kFlight];
+#pragma unroll 1
+  for (int s0 = 0; s0 < total; s0 += 4) {
+    float4 o[4];
+    float m[4], l[4];
 #pragma unroll
-    for (int t = 0; t < kFlight; ++t) {
+    for (int t = 0; t < 4; ++t) {
       const int s = s0 + t;
       m[t] = -INFINITY;
       l[t] = 0.f;
       o[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s >= total) continue;
-      const bool own = s >= n;
-      const float* u = own ? R + (s - n) * own_floats : U + s * unit_floats;
-      const int rows = own ? p.own_rows : kBM, at = own ? h % p.GH : in_tile;
-      m[t] = __ldcg(u + rows * dv + at);
-      l[t] = __ldcg(u + rows * dv + rows + at);
-      o[t] = __ldcg(reinterpret_cast<const float4*>(u) + (size_t)c * rows + at);
+      if (s < total) {
+        const bool own = s >= n;
+        const float* u = own ? R + (s - n) * own_floats : U + s * unit_floats;
+        const int rows = own ? p.own_rows : kBM, at = own ? g : in_tile;
+        m[t] = __ldcg(u + rows * dv + at);
+        l[t] = __ldcg(u + rows * dv + rows + at);
+        o[t] = __ldcg(reinterpret_cast<const float4*>(u) + (size_t)c * rows + at);
+      }
     }
-    float Mn = M;
+    const float Mn = fmaxf(fmaxf(fmaxf(M, m[0]), fmaxf(m[1], m[2])), m[3]);
+    const float f = M == -INFINITY ? 0.f : ex2f(M - Mn);
+    den = den == 0.f ? 0.f : den * f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    M = Mn;
 #pragma unroll
-    for (int t = 0; t < kFlight; ++t) Mn = fmaxf(Mn, m[t]);
-    if (Mn != M) {
-      const float f = M == -INFINITY ? 0.f : exp2f(M - Mn);
-      den *= f;  // (a sum that is NaN stays so)
-      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-      M = Mn;
-    }
-#pragma unroll
-    for (int t = 0; t < kFlight; ++t) {
-      if (l[t] == 0.f) continue;  // no visible key
-      const float w = exp2f(m[t] - M);
+    for (int t = 0; t < 4; ++t) {
+      if (l[t] == 0.f) continue;  // no visible key, whatever m and o hold (a NaN in l goes through)
+      const float w = ex2f(m[t] - M);
       den = fmaf(w, l[t], den);
       acc.x = fmaf(w, o[t].x, acc.x);
       acc.y = fmaf(w, o[t].y, acc.y);
@@ -760,10 +797,9 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const DenseCombine p
     }
   }
   const float inv = den != 0.f ? 1.f / den : 0.f;
-  uint2 v;
-  v.x = pack_bf16(acc.x * inv, acc.y * inv);
-  v.y = pack_bf16(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(p.out + (size_t)row * dv + 4 * c) = v;
+  const size_t row = ((size_t)b * p.n_i + i) * p.H + chunk * p.GH + g;
+  *reinterpret_cast<uint2*>(p.out + row * dv + 4 * c) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
 // A 4-D bf16 tensor of rows of d elements; box = 64 x b1 x b2 x 1, 128-byte swizzle.
@@ -777,7 +813,7 @@ bool make_map(CUtensorMap* m, const void* base, int d, uint64_t d1, uint64_t d2,
 
 template <int DK, int DV, bool ARMS>
 cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtensorMap& tk, const CUtensorMap& tv,
-                     const DenseParams& p, cudaStream_t st) {
+                     const CUtensorMap& to, const DenseParams& p, cudaStream_t st) {
   using C = DenseCfg<DK, DV>;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -803,7 +839,7 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtens
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dense_tc_kernel<DK, DV, ARMS>, tq, tq1, tk, tv, p);
+  return cudaLaunchKernelEx(&cfg, dense_tc_kernel<DK, DV, ARMS>, tq, tq1, tk, tv, to, p);
 }
 
 }  // namespace
@@ -827,7 +863,7 @@ void dense_rows(int G, int* GH, int* RPT) {
 cudaError_t launch_dense_tc(const void* q, const void* k, const void* v, const DenseParams& p, int n_b, int dk, int dv,
                             bool arms, cudaStream_t st) {
   if (!dense_tc_supported(1, dk, dv, p.tables ? p.bs : 0) || !(p.qscale > 0.f)) return cudaErrorNotSupported;
-  CUtensorMap tq, tq1, tk, tv;
+  CUtensorMap tq, tq1, tk, tv, to;
   if (!make_map(&tq, q, dk, p.H, p.n_i, n_b, p.GH, p.RPT)) return cudaErrorInvalidValue;
   if (!make_map(&tq1, q, dk, p.H, p.n_i, n_b, p.GH, 1)) return cudaErrorInvalidValue;
   if (p.tables) {
@@ -837,19 +873,30 @@ cudaError_t launch_dense_tc(const void* q, const void* k, const void* v, const D
     if (!make_map(&tk, k, dk, p.S_kv, p.Hkv, n_b, kBN, 1)) return cudaErrorInvalidValue;
     if (!make_map(&tv, v, dv, p.S_kv, p.Hkv, n_b, kBN, 1)) return cudaErrorInvalidValue;
   }
+  if (!make_map(&to, p.out, dv, p.H, p.n_i, n_b, p.GH, p.RPT)) return cudaErrorInvalidValue;
   if (arms) {
-    if (dk == 64) return launch_d<64, 64, true>(tq, tq1, tk, tv, p, st);
-    if (dk == 128) return launch_d<128, 128, true>(tq, tq1, tk, tv, p, st);
-    return launch_d<192, 128, true>(tq, tq1, tk, tv, p, st);
+    if (dk == 64) return launch_d<64, 64, true>(tq, tq1, tk, tv, to, p, st);
+    if (dk == 128) return launch_d<128, 128, true>(tq, tq1, tk, tv, to, p, st);
+    return launch_d<192, 128, true>(tq, tq1, tk, tv, to, p, st);
   }
-  if (dk == 64) return launch_d<64, 64, false>(tq, tq1, tk, tv, p, st);
-  if (dk == 128) return launch_d<128, 128, false>(tq, tq1, tk, tv, p, st);
-  return launch_d<192, 128, false>(tq, tq1, tk, tv, p, st);
+  if (dk == 64) return launch_d<64, 64, false>(tq, tq1, tk, tv, to, p, st);
+  if (dk == 128) return launch_d<128, 128, false>(tq, tq1, tk, tv, to, p, st);
+  return launch_d<192, 128, false>(tq, tq1, tk, tv, to, p, st);
 }
 
 cudaError_t launch_dense_combine(const DenseCombine& p, cudaStream_t st) {
-  if (p.n_rows <= 0) return cudaSuccess;
-  const long long blocks = (p.n_rows + 7) / 8;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static std::atomic<unsigned long long> attr_done{0};  // per device
+  if (dev >= 64 || !(attr_done.load(std::memory_order_acquire) >> dev & 1ull)) {
+    const cudaError_t e = cudaFuncSetAttribute(dense_combine_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                               cudaSharedmemCarveoutMaxL1);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  const int rows_here = 1024 / p.dv;
+  const long long blocks = (long long)p.n_b * (p.H / p.GH) * (((long long)p.n_i * p.GH + rows_here - 1) / rows_here);
+  if (blocks <= 0) return cudaSuccess;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);

@@ -225,8 +225,8 @@ struct alignas(16) SeqPlan {
 };
 
 struct DenseCombine {
-  long long n_rows;        // B * n_i * H output rows
-  int H, Hkv, G, GH, RPT, n_hchunks, n_i, dv;
+  int n_b, n_i, H;         // output rows [n_b, n_i, H] of dv (64 or 128) columns
+  int GH, RPT, dv;
   int n_tiles, n_splits;   // attn_cross
   const float* partial;
   const SeqPlan* seq;      // shared prefix

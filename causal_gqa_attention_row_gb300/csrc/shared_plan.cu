@@ -11,8 +11,10 @@
 // something for the longest unit, which the rest may have to wait for.
 // Every candidate c is tried, a thread each. Own units are listed longest first.
 //
-// The other kernels wait for this one, so its round trips to memory count: groups, their
-// bounds and the lengths are read at once, and up to kPlanGroups groups stay in shared memory.
+// The other kernels wait for this one. It runs on an SM that has run other code since the
+// last step, so most of its time is the fetch of its own: it is kept short (one copy of
+// each step, no unrolled loops, no 64-bit divisions), and up to kPlanGroups groups stay in
+// shared memory.
 #include "common.cuh"
 #include "internal.h"
 
@@ -25,10 +27,10 @@ constexpr int kBuckets = 64;
 constexpr int kMostTiles = 1 << 20;  // candidates for c
 
 // Exclusive prefix sum over the CTA; `total` receives the sum. Ends with a barrier.
-__device__ __forceinline__ int exclusive_scan(int v, int* warp_sums, int& total) {
+__device__ __noinline__ int exclusive_scan(int v, int* warp_sums, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
-#pragma unroll
+#pragma unroll 1
   for (int off = 1; off < 32; off <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, x, off);
     if (lane >= off) x += y;
@@ -36,7 +38,7 @@ __device__ __forceinline__ int exclusive_scan(int v, int* warp_sums, int& total)
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
   int w = warp_sums[lane];
-#pragma unroll
+#pragma unroll 1
   for (int off = 1; off < 32; off <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, w, off);
     if (lane >= off) w += y;
@@ -47,42 +49,57 @@ __device__ __forceinline__ int exclusive_scan(int v, int* warp_sums, int& total)
   return before + x - v;
 }
 
-// CTA-wide minimum and sum of 64-bit values (shuffles, then one value a warp: 64-bit
-// atomics on one shared word by every thread took the kernel 10 us). Ends with a barrier.
-__device__ __forceinline__ unsigned long long block_min(unsigned long long v, unsigned long long* warps) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) {
-    const unsigned long long o = __shfl_xor_sync(0xffffffffu, v, off);
-    v = o < v ? o : v;
-  }
+// CTA-wide sum of 32-bit values and minimum of 64-bit ones (shuffles, then one value a
+// warp: 64-bit atomics on one shared word by every thread took the kernel 10 us). End with a
+// barrier.
+__device__ __noinline__ int block_sum(int v, int* warps) {
+  v = __reduce_add_sync(0xffffffffu, v);
   if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = warps[threadIdx.x & 31];
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) {
-    const unsigned long long o = __shfl_xor_sync(0xffffffffu, v, off);
-    v = o < v ? o : v;
-  }
+  v = __reduce_add_sync(0xffffffffu, warps[threadIdx.x & 31]);
   __syncthreads();
   return v;
 }
-__device__ __forceinline__ unsigned long long block_sum(unsigned long long v, unsigned long long* warps) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = warps[threadIdx.x & 31];
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();
+__device__ __forceinline__ unsigned long long warp_min(unsigned long long v) {
+#pragma unroll 1
+  for (int off = 16; off >= 1; off >>= 1) {
+    const unsigned long long o = __shfl_xor_sync(0xffffffffu, v, off);
+    v = o < v ? o : v;
+  }
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlan s) {
+// What sequence b brings to the plan.
+struct Seq {
+  int g;          // its group, -1 without a prefix to share
+  int len;        // 0: out of range
+  int key0, nt;   // own keys [key0, len) in nt tiles, key0 on a block's boundary
+};
+// (not inlined: the kernel's time is mostly that of fetching its code)
+__device__ __noinline__ Seq sequence(const SharedPlan& s, const DenseGroup* groups, int n_groups, int b) {
+  Seq q = {-1, 0, 0, 0};
+  const int n = __ldg(s.seq_lens + b);
+  if (n < 1 || n > s.capacity) return q;
+  q.len = n;
+  if (n_groups > 0 && b >= groups[0].first) {
+    int lo = 0, hi = n_groups;  // first[lo] <= b < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (groups[mid].first <= b) lo = mid;
+      else hi = mid;
+    }
+    if (b < groups[lo].first + groups[lo].members) q.g = lo;
+  }
+  q.key0 = max(q.g < 0 ? 0 : groups[q.g].prefix, first_visible_key(n - 1, s.window) / s.bs * s.bs);
+  q.nt = max(n - q.key0 + 127, 0) / 128;
+  return q;
+}
+
+__global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_constant__ SharedPlan s) {
   __shared__ int warp_sums[32];
   __shared__ int bucket_at[kBuckets];
   __shared__ int bad, bad_len, max_tiles;
-  __shared__ unsigned long long warp_values[32];
+  __shared__ unsigned long long warp_best[32];
   __shared__ DenseGroup group_s[kPlanGroups];
   grid_dep_wait();
   grid_dep_launch();
@@ -103,50 +120,35 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlan 
     DenseGroup d = {};
     d.first = a;
     d.members = z - a;
-    d.prefix = nb;
+    d.prefix = z - a >= 2 ? nb * s.bs : 0;
     d.kv_hi = 0;            // largest length of a member ...
     d.key_lo = s.capacity;  // ... and the smallest
     groups[g] = d;
   }
-  const int len0 = tid < s.B ? s.seq_lens[tid] : 0;
-  // the length of sequence b, 0 if it is out of range
-  const auto length = [&](int b) {
-    const int n = b == tid ? len0 : s.seq_lens[b];
-    return n >= 1 && n <= s.capacity ? n : 0;
-  };
-  for (int b = tid; b < s.B; b += kThreads)
-    if (length(b) == 0) bad_len = 1;
   __syncthreads();
-  const bool ok = !bad;
-  if ((bad || bad_len) && tid == 0) raise_error(s.err, kErrBounds);
-  const auto find = [&](int b) {  // the group of sequence b, -1 without one
-    if (!ok || s.n_groups == 0 || b < groups[0].first) return -1;
-    int lo = 0, hi = s.n_groups;  // first[lo] <= b < first[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (groups[mid].first <= b) lo = mid;
-      else hi = mid;
-    }
-    return b < groups[lo].first + groups[lo].members ? lo : -1;
-  };
+  const int n_groups = bad ? 0 : s.n_groups;
+#pragma unroll 1
   for (int b0 = 0; b0 < s.B; b0 += kThreads) {
-    const int b = b0 + tid, len = b < s.B ? length(b) : 0, g = len ? find(b) : -1;
+    const int b = b0 + tid;
+    Seq q = {-1, 0, 0, 0};
+    if (b < s.B) {
+      q = sequence(s, groups, n_groups, b);
+      if (q.len == 0) bad_len = 1;
+    }
     // (most warps hold members of one group: one atomic a warp then)
-    if (__all_sync(0xffffffffu, g == __shfl_sync(0xffffffffu, g, 0))) {
-      const int most = __reduce_max_sync(0xffffffffu, len), least = __reduce_min_sync(0xffffffffu, len);
-      if (g >= 0 && (tid & 31) == 0) {
-        atomicMax(&groups[g].kv_hi, most);
-        atomicMin(&groups[g].key_lo, least);
-      }
-    } else if (g >= 0) {
-      atomicMax(&groups[g].kv_hi, len);
-      atomicMin(&groups[g].key_lo, len);
+    const int g0 = __shfl_sync(0xffffffffu, q.g, 0);
+    const bool one = __all_sync(0xffffffffu, q.g == g0);
+    const int most = __reduce_max_sync(0xffffffffu, one ? q.len : 0);
+    const int least = __reduce_min_sync(0xffffffffu, one ? q.len : 0);
+    if (q.g >= 0 && (!one || (tid & 31) == 0)) {
+      atomicMax(&groups[q.g].kv_hi, one ? most : q.len);
+      atomicMin(&groups[q.g].key_lo, one ? least : q.len);
     }
   }
   __syncthreads();
-  for (int g = tid; g < s.n_groups; g += kThreads) {
+  if ((bad || bad_len) && tid == 0) raise_error(s.err, kErrBounds);
+  for (int g = tid; g < n_groups; g += kThreads) {
     DenseGroup d = groups[g];
-    d.prefix = ok && d.members >= 2 ? d.prefix * s.bs : 0;
     d.kv_hi = min(d.prefix, d.kv_hi);
     // tiles that every member's window hides are left out
     d.key_lo = first_visible_key(d.key_lo - 1, s.window) / 128 * 128;
@@ -158,53 +160,52 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlan 
     if (nt > 0) atomicMax(&max_tiles, nt);
   }
   __syncthreads();
-  // ---- own keys [key0, key0 + n) of sequence b, key0 on a block's boundary
-  const auto own_keys = [&](int b, int& key0) {
-    const int g = find(b), len = length(b);
-    key0 = max(g < 0 ? 0 : groups[g].prefix, first_visible_key(len - 1, s.window) / s.bs * s.bs);
-    return max(len - key0, 0);
-  };
+  // ---- c (costs in floats: any c is right, the same one for the same batch)
   const int heads = s.Hkv * s.n_hchunks;
-  unsigned long long mine_own = 0;
-  int longest = 0;
+  int mine = 0, longest = 0;
+#pragma unroll 1
   for (int b = tid; b < s.B; b += kThreads) {
-    int key0;
-    const int nt = (own_keys(b, key0) + 127) / 128;
-    mine_own += (unsigned long long)nt * heads;
+    const int nt = sequence(s, groups, n_groups, b).nt;
+    mine += nt;
     longest = max(longest, nt);
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
-  if (longest > 1 && (tid & 31) == 0) atomicMax(&max_tiles, longest);
-  // ---- c
-  const long long own_tiles = (long long)block_sum(mine_own, warp_values), own_items = (long long)s.B * heads;
-  const long long c_own_least = (own_tiles + kOwnExtra - 1) / kOwnExtra;  // own parts <= items + kOwnExtra
+  if ((tid & 31) == 0) atomicMax(&max_tiles, longest);
+  const int own_tiles = block_sum(mine, warp_sums);  // of each head chunk
+  const float own_all = (float)own_tiles * (float)heads, own_items = (float)s.B * (float)heads;
+  const int c_own_least = (int)ceilf(own_all / (float)kOwnExtra);  // own parts <= items + kOwnExtra
   const int c_most = min(max_tiles, kMostTiles);
-  unsigned long long mine_best = ~0ull;
+  unsigned long long best = ~0ull;
+#pragma unroll 1
   for (int c = 1 + tid; c <= c_most; c += kThreads) {
-    long long units = 0, tiles = 0;
-    for (int g = 0; g < s.n_groups; ++g) {
-      const long long t = (long long)heads * groups[g].tiles;
-      units += t * ((groups[g].n_splits + c - 1) / c);
-      tiles += t * groups[g].n_splits;
+    float units = 0.f, tiles = 0.f;
+#pragma unroll 1
+    for (int g = 0; g < n_groups; ++g) {
+      const float t = (float)(heads * groups[g].tiles);
+      units += t * (float)((groups[g].n_splits + c - 1) / c);
+      tiles += t * (float)groups[g].n_splits;
     }
-    if (units > s.max_prefix_units) continue;
-    const long long rounds = (units + s.slots - 1) / s.slots * (c + kDenseUnitTiles);
-    const long long even =
-        (tiles + own_tiles + (units + own_tiles / max((long long)c, c_own_least) + own_items / 2) * kDenseUnitTiles) /
-        s.slots;
+    if (units > (float)s.max_prefix_units) continue;
+    const float rounds = ceilf(units / (float)s.slots) * (float)(c + kDenseUnitTiles);
+    const float even =
+        (tiles + own_all + (units + own_all / (float)max(c, c_own_least) + own_items * 0.5f) * (float)kDenseUnitTiles) /
+        (float)s.slots;
     // a quarter of a unit for the tail that one leaves behind; ties go to the longer units
-    const long long cost = 4 * max(rounds, even) + c;
-    const unsigned long long key = (unsigned long long)cost << 24 | (unsigned)(kMostTiles - c);
-    mine_best = key < mine_best ? key : mine_best;
+    const float cost = fmaxf(rounds, even) + 0.25f * (float)c;
+    const unsigned long long key = (unsigned long long)__float_as_uint(cost) << 32 | (unsigned)(kMostTiles - c);
+    best = key < best ? key : best;
   }
-  const unsigned long long best = block_min(mine_best, warp_values);
+  best = warp_min(best);
+  if ((tid & 31) == 0) warp_best[tid >> 5] = best;
+  __syncthreads();
+  best = warp_min(warp_best[tid & 31]);
   // (the largest c always fits: the caller sized max_prefix_units for it)
-  const int c = best == ~0ull ? c_most : kMostTiles - (int)(best & 0xffffff);
-  const int c_own = (int)max((long long)c, max(c_own_least, 1ll));
+  const int c = best == ~0ull ? c_most : kMostTiles - (int)(best & 0xffffffffu);
+  const int c_own = max(max(c, c_own_least), 1);
   // ---- key ranges per group and where its units start
   const int per = (s.n_groups + kThreads - 1) / kThreads;
-  const int lo = min(s.n_groups, tid * per), hi = min(s.n_groups, lo + per);
-  int mine = 0;
+  const int lo = min(n_groups, tid * per), hi = min(n_groups, lo + per);
+  mine = 0;
   for (int g = lo; g < hi; ++g) {
     DenseGroup& d = groups[g];
     d.n_splits = (d.n_splits + c - 1) / c;
@@ -217,32 +218,26 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlan 
     d.unit0 = at;
     at += heads * d.tiles * d.n_splits;
   }
-  // ---- own parts: of c_own tiles, the last of a sequence shorter
-  const auto own_parts = [&](int b, int& key0, int& rest) {  // rest: tiles of the last one if not c_own
-    const int nt = (own_keys(b, key0) + 127) / 128;
-    rest = nt % c_own;
-    return (nt + c_own - 1) / c_own;
-  };
-  const auto bucket = [&](int rest) {
-    return min((int)((long long)(c_own - rest) * kBuckets / c_own), kBuckets - 1);
-  };
+  // ---- own parts: of c_own tiles, the last of a sequence shorter (rest tiles)
+  const auto bucket = [&](int rest) { return (c_own - rest) * (kBuckets - 1) / c_own; };
   const int per_b = (s.B + kThreads - 1) / kThreads;
   const int b_lo = min(s.B, tid * per_b), b_hi = min(s.B, b_lo + per_b);
-  int mine_parts = 0, mine_full = 0;
+  int mine_full = 0;
+  mine = 0;
+#pragma unroll 1
   for (int b = b_lo; b < b_hi; ++b) {
-    int key0, rest;
-    const int n = own_parts(b, key0, rest);
-    mine_parts += n * heads;
-    mine_full += (n - (rest != 0)) * heads;
+    const int nt = sequence(s, groups, n_groups, b).nt, full = nt / c_own, rest = nt - full * c_own;
+    mine += (full + (rest != 0)) * heads;
+    mine_full += full * heads;
     if (rest) atomicAdd(&bucket_at[bucket(rest)], heads);
   }
   int n_parts, n_full;
-  int part_at = exclusive_scan(mine_parts, warp_sums, n_parts);  // (its barriers: unit0 and the buckets are in place)
+  int part_at = exclusive_scan(mine, warp_sums, n_parts);  // (its barriers: unit0 and the buckets are in place)
   int full_at = n_prefix + exclusive_scan(mine_full, warp_sums, n_full);
   if (tid < 32) {  // where the buckets start, two a lane
     const int x = bucket_at[2 * tid], y = bucket_at[2 * tid + 1];
     int sum = x + y;
-#pragma unroll
+#pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, sum, off);
       if (tid >= off) sum += up;
@@ -256,54 +251,55 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const SharedPlan 
   }
   __syncthreads();
   const int part_step = (int)(dense_part_floats(s.own_rows, s.dv) / 4);
+#pragma unroll 1
   for (int b = b_lo; b < b_hi; ++b) {
-    int key0, rest;
-    const int n = own_parts(b, key0, rest), len = length(b);
-    SeqPlan q = {};
-    q.n_own = n;
-    q.own_part0 = part_at;
-    const int g = len ? find(b) : -1;
-    if (g >= 0 && groups[g].prefix > 0) {
-      const DenseGroup d = groups[g];
-      const int i = b - d.first;
-      q.n_pre = d.n_splits;
-      q.pre_unit0 = d.unit0 + i / s.RPT * d.n_splits;
-      q.pre_stride = d.tiles * d.n_splits;
-      q.row0 = i % s.RPT * s.GH;
+    const Seq q = sequence(s, groups, n_groups, b);
+    const int full = q.nt / c_own, rest = q.nt - full * c_own;
+    SeqPlan r = {};
+    r.n_own = full + (rest != 0);
+    r.own_part0 = part_at;
+    if (q.g >= 0 && groups[q.g].prefix > 0) {
+      const DenseGroup& d = groups[q.g];
+      const int i = b - d.first, tile = i / s.RPT;
+      r.n_pre = d.n_splits;
+      r.pre_unit0 = d.unit0 + tile * d.n_splits;
+      r.pre_stride = d.tiles * d.n_splits;
+      r.row0 = (i - tile * s.RPT) * s.GH;
     }
-    s.seq[b] = q;
+    s.seq[b] = r;
     int rest_at = rest ? atomicAdd(&bucket_at[bucket(rest)], heads) : 0;
+#pragma unroll 1
     for (int x = 0; x < heads; ++x)
-      for (int y = 0; y < n; ++y) {
+#pragma unroll 1
+      for (int y = 0; y < r.n_own; ++y) {
         DenseUnit u;
         u.i0 = u.seq = b;
         u.n_i = 1;
         u.head0 = x * s.GH;  // (KV head x / n_hchunks, head chunk x % n_hchunks)
-        u.key0 = key0 + y * c_own * 128;
-        u.key1 = min(u.key0 + c_own * 128, len);
+        u.key0 = q.key0 + y * c_own * 128;
+        u.key1 = min(u.key0 + c_own * 128, q.len);
         u.part = s.own_part_at + part_at * part_step;
         u.batch_or_own = 1;
         ++part_at;
-        s.units[y == n - 1 && rest ? rest_at++ : full_at++] = u;
+        s.units[y == full ? rest_at++ : full_at++] = u;
       }
   }
   const int unit_step = (int)(dense_part_floats(128, s.dv) / 4);
+#pragma unroll 1
   for (int x = tid; x < n_prefix; x += kThreads) {
-    int a = 0, z = s.n_groups;  // the last group that starts at or below x
+    int a = 0, z = n_groups;  // the last group that starts at or below x
     while (z - a > 1) {
       const int mid = (a + z) / 2;
       if (groups[mid].unit0 <= x) a = mid;
       else z = mid;
     }
-    const DenseGroup d = groups[a];
-    int y = x - d.unit0;
-    const int split = y % d.n_splits;
-    y /= d.n_splits;
-    const int tile = y % d.tiles;
+    const DenseGroup& d = groups[a];
+    const int y = (x - d.unit0) / d.n_splits, split = x - d.unit0 - y * d.n_splits;
+    const int hc = y / d.tiles, tile = y - hc * d.tiles;
     DenseUnit u;
     u.i0 = d.first + tile * s.RPT;
     u.n_i = min(s.RPT, d.members - tile * s.RPT);
-    u.head0 = y / d.tiles * s.GH;
+    u.head0 = hc * s.GH;
     u.seq = d.first;
     u.key0 = d.key_lo + split * c * 128;
     u.key1 = min(u.key0 + c * 128, d.kv_hi);
