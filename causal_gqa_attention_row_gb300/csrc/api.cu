@@ -344,7 +344,7 @@ SharedLayout shared_layout(int B, int H, int Hkv, int d_v, int capacity, int n_g
   const long long each = tiles * ((capacity + 127) / 128), some = tiles ? tiles + 4 * gqa::kDenseSms : 0;
   const long long units = each < some ? each : some;
   s.max_prefix_units = units > INT_MAX ? INT_MAX : (int)units;
-  const size_t parts = (size_t)B * (size_t)heads + gqa::kOwnExtra;
+  const size_t parts = 2 * (size_t)B * (size_t)heads + gqa::kOwnExtra;
   size_t at = 256;  // [0]: units listed, [1]: ticket counter
   const auto take = [&](size_t n) {
     const size_t a = at;

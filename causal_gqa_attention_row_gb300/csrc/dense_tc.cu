@@ -48,10 +48,11 @@
 // max, lazily moved reference max, fp32 exponentials, P in bf16 for the second product
 // (rounded once, a relative 2^-8 at most that averages over the keys; the row sum keeps the fp32
 // p). At d_v = 64 S_{j+1} is issued as soon as S_j is in registers; at d_v = 128 P lies over
-// S, so S_{j+1} waits for PV_j, of which half is issued at half of P. A row's keys end at its
-// own limit, and in the tile that holds the last key the V rows behind it are zeroed in
-// shared memory before the product reads them, since 0 * NaN of an unwritten row would not
-// be 0. Warps whose rows are all padding only keep the barriers going.
+// S, so S_{j+1} waits for PV_j, of which half is issued at half of P. All rows of a unit see
+// the same keys: those behind the last one, and those in a sequence's own first tile that its
+// window hides, weigh zero, and their V rows are zeroed in shared memory before the product
+// reads them, since 0 * NaN of an unwritten row would not be 0. Warps whose rows are all
+// padding only keep the barriers going.
 
 #include <atomic>
 #include <climits>
@@ -90,6 +91,7 @@ struct HalfBars {
   uint64_t k_full[kDenseStagesMax], k_empty[kDenseStagesMax], v_full[kDenseStagesMax], v_empty[kDenseStagesMax];
   uint64_t s_full, s_free, p_half, p_full, o_done;  // a phase per tile
   uint64_t mma_final;
+  uint64_t out_turn;  // the four softmax warps have come to an output tile
   DenseUnit unit[2];  // n_i = 0: no more units
 };
 struct DenseBars {
@@ -161,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&h.p_full, 4);
       mbar_init(&h.o_done, 1);
       mbar_init(&h.mma_final, 1);
+      mbar_init(&h.out_turn, 4);
     }
     bars->abort_flag = 0;
     fence_barrier_init();
@@ -356,6 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait_tc(&hb.q_full[us], (n >> 1) & 1, bars, p.err);
         if (!ok) break;
         const int n_i = hb.unit[us].n_i, keys = hb.unit[us].key1 - hb.unit[us].key0;
+        // keys at the start of a sequence's own, on the first one's block, that its window hides
+        int hidden = 0;
+        if (ARMS && p.window > 0 && p.units && hb.unit[us].batch_or_own)
+          hidden = first_visible_key(__ldg(p.seq_lens + hb.unit[us].seq) - 1, p.window) - hb.unit[us].key0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&hb.unit_free[us]);
         if (n_i == 0) break;
@@ -388,7 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int t = t_all + k, st = t % kStages;
             if (lane == 0) ok = ok && wait_or_abort(&hb.v_full[st], (t / kStages) & 1, bars, p.err);
             const int valid = keys - k * kBN;  // keys of the tile
-            if (valid < kBN) {  // (uniform) the rows behind the last key; the swizzle moves chunks within a row only
+            // (uniform) the rows behind the last key; the swizzle moves chunks within a row only
+            if (valid < kBN) {
               ok = __shfl_sync(0xffffffffu, ok, 0);
               if (!ok) break;
               __syncwarp();
@@ -396,6 +404,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               dst += lane / 8 % C::kCBV * kBlk + lane % 8 * 16;
 #pragma unroll 4
               for (int row = valid + lane / (8 * C::kCBV); row < kBN; row += 4 / C::kCBV)
+                *reinterpret_cast<uint4*>(dst + row * 128) = make_uint4(0, 0, 0, 0);
+              tc::fence_async_smem();
+              __syncwarp();
+            }
+            if (ARMS && k == 0 && hidden > 0) {  // (uniform) and those before the first
+              ok = __shfl_sync(0xffffffffu, ok, 0);
+              if (!ok) break;
+              __syncwarp();
+              unsigned char* dst = sm + C::kOffV + st * kTileV + lane / 8 % C::kCBV * kBlk + lane % 8 * 16;
+#pragma unroll 1
+              for (int row = lane / (8 * C::kCBV); row < min(hidden, kBN); row += 4 / C::kCBV)
                 *reinterpret_cast<uint4*>(dst + row * 128) = make_uint4(0, 0, 0, 0);
               tc::fence_async_smem();
               __syncwarp();
@@ -449,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2 qs2 = make_float2(qs, qs);
     bool alive = wg < C::kHalves;
     int t_all = 0;  // tiles so far: the phase of every barrier of the tile loop
+    int turn = 0;   // output tiles so far
     for (int n = 0; alive; ++n) {
       const int us = n & 1;
       if (!warp_wait_tc(&hb.q_full[us], (n >> 1) & 1, bars, p.err)) break;
@@ -466,11 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rows = u.n_i * p.GH;  // rows of the tile in use
         warp_live = quarter * 32 < rows;
         lim = u.key1;
-        if (p.seq_lens) {  // a row is a sequence of its own length; its position is its last key's
-          const int len = __ldg(p.seq_lens + u.i0 + min(r, rows - 1) / p.GH);
-          pos = len - 1;
-          lim = len >= 1 && len <= p.S_kv ? min(lim, len) : 0;
-          if (ARMS) lo_key = first_visible_key(pos, p.window);
+        if (ARMS) {  // a row is a sequence of its own length; its position is its last key's
+          pos = __ldg(p.seq_lens + u.i0 + min(r, rows - 1) / p.GH) - 1;
+          if (p.units && u.batch_or_own) lo_key = first_visible_key(pos, p.window);
         }
         // a padding row beside live ones needs no mask and never moves its reference: whatever
         // it holds stays in its own row
@@ -677,7 +695,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int cb = 0; cb < C::kCBV; ++cb) {
           if ((threadIdx.x & 127) == 0) tc::bulk_wait_group_read0();  // the last store has read the buffer
-          named_bar_sync(1 + wg, 128);
+          if (cb > 0) {
+            named_bar_sync(1 + wg, 128);
+          } else {
+            // The first meeting has a bound: a warp that gave up does not come. From there on
+            // all four go through to the end of the tile, so a hardware barrier will do.
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&hb.out_turn);
+            if (!__all_sync(0xffffffffu, mbar_wait(&hb.out_turn, turn & 1))) {
+              if (lane == 0) {
+                *reinterpret_cast<volatile int*>(&bars->abort_flag) = 1;
+                raise_error(p.err, kErrTimeout);
+              }
+              alive = false;
+              break;
+            }
+            ++turn;
+          }
           if (warp_live) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -706,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (!alive) break;
       tc::fence_before_sync();  // O is read: the next unit's first PV may overwrite it
       __syncwarp();
       if (lane == 0) mbar_arrive(&hb.unit_free[us]);

@@ -213,7 +213,7 @@ cudaError_t launch_dense_tc(const void* q, const void* k, const void* v, const D
 // A group of sequences with a shared prefix (the planner's record).
 struct alignas(16) DenseGroup {
   int first, members, tiles, n_splits;  // row tiles, key ranges (key tiles until they are chosen)
-  int unit0, kv_hi, key_lo, prefix;     // its first unit, the keys [key_lo, kv_hi) that members see, all its rows
+  int unit0, sharers, key_lo, prefix;   // its first unit; the keys [key_lo, prefix) that the members who share all see
 };
 
 // One sequence of a shared-prefix step, for the combine: n_pre key ranges, for head chunk c
@@ -242,7 +242,7 @@ cudaError_t launch_dense_combine(const DenseCombine& p, cudaStream_t st);
 constexpr int kDenseUnitTiles = 1;
 constexpr int kDenseSms = 152;
 
-// Parts of own keys beyond one per item (sequence, KV head, head chunk) that a plan may make.
+// Parts of own keys beyond two per item (sequence, KV head, head chunk) that a plan may make.
 constexpr int kOwnExtra = 4 * kDenseSms;
 
 // The plan of a shared-prefix step: the units of the prefixes and of the own keys, and what

@@ -1,6 +1,12 @@
 // shared_plan.cu -- the plan of a shared-prefix decode step, by one CTA: which sequences
-// have a prefix to share (groups of two members or more), and the list of units that
-// dense_tc_kernel works off, the prefixes' first, then those of the sequences' own keys.
+// have a prefix to share, and the list of units that dense_tc_kernel works off, the
+// prefixes' first, then those of the sequences' own keys.
+//
+// A product with V mixes the keys of a tile before any mask can hold a key back whose V is
+// not finite (0 * NaN). So a group shares just the keys that every one of its sharers sees:
+// [key_lo, prefix), key_lo the highest that a sharer's window leaves. A member that ends
+// in the prefix, or whose window does not reach it, does not share; what a sharer sees
+// below key_lo and behind the prefix are its own keys, two ranges.
 //
 // The prefix of group g is tiles_g row tiles per KV head (and head chunk) times n_g key
 // tiles; the own keys of a sequence are one row tile per KV head (and head chunk). Units
@@ -71,16 +77,19 @@ __device__ __forceinline__ unsigned long long warp_min(unsigned long long v) {
 
 // What sequence b brings to the plan.
 struct Seq {
-  int g;          // its group, -1 without a prefix to share
-  int len;        // 0: out of range
-  int key0, nt;   // own keys [key0, len) in nt tiles, key0 on a block's boundary
+  int g;             // the group that it shares the prefix of, or -1
+  int len;           // 0: out of range
+  int first;         // the first key it sees
+  int key0[2], nt[2];  // own keys, below the shared ones and behind them: tiles from a block's boundary on
+  int end[2];
 };
 // (not inlined: the kernel's time is mostly that of fetching its code)
 __device__ __noinline__ Seq sequence(const SharedPlan& s, const DenseGroup* groups, int n_groups, int b) {
-  Seq q = {-1, 0, 0, 0};
+  Seq q = {-1, 0, 0, {0, 0}, {0, 0}, {0, 0}};
   const int n = __ldg(s.seq_lens + b);
   if (n < 1 || n > s.capacity) return q;
   q.len = n;
+  q.first = first_visible_key(n - 1, s.window);
   if (n_groups > 0 && b >= groups[0].first) {
     int lo = 0, hi = n_groups;  // first[lo] <= b < first[hi]
     while (hi - lo > 1) {
@@ -88,10 +97,17 @@ __device__ __noinline__ Seq sequence(const SharedPlan& s, const DenseGroup* grou
       if (groups[mid].first <= b) lo = mid;
       else hi = mid;
     }
-    if (b < groups[lo].first + groups[lo].members) q.g = lo;
+    const DenseGroup& d = groups[lo];
+    if (b < d.first + d.members && n >= d.prefix && q.first < d.prefix) q.g = lo;
   }
-  q.key0 = max(q.g < 0 ? 0 : groups[q.g].prefix, first_visible_key(n - 1, s.window) / s.bs * s.bs);
-  q.nt = max(n - q.key0 + 127, 0) / 128;
+  q.key0[0] = q.first / s.bs * s.bs;
+  q.end[0] = q.g < 0 ? n : groups[q.g].key_lo;
+  if (q.end[0] > q.first) q.nt[0] = (q.end[0] - q.key0[0] + 127) / 128;
+  if (q.g >= 0) {
+    q.key0[1] = groups[q.g].prefix;
+    q.end[1] = n;
+    q.nt[1] = (n - q.key0[1] + 127) / 128;
+  }
   return q;
 }
 
@@ -121,8 +137,6 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
     d.first = a;
     d.members = z - a;
     d.prefix = z - a >= 2 ? nb * s.bs : 0;
-    d.kv_hi = 0;            // largest length of a member ...
-    d.key_lo = s.capacity;  // ... and the smallest
     groups[g] = d;
   }
   __syncthreads();
@@ -130,31 +144,30 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
 #pragma unroll 1
   for (int b0 = 0; b0 < s.B; b0 += kThreads) {
     const int b = b0 + tid;
-    Seq q = {-1, 0, 0, 0};
+    int g = -1, first = 0;
     if (b < s.B) {
-      q = sequence(s, groups, n_groups, b);
+      const Seq q = sequence(s, groups, n_groups, b);
       if (q.len == 0) bad_len = 1;
+      g = q.g;
+      first = q.first;
     }
     // (most warps hold members of one group: one atomic a warp then)
-    const int g0 = __shfl_sync(0xffffffffu, q.g, 0);
-    const bool one = __all_sync(0xffffffffu, q.g == g0);
-    const int most = __reduce_max_sync(0xffffffffu, one ? q.len : 0);
-    const int least = __reduce_min_sync(0xffffffffu, one ? q.len : 0);
-    if (q.g >= 0 && (!one || (tid & 31) == 0)) {
-      atomicMax(&groups[q.g].kv_hi, one ? most : q.len);
-      atomicMin(&groups[q.g].key_lo, one ? least : q.len);
+    const int g0 = __shfl_sync(0xffffffffu, g, 0);
+    const bool one = __all_sync(0xffffffffu, g == g0);
+    const int most = __reduce_max_sync(0xffffffffu, one ? first : 0);
+    if (g >= 0 && (!one || (tid & 31) == 0)) {
+      atomicMax(&groups[g].key_lo, one ? most : first);
+      atomicAdd(&groups[g].sharers, one ? 32 : 1);
     }
   }
   __syncthreads();
   if ((bad || bad_len) && tid == 0) raise_error(s.err, kErrBounds);
   for (int g = tid; g < n_groups; g += kThreads) {
     DenseGroup d = groups[g];
-    d.kv_hi = min(d.prefix, d.kv_hi);
-    // tiles that every member's window hides are left out
-    d.key_lo = first_visible_key(d.key_lo - 1, s.window) / 128 * 128;
-    const int nt = (d.kv_hi - d.key_lo + 127) / 128;
-    if (nt <= 0) d.kv_hi = d.prefix = 0;
-    d.n_splits = max(nt, 0);
+    d.key_lo = (d.key_lo + s.bs - 1) / s.bs * s.bs;
+    const int nt = d.sharers >= 2 ? max(d.prefix - d.key_lo + 127, 0) / 128 : 0;
+    if (nt == 0) d.prefix = 0;
+    d.n_splits = nt;
     d.tiles = nt > 0 ? (d.members + s.RPT - 1) / s.RPT : 0;
     groups[g] = d;
     if (nt > 0) atomicMax(&max_tiles, nt);
@@ -165,15 +178,15 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
   int mine = 0, longest = 0;
 #pragma unroll 1
   for (int b = tid; b < s.B; b += kThreads) {
-    const int nt = sequence(s, groups, n_groups, b).nt;
-    mine += nt;
-    longest = max(longest, nt);
+    const Seq q = sequence(s, groups, n_groups, b);
+    mine += q.nt[0] + q.nt[1];
+    longest = max(longest, max(q.nt[0], q.nt[1]));
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
   if ((tid & 31) == 0) atomicMax(&max_tiles, longest);
   const int own_tiles = block_sum(mine, warp_sums);  // of each head chunk
   const float own_all = (float)own_tiles * (float)heads, own_items = (float)s.B * (float)heads;
-  const int c_own_least = (int)ceilf(own_all / (float)kOwnExtra);  // own parts <= items + kOwnExtra
+  const int c_own_least = (int)ceilf(own_all / (float)kOwnExtra);  // own parts <= 2 items + kOwnExtra
   const int c_most = min(max_tiles, kMostTiles);
   unsigned long long best = ~0ull;
 #pragma unroll 1
@@ -226,10 +239,14 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
   mine = 0;
 #pragma unroll 1
   for (int b = b_lo; b < b_hi; ++b) {
-    const int nt = sequence(s, groups, n_groups, b).nt, full = nt / c_own, rest = nt - full * c_own;
-    mine += (full + (rest != 0)) * heads;
-    mine_full += full * heads;
-    if (rest) atomicAdd(&bucket_at[bucket(rest)], heads);
+    const Seq q = sequence(s, groups, n_groups, b);
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+      const int nt = e ? q.nt[1] : q.nt[0], full = nt / c_own, rest = nt - full * c_own;
+      mine += (full + (rest != 0)) * heads;
+      mine_full += full * heads;
+      if (rest) atomicAdd(&bucket_at[bucket(rest)], heads);
+    }
   }
   int n_parts, n_full;
   int part_at = exclusive_scan(mine, warp_sums, n_parts);  // (its barriers: unit0 and the buckets are in place)
@@ -254,11 +271,11 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
 #pragma unroll 1
   for (int b = b_lo; b < b_hi; ++b) {
     const Seq q = sequence(s, groups, n_groups, b);
-    const int full = q.nt / c_own, rest = q.nt - full * c_own;
     SeqPlan r = {};
-    r.n_own = full + (rest != 0);
+    const int low = (q.nt[0] + c_own - 1) / c_own;
+    r.n_own = low + (q.nt[1] + c_own - 1) / c_own;
     r.own_part0 = part_at;
-    if (q.g >= 0 && groups[q.g].prefix > 0) {
+    if (q.g >= 0) {
       const DenseGroup& d = groups[q.g];
       const int i = b - d.first, tile = i / s.RPT;
       r.n_pre = d.n_splits;
@@ -267,22 +284,27 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
       r.row0 = (i - tile * s.RPT) * s.GH;
     }
     s.seq[b] = r;
-    int rest_at = rest ? atomicAdd(&bucket_at[bucket(rest)], heads) : 0;
 #pragma unroll 1
-    for (int x = 0; x < heads; ++x)
+    for (int e = 0; e < 2; ++e) {
+      const int nt = e ? q.nt[1] : q.nt[0], full = nt / c_own, rest = nt - full * c_own;
+      const int key0 = e ? q.key0[1] : q.key0[0], end = e ? q.end[1] : q.end[0], parts = full + (rest != 0);
+      int rest_at = rest ? atomicAdd(&bucket_at[bucket(rest)], heads) : 0;
 #pragma unroll 1
-      for (int y = 0; y < r.n_own; ++y) {
-        DenseUnit u;
-        u.i0 = u.seq = b;
-        u.n_i = 1;
-        u.head0 = x * s.GH;  // (KV head x / n_hchunks, head chunk x % n_hchunks)
-        u.key0 = q.key0 + y * c_own * 128;
-        u.key1 = min(u.key0 + c_own * 128, q.len);
-        u.part = s.own_part_at + part_at * part_step;
-        u.batch_or_own = 1;
-        ++part_at;
-        s.units[y == full ? rest_at++ : full_at++] = u;
-      }
+      for (int x = 0; x < heads; ++x)
+#pragma unroll 1
+        for (int y = 0; y < parts; ++y) {
+          DenseUnit u;
+          u.i0 = u.seq = b;
+          u.n_i = 1;
+          u.head0 = x * s.GH;  // (KV head x / n_hchunks, head chunk x % n_hchunks)
+          u.key0 = key0 + y * c_own * 128;
+          u.key1 = min(u.key0 + c_own * 128, end);
+          u.part = s.own_part_at + (part_at + x * r.n_own + (e ? low : 0) + y) * part_step;
+          u.batch_or_own = 1;
+          s.units[y == full ? rest_at++ : full_at++] = u;
+        }
+    }
+    part_at += heads * r.n_own;
   }
   const int unit_step = (int)(dense_part_floats(128, s.dv) / 4);
 #pragma unroll 1
@@ -302,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
     u.head0 = hc * s.GH;
     u.seq = d.first;
     u.key0 = d.key_lo + split * c * 128;
-    u.key1 = min(u.key0 + c * 128, d.kv_hi);
+    u.key1 = min(u.key0 + c * 128, d.prefix);
     u.part = x * unit_step;
     u.batch_or_own = 0;
     s.units[x] = u;

@@ -61,12 +61,14 @@ def attend(q, k, v, scale, window=0, softcap=0.0, sinks=None, slopes=None, posit
     the output, and sum_j w_j |v_j| and the largest scale * sum_i |q_i k_ji| of each row:
     the sizes that the arithmetic's errors go by."""
     S, H, _ = q.shape
+    first = max(0, position - window + 1) if window > 0 else 0  # the keys below take no part, whatever they hold
+    k, v = k[:, first:], v[:, first:]
     n, dv = v.shape[1], v.shape[2]
     out, size, reach = np.zeros((S, H, dv)), np.zeros((S, H, dv)), np.zeros((S, H, 1))
     if n == 0:
         return out, size, reach
     G = H // k.shape[0]
-    j = np.arange(n)
+    j = first + np.arange(n)
     for h in range(H):
         kh, vh = k[h // G], v[h // G]
         s = scale * (q[:, h] @ kh.T)
@@ -75,8 +77,6 @@ def attend(q, k, v, scale, window=0, softcap=0.0, sinks=None, slopes=None, posit
             s = softcap * np.tanh(s / softcap)
         if slopes is not None:
             s = s + slopes[h] * (j - position)
-        if window > 0:
-            s = np.where(j > position - window, s, -np.inf)
         m = s.max(-1, keepdims=True)
         if sinks is not None:
             m = np.maximum(m, sinks[h])

@@ -214,6 +214,38 @@ def test_nan_reaches_its_rows(gpu_lib):
     assert bad.nonzero().tolist() == [[1, 2]] and int(torch.isnan(out).sum()) == 64
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_that_hold_no_number(gpu_lib, d):
+    """Keys and values without a number reach the sequences that see them, and no other: a
+    member that ends before them in the prefix, one whose window hides them, rows of the
+    first block below the window."""
+    g = gpu_lib
+    bad = [float("nan"), float("inf"), -float("inf")]
+    # behind the end of members 1 and 3, within the prefix
+    c = case([4], [20], [5, -30, 40, -200], 4, 2, d, d)
+    for i, x in enumerate(bad):
+        c["v"][c["tables"][0, 18].item(), :, 3 + i], c["k"][c["tables"][0, 18].item(), :, 3 + i] = x, bad[0]
+    out = run(g, c, 0.11)
+    assert g.attn_get_device_error() == g.OK
+    assert torch.isnan(out[[0, 2]]).all()
+    verify(c, 0.11, out, skip=(0, 2))
+    # windows: members of unequal lengths see the prefix from rows 20, 131, 133 and 320 (none) on
+    c = case([4], [20], [0, 111, 113, 300], 4, 2, d, d)
+    assert c["lens"].tolist() == [320, 431, 433, 620]
+    for row, x in ((0, bad[0]), (19, bad[1]), (132, bad[0])):
+        e = c["tables"][0, row // 16].item()
+        c["v"][e, :, row % 16], c["k"][e, :, row % 16] = x, bad[0]
+    out = run(g, c, 0.11, window=300)
+    assert g.attn_get_device_error() == g.OK
+    assert torch.isnan(out[[0, 1]]).all()  # row 132 is theirs
+    verify(c, 0.11, out, skip=(0, 1), window=300)
+    # rows 0 and 19 are hidden from all
+    e = c["tables"][0, 132 // 16].item()
+    c["v"][e, :, 132 % 16], c["k"][e, :, 132 % 16] = 0.25, 0.5
+    out = run(g, c, 0.11, window=300)
+    verify(c, 0.11, out, window=300)
+
+
 def test_a_decode_loop_in_a_graph(gpu_lib):
     """Rows appended and attended step by step, as a server does, the step captured once and
     replayed; against the eager paged decode of the same history."""
