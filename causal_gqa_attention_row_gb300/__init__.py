@@ -525,8 +525,8 @@ def attn_qk_norm_rope(q, k, q_out, k_out, positions, rope=None, q_weight=None, k
     if positions is not None and positions.numel() != B * T:
         raise ValueError("positions must be [B, T]")
     _check(load().attn_qk_norm_rope(
-        _view(q, 4), _view(k, 4), _view(q_out, 4), _view(k_out, 4), _weight(q_weight, d),
-        _weight(k_weight, d), float(eps), _i32(positions), B, T, H, Hkv, d, _ref(rope), _dtype(q, k, q_out, k_out, q_weight, k_weight),
+        _view(q, 4), _view(k, 4), _view(q_out, 4), _view(k_out, 4), _weight(q_weight, d), _weight(k_weight, d),
+        float(eps), _i32(positions), B, T, H, Hkv, d, _ref(rope), _dtype(q, k, q_out, k_out, q_weight, k_weight),
         _stream(stream)), "attn_qk_norm_rope")
     return q_out, k_out
 
@@ -556,9 +556,9 @@ def kv_append_paged_rows(q, k_new, v_new, q_out, k_pool, v_pool, block_tables, r
           k_weight, rope.table if rope is not None else None)
     _writes_once(q_out)
     _check(load().kv_append_paged_rows(
-        _view(q, 3), _view(k_new, 3), _view(v_new, 3), _view(q_out, 3), _p(k_pool), _p(v_pool), _i32(block_tables), _i32(row_starts), _i32(seq_lens_in), _i32(seq_lens_out), N, B,
-        mbps, nb, bs, H, Hkv, dk, dv, _weight(q_weight, dk),
-        _weight(k_weight, dk), float(eps), _ref(rope),
+        _view(q, 3), _view(k_new, 3), _view(v_new, 3), _view(q_out, 3), _p(k_pool), _p(v_pool), _i32(block_tables),
+        _i32(row_starts), _i32(seq_lens_in), _i32(seq_lens_out), N, B, mbps, nb, bs, H, Hkv, dk, dv,
+        _weight(q_weight, dk), _weight(k_weight, dk), float(eps), _ref(rope),
         _dtype(q, k_new, v_new, q_out, k_pool, v_pool, q_weight, k_weight), _stream(stream)), "kv_append_paged_rows")
     return q_out
 

@@ -213,7 +213,9 @@ cudaError_t launch_dense_tc(const void* q, const void* k, const void* v, const D
 // A group of sequences with a shared prefix (the planner's record).
 struct alignas(16) DenseGroup {
   int first, members, tiles, n_splits;  // row tiles, key ranges (key tiles until they are chosen)
-  int unit0, sharers, key_lo, prefix;   // its first unit; the keys [key_lo, prefix) that the members who share all see
+  int unit0, key_lo, prefix;            // its first unit; the keys [key_lo, prefix) that the members who share all see
+  int sharers, source;                  // how many do, and the first of them, whose table entries are read
+  int pad[3];
 };
 
 // One sequence of a shared-prefix step, for the combine: n_pre key ranges, for head chunk c

@@ -168,8 +168,9 @@ cudaError_t launch_plan_units(const RowsParams& p, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // Split combine: out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the
 // splits of one (sequence, head), M = max_s m_s, in split order. Empty splits
-// (m = -inf; without a causal rule l = 0, so that NaN goes through) weigh zero. One warp per output row and group of up to 256
-// columns (a 512-wide row takes two warps, which read the same (m, l) pairs).
+// (m = -inf; without a causal rule l = 0, so that NaN goes through) weigh zero. One
+// warp per output row and group of up to 256 columns (a 512-wide row takes two warps,
+// which read the same (m, l) pairs).
 
 constexpr int kCombineCols = 256;  // output columns per warp
 

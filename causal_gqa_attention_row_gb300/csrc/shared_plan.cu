@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
     d.first = a;
     d.members = z - a;
     d.prefix = z - a >= 2 ? nb * s.bs : 0;
+    d.source = s.B;
     groups[g] = d;
   }
   __syncthreads();
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
     if (g >= 0 && (!one || (tid & 31) == 0)) {
       atomicMax(&groups[g].key_lo, one ? most : first);
       atomicAdd(&groups[g].sharers, one ? 32 : 1);
+      atomicMin(&groups[g].source, b);
     }
   }
   __syncthreads();
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
     u.i0 = d.first + tile * s.RPT;
     u.n_i = min(s.RPT, d.members - tile * s.RPT);
     u.head0 = hc * s.GH;
-    u.seq = d.first;
+    u.seq = d.source;
     u.key0 = d.key_lo + split * c * 128;
     u.key1 = min(u.key0 + c * 128, d.prefix);
     u.part = x * unit_step;

@@ -217,16 +217,19 @@ gqa_status attn_prefill_paged_ex(const void* q, const void* k_pool, const void* 
  *                  before the first and behind the last group share nothing
  *   shared_blocks  int32 [n_groups]: the first shared_blocks[g] entries of every member's
  *                  table row name the same blocks (0 .. max_blocks_per_seq). The entries
- *                  are read from the first member's row; the caller answers for the rest.
- * A member may be shorter than the prefix: it sees the rows below its own length. A
- * group of one member reads its rows itself. Groups out of order, or a prefix longer
- * than a table row, share nothing and set the device error word.
+ *                  are read from the row of the first member that shares; the caller
+ *                  answers for the rest.
+ * A member that ends within the prefix, or whose window does not reach into it, reads
+ * its own rows, as does the only one left to share. With a window the rows that all
+ * sharers see are shared. Groups out of order, or a prefix longer than a table row,
+ * share nothing and set the device error word. A length outside 1 .. capacity gives
+ * zeros for its sequence and sets it too.
  * bf16 with (d_k, d_v) = (64, 64), (128, 128) or (192, 128), block_size a multiple of
- * 8 dividing 128 and attention_scale > 0 runs the prefixes on the tcgen05 tensor-core
- * kernel (the probabilities rounded to bf16 for the product with V); every other
- * case reads every history whole, as attn_decode_paged does. How a prefix is split
- * depends on the batch, so the last bits of a sequence's result do too; repeated
- * calls give the same bits.
+ * 8 dividing 128 and attention_scale > 0 runs on the tcgen05 tensor-core kernel, prefixes
+ * and the sequences' own rows (the probabilities rounded to bf16 for the product with V);
+ * every other case reads every history whole, as attn_decode_paged does. How a prefix
+ * is split depends on the batch, so the last bits of a sequence's result do too;
+ * repeated calls give the same bits.
  * workspace: at least attn_decode_shared_prefix_workspace_bytes(B, H, Hkv, d_v,
  * max_blocks_per_seq * block_size, n_groups) bytes, 16-byte aligned, always needed;
  * calls whose kernels may overlap must not share one.
@@ -251,7 +254,7 @@ size_t attn_decode_shared_prefix_workspace_bytes(int B, int H, int Hkv, int d_v,
  *        without keys gets zeros. A length outside that range gives zeros and sets the
  *        device error word.
  * bf16 with (d_k, d_v) = (64, 64), (128, 128) or (192, 128), attention_scale > 0 and
- * seq_q * H / Hkv >= 16 runs on the tcgen05 tensor-core kernel (the probabilities
+ * seq_q * H / Hkv >= 3 runs on the tcgen05 tensor-core kernel (the probabilities
  * rounded to bf16 for the product with V), everything else on the SIMT kernel.
  * workspace: at least attn_cross_workspace_bytes(..) bytes, 16-byte aligned (NULL
  * allowed when that is 0); calls whose kernels may overlap must not share one.
@@ -449,8 +452,8 @@ gqa_status attn_qk_norm_rope(const gqa_heads* q, const gqa_heads* k, const gqa_h
  *   q, q_out    [N, H, d_k]   (gqa_heads, batch_stride unused); NULL with H = 0
  *   k_new       [N, Hkv, d_k], v_new [N, Hkv, d_v]
  *   row_starts  int32 [B + 1], ascending: rows row_starts[b] .. row_starts[b + 1] - 1
- *               belong to sequence b, which may have none; rows outside every
- *               sequence (padding) are neither read nor written
+ *               belong to sequence b, which may have none; for rows outside every
+ *               sequence (padding) nothing is written
  *   seq_lens_in int32 [B]: rows present before the call; row i of sequence b sits at
  *               position p = seq_lens_in[b] + i, in block block_tables[b][p / block_size],
  *               slot p % block_size

@@ -246,6 +246,46 @@ def test_rows_that_hold_no_number(gpu_lib, d):
     verify(c, 0.11, out, window=300)
 
 
+def test_entries_that_a_member_no_longer_has(gpu_lib):
+    """The shared entries come from a member that shares: not from one that ends before them,
+    nor from one whose window has left them behind and whose blocks are gone."""
+    g = gpu_lib
+    c = case([4], [20], [-200, 5, 60, 16], 4, 2, 128, 128)
+    c["tables"][0, -(-int(c["lens"][0]) // 16):] = -1
+    out = run(g, c, 0.11)
+    assert g.attn_get_device_error() == g.OK
+    verify(c, 0.11, out)
+    c = case([4], [20], [500, 5, 60, 16], 4, 2, 128, 128)
+    keep = c["tables"].clone()
+    c["tables"][0, :32] = -1  # rows below 820 - 300 = 520
+    c["tables"][1:, :1] = -1  # rows below 325 - 300 = 25
+    out = run(g, c, 0.11, window=300)
+    assert g.attn_get_device_error() == g.OK
+    c["tables"] = keep
+    verify(c, 0.11, out, window=300)
+
+
+def test_two_streams_at_once(gpu_lib):
+    """Two calls in flight at once, each with a workspace of its own."""
+    g = gpu_lib
+    cs = [case([4, 3], [20, 9], [1, 90, 200, 7, 16, 20, 50], 8, 2, 128, 128, seed=s) for s in (1, 2)]
+    want = [run(g, c, 0.11) for c in cs]
+    torch.cuda.synchronize()
+    outs, spaces, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for c in cs:
+        B, H, _ = c["q"].shape
+        spaces.append(g.shared_prefix_workspace(B, H, 2, 128, c["tables"].shape[1] * c["bs"], 2))
+        outs.append(torch.empty_like(want[0]))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, ws, out, st in zip(cs, spaces, outs, streams):
+            g.attn_decode_shared_prefix(c["q"], c["k"], c["v"], c["tables"], c["lens"], c["starts"], c["shared"], out,
+                                        0.11, ws, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    assert g.attn_get_device_error() == g.OK
+
+
 def test_a_decode_loop_in_a_graph(gpu_lib):
     """Rows appended and attended step by step, as a server does, the step captured once and
     replayed; against the eager paged decode of the same history."""
