@@ -1,10 +1,6 @@
 // attn_tc.cuh -- what the tcgen05 attention kernels (prefill_tc.cu, dense_tc.cu)
-// share: the roles of the warps, the shared-memory and TMEM maps, bounded waits,
-// the exponential and packing steps, register hand-over, and the loads of K and V
-// tiles (contiguous, or gathered from a paged pool).
-//
-// The parameter struct P of the loads has the fields tables (NULL: contiguous),
-// mbps, bs, num_blocks and err.
+// share: the roles of the warps and their registers, bounded waits, and the exponential
+// and packing steps.
 #pragma once
 
 #include "tc_ptx.cuh"
@@ -26,50 +22,6 @@ constexpr int kLaunchRegs = 168, kCtrlRegs = 72, kSoftmaxRegs = 216;
 static_assert(128 * kCtrlRegs + kWG * 128 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split over budget");
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kTabEntries = 4096;  // paged: the CTA's block-table entries
-constexpr int kMaxStages = 4;
-
-// Sizes and maps of the kernel for head widths DK (Q, K) and DV (V, out).
-template <int DK, int DV>
-struct Cfg {
-  static constexpr int kCBK = DK / 64, kCBV = DV / 64;  // 64-column blocks of a Q/K row, of a V/out row
-  static constexpr int kTileK = kCBK * kBlk;            // one Q or K tile (128 rows)
-  static constexpr int kTileV = kCBV * kBlk;            // one V or output tile
-  static constexpr bool kAlias = DV > 64;               // P_w over the first 64 columns of S_w
-  // rings: stage s only ever holds key tiles of warpgroup s % 2
-  static constexpr int kStagesK = DK > 64 ? 2 : 4, kStagesV = DK > 64 ? 2 : 4;
-  static_assert(kStagesK % kWG == 0 && kStagesV % kWG == 0 && kStagesK <= kMaxStages && kStagesV <= kMaxStages,
-                "ring stages shared between warpgroups");
-  static_assert(DV <= DK, "the output tile is staged over Q");
-  // TMEM columns of S_w, O_w and P_w
-  __host__ __device__ static constexpr uint32_t col_s(int w) { return kAlias ? (128 + DV) * w : 128 * w; }
-  __host__ __device__ static constexpr uint32_t col_o(int w) { return kAlias ? (128 + DV) * w + 128 : 256 + 64 * w; }
-  __host__ __device__ static constexpr uint32_t col_p(int w) { return kAlias ? (128 + DV) * w : 384 + 64 * w; }
-  static_assert(col_o(kWG - 1) + DV <= kTmemCols && col_p(kWG - 1) + 64 <= kTmemCols, "TMEM map");
-  // shared-memory map (from a 1024-byte aligned base)
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kTileK;                             // K ring
-  static constexpr int kOffV = kOffK + kStagesK * kTileK;          // V ring
-  static constexpr int kOffTab = kOffV + kStagesV * kTileV;        // paged: block-table entries
-  static constexpr int kOffBar = kOffTab + kTabEntries * 4;
-  static constexpr int kSmemBytes = kOffBar + 256 + 1024;          // + alignment slack
-  // At the end, once every MMA is done: the output tile over Q, and warpgroup
-  // w's row max and sum over K stage w (which only ever held warpgroup w's tiles).
-  static constexpr int kOffOut = kOffQ;
-  static constexpr int kOffML = kOffK;
-  static_assert(kSmemBytes <= 232448, "over the 227 KiB a CTA may use");
-};
-
-struct Bars {
-  uint64_t q_full, k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
-  uint64_t s_full[kWG], s_free[kWG], p_full[kWG], mma_final[kWG];
-  uint64_t p_half[kWG];  // P over S (d_v = 128): keys 0-63 of the warpgroup's P are in place
-  uint64_t o_done[kWG];  // every PV of warpgroup w issued so far is done (a phase per PV)
-  uint32_t tmem_base;
-  int abort_flag;
-};
-static_assert(sizeof(Bars) <= 256, "barrier block");
-
 template <typename BarsT>
 __device__ __forceinline__ bool aborted(BarsT* bars) {
   return *reinterpret_cast<volatile int*>(&bars->abort_flag);
@@ -151,67 +103,6 @@ __device__ __forceinline__ void regs_inc() {
 
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
-// The TMA loads of key tile j (128 rows of D) of KV head kvh, sequence b, into
-// `dst`, completing a tile's bytes on `bar`: one box per 64-column block of the
-// rows, at that block's 16 KiB slot. Contiguous: the tile's 128 rows in one box
-// per block. Paged: one box per pool block and column block, addressed through
-// the block table (the 128-byte swizzle is a function of the shared address, so
-// the pool blocks land exactly where one box would put them). A pool block that
-// holds no key below kv_hi, or whose table entry is out of range (flagged),
-// loads from past the end of the pool: the TMA engine fills it with zeros.
-template <typename P>
-__device__ __forceinline__ int pool_block(const P& p, int t, int kv_hi, int e) {
-  if (t >= p.mbps || t * p.bs >= kv_hi) return p.num_blocks;
-  if (e >= 0 && e < p.num_blocks) return e;
-  raise_error(p.err, kErrBounds);
-  return p.num_blocks;
-}
-
-// One thread, the table read from global memory (the first tile, before the
-// CTA's shared copy of the table exists).
-template <int NCB, typename P>
-__device__ __forceinline__ void load_kv_tile(const CUtensorMap* tm, unsigned char* dst, uint64_t* bar, int j, int kvh,
-                                             int b, const P& p, int kv_hi) {
-  mbar_arrive_expect_tx(bar, NCB * kBlk);
-  if (!p.tables) {
-#pragma unroll
-    for (int cb = 0; cb < NCB; ++cb) tc::tma_load_4d(dst + cb * kBlk, tm, cb * 64, j * kBN, kvh, b, bar);
-    return;
-  }
-  const int per = kBN / p.bs;
-  for (int i = 0; i < per; ++i) {
-    const int t = j * per + i;
-    const int e = (t < p.mbps && t * p.bs < kv_hi) ? __ldg(p.tables + (size_t)b * p.mbps + t) : 0;
-    const int blk = pool_block(p, t, kv_hi, e);
-#pragma unroll
-    for (int cb = 0; cb < NCB; ++cb)
-      tc::tma_load_4d(dst + cb * kBlk + i * p.bs * 128, tm, cb * 64, 0, kvh, blk, bar);
-  }
-}
-
-// The whole producer warp: lane 0 sets the expected bytes, then each lane issues
-// one box (each TMA instruction holds its thread for a few hundred cycles, so
-// the boxes of a tile go out side by side), the entries read from the CTA's
-// shared copy of its table row.
-template <int NCB, typename P>
-__device__ __forceinline__ void load_kv_tile_warp(const CUtensorMap* tm, unsigned char* dst, uint64_t* bar, int j,
-                                                  int kvh, int b, const P& p, int kv_hi, const int* tab, int lane) {
-  if (lane == 0) mbar_arrive_expect_tx(bar, NCB * kBlk);
-  __syncwarp();
-  if (!p.tables) {
-    if (lane < NCB) tc::tma_load_4d(dst + lane * kBlk, tm, lane * 64, j * kBN, kvh, b, bar);
-  } else {
-    const int per = kBN / p.bs;  // per * NCB boxes: one lane each while they fit the warp
-    for (int x = lane; x < per * NCB; x += 32) {
-      const int i = x % per, cb = x / per;
-      const int t = j * per + i;
-      const int e = (t < p.mbps && t * p.bs < kv_hi) ? tab[t] : 0;  // the shared copy covers every such t
-      tc::tma_load_4d(dst + cb * kBlk + i * p.bs * 128, tm, cb * 64, 0, kvh, pool_block(p, t, kv_hi, e), bar);
-    }
-  }
-  __syncwarp();
 }
 
 }  // namespace gqa

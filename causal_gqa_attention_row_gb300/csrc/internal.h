@@ -223,7 +223,7 @@ struct alignas(16) DenseGroup {
 // parts of its own keys, for head chunk c in own parts own_part0 + c * n_own on.
 struct alignas(16) SeqPlan {
   int n_pre, pre_unit0, pre_stride, row0;
-  int n_own, own_part0, pad[2];
+  int n_own, own_part0, full0, pad;  // full0: the first of its full own units (the planner's)
 };
 
 struct DenseCombine {

@@ -32,27 +32,37 @@ constexpr int kPlanGroups = 128;
 constexpr int kBuckets = 64;
 constexpr int kMostTiles = 1 << 20;  // candidates for c
 
-// Exclusive prefix sum over the CTA; `total` receives the sum. Ends with a barrier.
-__device__ __noinline__ int exclusive_scan(int v, int* warp_sums, int& total) {
+// Exclusive prefix sums of three values over the CTA; `total` receives the sums. Ends with
+// a barrier.
+__device__ __forceinline__ void exclusive_scans(int (&v)[3], int (&total)[3], int (*warp_sums)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  int x[3] = {v[0], v[1], v[2]};
 #pragma unroll 1
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += y;
-  }
-  if (lane == 31) warp_sums[warp] = x;
+  for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int y = __shfl_up_sync(0xffffffffu, x[k], off);
+      if (lane >= off) x[k] += y;
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) warp_sums[k][warp] = x[k];
   __syncthreads();
-  int w = warp_sums[lane];
+  int w[3] = {warp_sums[0][lane], warp_sums[1][lane], warp_sums[2][lane]};
 #pragma unroll 1
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, w, off);
-    if (lane >= off) w += y;
+  for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int y = __shfl_up_sync(0xffffffffu, w[k], off);
+      if (lane >= off) w[k] += y;
+    }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    total[k] = __shfl_sync(0xffffffffu, w[k], 31);
+    const int before = __shfl_sync(0xffffffffu, w[k], max(warp - 1, 0));
+    v[k] = (warp == 0 ? 0 : before) + x[k] - v[k];
   }
-  total = __shfl_sync(0xffffffffu, w, 31);
-  const int before = warp == 0 ? 0 : __shfl_sync(0xffffffffu, w, warp - 1);
   __syncthreads();
-  return before + x - v;
 }
 
 // CTA-wide sum of 32-bit values and minimum of 64-bit ones (shuffles, then one value a
@@ -75,7 +85,7 @@ __device__ __forceinline__ unsigned long long warp_min(unsigned long long v) {
   return v;
 }
 
-// What sequence b brings to the plan.
+// What sequence b, of length n, brings to the plan.
 struct Seq {
   int g;             // the group that it shares the prefix of, or -1
   int len;           // 0: out of range
@@ -84,9 +94,8 @@ struct Seq {
   int end[2];
 };
 // (not inlined: the kernel's time is mostly that of fetching its code)
-__device__ __noinline__ Seq sequence(const SharedPlan& s, const DenseGroup* groups, int n_groups, int b) {
+__device__ __noinline__ Seq sequence(const SharedPlan& s, const DenseGroup* groups, int n_groups, int b, int n) {
   Seq q = {-1, 0, 0, {0, 0}, {0, 0}, {0, 0}};
-  const int n = __ldg(s.seq_lens + b);
   if (n < 1 || n > s.capacity) return q;
   q.len = n;
   q.first = first_visible_key(n - 1, s.window);
@@ -112,7 +121,7 @@ __device__ __noinline__ Seq sequence(const SharedPlan& s, const DenseGroup* grou
 }
 
 __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_constant__ SharedPlan s) {
-  __shared__ int warp_sums[32];
+  __shared__ int warp_sums[3][32];
   __shared__ int bucket_at[kBuckets];
   __shared__ int bad, bad_len, max_tiles;
   __shared__ unsigned long long warp_best[32];
@@ -126,6 +135,11 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
     max_tiles = 1;
   }
   if (tid < kBuckets) bucket_at[tid] = 0;
+  // (the thread's own length is on its way while the groups are read)
+  const int len_tid = tid < s.B ? __ldg(s.seq_lens + tid) : 0;
+  const auto seq_of = [&](int b) {
+    return sequence(s, groups, bad ? 0 : s.n_groups, b, b == tid ? len_tid : __ldg(s.seq_lens + b));
+  };
   __syncthreads();
   // ---- groups: ascending starts within the batch, prefixes within the tables; with
   // anything else no prefix is shared (every sequence reads its own rows) and the
@@ -147,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
     const int b = b0 + tid;
     int g = -1, first = 0;
     if (b < s.B) {
-      const Seq q = sequence(s, groups, n_groups, b);
+      const Seq q = seq_of(b);
       if (q.len == 0) bad_len = 1;
       g = q.g;
       first = q.first;
@@ -180,13 +194,13 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
   int mine = 0, longest = 0;
 #pragma unroll 1
   for (int b = tid; b < s.B; b += kThreads) {
-    const Seq q = sequence(s, groups, n_groups, b);
+    const Seq q = seq_of(b);
     mine += q.nt[0] + q.nt[1];
     longest = max(longest, max(q.nt[0], q.nt[1]));
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
   if ((tid & 31) == 0) atomicMax(&max_tiles, longest);
-  const int own_tiles = block_sum(mine, warp_sums);  // of each head chunk
+  const int own_tiles = block_sum(mine, warp_sums[0]);  // of each head chunk
   const float own_all = (float)own_tiles * (float)heads, own_items = (float)s.B * (float)heads;
   const int c_own_least = (int)ceilf(own_all / (float)kOwnExtra);  // own parts <= 2 items + kOwnExtra
   const int c_most = min(max_tiles, kMostTiles);
@@ -217,66 +231,61 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
   // (the largest c always fits: the caller sized max_prefix_units for it)
   const int c = best == ~0ull ? c_most : kMostTiles - (int)(best & 0xffffffffu);
   const int c_own = max(max(c, c_own_least), 1);
-  // ---- key ranges per group and where its units start
+  // ---- key ranges per group; own parts: of c_own tiles, the last of a range shorter (rest tiles)
   const int per = (s.n_groups + kThreads - 1) / kThreads;
   const int lo = min(n_groups, tid * per), hi = min(n_groups, lo + per);
-  mine = 0;
+  int at[3] = {0, 0, 0};  // prefix units, own parts, those of them that are full
   for (int g = lo; g < hi; ++g) {
     DenseGroup& d = groups[g];
     d.n_splits = (d.n_splits + c - 1) / c;
-    mine += heads * d.tiles * d.n_splits;
+    at[0] += heads * d.tiles * d.n_splits;
   }
-  int n_prefix;
-  int at = exclusive_scan(mine, warp_sums, n_prefix);
-  for (int g = lo; g < hi; ++g) {
-    DenseGroup& d = groups[g];
-    d.unit0 = at;
-    at += heads * d.tiles * d.n_splits;
-  }
-  // ---- own parts: of c_own tiles, the last of a sequence shorter (rest tiles)
   const auto bucket = [&](int rest) { return (c_own - rest) * (kBuckets - 1) / c_own; };
   const int per_b = (s.B + kThreads - 1) / kThreads;
   const int b_lo = min(s.B, tid * per_b), b_hi = min(s.B, b_lo + per_b);
-  int mine_full = 0;
-  mine = 0;
 #pragma unroll 1
   for (int b = b_lo; b < b_hi; ++b) {
-    const Seq q = sequence(s, groups, n_groups, b);
+    const Seq q = seq_of(b);
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
       const int nt = e ? q.nt[1] : q.nt[0], full = nt / c_own, rest = nt - full * c_own;
-      mine += (full + (rest != 0)) * heads;
-      mine_full += full * heads;
+      at[1] += (full + (rest != 0)) * heads;
+      at[2] += full * heads;
       if (rest) atomicAdd(&bucket_at[bucket(rest)], heads);
     }
   }
-  int n_parts, n_full;
-  int part_at = exclusive_scan(mine, warp_sums, n_parts);  // (its barriers: unit0 and the buckets are in place)
-  int full_at = n_prefix + exclusive_scan(mine_full, warp_sums, n_full);
+  int sum[3];
+  exclusive_scans(at, sum, warp_sums);  // (its barriers: the buckets are in place)
+  const int n_prefix = sum[0], n_full = sum[2];
+  for (int g = lo; g < hi; ++g) {
+    DenseGroup& d = groups[g];
+    d.unit0 = at[0];
+    at[0] += heads * d.tiles * d.n_splits;
+  }
   if (tid < 32) {  // where the buckets start, two a lane
     const int x = bucket_at[2 * tid], y = bucket_at[2 * tid + 1];
-    int sum = x + y;
+    int before = x + y;
 #pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, sum, off);
-      if (tid >= off) sum += up;
+      const int up = __shfl_up_sync(0xffffffffu, before, off);
+      if (tid >= off) before += up;
     }
-    bucket_at[2 * tid] = n_prefix + n_full + sum - x - y;
-    bucket_at[2 * tid + 1] = n_prefix + n_full + sum - y;
+    bucket_at[2 * tid] = n_prefix + n_full + before - x - y;
+    bucket_at[2 * tid + 1] = n_prefix + n_full + before - y;
     if (tid == 31) {
-      s.units_listed[0] = n_prefix + n_full + sum;
+      s.units_listed[0] = n_prefix + n_full + before;
       s.units_listed[1] = 0;  // the ticket counter
     }
   }
   __syncthreads();
-  const int part_step = (int)(dense_part_floats(s.own_rows, s.dv) / 4);
+  // ---- the sequences' records, the first of their full units left in the last field ...
 #pragma unroll 1
   for (int b = b_lo; b < b_hi; ++b) {
-    const Seq q = sequence(s, groups, n_groups, b);
+    const Seq q = seq_of(b);
     SeqPlan r = {};
-    const int low = (q.nt[0] + c_own - 1) / c_own;
-    r.n_own = low + (q.nt[1] + c_own - 1) / c_own;
-    r.own_part0 = part_at;
+    r.n_own = (q.nt[0] + c_own - 1) / c_own + (q.nt[1] + c_own - 1) / c_own;
+    r.own_part0 = at[1];
+    r.full0 = n_prefix + at[2];
     if (q.g >= 0) {
       const DenseGroup& d = groups[q.g];
       const int i = b - d.first, tile = i / s.RPT;
@@ -286,27 +295,36 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
       r.row0 = (i - tile * s.RPT) * s.GH;
     }
     s.seq[b] = r;
+    at[1] += heads * r.n_own;
+    at[2] += heads * (q.nt[0] / c_own + q.nt[1] / c_own);
+  }
+  __syncthreads();
+  // ---- ... and the units, a thread per sequence and head chunk
+  const int part_step = (int)(dense_part_floats(s.own_rows, s.dv) / 4);
+#pragma unroll 1
+  for (int w = tid; w < s.B * heads; w += kThreads) {
+    const int b = w / heads, x = w - b * heads;
+    const Seq q = seq_of(b);
+    const int full0 = q.nt[0] / c_own, full1 = q.nt[1] / c_own;
+    int part = s.seq[b].own_part0 + x * s.seq[b].n_own;
+    int full_at = s.seq[b].full0 + x * (full0 + full1);
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
-      const int nt = e ? q.nt[1] : q.nt[0], full = nt / c_own, rest = nt - full * c_own;
-      const int key0 = e ? q.key0[1] : q.key0[0], end = e ? q.end[1] : q.end[0], parts = full + (rest != 0);
-      int rest_at = rest ? atomicAdd(&bucket_at[bucket(rest)], heads) : 0;
+      const int full = e ? full1 : full0, rest = (e ? q.nt[1] : q.nt[0]) - full * c_own;
+      const int key0 = e ? q.key0[1] : q.key0[0], end = e ? q.end[1] : q.end[0];
 #pragma unroll 1
-      for (int x = 0; x < heads; ++x)
-#pragma unroll 1
-        for (int y = 0; y < parts; ++y) {
-          DenseUnit u;
-          u.i0 = u.seq = b;
-          u.n_i = 1;
-          u.head0 = x * s.GH;  // (KV head x / n_hchunks, head chunk x % n_hchunks)
-          u.key0 = key0 + y * c_own * 128;
-          u.key1 = min(u.key0 + c_own * 128, end);
-          u.part = s.own_part_at + (part_at + x * r.n_own + (e ? low : 0) + y) * part_step;
-          u.batch_or_own = 1;
-          s.units[y == full ? rest_at++ : full_at++] = u;
-        }
+      for (int y = 0; y < full + (rest != 0); ++y) {
+        DenseUnit u;
+        u.i0 = u.seq = b;
+        u.n_i = 1;
+        u.head0 = x * s.GH;  // (KV head x / n_hchunks, head chunk x % n_hchunks)
+        u.key0 = key0 + y * c_own * 128;
+        u.key1 = min(u.key0 + c_own * 128, end);
+        u.part = s.own_part_at + part++ * part_step;
+        u.batch_or_own = 1;
+        s.units[y == full ? atomicAdd(&bucket_at[bucket(rest)], 1) : full_at++] = u;
+      }
     }
-    part_at += heads * r.n_own;
   }
   const int unit_step = (int)(dense_part_floats(128, s.dv) / 4);
 #pragma unroll 1
