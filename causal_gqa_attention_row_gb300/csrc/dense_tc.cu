@@ -29,15 +29,16 @@
 // and a first load. Units of unequal length (the shared prefixes) are drawn from a ticket
 // counter; those of attn_cross are alike and go round by slot.
 //
-// Measured at 32 heads on 8 KV heads of 128, combine included: 64 sequences behind a prefix
-// of 8,192 keys with up to 512 of their own 48 us with their plan; 256 sequences behind four
-// prefixes of 16,384 keys 202 us (0.59 of the measured bf16 rate); attn_cross of 8 x 1,024 rows
-// on 2,048 to 4,096 keys 385 us, 1.07 PFLOP/s (0.57). What bounds the long cases is the time
-// between a half's tiles, about 2.1 us for 1,024 cycles of products: S, softmax and PV of a
-// half follow one another, and the K and V tiles, which the halves do not share, come from
-// L2 at 8.4 TB/s. (One CTA per unit, with two warpgroups that shared a unit and merged at its
-// end: 357 us for that attn_cross call, but 62 us for the first, whose units are many and
-// short.)
+// Measured at 32 heads on 8 KV heads of 128, plan and combine included: 64 sequences behind
+// a prefix of 8,192 keys with up to 512 of their own 47.8 us; 256 sequences behind four
+// prefixes of 16,384 keys with up to 1,024 of their own 202 us (4.0 TB/s of rows read once,
+// 0.59 of the copy bandwidth); attn_cross of 8 x 1,024 rows on 2,048 to 4,096 keys 390 us (1.06
+// PFLOP/s, 0.55 of the measured bf16 rate). What bounds the long cases is a half's time from
+// tile to tile: about 4,000 cycles for 1,024 of products where K and V come from L2 (S, softmax
+// and PV of a half follow one another; half the bytes loaded gained 1.6%), 5,200 in the second
+// case, of which the MMA warp waits 1,900 for K and V at one stage each. (One CTA per unit,
+// with two warpgroups that shared a unit and merged at its end: 357 us for that attn_cross
+// call, but 62 us for the first, whose units are many and short.)
 //
 //   warps 0-3, 4-7   softmax of half 0, 1: thread t owns row t of the tile (TMEM lane t)
 //   warps 8, 11      TMA producer of half 0, 1 (Q once a unit, then K and V tiles; paged:
