@@ -30,15 +30,12 @@
 // counter; those of attn_cross are alike and go round by slot.
 //
 // Measured at 32 heads on 8 KV heads of 128, plan and combine included: 64 sequences behind
-// a prefix of 8,192 keys with up to 512 of their own 47.8 us; 256 sequences behind four
-// prefixes of 16,384 keys with up to 1,024 of their own 202 us (4.0 TB/s of rows read once,
-// 0.59 of the copy bandwidth); attn_cross of 8 x 1,024 rows on 2,048 to 4,096 keys 390 us (1.06
-// PFLOP/s, 0.55 of the measured bf16 rate). What bounds the long cases is a half's time from
-// tile to tile: about 4,000 cycles for 1,024 of products where K and V come from L2 (S, softmax
-// and PV of a half follow one another; half the bytes loaded gained 1.6%), 5,200 in the second
-// case, of which the MMA warp waits 1,900 for K and V at one stage each. (One CTA per unit,
-// with two warpgroups that shared a unit and merged at its end: 357 us for that attn_cross
-// call, but 62 us for the first, whose units are many and short.)
+// a prefix of 8,192 keys with up to 512 of their own 46 us; 256 sequences behind four prefixes
+// of 16,384 keys with up to 1,024 of their own 193 us (4.2 TB/s of rows read once, 0.62 of the
+// copy bandwidth); attn_cross of 8 x 1,024 rows on 2,048 to 4,096 keys 306 us (1.35 PFLOP/s, 0.71
+// of the measured bf16 rate). What bounds them is a half's time from tile to tile, of 1,024 cycles
+// of products: in the last case about 3,200 cycles, S, softmax and PV of a half one after
+// another; in the second 5,000, of which the MMA warp waits 1,800 for K and V at one stage each.
 //
 //   warps 0-3, 4-7   softmax of half 0, 1: thread t owns row t of the tile (TMEM lane t)
 //   warps 8, 11      TMA producer of half 0, 1 (Q once a unit, then K and V tiles; paged:
@@ -263,12 +260,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the record's slot is free once the unit before last has been taken; Q once the
         // last S of the previous unit is done
         bool ok = true;
-        if (lane == 0) {
-          if (n >= 2) ok = wait_or_abort(&hb.unit_free[us], ((n >> 1) - 1) & 1, bars, p.err);
-          if (ok && t_all > 0)
-            ok = wait_or_abort(&hb.k_empty[(t_all - 1) % kStages], ((t_all - 1) / kStages) & 1, bars, p.err);
-        }
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        if (n >= 2) ok = warp_wait_tc(&hb.unit_free[us], ((n >> 1) - 1) & 1, bars, p.err);
+        if (ok && t_all > 0)
+          ok = warp_wait_tc(&hb.k_empty[(t_all - 1) % kStages], ((t_all - 1) / kStages) & 1, bars, p.err);
+        if (!ok) break;
         const bool small = p.units && u.batch_or_own;
         if (lane == 0) {
           hb.unit[us] = u;
@@ -301,9 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kv = 0; kv < 2; ++kv) {  // the K tile, then the V tile
             uint64_t* full = kv ? &hb.v_full[st] : &hb.k_full[st];
             if (t_all >= kStages) {
-              if (lane == 0)
-                ok = wait_or_abort(kv ? &hb.v_empty[st] : &hb.k_empty[st], (t_all / kStages - 1) & 1, bars, p.err);
-              ok = __shfl_sync(0xffffffffu, ok, 0);
+              ok = warp_wait_tc(kv ? &hb.v_empty[st] : &hb.k_empty[st], (t_all / kStages - 1) & 1, bars, p.err);
               if (!ok) break;
             }
             // test hook: withheld, the first K tile is never requested (nothing is left in
@@ -344,11 +337,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (w < C::kHalves) {
       // ================= MMA warp of half w =================
-      // The whole warp walks the loop (it zeroes V rows together); lane 0 waits and issues.
-      const uint32_t idS = tc::idesc_bf16_f32(kBM, kBN, false);
-      const uint32_t idO = tc::idesc_bf16_f32(kBM, DV, true);
+      // The warp runs the loop converged, waits included, and an elected lane issues a product's
+      // MMAs and its commits in one turn. (Waits and MMAs from lane 0 alone: attn_cross of 8 x 1024
+      // rows 389 us; two MMAs an election 333, a whole product 306.)
+      const uint32_t idS = tc::idesc_bf16_f32(kBM, kBN, false), idO = tc::idesc_bf16_f32(kBM, DV, true);
       constexpr uint64_t kHi = tc::desc_sw128_hi(0, 1024), kHiV = tc::desc_sw128_hi(C::kCBV > 1 ? kBlk : 0, 1024);
-      const uint32_t dS = tmem + C::col_s(w), dO = tmem + C::col_o(w), tP = tmem + C::col_p(w);
+      const uint32_t dS0 = tmem + C::col_s(w), dO = tmem + C::col_o(w), tP0 = tmem + C::col_p(w);
       // One place that issues S and one that issues PV, whatever tile or unit they are for: a
       // second copy of either, run once a unit, was fetched from L2 instruction by instruction
       // (2,000 cycles for eight MMAs). At d_v = 64 PV runs a tile behind S.
@@ -370,83 +364,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tiles = (keys + kBN - 1) / kBN;
 #pragma unroll 1
         for (int i = 0; ok && i < tiles + kLag && tiles > 0; ++i) {
-          if (lane == 0 && i < tiles) {  // S = Q K^T of tile i
+          if (i < tiles) {  // S = Q K^T of tile i
             const int t = t_all + i, st = t % kStages;
             // its columns are free once the previous tile's S is in registers (d_v = 64), or its
             // PV has read the P that lies over them (d_v = 128)
-            if (t > 0) ok = wait_or_abort(C::kAlias ? &hb.o_done : &hb.s_free, (t - 1) & 1, bars, p.err);
-            ok = ok && wait_or_abort(&hb.k_full[st], (t / kStages) & 1, bars, p.err);
-            if (ok) {
-              tc::fence_after_sync();
-              // (the descriptors are built here from the buffers' addresses: as loop invariants
-              // all of them were kept, in more registers than the control warps have)
-              const uint64_t dQ = kHi | fresh(smem_u32(sm) >> 4);
-              const uint64_t dK = kHi | fresh(smem_u32(sm + C::kOffK + st * kTileK) >> 4);
+            if (t > 0) ok = warp_wait_tc(C::kAlias ? &hb.o_done : &hb.s_free, (t - 1) & 1, bars, p.err);
+            ok = ok && warp_wait_tc(&hb.k_full[st], (t / kStages) & 1, bars, p.err);
+            if (!ok) break;
+            tc::fence_after_sync();
+            // (the descriptors are built here from the buffers' addresses: as loop invariants
+            // all of them were kept, in more registers than the control warps have)
+            const uint64_t dQ = kHi | fresh(smem_u32(sm) >> 4);
+            const uint64_t dK = kHi | fresh(smem_u32(sm + C::kOffK + st * kTileK) >> 4);
+            if (tc::elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < DK / 16; ++kk) {
                 const uint32_t at = (kk / 4) * kBlk + (kk % 4) * 32;
-                tc::mma_f16_ss(dS, dQ + (at >> 4), dK + (at >> 4), idS, kk > 0);
+                tc::mma_f16_ss(dS0, dQ + (at >> 4), dK + (at >> 4), idS, kk > 0);
               }
               tc::mma_commit(&hb.s_full);
               tc::mma_commit(&hb.k_empty[st]);  // the K stage is free once S is done
             }
+            __syncwarp();
           }
           const int k = i - kLag;
           if (k >= 0) {  // O += P V of tile k
             const int t = t_all + k, st = t % kStages;
-            if (lane == 0) ok = ok && wait_or_abort(&hb.v_full[st], (t / kStages) & 1, bars, p.err);
-            const int valid = keys - k * kBN;  // keys of the tile
-            // (uniform) the rows behind the last key; the swizzle moves chunks within a row only
-            if (valid < kBN) {
-              ok = __shfl_sync(0xffffffffu, ok, 0);
-              if (!ok) break;
-              __syncwarp();
-              unsigned char* dst = sm + C::kOffV + st * kTileV;
-              dst += lane / 8 % C::kCBV * kBlk + lane % 8 * 16;
-#pragma unroll 4
-              for (int row = valid + lane / (8 * C::kCBV); row < kBN; row += 4 / C::kCBV)
-                *reinterpret_cast<uint4*>(dst + row * 128) = make_uint4(0, 0, 0, 0);
-              tc::fence_async_smem();
-              __syncwarp();
-            }
-            if (ARMS && k == 0 && hidden > 0) {  // (uniform) and those before the first
-              ok = __shfl_sync(0xffffffffu, ok, 0);
-              if (!ok) break;
-              __syncwarp();
+            ok = warp_wait_tc(&hb.v_full[st], (t / kStages) & 1, bars, p.err);
+            if (!ok) break;
+            // zeros for the rows behind the last key and for those before the first one that the row
+            // sees (the swizzle moves chunks within a row only)
+            const int valid = keys - k * kBN, skip = ARMS ? hidden - k * kBN : 0;
+            if (valid < kBN || (ARMS && skip > 0)) {
               unsigned char* dst = sm + C::kOffV + st * kTileV + lane / 8 % C::kCBV * kBlk + lane % 8 * 16;
 #pragma unroll 1
-              for (int row = lane / (8 * C::kCBV); row < min(hidden, kBN); row += 4 / C::kCBV)
-                *reinterpret_cast<uint4*>(dst + row * 128) = make_uint4(0, 0, 0, 0);
+              for (int row = (ARMS && skip > 0 ? 0 : valid) + lane / (8 * C::kCBV); row < kBN; row += 4 / C::kCBV)
+                if (!ARMS || row >= valid || row < skip)
+                  *reinterpret_cast<uint4*>(dst + row * 128) = make_uint4(0, 0, 0, 0);
               tc::fence_async_smem();
               __syncwarp();
             }
-            if (lane == 0) {
-              ok = ok && wait_or_abort(C::kAlias ? &hb.p_half : &hb.p_full, t & 1, bars, p.err);
-              if (ok) {
-                tc::fence_after_sync();
-                const uint64_t dV = kHiV | fresh(smem_u32(sm + C::kOffV + st * kTileV) >> 4);
+            ok = warp_wait_tc(C::kAlias ? &hb.p_half : &hb.p_full, t & 1, bars, p.err);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint64_t dV = kHiV | fresh(smem_u32(sm + C::kOffV + st * kTileV) >> 4);
+            constexpr int kSteps = kBN / 16, kTurn = C::kAlias ? kSteps / 2 : kSteps;
 #pragma unroll
-                for (int kk = 0; kk < kBN / 16; ++kk) {
-                  if (C::kAlias && kk == kBN / 32) {
-                    ok = wait_or_abort(&hb.p_full, t & 1, bars, p.err);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                  }
-                  tc::mma_f16_ts(dO, tP + kk * 8, dV + kk * (2048 >> 4), idO, (k > 0 || kk > 0));
+            for (int k0 = 0; k0 < kSteps; k0 += kTurn) {
+              if (k0 > 0) {
+                ok = warp_wait_tc(&hb.p_full, t & 1, bars, p.err);
+                if (!ok) break;
+                tc::fence_after_sync();
+              }
+              if (tc::elect_one()) {
+#pragma unroll
+                for (int kk = k0; kk < k0 + kTurn; ++kk)
+                  tc::mma_f16_ts(dO, tP0 + kk * 8, dV + kk * (2048 >> 4), idO, (k > 0 || kk > 0));
+                if (k0 + kTurn == kSteps) {
+                  tc::mma_commit(&hb.o_done);
+                  tc::mma_commit(&hb.v_empty[st]);
                 }
               }
-              if (ok) {
-                tc::mma_commit(&hb.o_done);
-                tc::mma_commit(&hb.v_empty[st]);
-              }
+              __syncwarp();
             }
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
         }
         t_all += tiles;
       }
       // every MMA issued above has completed before TMEM is released
-      if (lane == 0) {
+      if (tc::elect_one()) {  // (the lane that issued them)
         tc::mma_commit(&hb.mma_final);
         if (!mbar_wait(&hb.mma_final, 0)) raise_error(p.err, kErrTimeout);
       }
@@ -514,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if (lane == 0) {
-            mbar_arrive(&hb.s_free);
+            if (!C::kAlias) mbar_arrive(&hb.s_free);
             if (C::kAlias) mbar_arrive(&hb.p_half);
             mbar_arrive(&hb.p_full);
           }
@@ -526,9 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::tmem_ld_32x32b_x32(tS + c * 32, sv[c]);
         tc::tmem_ld_wait();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&hb.s_free);
+        if (!C::kAlias) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&hb.s_free);
+        }
         if (ARMS) {  // scale, softcap, ALiBi: log2 units, as in prefill_tc.cu
           const float base = alibi2 * (float)(j0 - pos);
           if (p.cap_out > 0.f) {
