@@ -498,10 +498,12 @@ struct CrossPlan {
 
 // Rows of a KV head (query rows times heads of its group) from which the tensor cores
 // are taken: the SIMT kernel reads the keys once for up to NV rows (a power of two), the
-// tensor-core kernel once for 128. Measured at 64 sequences of up to 1500 keys: one row of 16
-// KV heads of 64 40.9 us on the SIMT kernel and 65 us on the tensor cores, two rows 58 and 66,
-// four 89 and 66, eight 147 and 66; one row of 8 groups of four, d = 128, 56 and 55.
-constexpr int kCrossTcRows = 3;
+// tensor-core kernel once for 128. Measured (SIMT, tensor cores) at 64 sequences of up to 1500
+// keys: one row of 16 KV heads of 64 39.9 and 48.8 us, of 128 64 and 84 us; two rows of 64 58 and
+// 55, of 8 heads of 128 60 and 51; four rows of 64 85 and 53; at 4 sequences of up to 4000 keys,
+// 8 heads of 64, one row 17.0 and 15.4 us, two 70 and 15.4 (the SIMT kernel splits single rows
+// only).
+constexpr int kCrossTcRows = 2;
 
 bool cross_plan(int B, int S, int L, int H, int Hkv, int d_k, int d_v, int bf16, bool scale_ok, CrossPlan* c) {
   *c = CrossPlan{};

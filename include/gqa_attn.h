@@ -254,7 +254,7 @@ size_t attn_decode_shared_prefix_workspace_bytes(int B, int H, int Hkv, int d_v,
  *        without keys gets zeros. A length outside that range gives zeros and sets the
  *        device error word.
  * bf16 with (d_k, d_v) = (64, 64), (128, 128) or (192, 128), attention_scale > 0 and
- * seq_q * H / Hkv >= 3 runs on the tcgen05 tensor-core kernel (the probabilities
+ * seq_q * H / Hkv >= 2 runs on the tcgen05 tensor-core kernel (the probabilities
  * rounded to bf16 for the product with V), everything else on the SIMT kernel.
  * workspace: at least attn_cross_workspace_bytes(..) bytes, 16-byte aligned (NULL
  * allowed when that is 0); calls whose kernels may overlap must not share one.
