@@ -30,7 +30,7 @@
 // counter; those of attn_cross are alike and go round by slot.
 //
 // Measured at 32 heads on 8 KV heads of 128, plan and combine included: 64 sequences behind
-// a prefix of 8,192 keys with up to 512 of their own 46 us; 256 sequences behind four prefixes
+// a prefix of 8,192 keys with up to 512 of their own 45 us; 256 sequences behind four prefixes
 // of 16,384 keys with up to 1,024 of their own 193 us (4.2 TB/s of rows read once, 0.62 of the
 // copy bandwidth); attn_cross of 8 x 1,024 rows on 2,048 to 4,096 keys 306 us (1.35 PFLOP/s, 0.71
 // of the measured bf16 rate). What bounds them is a half's time from tile to tile, of 1,024 cycles

@@ -27,14 +27,14 @@
 namespace gqa {
 namespace {
 
-constexpr int kThreads = 1024;
 constexpr int kPlanGroups = 128;
 constexpr int kBuckets = 64;
 constexpr int kMostTiles = 1 << 20;  // candidates for c
 
 // Exclusive prefix sums of three values over the CTA; `total` receives the sums. Ends with
 // a barrier.
-__device__ __forceinline__ void exclusive_scans(int (&v)[3], int (&total)[3], int (*warp_sums)[32]) {
+template <int kWarps>
+__device__ __forceinline__ void exclusive_scans(int (&v)[3], int (&total)[3], int (*warp_sums)[kWarps]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x[3] = {v[0], v[1], v[2]};
 #pragma unroll 1
@@ -48,7 +48,9 @@ __device__ __forceinline__ void exclusive_scans(int (&v)[3], int (&total)[3], in
 #pragma unroll
     for (int k = 0; k < 3; ++k) warp_sums[k][warp] = x[k];
   __syncthreads();
-  int w[3] = {warp_sums[0][lane], warp_sums[1][lane], warp_sums[2][lane]};
+  int w[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) w[k] = lane < kWarps ? warp_sums[k][lane] : 0;
 #pragma unroll 1
   for (int off = 1; off < 32; off <<= 1)
 #pragma unroll
@@ -68,11 +70,12 @@ __device__ __forceinline__ void exclusive_scans(int (&v)[3], int (&total)[3], in
 // CTA-wide sum of 32-bit values and minimum of 64-bit ones (shuffles, then one value a
 // warp: 64-bit atomics on one shared word by every thread took the kernel 10 us). End with a
 // barrier.
+template <int kWarps>
 __device__ __noinline__ int block_sum(int v, int* warps) {
   v = __reduce_add_sync(0xffffffffu, v);
   if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = __reduce_add_sync(0xffffffffu, warps[threadIdx.x & 31]);
+  v = __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < kWarps ? warps[threadIdx.x & 31] : 0);
   __syncthreads();
   return v;
 }
@@ -120,11 +123,13 @@ __device__ __noinline__ Seq sequence(const SharedPlan& s, const DenseGroup* grou
   return q;
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_constant__ SharedPlan s) {
-  __shared__ int warp_sums[3][32];
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int warp_sums[3][kWarps];
   __shared__ int bucket_at[kBuckets];
   __shared__ int bad, bad_len, max_tiles;
-  __shared__ unsigned long long warp_best[32];
+  __shared__ unsigned long long warp_best[kWarps];
   __shared__ DenseGroup group_s[kPlanGroups];
   grid_dep_wait();
   grid_dep_launch();
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
   if ((tid & 31) == 0) atomicMax(&max_tiles, longest);
-  const int own_tiles = block_sum(mine, warp_sums[0]);  // of each head chunk
+  const int own_tiles = block_sum<kWarps>(mine, warp_sums[0]);  // of each head chunk
   const float own_all = (float)own_tiles * (float)heads, own_items = (float)s.B * (float)heads;
   const int c_own_least = (int)ceilf(own_all / (float)kOwnExtra);  // own parts <= 2 items + kOwnExtra
   const int c_most = min(max_tiles, kMostTiles);
@@ -227,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
   best = warp_min(best);
   if ((tid & 31) == 0) warp_best[tid >> 5] = best;
   __syncthreads();
-  best = warp_min(warp_best[tid & 31]);
+  best = warp_min(warp_best[tid & (kWarps - 1)]);
   // (the largest c always fits: the caller sized max_prefix_units for it)
   const int c = best == ~0ull ? c_most : kMostTiles - (int)(best & 0xffffffffu);
   const int c_own = max(max(c, c_own_least), 1);
@@ -354,14 +359,18 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
 }  // namespace
 
 cudaError_t launch_shared_plan(const SharedPlan& s, cudaStream_t st) {
+  // Barriers cost less with fewer warps, the units' records with more threads: at 8 items
+  // (sequences times head chunks) 17.3 us a call with 256 threads and 18.4 with 1024, at 512
+  // items 45.4 and 45.7, at 2048 items 197.5 and 193.5.
+  const bool few = (long long)s.B * s.Hkv * s.n_hchunks <= 1024;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(few ? 256 : 1024);
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_plan_kernel, s);
+  return few ? cudaLaunchKernelEx(&cfg, shared_plan_kernel<256>, s) : cudaLaunchKernelEx(&cfg, shared_plan_kernel<1024>, s);
 }
 
 }  // namespace gqa

@@ -157,14 +157,16 @@ def test_no_groups_is_the_paged_decode(gpu_lib):
     verify(c, 0.125, want, tc=False)
 
 
-def test_many_groups_and_sequences(gpu_lib):
-    """More groups than the planner keeps in shared memory, more sequences than its threads."""
+@pytest.mark.parametrize("Hkv,alone", [(1, 400), (2, 900)])
+def test_many_groups_and_sequences(gpu_lib, Hkv, alone):
+    """More groups than the planner keeps in shared memory, more sequences than its threads,
+    of which it takes 256 or 1024."""
     g = gpu_lib
     n = 150
     members = [(i % 4) * 3 for i in range(n)]
     B = sum(members)
-    c = case(members, [i % 5 for i in range(n)], [1 + (i * 7) % 40 for i in range(B)] + [3] * 400, 2, 1, 64, 64, bs=8,
-             alone=400, seed=9)
+    c = case(members, [i % 5 for i in range(n)], [1 + (i * 7) % 40 for i in range(B)] + [3] * alone, 2, Hkv, 64, 64, bs=8,
+             alone=alone, seed=9)
     out = run(g, c, 0.125)
     assert g.attn_get_device_error() == g.OK
     verify(c, 0.125, out)
