@@ -39,7 +39,7 @@
 //
 //   warps 0-3, 4-7   softmax of half 0, 1: thread t owns row t of the tile (TMEM lane t)
 //   warps 8, 11      TMA producer of half 0, 1 (Q once a unit, then K and V tiles; paged:
-//                    a lane per box, its table entry fetched a tile ahead)
+//                    a lane per block, its table entry fetched a tile ahead)
 //   warps 9, 10      MMA of half 0, 1 (warp 9 also allocates and frees TMEM)
 //
 // Per tile and half, as in the causal prefill (see prefill_tc.cu): S into registers, row
@@ -130,7 +130,7 @@ __device__ __forceinline__ DenseUnit cross_unit(const DenseParams& p, int x, int
 
 __device__ __forceinline__ int unit_tiles(const DenseUnit& u) { return (u.key1 - u.key0 + kBN - 1) / kBN; }
 
-template <int DK, int DV, bool ARMS>
+template <int DK, int DV, bool ARMS, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the plan's units, the lengths and everything else may come from the kernel before
   grid_dep_wait();
   grid_dep_launch();  // the next launch may start setting up on the SMs this grid frees
-  const int n_units = p.units ? __ldcg(p.units_listed) : p.n_units;
+  const int n_units = PAGED ? __ldcg(p.units_listed) : p.n_units;
   const int slots = (int)gridDim.x * C::kHalves;
 
   if (warp >= kProducerWarp) {
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int next_e = 0;
       // boxes of a paged tile: this lane's lie in block my_block of its `per` (both powers of
       // two or less than the warp: y and y + 32 fall on one block)
-      const int per = p.tables ? kBN / p.bs : 1;
+      const int per = PAGED ? kBN / p.bs : 1;
       const int my_block = lane % per;
       // table entry of this lane's rows of tile j (num_blocks where it holds no key); checked
       // where it is used
@@ -214,17 +214,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const auto fetch_ahead = [&](int steps) {
         if (ahead == 0) {
-          if (p.units) {
+          if (PAGED) {
             if (lane == 0) next_x = slots + atomicAdd(p.ticket, 1);
           } else {
             next_x += slots;
           }
           ahead = 1;
         } else if (ahead == 1 && steps >= 2) {
-          if (p.units) next_x = __shfl_sync(0xffffffffu, next_x, 0);
+          if (PAGED) next_x = __shfl_sync(0xffffffffu, next_x, 0);
           next_u = DenseUnit{};
           if (next_x < n_units) {
-            if (p.units) {
+            if (PAGED) {
               const int4 a = __ldcg(reinterpret_cast<const int4*>(p.units + next_x));
               const int4 c = __ldcg(reinterpret_cast<const int4*>(p.units + next_x) + 1);
               next_u = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
@@ -234,16 +234,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ahead = 2;
         } else if (ahead == 2 && steps >= 3) {
-          if (p.tables) next_e = entry(next_u, 0);
+          if (PAGED) next_e = entry(next_u, 0);
           // its Q and (contiguous) first K and V tiles on their way to L2: units that end
           // together would all wait for HBM at their next one's start
           if (next_u.n_i && next_u.key1 > next_u.key0) {
-            const int own = p.units && next_u.batch_or_own, seq = p.units ? 0 : next_u.batch_or_own;
+            const int own = PAGED && next_u.batch_or_own, seq = PAGED ? 0 : next_u.batch_or_own;
             if (lane < C::kCBK)
               tc::tma_prefetch_4d(own ? &tm_q1 : &tm_q, lane * 64, next_u.head0, next_u.i0, seq);
-            if (!p.tables && lane < C::kCBK)
+            if (!PAGED && lane < C::kCBK)
               tc::tma_prefetch_4d(&tm_k, lane * 64, next_u.key0, next_u.head0 / p.G, next_u.seq);
-            if (!p.tables && lane < C::kCBV)
+            if (!PAGED && lane < C::kCBV)
               tc::tma_prefetch_4d(&tm_v, lane * 64, next_u.key0, next_u.head0 / p.G, next_u.seq);
           }
           ahead = 3;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && t_all > 0)
           ok = warp_wait_tc(&hb.k_empty[(t_all - 1) % kStages], ((t_all - 1) / kStages) & 1, bars, p.err);
         if (!ok) break;
-        const bool small = p.units && u.batch_or_own;
+        const bool small = PAGED && u.batch_or_own;
         if (lane == 0) {
           hb.unit[us] = u;
           if (tiles > 0)
@@ -279,13 +279,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u.n_i == 0) break;  // the end
         if (tiles > 0 && lane < C::kCBK)
           tc::tma_load_4d(sm + lane * kBlk, small ? &tm_q1 : &tm_q, lane * 64, u.head0, u.i0,
-                          p.units ? 0 : u.batch_or_own, &hb.q_full[us]);
+                          PAGED ? 0 : u.batch_or_own, &hb.q_full[us]);
         for (int j = 0; j < tiles; ++j, ++t_all) {
           const int st = t_all % kStages;
           // a block that holds no key, or whose entry is out of range (flagged), loads from
           // past the end of the pool: the TMA engine fills it with zeros
           int blk = e;
-          if (p.tables) {
+          if (PAGED) {
             if ((blk < 0 || blk >= p.num_blocks) && u.key0 + j * kBN + my_block * p.bs < u.key1) {
               raise_error(p.err, kErrBounds);
               blk = p.num_blocks;
@@ -307,11 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const CUtensorMap* tm = kv ? &tm_v : &tm_k;
             if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(ncb * kBlk));
             __syncwarp();
-            if (!p.tables) {
+            if (!PAGED) {
               if (lane < ncb) tc::tma_load_4d(dst + lane * kBlk, tm, lane * 64, u.key0 + j * kBN, kvh, u.seq, full);
-            } else {
-              for (int y = lane; y < per * ncb; y += 32)
-                tc::tma_load_4d(dst + y / per * kBlk + my_block * p.bs * 128, tm, y / per * 64, 0, kvh, blk, full);
+            } else if (lane < per) {
+              tc::tma_load_4d(dst + lane * p.bs * 128 * ncb, tm, 0, 0, 0, (blk * p.Hkv + kvh) * (p.bs / 8), full);
             }
             __syncwarp();
             (kv ? v_sent : k_sent) = t_all + 1;
@@ -341,7 +340,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // MMAs and its commits in one turn. (Waits and MMAs from lane 0 alone: attn_cross of 8 x 1024
       // rows 389 us; two MMAs an election 333, a whole product 306.)
       const uint32_t idS = tc::idesc_bf16_f32(kBM, kBN, false), idO = tc::idesc_bf16_f32(kBM, DV, true);
-      constexpr uint64_t kHi = tc::desc_sw128_hi(0, 1024), kHiV = tc::desc_sw128_hi(C::kCBV > 1 ? kBlk : 0, 1024);
+      // a K or V tile: squares of 8 rows x 64 columns, 1 KB each; those of the next columns and of
+      // the next rows (paged: a block's columns next to one another, see make_pool_map)
+      constexpr uint32_t kNextCols = PAGED ? 1024 : kBlk;
+      constexpr uint32_t kNextRowsK = PAGED ? 1024 * C::kCBK : 1024, kNextRowsV = PAGED ? 1024 * C::kCBV : 1024;
+      constexpr uint64_t kHiQ = tc::desc_sw128_hi(0, 1024), kHiK = tc::desc_sw128_hi(0, kNextRowsK);
+      constexpr uint64_t kHiV = tc::desc_sw128_hi(C::kCBV > 1 ? kNextCols : 0, kNextRowsV);
       const uint32_t dS0 = tmem + C::col_s(w), dO = tmem + C::col_o(w), tP0 = tmem + C::col_p(w);
       // One place that issues S and one that issues PV, whatever tile or unit they are for: a
       // second copy of either, run once a unit, was fetched from L2 instruction by instruction
@@ -356,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_i = hb.unit[us].n_i, keys = hb.unit[us].key1 - hb.unit[us].key0;
         // keys at the start of a sequence's own, on the first one's block, that its window hides
         int hidden = 0;
-        if (ARMS && p.window > 0 && p.units && hb.unit[us].batch_or_own)
+        if (ARMS && p.window > 0 && hb.unit[us].batch_or_own)
           hidden = first_visible_key(__ldg(p.seq_lens + hb.unit[us].seq) - 1, p.window) - hb.unit[us].key0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&hb.unit_free[us]);
@@ -374,13 +378,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_after_sync();
             // (the descriptors are built here from the buffers' addresses: as loop invariants
             // all of them were kept, in more registers than the control warps have)
-            const uint64_t dQ = kHi | fresh(smem_u32(sm) >> 4);
-            const uint64_t dK = kHi | fresh(smem_u32(sm + C::kOffK + st * kTileK) >> 4);
+            const uint64_t dQ = kHiQ | fresh(smem_u32(sm) >> 4);
+            const uint64_t dK = kHiK | fresh(smem_u32(sm + C::kOffK + st * kTileK) >> 4);
             if (tc::elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < DK / 16; ++kk) {
-                const uint32_t at = (kk / 4) * kBlk + (kk % 4) * 32;
-                tc::mma_f16_ss(dS0, dQ + (at >> 4), dK + (at >> 4), idS, kk > 0);
+                const uint32_t at = (kk / 4) * kBlk + (kk % 4) * 32, at_k = (kk / 4) * kNextCols + (kk % 4) * 32;
+                tc::mma_f16_ss(dS0, dQ + (at >> 4), dK + (at_k >> 4), idS, kk > 0);
               }
               tc::mma_commit(&hb.s_full);
               tc::mma_commit(&hb.k_empty[st]);  // the K stage is free once S is done
@@ -396,11 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // sees (the swizzle moves chunks within a row only)
             const int valid = keys - k * kBN, skip = ARMS ? hidden - k * kBN : 0;
             if (valid < kBN || (ARMS && skip > 0)) {
-              unsigned char* dst = sm + C::kOffV + st * kTileV + lane / 8 % C::kCBV * kBlk + lane % 8 * 16;
+              unsigned char* dst = sm + C::kOffV + st * kTileV + lane / 8 % C::kCBV * kNextCols + lane % 8 * 16;
 #pragma unroll 1
               for (int row = (ARMS && skip > 0 ? 0 : valid) + lane / (8 * C::kCBV); row < kBN; row += 4 / C::kCBV)
                 if (!ARMS || row >= valid || row < skip)
-                  *reinterpret_cast<uint4*>(dst + row * 128) = make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4*>(dst + row / 8 * kNextRowsV + row % 8 * 128) = make_uint4(0, 0, 0, 0);
               tc::fence_async_smem();
               __syncwarp();
             }
@@ -419,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (tc::elect_one()) {
 #pragma unroll
                 for (int kk = k0; kk < k0 + kTurn; ++kk)
-                  tc::mma_f16_ts(dO, tP0 + kk * 8, dV + kk * (2048 >> 4), idO, (k > 0 || kk > 0));
+                  tc::mma_f16_ts(dO, tP0 + kk * 8, dV + kk * (kNextRowsV >> 3), idO, (k > 0 || kk > 0));
                 if (k0 + kTurn == kSteps) {
                   tc::mma_commit(&hb.o_done);
                   tc::mma_commit(&hb.v_empty[st]);
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         lim = u.key1;
         if (ARMS) {  // a row is a sequence of its own length; its position is its last key's
           pos = __ldg(p.seq_lens + u.i0 + min(r, rows - 1) / p.GH) - 1;
-          if (p.units && u.batch_or_own) lo_key = first_visible_key(pos, p.window);
+          if (u.batch_or_own) lo_key = first_visible_key(pos, p.window);
         }
         // a padding row beside live ones needs no mask and never moves its reference: whatever
         // it holds stays in its own row
@@ -651,9 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (a NaN among a row's scores makes its l NaN, and has to reach the output)
       const bool some = l_run != 0.f;
       const int at = u.part;
-      if (at >= 0) {
+      if (PAGED || at >= 0) {
         if (warp_live) {
-          const int rows = u.n_i * p.GH, R = p.units && u.batch_or_own ? p.own_rows : kBM;
+          const int rows = u.n_i * p.GH, R = PAGED && u.batch_or_own ? p.own_rows : kBM;
           float* part = p.partial + (size_t)at * 4;
 #pragma unroll 1
           for (int cc = 0; cc < DV / 32; ++cc) {
@@ -734,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&hb.unit_free[us]);
     }
-    if ((threadIdx.x & 127) == 0) tc::bulk_wait_group_read0();  // shared memory stays valid until then
+    if (!PAGED && (threadIdx.x & 127) == 0) tc::bulk_wait_group_read0();  // shared memory stays valid until then
   }
 
   tc::fence_before_sync();
@@ -835,7 +839,20 @@ bool make_map(CUtensorMap* m, const void* base, int d, uint64_t d1, uint64_t d2,
   return make_tmap_bf16(m, base, dims, strides, box);
 }
 
-template <int DK, int DV, bool ARMS>
+// The pool as [groups of 8 rows, d / 64, 8, 64]: a block of a KV head, all its columns, is one
+// box, and in shared memory a group's squares of 8 x 64 lie next to one another. (A box of each 64
+// columns, at 16-row blocks of 128 columns twice as many: shared prefixes 193 us, now 184.)
+bool make_pool_map(CUtensorMap* m, const void* base, int d, const DenseParams& p) {
+  const uint64_t groups = (uint64_t)p.num_blocks * p.Hkv * (p.bs / 8);
+  // (the block past the end, which stands for none, has to have a coordinate too)
+  if (groups + (uint64_t)p.Hkv * (p.bs / 8) > INT_MAX) return false;
+  const uint64_t dims[4] = {64, 8, (uint64_t)d / 64, groups};
+  const uint64_t strides[3] = {(uint64_t)d * 2, 128, (uint64_t)d * 16};
+  const uint32_t box[4] = {64, 8, (uint32_t)d / 64, (uint32_t)p.bs / 8};
+  return make_tmap_bf16(m, base, dims, strides, box);
+}
+
+template <int DK, int DV, bool ARMS, bool PAGED>
 cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtensorMap& tk, const CUtensorMap& tv,
                      const CUtensorMap& to, const DenseParams& p, cudaStream_t st) {
   using C = DenseCfg<DK, DV>;
@@ -846,10 +863,10 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtens
     // The register hand-over inside the kernel assumes exactly kLaunchRegs per
     // thread at launch; a build with any other allocation is refused.
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, dense_tc_kernel<DK, DV, ARMS>);
+    cudaError_t e = cudaFuncGetAttributes(&fa, dense_tc_kernel<DK, DV, ARMS, PAGED>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
-    e = cudaFuncSetAttribute(dense_tc_kernel<DK, DV, ARMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    e = cudaFuncSetAttribute(dense_tc_kernel<DK, DV, ARMS, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
   }
@@ -863,7 +880,16 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtens
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dense_tc_kernel<DK, DV, ARMS>, tq, tq1, tk, tv, to, p);
+  return cudaLaunchKernelEx(&cfg, dense_tc_kernel<DK, DV, ARMS, PAGED>, tq, tq1, tk, tv, to, p);
+}
+
+// (the arms belong to the shared-prefix step, which is paged)
+template <int DK, int DV>
+cudaError_t launch_w(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtensorMap& tk, const CUtensorMap& tv,
+                     const CUtensorMap& to, const DenseParams& p, bool arms, cudaStream_t st) {
+  if (!p.tables) return launch_d<DK, DV, false, false>(tq, tq1, tk, tv, to, p, st);
+  return arms ? launch_d<DK, DV, true, true>(tq, tq1, tk, tv, to, p, st)
+              : launch_d<DK, DV, false, true>(tq, tq1, tk, tv, to, p, st);
 }
 
 }  // namespace
@@ -891,21 +917,15 @@ cudaError_t launch_dense_tc(const void* q, const void* k, const void* v, const D
   if (!make_map(&tq, q, dk, p.H, p.n_i, n_b, p.GH, p.RPT)) return cudaErrorInvalidValue;
   if (!make_map(&tq1, q, dk, p.H, p.n_i, n_b, p.GH, 1)) return cudaErrorInvalidValue;
   if (p.tables) {
-    if (!make_map(&tk, k, dk, p.bs, p.Hkv, p.num_blocks, p.bs, 1)) return cudaErrorInvalidValue;
-    if (!make_map(&tv, v, dv, p.bs, p.Hkv, p.num_blocks, p.bs, 1)) return cudaErrorInvalidValue;
+    if (!make_pool_map(&tk, k, dk, p) || !make_pool_map(&tv, v, dv, p)) return cudaErrorInvalidValue;
   } else {
     if (!make_map(&tk, k, dk, p.S_kv, p.Hkv, n_b, kBN, 1)) return cudaErrorInvalidValue;
     if (!make_map(&tv, v, dv, p.S_kv, p.Hkv, n_b, kBN, 1)) return cudaErrorInvalidValue;
   }
   if (!make_map(&to, p.out, dv, p.H, p.n_i, n_b, p.GH, p.RPT)) return cudaErrorInvalidValue;
-  if (arms) {
-    if (dk == 64) return launch_d<64, 64, true>(tq, tq1, tk, tv, to, p, st);
-    if (dk == 128) return launch_d<128, 128, true>(tq, tq1, tk, tv, to, p, st);
-    return launch_d<192, 128, true>(tq, tq1, tk, tv, to, p, st);
-  }
-  if (dk == 64) return launch_d<64, 64, false>(tq, tq1, tk, tv, to, p, st);
-  if (dk == 128) return launch_d<128, 128, false>(tq, tq1, tk, tv, to, p, st);
-  return launch_d<192, 128, false>(tq, tq1, tk, tv, to, p, st);
+  if (dk == 64) return launch_w<64, 64>(tq, tq1, tk, tv, to, p, arms, st);
+  if (dk == 128) return launch_w<128, 128>(tq, tq1, tk, tv, to, p, arms, st);
+  return launch_w<192, 128>(tq, tq1, tk, tv, to, p, arms, st);
 }
 
 cudaError_t launch_dense_combine(const DenseCombine& p, cudaStream_t st) {
