@@ -30,12 +30,12 @@
 // counter; those of attn_cross are alike and go round by slot.
 //
 // Measured at 32 heads on 8 KV heads of 128, plan and combine included: 64 sequences behind
-// a prefix of 8,192 keys with up to 512 of their own 45 us; 256 sequences behind four prefixes
-// of 16,384 keys with up to 1,024 of their own 193 us (4.2 TB/s of rows read once, 0.62 of the
-// copy bandwidth); attn_cross of 8 x 1,024 rows on 2,048 to 4,096 keys 306 us (1.35 PFLOP/s, 0.71
+// a prefix of 8,192 keys with up to 512 of their own 43 us; 256 sequences behind four prefixes
+// of 16,384 keys with up to 1,024 of their own 173 us (4.7 TB/s of rows read once, 0.69 of the
+// copy bandwidth); attn_cross of 8 x 1,024 rows on 2,048 to 4,096 keys 303 us (1.36 PFLOP/s, 0.71
 // of the measured bf16 rate). What bounds them is a half's time from tile to tile, of 1,024 cycles
 // of products: in the last case about 3,200 cycles, S, softmax and PV of a half one after
-// another; in the second 5,000, of which the MMA warp waits 1,800 for K and V at one stage each.
+// another; in the second a third more, for K and V that come from HBM through one stage each.
 //
 //   warps 0-3, 4-7   softmax of half 0, 1: thread t owns row t of the tile (TMEM lane t)
 //   warps 8, 11      TMA producer of half 0, 1 (Q once a unit, then K and V tiles; paged:
@@ -841,7 +841,7 @@ bool make_map(CUtensorMap* m, const void* base, int d, uint64_t d1, uint64_t d2,
 
 // The pool as [groups of 8 rows, d / 64, 8, 64]: a block of a KV head, all its columns, is one
 // box, and in shared memory a group's squares of 8 x 64 lie next to one another. (A box of each 64
-// columns, at 16-row blocks of 128 columns twice as many: shared prefixes 193 us, now 184.)
+// columns, twice as many at 128 columns: 256 sequences behind four prefixes 193 us, so 184.)
 bool make_pool_map(CUtensorMap* m, const void* base, int d, const DenseParams& p) {
   const uint64_t groups = (uint64_t)p.num_blocks * p.Hkv * (p.bs / 8);
   // (the block past the end, which stands for none, has to have a coordinate too)

@@ -11,7 +11,7 @@
 // The prefix of group g is tiles_g row tiles per KV head (and head chunk) times n_g key
 // tiles; the own keys of a sequence are one row tile per KV head (and head chunk). Units
 // take c key tiles each, c the same for all and chosen to minimise
-//   max(ceil(prefix units / slots) * (c + kDenseUnitTiles), (all tiles + units * kDenseUnitTiles) / slots) + c / 4,
+//   max(ceil(prefix units / slots) * (c + kDenseUnitTiles), (all tiles + units * kDenseUnitTiles) / slots) + c / 8,
 // in key tiles: the rounds that the prefixes' equal units take on the slots (units worked on
 // at a time), in whose last round own units fill the rest, or all work spread evenly; and
 // something for the longest unit, which the rest may have to wait for.
@@ -224,8 +224,11 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
     const float even =
         (tiles + own_all + (units + own_all / (float)max(c, c_own_least) + own_items * 0.5f) * (float)kDenseUnitTiles) /
         (float)s.slots;
-    // a quarter of a unit for the tail that one leaves behind; ties go to the longer units
-    const float cost = fmaxf(rounds, even) + 0.25f * (float)c;
+    // an eighth of a unit for the tail that one leaves behind (the geometric mean of a step's time
+    // over twelve batches, 8 to 300 sequences behind 1,000 to 60,000 keys: with a quarter 62.1 us,
+    // an eighth 59.8; with a quarter and units that cost 2, 3 or 4 tiles 59.9, 60.4, 60.7); ties go
+    // to the longer units
+    const float cost = fmaxf(rounds, even) + 0.125f * (float)c;
     const unsigned long long key = (unsigned long long)__float_as_uint(cost) << 32 | (unsigned)(kMostTiles - c);
     best = key < best ? key : best;
   }
