@@ -81,7 +81,7 @@ struct DenseCfg {
   static_assert(kSmemBytes <= 232448, "over the 227 KiB a CTA may use");
 };
 
-constexpr int kDenseStagesMax = 3;
+constexpr int kDenseStagesMax = 2;
 
 struct HalfBars {
   uint64_t q_full[2];     // a unit's record (and its Q) is in place; by unit parity
@@ -202,8 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int next_x = (int)blockIdx.x + (int)gridDim.x * w, ahead = 1;  // steps done: 1 number, 2 record, 3 entry
       DenseUnit next_u = {};
       int next_e = 0;
-      // boxes of a paged tile: this lane's lie in block my_block of its `per` (both powers of
-      // two or less than the warp: y and y + 32 fall on one block)
+      // paged: lane y < per brings block y of a tile and holds its table entry
       const int per = PAGED ? kBN / p.bs : 1;
       const int my_block = lane % per;
       // table entry of this lane's rows of tile j (num_blocks where it holds no key); checked
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = (u.key0 + j * kBN) / p.bs + my_block;
         return t < p.mbps && t * p.bs < u.key1 ? __ldg(p.tables + (size_t)u.seq * p.mbps + t) : p.num_blocks;
       };
-      const auto fetch_ahead = [&](int steps) {
+      const auto fetch_ahead = [&] {
         if (ahead == 0) {
           if (PAGED) {
             if (lane == 0) next_x = slots + atomicAdd(p.ticket, 1);
@@ -220,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             next_x += slots;
           }
           ahead = 1;
-        } else if (ahead == 1 && steps >= 2) {
+        } else if (ahead == 1) {
           if (PAGED) next_x = __shfl_sync(0xffffffffu, next_x, 0);
           next_u = DenseUnit{};
           if (next_x < n_units) {
@@ -233,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           ahead = 2;
-        } else if (ahead == 2 && steps >= 3) {
+        } else if (ahead == 2) {
           if (PAGED) next_e = entry(next_u, 0);
           // its Q and (contiguous) first K and V tiles on their way to L2: units that end
           // together would all wait for HBM at their next one's start
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (; alive; ++n) {
         const int us = n & 1;
-        while (ahead < 3) fetch_ahead(3);
+        while (ahead < 3) fetch_ahead();
         const DenseUnit u = next_u;
         int e = next_e;
         ahead = 0;
@@ -319,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             alive = false;
             break;
           }
-          fetch_ahead(3);  // one step a tile
+          fetch_ahead();  // one step a tile
         }
       }
       if (lane == 0) {
