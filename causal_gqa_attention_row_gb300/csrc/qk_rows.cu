@@ -24,7 +24,8 @@
 // bytes (no barrier), requested before the token's position and slot are known. Few
 // tokens (a decode step): a token's rows are cut into as many items as fill the GPU,
 // down to one round each; many tokens: one item per token, so that its angles and
-// factors are formed once (dispatch_qk).
+// factors are formed once; many tokens of few rows: up to eight tokens a warp, side by
+// side (dispatch_qk).
 //
 // Measured (bf16, 32 + 8 heads of 128): 16384 tokens 64.4 us (5.2 TB/s of rows read and
 // written, 0.77 of the copy bandwidth), four 2048-row chunks appended 40.1 us (5.0 TB/s).
@@ -43,7 +44,6 @@ namespace {
 constexpr int kQkWarps = 4;     // warps (items) per CTA
 constexpr int kQkRows = 2;      // rows of a round per lane group
 constexpr int kQkStages = 2;    // rounds in flight per warp (2 KB each)
-constexpr int kMaxPairs = 128;  // rot_dim <= 256
 
 // How pairs turn: columns that cross 16-byte chunks, half pairs by whole chunks,
 // adjacent pairs by whole chunks (or no rotation).
@@ -147,14 +147,16 @@ __device__ __forceinline__ void advance_length(const QkParams& p, int b, int lan
   }
 }
 
-// L lanes per row: a power of two >= the row's chunk pairs.
-template <typename ET, int L, int TURN, bool PAGED>
+// L lanes per row: a power of two >= the row's chunk pairs. W tokens per warp, side by side (more
+// than one: each a whole token).
+template <typename ET, int L, int TURN, bool PAGED, int W>
 __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p) {
   constexpr int V = Elem<ET>::kPerChunk;  // elements of a 16-byte chunk
   constexpr int H2 = V / 2;
-  constexpr int kGroups = 32 / L;         // rows a warp works on side by side
+  constexpr int kSub = 32 / W;            // lanes of a token
+  constexpr int kGroups = kSub / L;       // rows of a token side by side
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ float2 cs_s[kQkWarps][kMaxPairs];
+  __shared__ float2 cs_s[kQkWarps * W][L * V];  // (a row has at most 2 L V columns)
   // rounds of rows in flight: [stage][row][chunk][lane], each lane its own 16 bytes
   __shared__ uint4 ring_s[kQkWarps][kQkStages][kQkRows][2][32];
   // kTurnAny: the rows being turned, one per lane group
@@ -165,16 +167,20 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p
   grid_dep_launch();
   // block row y: share y of the tokens' rows; PAGED: then the tokens' values (with a single
   // share they go with it: half as many warps wait for a position), then the lengths
-  const int tok = (int)(blockIdx.x * kQkWarps) + warp, part = (int)blockIdx.y + p.first_part;
+  const int item = (int)(blockIdx.x * kQkWarps) + warp, part = (int)blockIdx.y + p.first_part;
   if (PAGED && part == p.lens_part) {
-    if (tok < p.lens_items) advance_length(p, tok, lane);
+    if (item < p.lens_items) advance_length(p, item, lane);
     return;
   }
-  if ((unsigned)tok >= (unsigned)p.N) return;
+  const long long first_tok = (long long)item * W;
+  if (first_tok >= p.N) return;
+  const int ts = lane / kSub, sl = lane % kSub;  // the token of this lane, the lane within it
+  bool alive = W == 1 || first_tok + ts < p.N;   // (W > 1: the others' lanes come along and write nothing)
+  const int tok = W == 1 ? item : alive ? (int)first_tok + ts : p.N - 1;
   const long long tb = PAGED ? 0 : tok / p.T, tt = PAGED ? tok : tok % p.T;
 
   // ---- this lane's two chunks of every row (-1: none)
-  const int li = lane % L, grp = lane / L;
+  const int li = lane % L, grp = sl / L;
   const int cpr = p.d / V;
   const int half = p.rot_dim / 2;
   int c0, c1;
@@ -241,37 +247,56 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p
   int pos = 0;
   long long slot = 0;  // pool row of KV head 0: (block * Hkv) * bs + row
   if (PAGED) {
-    int len = 0;
+    int len = 0, b = -1;
     long long row = 0;
-    const int b = find_sequence(p, tok, lane, len, row);
-    if (b < 0) {  // behind the last sequence: left as it is
+    if (W == 1) {
+      b = find_sequence(p, tok, lane, len, row);
+    } else {
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        int n;
+        long long r;
+        const int x = find_sequence(p, (int)min(first_tok + w, (long long)p.N - 1), lane, n, r);
+        if (w == ts) {
+          b = x;
+          len = n;
+          row = r;
+        }
+      }
+    }
+    alive = alive && b >= 0;  // behind the last sequence: left as it is
+    if (W == 1 && !alive) {
       async_wait<0>();  // never exit with a copy in flight
       return;
     }
-    const long long at = (long long)len + row;
-    const bool fits = len >= 0 && at < (long long)p.mbps * p.bs;
+    const long long at = alive ? (long long)len + row : 0;
+    const bool fits = alive && len >= 0 && at < (long long)p.mbps * p.bs;
     const int blk = fits ? __ldg(p.tables + (size_t)b * p.mbps + at / p.bs) : -1;
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (lane == 0) raise_error(p.err, kErrBounds);
+    if (alive && (blk < 0 || blk >= p.num_blocks)) {
+      if (sl == 0) raise_error(p.err, kErrBounds);
+      alive = false;
+    }
+    if (W == 1 ? !alive : !__any_sync(0xffffffffu, alive)) {
       async_wait<0>();
       return;
     }
-    pos = (int)at;
+    if (W == 1) alive = true;
+    pos = alive ? (int)at : 0;
     slot = (long long)blk * p.Hkv * p.bs + at % p.bs;
     if (values || p.parts == 1) {  // the values, copied as they are, four chunks in flight per lane
       const int cpv = p.dv / V, n = p.Hkv * cpv;
-      for (int i0 = lane; i0 < n; i0 += 4 * 32) {
+      for (int i0 = sl; alive && i0 < n; i0 += 4 * kSub) {
         uint4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int i = i0 + u * 32;
+          const int i = i0 + u * kSub;
           if (i < n)
             v[u] = ld16(static_cast<const ET*>(p.v.data) + tt * p.v.token_stride + (i / cpv) * p.v.head_stride +
                         (i % cpv) * V);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int i = i0 + u * 32;
+          const int i = i0 + u * kSub;
           if (i < n)
             *reinterpret_cast<uint4*>(static_cast<ET*>(p.v_pool) + (slot + (long long)(i / cpv) * p.bs) * p.dv +
                                       (i % cpv) * V) = v[u];
@@ -282,8 +307,8 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p
   } else if (p.rot_dim) {
     pos = __ldg(p.positions + tok);
   }
-  float2* cs = cs_s[warp];
-  for (int t = lane; t < half; t += 32) {
+  float2* cs = cs_s[warp * W + ts];
+  for (int t = sl; t < half; t += kSub) {
     const float2 w = __ldg(reinterpret_cast<const float2*>(p.freqs) + t);
     float c, s;
     rope_cos_sin_pair(pos, w.x, w.y, &c, &s);
@@ -402,7 +427,7 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p
         }
         if (TURN == kTurnAny) {
           // pairs that cross chunks: the weighted row through shared memory, column by column
-          float* row = row_s[warp] + grp * (2 * L * V);
+          float* row = row_s[warp] + lane / L * (2 * L * V);
           __syncwarp();
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
@@ -439,7 +464,7 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p
             y[1][e] = __fmul2_rn(y[1][e], rs2);
           }
         }
-        if (r < hi) {
+        if (r < hi && alive) {
           if (c0 >= 0) *reinterpret_cast<uint4*>(to) = Chunk<ET>::pack(y[0]);
           if (c1 >= 0) *reinterpret_cast<uint4*>(to + apart) = Chunk<ET>::pack(y[1]);
         }
@@ -449,9 +474,10 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p
   }
 }
 
-template <typename ET, int L, int TURN, bool PAGED>
+template <typename ET, int L, int TURN, bool PAGED, int W>
 cudaError_t launch_qk(QkParams p, cudaStream_t st) {
-  const int n = p.run_rows ? p.N : 0, lens = PAGED ? p.lens_items : 0, most = n > lens ? n : lens;
+  const int n = p.run_rows ? (int)(((long long)p.N + W - 1) / W) : 0, lens = PAGED ? p.lens_items : 0;
+  const int most = n > lens ? n : lens;
   if (most == 0) return cudaSuccess;
   p.lens_part = p.parts > 1 ? p.parts + 1 : 1;
   p.first_part = n ? 0 : p.lens_part;  // the lengths alone
@@ -463,7 +489,7 @@ cudaError_t launch_qk(QkParams p, cudaStream_t st) {
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, qk_rows_kernel<ET, L, TURN, PAGED>, p);
+  return cudaLaunchKernelEx(&cfg, qk_rows_kernel<ET, L, TURN, PAGED, W>, p);
 }
 
 template <typename ET, int TURN, bool PAGED>
@@ -474,16 +500,24 @@ cudaError_t dispatch_qk(QkParams p, cudaStream_t st) {
   const int L = pairs <= 4 ? 4 : pairs <= 8 ? 8 : pairs <= 16 ? 16 : 32;
   // Items per token: as few as keep 16 warps on each of the 152 SMs, at most one
   // round of loads each.
-  const int rows = p.H + p.Hk, most = (rows + kQkRows * (32 / L) - 1) / (kQkRows * (32 / L));
+  const int rows = p.H + p.Hk, rounds = (rows + kQkRows * (32 / L) - 1) / (kQkRows * (32 / L));
   const long long want = (152 * 16 + (long long)p.N - 1) / (p.N > 0 ? p.N : 1);
-  const int parts = rows == 0 ? 1 : (int)(want < 1 ? 1 : want > most ? most : want);
+  const int parts = rows == 0 ? 1 : (int)(want < 1 ? 1 : want > rounds ? rounds : want);
   p.part_rows = rows == 0 ? 1 : (rows + parts - 1) / parts;
   p.parts = rows == 0 ? 1 : (rows + p.part_rows - 1) / p.part_rows;
+  // Many tokens of few rows: a token for each L lanes, so that no lanes idle and what a token
+  // takes beside its rows is shared by as many. Measured, a warp per token and side by side (bf16):
+  // 524,288 tokens of 1 + 1 heads of 64 693 and 152 us, 16,384 of 8 + 2 of 128 27.7 and 19.3, of 32 +
+  // 8 of 128 (five rounds a warp) 64.2 and 68.4; 8,192 of 14 + 2 of 64 14.0 and 10.0; 4,096 of 8 + 8
+  // of 64 7.8 and 8.8, 2,048 of 14 + 2 of 64 (256 warps for the GPU) 4.8 and 8.9. An append's rows
+  // may be padding in good part (7,261 rows of 14 + 2 + 2 heads of 64, half of them padding: 9.7
+  // and 10.4), so twice as many are asked for.
+  const bool side = p.parts == 1 && rounds <= 3 && p.N >= (PAGED ? 8 : 4) * 152 * (32 / L);
   switch (L) {
-    case 4: return launch_qk<ET, 4, TURN, PAGED>(p, st);
-    case 8: return launch_qk<ET, 8, TURN, PAGED>(p, st);
-    case 16: return launch_qk<ET, 16, TURN, PAGED>(p, st);
-    default: return launch_qk<ET, 32, TURN, PAGED>(p, st);
+    case 4: return side ? launch_qk<ET, 4, TURN, PAGED, 8>(p, st) : launch_qk<ET, 4, TURN, PAGED, 1>(p, st);
+    case 8: return side ? launch_qk<ET, 8, TURN, PAGED, 4>(p, st) : launch_qk<ET, 8, TURN, PAGED, 1>(p, st);
+    case 16: return side ? launch_qk<ET, 16, TURN, PAGED, 2>(p, st) : launch_qk<ET, 16, TURN, PAGED, 1>(p, st);
+    default: return launch_qk<ET, 32, TURN, PAGED, 1>(p, st);
   }
 }
 

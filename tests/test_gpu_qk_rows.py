@@ -159,6 +159,42 @@ def test_sizes(gpu_lib, shape):
         check(excess(got, want, size, dt, p), 1.0)
 
 
+@pytest.mark.parametrize("shape", [
+    # type, tokens, H, Hkv, d, layout, rotated columns, offset: tokens side by side in a warp,
+    # 8 (64 columns of bf16), 4 (128, or 64 of fp32), 2 (256); none a multiple of that
+    (torch.bfloat16, 4867, 3, 1, 64, "half", 64, 0),
+    (torch.bfloat16, 5003, 8, 2, 32, "half", 8, 4),
+    (torch.bfloat16, 4865, 1, 1, 64, "interleaved", 32, 16),
+    (torch.bfloat16, 2435, 8, 2, 128, "half", 64, 64),
+    (torch.float32, 2433, 3, 2, 64, "interleaved", 64, 0),
+    (torch.float32, 2439, 5, 1, 64, "half", 22, 3),
+    (torch.bfloat16, 1217, 6, 1, 256, "half", 256, 0),
+    (torch.bfloat16, 5001, 2, 1, 64, None, 0, 0),
+], ids=str)
+def test_many_tokens_of_few_rows(gpu_lib, shape):
+    g = gpu_lib
+    dt, T, H, Hkv, d, layout, rot, off = shape
+    gg = gen(T)
+    q, k, _ = packed([H, Hkv, Hkv], (1, T), d, dt, gg)
+    wq, wk = weight(d, dt, gg), weight(d, dt, gg)
+    pos = torch.randint(0, 1 << 20, (1, T), generator=gg, dtype=torch.int32).to(DEV)
+    r = g.rope_init(rot, 1e6, layout=layout, rot_offset=off) if layout else None
+    qo, ko = torch.empty(1, T, H, d, dtype=dt, device=DEV), torch.empty(1, T, Hkv, d, dtype=dt, device=DEV)
+    g.attn_qk_norm_rope(q, k, qo, ko, pos, r, q_weight=wq, k_weight=wk)
+    p = pos.cpu().numpy()
+    for got, x, wt in ((qo, q, wq), (ko, k, wk)):
+        want = R.norm(f64(x), f64(wt), 1e-6)
+        size = np.abs(want)
+        if layout:
+            want, size = R.rotate(want, p, R.frequencies(rot, 1e6), layout, off)
+        check(excess(got, want, size, dt, p), 1.0)
+    # the same bits as a few tokens at a time
+    for a, b in ((0, 5), (T - 700, T)):
+        q2, k2 = torch.empty_like(qo[:, a:b]), torch.empty_like(ko[:, a:b])
+        g.attn_qk_norm_rope(q[:, a:b], k[:, a:b], q2, k2, pos[:, a:b].contiguous(), r, q_weight=wq, k_weight=wk)
+        assert torch.equal(q2, qo[:, a:b]) and torch.equal(k2, ko[:, a:b])
+
+
 def test_same_bits_as_the_present_rotation(gpu_lib):
     """Adjacent pairs, no norm, no scaling: attn_rope_interleaved_qk's operation."""
     g = gpu_lib
@@ -251,6 +287,43 @@ def test_append_rows(gpu_lib, dt, shape):
                            k_weight=c["wk"])
     assert torch.equal(kp, kp2) and torch.equal(vp, vp2) and torch.equal(lens, out)
     assert g.attn_get_device_error() == g.OK
+
+
+@pytest.mark.parametrize("H,Hkv,dk,dv,B", [(3, 1, 64, 64, 9), (1, 1, 128, 64, 9), (2, 1, 64, 128, 70)])
+def test_append_many_rows(gpu_lib, H, Hkv, dk, dv, B):
+    """Many rows, several to a warp, sequences that start within one, empty ones, one that does
+    not fit its table, padding: the same bits as sequence by sequence."""
+    g = gpu_lib
+    rng = np.random.default_rng(B)
+    counts = [int(x) for x in rng.multinomial(10203, np.ones(B) / B)]
+    counts[3] = 0
+    lens = [int(x) for x in rng.integers(0, 40, B)]
+    c = append_case(torch.bfloat16, counts, lens, H=H, Hkv=Hkv, dk=dk, dv=dv, pad=13, seed=B)
+    c["tables"][5, lens[5] // c["bs"]] = -1  # sequence 5: its first new block is missing
+    r = g.rope_init(dk, 1e6, layout="half")
+    N = c["q"].shape[0]
+    out = []
+    for whole in (True, False):
+        kp, vp, lens_out = c["kp"].clone(), c["vp"].clone(), torch.full_like(c["lens"], -7)
+        qo = torch.full((N, H, dk), 9.0, dtype=torch.bfloat16, device=DEV)
+        if whole:
+            g.kv_append_paged_rows(c["q"], c["k"], c["v"], qo, kp, vp, c["tables"], c["starts"], c["lens"], lens_out,
+                                   rope=r, q_weight=c["wq"], k_weight=c["wk"])
+        for b in [] if whole else range(B):
+            a, z = int(c["starts"][b]), int(c["starts"][b + 1])
+            starts = torch.tensor([0, z - a], dtype=torch.int32, device=DEV)
+            g.kv_append_paged_rows(c["q"][a:z], c["k"][a:z], c["v"][a:z], qo[a:z], kp, vp, c["tables"][b:b + 1], starts,
+                                   c["lens"][b:b + 1], lens_out[b:b + 1], rope=r, q_weight=c["wq"], k_weight=c["wk"])
+        assert g.attn_get_device_error() == g.ERR_DEVICE_BOUNDS
+        out.append((kp, vp, lens_out, qo))
+    a, z = int(c["starts"][5]), int(c["starts"][6])  # (its q rows are unspecified)
+    out[0][3][a:z] = out[1][3][a:z] = 0
+    for x, y in zip(*out):
+        assert torch.equal(x, y)
+    want = [n + k for n, k in zip(lens, counts)]
+    want[5] = lens[5]
+    assert out[0][2].tolist() == want
+    assert bool((out[0][3][int(c["starts"][-1]):] == 9).all())
 
 
 def test_append_one_row_matches_the_present_append(gpu_lib):
