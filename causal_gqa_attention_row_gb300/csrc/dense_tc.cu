@@ -750,22 +750,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the partial results of a row, in a fixed order (key ranges of the row's tile,
 // then, for the shared-prefix step, the parts of the sequence's own keys):
 //   M = max m_s (and the sink logit),  out = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s
-// A CTA takes rows (i, head) of one head chunk, next to one another in the parts: 256 / (d_v /
-// 4) rows by d_v / 4 threads of four columns, rows along the lanes, so that a warp's loads of
-// a part fall on few lines. Latency bounds it: four parts are in flight a thread, M moves from
-// round to round as the sums are rescaled. (A row per warp touched 32 lines a part; on an SM
-// whose shared memory the kernel above had just used, with 28 KB left for L1, each round of
-// loads took 3 us. The L1 is asked for in full at the launch.)
-__global__ void __launch_bounds__(256) dense_combine_kernel(const DenseCombine p) {
+// A CTA takes rows (i, head) of one head chunk, next to one another in the parts, rows along
+// the lanes, so that a warp's loads of a part fall on few lines: rows by d_v / 4 threads of four
+// columns by `groups` shares of the parts (four parts at a time in turn, joined at the end in the
+// shares' order; more than one where few rows would leave SMs without work: 9 sequences of 7 heads
+// behind 10,600 keys 41.4 us, with eight shares 19.9). Latency bounds it:
+// four parts are in flight a thread, M moves from round to round as the sums are rescaled. (A
+// row per warp touched 32 lines a part; on an SM whose shared memory the kernel above had just
+// used, with 28 KB left for L1, each round of loads took 3 us. The L1 is asked for in full at
+// the launch.)
+// SHARES: groups > 1 (an instantiation of its own: with the shared memory and the shares in one
+// kernel 256 sequences behind four prefixes took 186 us instead of 173).
+template <bool SHARES>
+__global__ void __launch_bounds__(256) dense_combine_kernel(const DenseCombine p, int shares) {
+  __shared__ float4 acc_s[SHARES ? 256 : 1];
+  __shared__ float2 md_s[SHARES ? 256 : 1];
+  const int groups = SHARES ? shares : 1;
   grid_dep_wait();
-  const int dv = p.dv, rows_here = 1024 / dv;  // a power of two, as dv is
-  const int r = threadIdx.x & (rows_here - 1), c = threadIdx.x / rows_here;
+  const int dv = p.dv, rows_here = 1024 / dv / groups;  // powers of two, as dv is
+  const int r = threadIdx.x & (rows_here - 1), c = threadIdx.x / rows_here % (dv / 4);
+  const int share = SHARES ? threadIdx.x / (256 / groups) : 0;
   const int chunks = p.H / p.GH, per_chunk = (p.n_i * p.GH + rows_here - 1) / rows_here;
   int x = blockIdx.x;
-  const int at_row = x % per_chunk * rows_here + r;  // i * GH + head within the chunk
+  const int in_chunk = x % per_chunk * rows_here + r;
+  const bool live = in_chunk < p.n_i * p.GH;
+  if (!SHARES && !live) return;
+  const int at_row = live ? in_chunk : p.n_i * p.GH - 1;  // i * GH + head within the chunk
   x /= per_chunk;
   const int chunk = x % chunks, b = x / chunks;  // chunk: (KV head, head chunk)
-  if (at_row >= p.n_i * p.GH) return;
   const int i = at_row / p.GH, g = at_row - i * p.GH;  // shared prefix: i is the sequence
   // ---- the row's parts: n units of 128 rows, then n_own of own_rows
   const size_t unit_floats = dense_part_floats(kBM, dv), own_floats = dense_part_floats(p.own_rows, dv);
@@ -786,10 +798,10 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const DenseCombine p
   }
   const int total = n + n_own;
   const float z2 = p.sinks ? __ldg(p.sinks + chunk * p.GH + g) * kLog2e : -INFINITY;
-  float M = z2, den = z2 != -INFINITY ? 1.f : 0.f;
+  float M = share == 0 ? z2 : -INFINITY, den = M != -INFINITY ? 1.f : 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int s0 = 0; s0 < total; s0 += 4) {
+  for (int s0 = 4 * share; s0 < total; s0 += 4 * groups) {
     float4 o[4];
     float m[4], l[4];
 #pragma unroll
@@ -823,6 +835,23 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const DenseCombine p
       acc.w = fmaf(w, o[t].w, acc.w);
     }
   }
+  if (SHARES) {
+    md_s[threadIdx.x] = make_float2(M, den);
+    acc_s[threadIdx.x] = acc;
+    __syncthreads();
+    if (share > 0) return;
+    for (int k = 1; k < groups; ++k) {
+      const float2 md = md_s[threadIdx.x + k * (256 / groups)];
+      const float4 a = acc_s[threadIdx.x + k * (256 / groups)];
+      if (md.y == 0.f) continue;
+      const float Mn = fmaxf(M, md.x), f = den == 0.f ? 0.f : ex2f(M - Mn), w = ex2f(md.x - Mn);
+      den = fmaf(w, md.y, den == 0.f ? 0.f : den * f);
+      acc = make_float4(fmaf(w, a.x, acc.x * f), fmaf(w, a.y, acc.y * f), fmaf(w, a.z, acc.z * f),
+                        fmaf(w, a.w, acc.w * f));
+      M = Mn;
+    }
+  }
+  if (!live) return;
   const float inv = den != 0.f ? 1.f / den : 0.f;
   const size_t row = ((size_t)b * p.n_i + i) * p.H + chunk * p.GH + g;
   *reinterpret_cast<uint2*>(p.out + row * dv + 4 * c) =
@@ -932,13 +961,23 @@ cudaError_t launch_dense_combine(const DenseCombine& p, cudaStream_t st) {
   cudaGetDevice(&dev);
   static std::atomic<unsigned long long> attr_done{0};  // per device
   if (dev >= 64 || !(attr_done.load(std::memory_order_acquire) >> dev & 1ull)) {
-    const cudaError_t e = cudaFuncSetAttribute(dense_combine_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                               cudaSharedmemCarveoutMaxL1);
+    cudaError_t e = cudaFuncSetAttribute(dense_combine_kernel<false>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxL1);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(dense_combine_kernel<true>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxL1);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
   }
-  const int rows_here = 1024 / p.dv;
-  const long long blocks = (long long)p.n_b * (p.H / p.GH) * (((long long)p.n_i * p.GH + rows_here - 1) / rows_here);
+  int rows_here = 1024 / p.dv, groups = 1;
+  const auto blocks_of = [&](int rows) {
+    return (long long)p.n_b * (p.H / p.GH) * (((long long)p.n_i * p.GH + rows - 1) / rows);
+  };
+  while (rows_here > 1 && groups < 8 && blocks_of(rows_here / 2) <= 2 * kDenseSms) {
+    rows_here /= 2;
+    groups *= 2;
+  }
+  const long long blocks = blocks_of(rows_here);
   if (blocks <= 0) return cudaSuccess;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -948,7 +987,8 @@ cudaError_t launch_dense_combine(const DenseCombine& p, cudaStream_t st) {
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dense_combine_kernel, p);
+  return groups > 1 ? cudaLaunchKernelEx(&cfg, dense_combine_kernel<true>, p, groups)
+                    : cudaLaunchKernelEx(&cfg, dense_combine_kernel<false>, p, groups);
 }
 
 }  // namespace gqa

@@ -157,15 +157,16 @@ def test_no_groups_is_the_paged_decode(gpu_lib):
     verify(c, 0.125, want, tc=False)
 
 
-@pytest.mark.parametrize("Hkv,alone", [(1, 400), (2, 900)])
-def test_many_groups_and_sequences(gpu_lib, Hkv, alone):
+@pytest.mark.parametrize("H,Hkv,alone", [(2, 1, 400), (2, 2, 900), (10, 2, 500)])
+def test_many_groups_and_sequences(gpu_lib, H, Hkv, alone):
     """More groups than the planner keeps in shared memory, more sequences than its threads,
-    of which it takes 256 or 1024."""
+    of which it takes 256 or 1024; rows enough that the parts of one are joined by one thread
+    a column (the last)."""
     g = gpu_lib
     n = 150
     members = [(i % 4) * 3 for i in range(n)]
     B = sum(members)
-    c = case(members, [i % 5 for i in range(n)], [1 + (i * 7) % 40 for i in range(B)] + [3] * alone, 2, Hkv, 64, 64, bs=8,
+    c = case(members, [i % 5 for i in range(n)], [1 + (i * 7) % 40 for i in range(B)] + [3] * alone, H, Hkv, 64, 64, bs=8,
              alone=alone, seed=9)
     out = run(g, c, 0.125)
     assert g.attn_get_device_error() == g.OK
