@@ -83,6 +83,10 @@ constexpr int kSmemBudget = 74 * 1024;  // shared memory per CTA (three CTAs per
 constexpr int kSmemPerSM = 228 * 1024;  // shared memory of one SM
 constexpr int kSmemPerCTAReserved = 1024;
 constexpr float kRescaleLog2 = 8.0f;
+// The reference max before any score. Finite, so that a score of -infinity weighs
+// 2^(-inf - m) = 0 and not 2^(-inf + inf); any other score moves it. A row group that has seen
+// no other has l = 0, o = 0, and what 2^(m - M) weighs them with is 0 or 1.
+constexpr float kLowestMax = -3.402823466e+38f;
 
 constexpr int cmin(int a, int b) { return a < b ? a : b; }
 constexpr int cmax(int a, int b) { return a > b ? a : b; }
@@ -511,14 +515,11 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
   float* qw = qbuf + warp * NV * DK;
   // output accumulators (all heads, this lane's chunks) and the owned head's state
   float2 o2[NV][H2V];
-  float m_ref = -INFINITY, l_sum = 0.f;
+  float m_ref = kLowestMax, l_sum = 0.f;
   int lim_own = 0;    // keys < lim_own are causal for the owned head's row
   int lo_own = 0;     // ... and keys >= lo_own inside its window
   int lo_unit = 0;    // first key the unit reads; rows below it in its first tile may hold anything
   float slope2 = 0.f; // the owned head's ALiBi slope in the log2 domain
-  // Without a causal rule a NaN among a row's scores goes through to its output: a row
-  // group is empty when its sum is zero, not when its reference max is still -infinity
-  // (which a row of NaN alone leaves it at).
   const float cap_k = ARMS && p.softcap2 > 0.f ? 2.8853900817779268f / p.softcap2 : 0.f;  // 2 log2(e) / cap
   int merges = 0;
   for (int gt = 0;; ++gt) {
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
           }
         }
       }
-      m_ref = -INFINITY;
+      m_ref = kLowestMax;
       l_sum = 0.f;
       __syncwarp();
     }
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
         const bool grow = mx > m_ref + kRescaleLog2;
         float f = 1.f;
         if (grow) {
-          f = ex2(m_ref - mx);  // 0 while m_ref = -inf
+          f = ex2(m_ref - mx);  // 0 at the first score
           l_sum *= f;
           m_ref = mx;
         }
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
       float M = mg;
 #pragma unroll
       for (int off = L; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      const float w = (FULL ? lg == 0.f : mg == -INFINITY) ? 0.f : ex2(mg - M);
+      const float w = ex2(mg - M);
       float lsum = w * lg;
 #pragma unroll
       for (int off = L; off < 32; off <<= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
@@ -720,21 +721,21 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<ET, DK, DV, DROT, NV>::M
       float M = -INFINITY;
       for (int g = 0; g < kRowsWarps; ++g) M = fmaxf(M, mm[g * NV + vh]);
       float ls = 0.f, os = 0.f;
-      if (M != -INFINITY || FULL) {
+      if (FULL || M != kLowestMax) {  // (with a causal rule a split without a score counts for nothing)
         for (int g = 0; g < kRowsWarps; ++g) {
-          const float mg = mm[g * NV + vh];
-          const float wg = (FULL ? ml[g * NV + vh] == 0.f : mg == -INFINITY) ? 0.f : ex2(mg - M);
+          const float wg = ex2(mm[g * NV + vh] - M);
           ls = fmaf(wg, ml[g * NV + vh], ls);
           os = fmaf(wg, mo[(g * NV + vh) * DV + d], os);
         }
       }
       const size_t row = unit_out_row(p, u, vh);
       if (u.nsplit == 1) {
+        // (without a causal rule a NaN among a row's scores goes through to its output)
         float res = (FULL ? ls != 0.f : ls > 0.f) ? os / ls : 0.f;
         if (ARMS && p.sinks) {  // the sink logit joins the denominator (once per row and head)
           const float z2 = __ldg(p.sinks + u.kvh * p.G + u.hc * p.GH + vh % p.GH) * kLog2e;
           const float Mx = fmaxf(M, z2);
-          const float a = M == -INFINITY ? 0.f : ex2(M - Mx);
+          const float a = ex2(M - Mx);
           const float den = fmaf(ls, a, ex2(z2 - Mx));
           res = den > 0.f ? os * a / den : 0.f;
         }
