@@ -89,7 +89,7 @@ struct HalfBars {
   uint64_t k_full[kDenseStagesMax], k_empty[kDenseStagesMax], v_full[kDenseStagesMax], v_empty[kDenseStagesMax];
   uint64_t s_full, s_free, p_half, p_full, o_done;  // a phase per tile
   uint64_t mma_final;
-  uint64_t out_turn;  // the four softmax warps have come to an output tile
+  uint64_t out_turn;  // the four softmax warps have come to a step of an output tile
   DenseUnit unit[2];  // n_i = 0: no more units
 };
 struct DenseBars {
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2 qs2 = make_float2(qs, qs);
     bool alive = wg < C::kHalves;
     int t_all = 0;  // tiles so far: the phase of every barrier of the tile loop
-    int turn = 0;   // output tiles so far
+    int turn = 0;   // steps of output tiles so far: the phase of out_turn
     for (int n = 0; alive; ++n) {
       const int us = n & 1;
       if (!warp_wait_tc(&hb.q_full[us], (n >> 1) & 1, bars, p.err)) break;
@@ -684,48 +684,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tile held the load/store unit for 8,000 cycles, the other half's barriers with it
         const float inv = some ? 1.f / l_run : 0.f;
         unsigned char* so = smem + C::kOffOut + wg * kBlk;
+        // Two steps for each 64 columns: the rows into the buffer once the last store has read it,
+        // the store once all rows are there. The warps meet before each on an mbarrier, whose wait
+        // has a bound: a warp that gave up does not come, and a hardware barrier would wait for it
+        // without end. (8 x 1,024 rows: 279 us, with hardware barriers 276; with an mbarrier for each
+        // step, so that only the storing warp waits before the store, 284: a second wait in the code.)
 #pragma unroll 1
-        for (int cb = 0; cb < C::kCBV; ++cb) {
-          if ((threadIdx.x & 127) == 0) tc::bulk_wait_group_read0();  // the last store has read the buffer
-          if (cb > 0) {
-            named_bar_sync(1 + wg, 128);
-          } else {
-            // The first meeting has a bound: a warp that gave up does not come. From there on
-            // all four go through to the end of the tile, so a hardware barrier will do.
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&hb.out_turn);
-            if (!__all_sync(0xffffffffu, mbar_wait(&hb.out_turn, turn & 1))) {
-              if (lane == 0) {
-                *reinterpret_cast<volatile int*>(&bars->abort_flag) = 1;
-                raise_error(p.err, kErrTimeout);
-              }
-              alive = false;
-              break;
-            }
-            ++turn;
+        for (int x = 0; x < 2 * C::kCBV; ++x, ++turn) {
+          const int cb = x >> 1;
+          if (!(x & 1) && (threadIdx.x & 127) == 0) tc::bulk_wait_group_read0();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&hb.out_turn);
+          if (!warp_wait_tc(&hb.out_turn, turn & 1, bars, p.err)) {
+            alive = false;
+            break;
           }
-          if (warp_live) {
+          if (!(x & 1)) {
+            if (warp_live) {
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              uint32_t o[32];
-              tc::tmem_ld_32x32b_x32(tO + cb * 64 + hf * 32, o);
-              tc::tmem_ld_wait();
+              for (int hf = 0; hf < 2; ++hf) {
+                uint32_t o[32];
+                tc::tmem_ld_32x32b_x32(tO + cb * 64 + hf * 32, o);
+                tc::tmem_ld_wait();
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                uint32_t w4[4];
+                for (int t = 0; t < 4; ++t) {
+                  uint32_t w4[4];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                  const float x0 = __uint_as_float(o[t * 8 + 2 * v]) * inv, x1 = __uint_as_float(o[t * 8 + 2 * v + 1]) * inv;
-                  w4[v] = some ? pack_bf16(x0, x1) : 0u;
+                  for (int v = 0; v < 4; ++v) {
+                    const float x0 = __uint_as_float(o[t * 8 + 2 * v]) * inv, x1 = __uint_as_float(o[t * 8 + 2 * v + 1]) * inv;
+                    w4[v] = some ? pack_bf16(x0, x1) : 0u;
+                  }
+                  *reinterpret_cast<uint4*>(so + r * 128 + (((hf * 4 + t) ^ (r & 7)) * 16)) =
+                      make_uint4(w4[0], w4[1], w4[2], w4[3]);
                 }
-                *reinterpret_cast<uint4*>(so + r * 128 + (((hf * 4 + t) ^ (r & 7)) * 16)) =
-                    make_uint4(w4[0], w4[1], w4[2], w4[3]);
               }
             }
-          }
-          tc::fence_async_smem();
-          named_bar_sync(1 + wg, 128);
-          if ((threadIdx.x & 127) == 0) {
+            tc::fence_async_smem();
+          } else if ((threadIdx.x & 127) == 0) {
             // rows past the end of the sequence fall outside the tensor and are not written
             tc::tma_store_4d(&tm_o, so, cb * 64, u.head0, u.i0, u.batch_or_own);
             tc::bulk_commit_group();
