@@ -399,9 +399,10 @@ gqa_status attn_decode_shared_prefix(const void* q, const void* k_pool, const vo
                                 block_size, H, Hkv, d_k, d_v, attention_scale, dt, workspace, workspace_bytes, arms,
                                 stream);
   const SharedLayout s = shared_layout(B, H, Hkv, d_v, capacity, n_groups);
-  // offsets of partial results are 32-bit counts of 16 bytes, units 32-bit
+  // offsets of partial results are 32-bit counts of 16 bytes; units, and the key tiles of all
+  // sequences (two ranges each), are counted in 32 bits
   if ((s.bytes - s.partial) / 16 > (size_t)INT_MAX || (s.own - s.partial) % 16 ||
-      (long long)B * H > INT_MAX / 2)
+      (long long)B * H > INT_MAX / 2 || (long long)B * (capacity / 128 + 2) > INT_MAX)
     return GQA_ERR_INVALID_ARG;
   unsigned* err = error_word();
   if (!err) return GQA_ERR_CUDA;

@@ -21,6 +21,8 @@
 // last step, so most of its time is the fetch of its own: it is kept short (one copy of
 // each step, no unrolled loops, no 64-bit divisions), and up to kPlanGroups groups stay in
 // shared memory.
+#include <climits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -29,7 +31,10 @@ namespace {
 
 constexpr int kPlanGroups = 128;
 constexpr int kBuckets = 64;
-constexpr int kMostTiles = 1 << 20;  // candidates for c
+// Candidates for c: all lengths up to the longest range's, so that the last one, a single key
+// range for each row tile, is among them however long the tables are.
+constexpr int kMostTiles = 1 << 23;
+static_assert((long long)kMostTiles * 128 >= INT_MAX / 2, "a table row names up to INT_MAX / 2 keys");
 
 // Exclusive prefix sums of three values over the CTA; `total` receives the sums. Ends with
 // a barrier.
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
   const int own_tiles = block_sum<kWarps>(mine, warp_sums[0]);  // of each head chunk
   const float own_all = (float)own_tiles * (float)heads, own_items = (float)s.B * (float)heads;
   const int c_own_least = (int)ceilf(own_all / (float)kOwnExtra);  // own parts <= 2 items + kOwnExtra
-  const int c_most = min(max_tiles, kMostTiles);
+  const int c_most = max_tiles;
   unsigned long long best = ~0ull;
 #pragma unroll 1
   for (int c = 1 + tid; c <= c_most; c += kThreads) {
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const __grid_cons
   best = warp_min(warp_best[tid & (kWarps - 1)]);
   // (the largest c always fits: the caller sized max_prefix_units for it)
   const int c = best == ~0ull ? c_most : kMostTiles - (int)(best & 0xffffffffu);
-  const int c_own = max(max(c, c_own_least), 1);
+  const int c_own = min(max(c, c_own_least), max_tiles);  // (the longest range in one part)
   // ---- key ranges per group; own parts: of c_own tiles, the last of a range shorter (rest tiles)
   const int per = (s.n_groups + kThreads - 1) / kThreads;
   const int lo = min(n_groups, tid * per), hi = min(n_groups, lo + per);

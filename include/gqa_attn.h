@@ -227,7 +227,8 @@ gqa_status attn_prefill_paged_ex(const void* q, const void* k_pool, const void* 
  * bf16 with (d_k, d_v) = (64, 64), (128, 128) or (192, 128), block_size a multiple of
  * 8 dividing 128 and attention_scale > 0 runs on the tcgen05 tensor-core kernel, prefixes
  * and the sequences' own rows (the probabilities rounded to bf16 for the product with V);
- * every other case reads every history whole, as attn_decode_paged does. How a prefix
+ * every other case reads every history whole, as attn_decode_paged does (the groups are
+ * not looked at). B * (max_blocks_per_seq * block_size / 128 + 2) is at most INT_MAX. How a prefix
  * is split depends on the batch, so the last bits of a sequence's result do too;
  * repeated calls give the same bits.
  * workspace: at least attn_decode_shared_prefix_workspace_bytes(B, H, Hkv, d_v,
