@@ -449,7 +449,8 @@ def attn_cross_workspace_bytes(B, seq_q, seq_kv_max, H, Hkv, d_k, d_v, dtype=tor
 
 
 def cross_workspace(B, seq_q, H, Hkv, d_k, d_v, seq_kv_max, dtype=torch.bfloat16, device="cuda"):
-    """A workspace tensor of the size attn_cross needs (None when none)."""
+    """A workspace tensor of the size attn_cross needs (None when none); it does for any smaller B and
+    seq_kv_max too, not for another seq_q."""
     n = attn_cross_workspace_bytes(B, seq_q, seq_kv_max, H, Hkv, d_k, d_v, dtype)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 

@@ -495,6 +495,7 @@ struct CrossPlan {
   long long units;
   int simt_GH, simt_QR, split_rows, max_splits;
   size_t bytes;
+  size_t bound;  // of the bytes of every smaller B and every shorter L: fewer items make more splits
 };
 
 // Rows of a KV head (query rows times heads of its group) from which the tensor cores
@@ -531,7 +532,10 @@ bool cross_plan(int B, int S, int L, int H, int Hkv, int d_k, int d_v, int bf16,
       }
     }
     c->units = tiles * c->n_splits;
-    c->bytes = c->n_splits > 1 ? (size_t)c->units * gqa::dense_part_floats(128, d_v) * 4 : 0;
+    const size_t part = gqa::dense_part_floats(128, d_v) * 4;
+    c->bytes = c->n_splits > 1 ? (size_t)c->units * part : 0;
+    // more ranges than one leave at most 4 * slots units (the loop's condition, from one sequence on)
+    if (nt > 1 && tiles / B * 2 <= 4 * slots) c->bound = (size_t)(tiles * nt < 4 * slots ? tiles * nt : 4 * slots) * part;
     return true;
   }
   const int nvmax = gqa::rows_max_nv(bf16, d_k, d_v, 0);
@@ -547,14 +551,20 @@ bool cross_plan(int B, int S, int L, int H, int Hkv, int d_k, int d_v, int bf16,
     // items of up to 1500 keys 51.6 us whole, 42.2 / 40.9 / 43.2 us in splits of 1024 / 512 /
     // 256; 16 items of 4000 keys 40.2, 24.9, 17.4, 15.1 us.
     const long long items = (long long)B * Hkv * (G / c->simt_GH);
+    const auto few = [](int r) { return r > 512 ? 3 * 1024 : r > gqa::kLeastSplitRows ? 2 * gqa::kDenseSms : 0; };
+    const auto bytes_of = [&](size_t units) { return gqa::plan_bytes(units) + units * (size_t)(d_v + 2) * 4; };
     int r = gqa::kSplitRows;
-    while ((r > 512 && items * ceil_div(L, r) < 3 * 1024) || (r > 256 && items * ceil_div(L, r) < 2 * gqa::kDenseSms))
-      r /= 2;
+    while (items * ceil_div(L, r) < few(r)) r /= 2;
     c->max_splits = ceil_div(L, r);
     if (c->max_splits > 1) {
       c->split_rows = r;
-      const size_t units = (size_t)B * (size_t)H * (size_t)c->max_splits;
-      c->bytes = gqa::plan_bytes(units) + units * (size_t)(d_v + 2) * 4;
+      c->bytes = bytes_of((size_t)B * (size_t)H * (size_t)c->max_splits);
+    }
+    // splits of r rows are taken where those of 2r were fewer than few(2r), so they are fewer than twice that
+    for (r = gqa::kSplitRows; r >= gqa::kLeastSplitRows; r /= 2) {
+      const long long all = items * ceil_div(L, r), most = r == gqa::kSplitRows ? all : 2 * few(2 * r);
+      const size_t n = bytes_of((size_t)(all < most ? all : most) * c->simt_GH);
+      if (ceil_div(L, r) > 1 && n > c->bound) c->bound = n;
     }
   }
   return true;
@@ -569,7 +579,7 @@ size_t attn_cross_workspace_bytes(int B, int seq_q, int seq_kv_max, int H, int H
   size_t n = 0;
   for (int scale_ok = 0; scale_ok < 2; ++scale_ok) {  // (a scale that is not positive takes the SIMT kernel)
     CrossPlan c;
-    if (cross_plan(B, seq_q, seq_kv_max, H, Hkv, d_k, d_v, bf16, scale_ok, &c) && c.bytes > n) n = c.bytes;
+    if (cross_plan(B, seq_q, seq_kv_max, H, Hkv, d_k, d_v, bf16, scale_ok, &c) && c.bound > n) n = c.bound;
   }
   return n;
 }

@@ -16,6 +16,7 @@ enum : unsigned { kErrBounds = 1u, kErrTimeout = 2u };
 // fixed number independent of the layout and of the rest of the batch, so the
 // paged and contiguous decodes of one history do identical arithmetic.
 constexpr int kSplitRows = 2048;
+constexpr int kLeastSplitRows = 256;  // the shortest split that attn_cross takes
 
 // Parameters of the SIMT attention kernel (decode, and prefill shapes that the
 // tensor-core kernel does not take). All pointers are device pointers.

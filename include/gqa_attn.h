@@ -258,7 +258,9 @@ size_t attn_decode_shared_prefix_workspace_bytes(int B, int H, int Hkv, int d_v,
  * seq_q * H / Hkv >= 2 runs on the tcgen05 tensor-core kernel (the probabilities
  * rounded to bf16 for the product with V), everything else on the SIMT kernel.
  * workspace: at least attn_cross_workspace_bytes(..) bytes, 16-byte aligned (NULL
- * allowed when that is 0); calls whose kernels may overlap must not share one.
+ * allowed when that is 0); calls whose kernels may overlap must not share one. The size
+ * does for the same arguments with any smaller B and seq_kv_max too; another seq_q or
+ * other heads and widths have a size of their own, which may be larger.
  */
 gqa_status attn_cross(const void* q, const void* k, const void* v, const int32_t* kv_lens, void* out, int B, int seq_q,
                       int seq_kv_max, int H, int Hkv, int d_k, int d_v, float attention_scale, gqa_dtype dt,
