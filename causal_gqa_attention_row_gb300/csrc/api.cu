@@ -415,7 +415,6 @@ gqa_status attn_decode_shared_prefix(const void* q, const void* k_pool, const vo
   plan.shared_blocks = shared_blocks;
   plan.B = B;
   plan.Hkv = Hkv;
-  plan.G = H / Hkv;
   plan.capacity = capacity;
   plan.bs = block_size;
   plan.mbps = max_blocks_per_seq;
@@ -440,7 +439,7 @@ gqa_status attn_decode_shared_prefix(const void* q, const void* k_pool, const vo
   gqa::DenseParams d{};
   d.H = H;
   d.Hkv = Hkv;
-  d.G = plan.G;
+  d.G = H / Hkv;
   d.GH = s.GH;
   d.RPT = s.RPT;
   d.n_hchunks = s.n_hchunks;
@@ -768,8 +767,6 @@ gqa_status gqa_rope_frequencies(float* freqs_host, float* magnitude, int rot_dim
   return GQA_OK;
 }
 
-// The checks that attn_qk_norm_rope and kv_append_paged_rows share, and the norm
-// and the rotation into the kernel's parameters.
 // A call's view of a tensor of B sequences (0: no batch axis), T tokens, heads heads:
 // an axis of one element has no stride.
 static gqa::HeadsView heads_view(const gqa_heads* x, int B, int T, int heads) {
@@ -788,6 +785,8 @@ static bool in_place_ok(const gqa::HeadsView& x, const gqa::HeadsView& y) {
          (x.batch_stride == y.batch_stride && x.token_stride == y.token_stride && x.head_stride == y.head_stride);
 }
 
+// The checks that attn_qk_norm_rope and kv_append_paged_rows share, and the norm
+// and the rotation into the kernel's parameters.
 static gqa_status qk_norm_and_rope(gqa::QkParams& p, const void* q_weight, const void* k_weight, float eps,
                                    const gqa_rope* rope, int d) {
   if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight))) return GQA_ERR_INVALID_ARG;

@@ -61,12 +61,14 @@
 // and on the tiles a unit streams; a sink logit joins the softmax denominator
 // in the final merge (single split) or in the combine kernel.
 //
-// Determinism: split boundaries are multiples of kSplitRows, tiles multiples of
-// T rows from the split start, and the row -> row-group assignment a function of
-// the key index only. The arithmetic on a key row therefore does not depend on
-// where the row lives (contiguous or paged), on the block table, on the other
-// sequences of the batch or on which CTA takes the unit: paged and contiguous
-// results are bit-identical, and so are repeated calls.
+// Determinism: the decodes' split boundaries are multiples of kSplitRows, tiles
+// multiples of T rows from the split start, and the row -> row-group assignment a
+// function of the key index only. The arithmetic on a key row therefore does not
+// depend on where the row lives (contiguous or paged), on the block table, on the
+// other sequences of the batch or on which CTA takes the unit: paged and contiguous
+// results are bit-identical, and so are repeated calls. (attn_cross takes splits of
+// kLeastSplitRows rows or more, doubled up to kSplitRows with the number of items: the
+// last bits of its results depend on the batch's size, and repeat too.)
 #pragma once
 
 #include <atomic>
@@ -133,7 +135,8 @@ struct RowsCfg {
   static_assert(KCH % L == 0 && VCH % L == 0 && NCH % L == 0, "chunks must split evenly over a row group");
   static_assert(32 % L == 0, "row groups must tile a warp");
   static_assert(NV <= L, "a row group needs at least one lane per virtual head");
-  static_assert(kSplitRows % T == 0, "split boundaries must fall on tile boundaries");
+  static_assert(kLeastSplitRows % T == 0 && kSplitRows % kLeastSplitRows == 0,
+                "split boundaries must fall on tile boundaries");
   static_assert(sizeof(RowsHeader) <= kHeader, "the header must fit its reserved space");
 };
 

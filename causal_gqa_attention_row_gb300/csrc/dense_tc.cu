@@ -26,8 +26,9 @@
 // half, so that a list shorter than the slots spreads over the SMs first). While one half
 // is in its softmax the other's products run. The producer runs ahead into the next unit
 // as stages come free, so a unit costs its tiles plus one epilogue, not a launch, a set-up
-// and a first load. Units of unequal length (the shared prefixes) are drawn from a ticket
-// counter; those of attn_cross are alike and go round by slot.
+// and a first load. The shared prefixes' units are drawn from a ticket counter; those of
+// attn_cross go round by slot: alike but for lengths on the device, which shorten a sequence's
+// last unit and leave those behind it empty.
 //
 // Measured at 32 heads on 8 KV heads of 128, plan and combine included: 64 sequences behind
 // a prefix of 8,192 keys with up to 512 of their own 43 us; 256 sequences behind four prefixes

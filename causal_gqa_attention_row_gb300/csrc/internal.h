@@ -12,11 +12,12 @@ namespace gqa {
 // Bits of the device error word.
 enum : unsigned { kErrBounds = 1u, kErrTimeout = 2u };
 
-// Rows of one split-K work item. Split boundaries are multiples of this, a
-// fixed number independent of the layout and of the rest of the batch, so the
+// Rows of one split-K work item of the decodes. Their split boundaries are multiples of
+// this, a fixed number independent of the layout and of the rest of the batch, so the
 // paged and contiguous decodes of one history do identical arithmetic.
 constexpr int kSplitRows = 2048;
-constexpr int kLeastSplitRows = 256;  // the shortest split that attn_cross takes
+// The shortest split that attn_cross takes (from there up to kSplitRows by powers of two).
+constexpr int kLeastSplitRows = 256;
 
 // Parameters of the SIMT attention kernel (decode, and prefill shapes that the
 // tensor-core kernel does not take). All pointers are device pointers.
@@ -40,7 +41,7 @@ struct RowsParams {
   int max_len;              // contiguous rows per (b, kvh); 0 when paged
   int capacity;             // largest valid key count of one sequence
   int mbps, bs, num_blocks; // paged
-  int split_rows;           // rows per split (kSplitRows, or >= capacity for no split)
+  int split_rows;           // rows per split (kLeastSplitRows .. kSplitRows, or >= capacity for no split)
   int max_splits;
   float qscale;             // attention_scale * log2(e)
   int debug_withhold;       // test hook: withhold the first tile of every CTA
@@ -254,7 +255,7 @@ struct SharedPlan {
   const int32_t* seq_lens;
   const int32_t* group_starts;   // [n_groups + 1]
   const int32_t* shared_blocks;  // [n_groups]
-  int B, Hkv, G, capacity, bs, mbps, window, dv;
+  int B, Hkv, capacity, bs, mbps, window, dv;
   int n_groups, max_prefix_units, slots;
   int GH, RPT, n_hchunks, own_rows;
   int own_part_at;               // where the own parts begin, in 16-byte steps from the partial results

@@ -568,6 +568,8 @@ const char* gqa_status_string(gqa_status status);
  *   - the SIMT attention kernel (decode; SIMT prefill): the first K/V tile of
  *     every CTA;
  *   - the tensor-core prefill: the first K tile of every CTA;
+ *   - the tensor-core kernel of attn_cross and attn_decode_shared_prefix: the first K
+ *     tile of each of a CTA's halves;
  *   - the absorbed MLA decode: the first cache tile of the second CTA of every
  *     pair, so the first CTA also gives up waiting for its peer's tile maxima;
  *     both let what they sent each other land before releasing their memory.
