@@ -31,10 +31,11 @@
 // last unit and leave those behind it empty.
 //
 // Measured at 32 heads on 8 KV heads of 128, plan and combine included: 64 sequences behind
-// a prefix of 8,192 keys with up to 512 of their own 43 us; 256 sequences behind four prefixes
-// of 16,384 keys with up to 1,024 of their own 173 us (4.7 TB/s of rows read once, 0.69 of the
-// copy bandwidth); attn_cross of 8 x 1,024 rows on 2,048 to 4,096 keys 303 us (1.36 PFLOP/s, 0.71
-// of the measured bf16 rate). What bounds them is a half's time from tile to tile, of 1,024 cycles
+// a prefix of 8,192 keys with up to 512 of their own 42 us; 256 sequences behind four prefixes
+// of 16,384 keys with up to 1,024 of their own 170 us (4.7 TB/s of rows read once, 0.70 of the
+// copy bandwidth); attn_cross of 8 x 1,024 rows on 2,048 to 4,096 keys (364 GFLOP) 282 us in a burst
+// at 2,070 MHz (1.29 PFLOP/s, 0.68 of the measured bf16 rate), 292 us after seconds at the power
+// cap (1,390 W, 1,980 MHz). What bounds them is a half's time from tile to tile, of 1,024 cycles
 // of products: in the last case about 3,200 cycles, S, softmax and PV of a half one after
 // another; in the second a third more, for K and V that come from HBM through one stage each.
 //

@@ -27,8 +27,9 @@
 // factors are formed once; many tokens of few rows: up to eight tokens a warp, side by
 // side (dispatch_qk).
 //
-// Measured (bf16, 32 + 8 heads of 128): 16384 tokens 64.4 us (5.2 TB/s of rows read and
-// written, 0.77 of the copy bandwidth), four 2048-row chunks appended 40.1 us (5.0 TB/s).
+// Measured (32 + 8 heads of 128): 16384 tokens 63.9 us (5.3 TB/s of rows read and written,
+// 0.78 of the copy bandwidth), four 2048-row chunks appended 37.5 us (5.4 TB/s); fp32 115.2
+// and 63.4 us (5.8 and 6.4 TB/s).
 // The first form (rows through registers, weights and rotation apart, a division per
 // address) took 82.5 and 76.1 us at twice the instructions and half the warps. Two rows a
 // round against one: 4.8 and 6.1 us for 2048 tokens of 14 + 2 heads of 64, alike for the
