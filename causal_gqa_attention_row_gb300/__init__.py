@@ -29,7 +29,7 @@ EXPORTS = ("attn_prefill_causal", "attn_decode_contig", "attn_decode_paged", "kv
            "attn_decode_mla_absorbed_workspace_bytes", "mla_unabsorb_out", "attn_decode_mla_absorbed_paged",
            "attn_rope_interleaved_qk", "gqa_rope_frequencies", "attn_qk_norm_rope", "kv_append_paged_rows",
            "attn_decode_shared_prefix", "attn_decode_shared_prefix_workspace_bytes", "attn_cross",
-           "attn_cross_workspace_bytes")
+           "attn_cross_workspace_bytes", "kv_plan_rows", "kv_append_slots", "kv_commit_rows")
 
 
 class GqaArms(ctypes.Structure):
@@ -106,6 +106,9 @@ def load(path: str = None):
         "gqa_rope_frequencies": [P, P, I, D, P],
         "attn_qk_norm_rope": [P, P, P, P, P, P, F, P, I, I, I, I, I, P, I, P],
         "kv_append_paged_rows": [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P, F, P, I, P],
+        "kv_plan_rows": [P] * 14 + [I] * 6 + [P],
+        "kv_append_slots": [P] * 8 + [I] * 7 + [P, P, F, P, I, P],
+        "kv_commit_rows": [P, P, I] + [P] * 6 + [I] * 8 + [I, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -562,6 +565,92 @@ def kv_append_paged_rows(q, k_new, v_new, q_out, k_pool, v_pool, block_tables, r
         _weight(q_weight, dk), _weight(k_weight, dk), float(eps), _ref(rope),
         _dtype(q, k_new, v_new, q_out, k_pool, v_pool, q_weight, k_weight), _stream(stream)), "kv_append_paged_rows")
     return q_out
+
+
+def _i64(t):
+    if t is not None and t.dtype != torch.int64:
+        raise TypeError("slots and tree masks must be int64")
+    return _p(t)
+
+
+def kv_plan_rows(seq_lens, new_rows, block_tables, blocks_in, blocks_out, free_list, free_in, free_out, row_starts, positions,
+                 slots, block_size, keep_blocks=None, parents=None, tree_mask=None, stream=None):
+    """The index arrays of a step that adds new_rows[b] rows to the seq_lens[b] of sequence b (int32 [B]):
+    grows block_tables int32 [B, mbps] from free_list (int32 [num_blocks], a stack of free_in[0] blocks) and
+    gives back what is no longer needed; blocks_in / blocks_out int32 [B] are the entries in use before and
+    after (keep_blocks of them never given back), free_out int32 [2] the blocks free afterwards and those that
+    were wanting. Writes row_starts int32 [B + 1], positions int32 [N] and slots int64 [N] (-1: none). With
+    parents int32 [N] (-1: the history) positions go by depth, and tree_mask int64 [N, words] gets each row's
+    bits for itself and its ancestors. blocks_out and free_out may be blocks_in and free_in."""
+    B, mbps = block_tables.shape
+    N = positions.shape[0]
+    words = 0
+    if (parents is None) != (tree_mask is None):
+        raise ValueError("parents and tree_mask go together")
+    if parents is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != N or parents.numel() != N:
+            raise ValueError("parents must be [N] and tree_mask [N, words]")
+        words = tree_mask.shape[1]
+    if (any(x is not None and x.numel() != B for x in (seq_lens, new_rows, blocks_in, blocks_out, keep_blocks)) or
+            row_starts.numel() != B + 1 or slots.numel() != N or free_in.numel() < 1 or free_out.numel() != 2):
+        raise ValueError("the lengths, the blocks, row_starts, positions, slots and the list's counts do not agree")
+    _here(seq_lens, new_rows, block_tables, blocks_in, blocks_out, keep_blocks, free_list, free_in, free_out, row_starts,
+          positions, slots, parents, tree_mask)
+    _check(load().kv_plan_rows(
+        _i32(seq_lens), _i32(new_rows), _i32(block_tables), _i32(blocks_in), _i32(blocks_out), _i32(keep_blocks),
+        _i32(free_list), _i32(free_in), _i32(free_out), _i32(row_starts), _i32(positions), _i64(slots), _i32(parents),
+        _i64(tree_mask), words, N, B, mbps, free_list.numel(), int(block_size), _stream(stream)), "kv_plan_rows")
+
+
+def kv_append_slots(q, k_new, v_new, q_out, k_pool, v_pool, slots, positions=None, rope=None, q_weight=None, k_weight=None,
+                    eps=1e-6, stream=None):
+    """kv_append_paged_rows with each row's place given: row n is turned by positions[n] (int32 [N]) and its key
+    and value go to slot slots[n] = block * bs + row of the pools (int64 [N]; below 0: the row is left out)."""
+    N, Hkv, dk = k_new.shape
+    nb, _, bs, dv = v_pool.shape
+    H = 0
+    if v_new.shape != (N, Hkv, dv) or k_pool.shape != (nb, Hkv, bs, dk) or v_pool.shape[1] != Hkv:
+        raise ValueError("k_new, v_new and the pools do not agree")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        H = q.shape[1]
+        if q.shape != (N, H, dk) or q_out.shape != (N, H, dk):
+            raise ValueError("q and q_out must both be [N, H, dk]")
+    if slots.numel() != N or (positions is not None and positions.numel() != N):
+        raise ValueError("slots and positions must be [N]")
+    _here(q, k_new, v_new, q_out, k_pool, v_pool, slots, positions, q_weight, k_weight,
+          rope.table if rope is not None else None)
+    _writes_once(q_out)
+    _check(load().kv_append_slots(
+        _view(q, 3), _view(k_new, 3), _view(v_new, 3), _view(q_out, 3), _p(k_pool), _p(v_pool), _i64(slots),
+        _i32(positions), N, nb, bs, H, Hkv, dk, dv, _weight(q_weight, dk), _weight(k_weight, dk), float(eps), _ref(rope),
+        _dtype(q, k_new, v_new, q_out, k_pool, v_pool, q_weight, k_weight), _stream(stream)), "kv_append_slots")
+    return q_out
+
+
+def kv_commit_rows(k_pools, v_pools, block_tables, seq_lens_in, row_starts, path, n_path, seq_lens_out, stream=None):
+    """Moves row seq_lens_in[b] + path[b][j] to row seq_lens_in[b] + j, j < n_path[b], in every layer's pools
+    (k_pools, v_pools: a tensor [num_blocks, Hkv, bs, d] each layer; v_pools None: keys alone) and sets
+    seq_lens_out[b] = seq_lens_in[b] + n_path[b] (may be the same tensor). path int32 [B, max_path], ascending
+    indices among the row_starts[b + 1] - row_starts[b] drafted rows; n_path int32 [B]."""
+    k_pools, v_pools = list(k_pools), None if v_pools is None else list(v_pools)
+    B, mbps = block_tables.shape
+    if not k_pools or (v_pools is not None and len(v_pools) != len(k_pools)):
+        raise ValueError("a pool of keys, and with values one of those, for each layer")
+    nb, Hkv, bs, dk = k_pools[0].shape
+    dv = v_pools[0].shape[-1] if v_pools is not None else 0
+    if (any(x.shape != (nb, Hkv, bs, dk) for x in k_pools) or
+            any(x.shape != (nb, Hkv, bs, dv) for x in v_pools or ()) or path.dim() != 2 or path.shape[0] != B or
+            row_starts.numel() != B + 1 or any(x.numel() != B for x in (seq_lens_in, n_path, seq_lens_out))):
+        raise ValueError("the pools, the tables, the lengths and the paths do not agree")
+    _here(block_tables, seq_lens_in, row_starts, path, n_path, seq_lens_out, *k_pools, *(v_pools or ()))
+    dt = _dtype(*k_pools, *(v_pools or ()))
+    pointers = ctypes.c_void_p * len(k_pools)
+    _check(load().kv_commit_rows(
+        pointers(*[_p(x).value for x in k_pools]), None if v_pools is None else pointers(*[_p(x).value for x in v_pools]),
+        len(k_pools), _i32(block_tables), _i32(seq_lens_in), _i32(row_starts), _i32(path), _i32(n_path), _i32(seq_lens_out),
+        B, path.shape[1], mbps, nb, bs, Hkv, dk, dv, dt, _stream(stream)), "kv_commit_rows")
 
 
 def attn_get_device_error(stream=None):

@@ -894,6 +894,145 @@ gqa_status kv_append_paged_rows(const gqa_heads* q, const gqa_heads* k_new, cons
   return from_cuda(gqa::launch_qk_rows(p, bf16, 1, static_cast<cudaStream_t>(stream)));
 }
 
+// ---- a step that verifies drafted tokens ------------------------------------------
+static bool aligned_to(const void* p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+gqa_status kv_plan_rows(const int32_t* seq_lens, const int32_t* new_rows, int32_t* block_tables,
+                        const int32_t* blocks_in, int32_t* blocks_out, const int32_t* keep_blocks, int32_t* free_list,
+                        const int32_t* free_in, int32_t* free_out, int32_t* row_starts, int32_t* positions,
+                        int64_t* slots, const int32_t* parents, uint64_t* tree_mask, int mask_words, int N, int B,
+                        int max_blocks_per_seq, int num_blocks, int block_size, void* stream) {
+  if (N < 0 || B < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || block_size <= 0 ||
+      (long long)max_blocks_per_seq * block_size > INT_MAX / 2 || (long long)B * max_blocks_per_seq > INT_MAX)
+    return GQA_ERR_INVALID_ARG;
+  if ((parents == nullptr) != (tree_mask == nullptr) || (parents != nullptr) != (mask_words > 0)) return GQA_ERR_INVALID_ARG;
+  if (B > gqa::kPlanRowsMaxB) return GQA_ERR_UNSUPPORTED;
+  if (B == 0) return GQA_OK;
+  if (!seq_lens || !new_rows || !block_tables || !blocks_in || !blocks_out || !free_list || !free_in || !free_out ||
+      !row_starts || (N > 0 && (!positions || !slots)))
+    return GQA_ERR_INVALID_ARG;
+  if (!aligned_to(slots, 8) || !aligned_to(tree_mask, 8)) return GQA_ERR_INVALID_ARG;
+  const bool same = blocks_in == blocks_out;
+  if (!same && blocks_in < blocks_out + B && blocks_out < blocks_in + B) return GQA_ERR_INVALID_ARG;
+  if (free_in == free_out + 1) return GQA_ERR_INVALID_ARG;
+  gqa::PlanRows p{};
+  p.lens = seq_lens;
+  p.new_rows = new_rows;
+  p.keep = keep_blocks;
+  p.parents = parents;
+  p.tables = block_tables;
+  p.held_in = blocks_in;
+  p.held_out = blocks_out;
+  p.free_list = free_list;
+  p.free_in = free_in;
+  p.free_out = free_out;
+  p.row_starts = row_starts;
+  p.positions = positions;
+  p.slots = slots;
+  p.mask = reinterpret_cast<unsigned long long*>(tree_mask);
+  p.err = error_word();
+  if (!p.err) return GQA_ERR_CUDA;
+  p.N = N;
+  p.B = B;
+  p.words = mask_words;
+  p.mbps = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.bs = block_size;
+  return from_cuda(gqa::launch_plan_rows(p, static_cast<cudaStream_t>(stream)));
+}
+
+gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa_heads* v_new, const gqa_heads* q_out,
+                           void* k_pool, void* v_pool, const int64_t* slots, const int32_t* positions, int N,
+                           int num_blocks, int block_size, int H, int Hkv, int d_k, int d_v, const void* q_weight,
+                           const void* k_weight, float eps, const gqa_rope* rope, gqa_dtype dt, void* stream) {
+  const int bf16 = dtype_flag(dt);
+  if (bf16 < 0 || N < 0 || num_blocks <= 0 || block_size <= 0 || H < 0 || Hkv <= 0 || !width_ok(d_k) ||
+      !width_ok(d_v) || (long long)H + Hkv > INT_MAX / 2)
+    return GQA_ERR_INVALID_ARG;
+  if ((q == nullptr) != (H == 0) || (q == nullptr) != (q_out == nullptr)) return GQA_ERR_INVALID_ARG;
+  gqa::QkParams p{};
+  const gqa_status s = qk_norm_and_rope(p, q_weight, k_weight, eps, rope, d_k);
+  if (s != GQA_OK) return s;
+  if (N == 0) return GQA_OK;
+  if (!k_new || !v_new || !k_pool || !v_pool || !slots || (rope && !positions)) return GQA_ERR_INVALID_ARG;
+  p.q = heads_view(q, 0, N, H);
+  p.q_out = heads_view(q_out, 0, N, H);
+  p.k = heads_view(k_new, 0, N, Hkv);
+  p.v = heads_view(v_new, 0, N, Hkv);
+  if (!heads_view_ok(p.k, bf16) || !heads_view_ok(p.v, bf16) ||
+      (q && (!heads_view_ok(p.q, bf16) || !heads_view_ok(p.q_out, bf16) || !in_place_ok(p.q, p.q_out))))
+    return GQA_ERR_INVALID_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned_to(slots, 8)) return GQA_ERR_INVALID_ARG;
+  p.k_out.data = k_pool;
+  p.v_pool = v_pool;
+  p.slots = slots;
+  p.positions = positions;
+  p.err = error_word();
+  if (!p.err) return GQA_ERR_CUDA;
+  p.N = N;
+  p.H = H;
+  p.Hk = p.Hkv = Hkv;
+  p.dv = d_v;
+  p.bs = block_size;
+  p.num_blocks = num_blocks;
+  p.run_rows = 1;
+  return from_cuda(gqa::launch_qk_rows(p, bf16, 1, static_cast<cudaStream_t>(stream)));
+}
+
+gqa_status kv_commit_rows(void* const* k_pools, void* const* v_pools, int n_layers, const int32_t* block_tables,
+                          const int32_t* seq_lens_in, const int32_t* row_starts, const int32_t* path,
+                          const int32_t* n_path, int32_t* seq_lens_out, int B, int max_path, int max_blocks_per_seq,
+                          int num_blocks, int block_size, int Hkv, int d_k, int d_v, gqa_dtype dt, void* stream) {
+  const int bf16 = dtype_flag(dt);
+  const auto width = [](int d) { return d > 0 && d % 8 == 0 && d <= 1024; };
+  if (bf16 < 0 || n_layers <= 0 || n_layers > INT_MAX / 2 || B < 0 || max_path < 0 || max_blocks_per_seq <= 0 ||
+      num_blocks <= 0 || block_size <= 0 || Hkv <= 0 || !width(d_k) || (v_pools && !width(d_v)) ||
+      (long long)Hkv * (d_k > d_v ? d_k : d_v) > INT_MAX / 8)
+    return GQA_ERR_INVALID_ARG;
+  if ((long long)max_blocks_per_seq * block_size > INT_MAX / 2) return GQA_ERR_INVALID_ARG;
+  if (B == 0) return GQA_OK;
+  if (!k_pools || !block_tables || !seq_lens_in || !row_starts || (max_path > 0 && !path) || !n_path || !seq_lens_out)
+    return GQA_ERR_INVALID_ARG;
+  for (int i = 0; i < n_layers; ++i)
+    if (!k_pools[i] || !aligned16(k_pools[i]) || (v_pools && (!v_pools[i] || !aligned16(v_pools[i]))))
+      return GQA_ERR_INVALID_ARG;
+  const bool same = seq_lens_in == seq_lens_out;
+  if (!same && seq_lens_in < seq_lens_out + B && seq_lens_out < seq_lens_in + B) return GQA_ERR_INVALID_ARG;
+  gqa::CommitRows p{};
+  p.tables = block_tables;
+  p.lens_in = seq_lens_in;
+  p.row_starts = row_starts;
+  p.path = path;
+  p.n_path = n_path;
+  p.lens_out = seq_lens_out;
+  p.err = error_word();
+  if (!p.err) return GQA_ERR_CUDA;
+  p.B = B;
+  p.max_path = max_path;
+  p.mbps = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.bs = block_size;
+  p.Hkv = Hkv;
+  p.k_bytes = d_k * (bf16 ? 2 : 4);
+  p.v_bytes = d_v * (bf16 ? 2 : 4);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // the lengths are read by every layer's CTAs: written with the first layers only to another array
+  p.lens_later = same;
+  for (int l0 = 0; l0 < n_layers; l0 += gqa::kCommitLayers) {
+    p.n_layers = n_layers - l0 < gqa::kCommitLayers ? n_layers - l0 : gqa::kCommitLayers;
+    for (int i = 0; i < p.n_layers; ++i) {
+      p.k_pools[i] = k_pools[l0 + i];
+      p.v_pools[i] = v_pools ? v_pools[l0 + i] : nullptr;
+    }
+    const cudaError_t e = gqa::launch_commit_rows(p, st);
+    if (e != cudaSuccess) return from_cuda(e);
+    p.lens_later = 1;
+  }
+  if (!same) return GQA_OK;
+  p.lens_only = 1;
+  return from_cuda(gqa::launch_commit_rows(p, st));
+}
+
 size_t attn_decode_mla_absorbed_workspace_bytes(int B, int H, int d_c, int max_len) {
   if (B <= 0 || H <= 0 || d_c <= 0 || max_len <= 0) return 0;
   const int chunk = gqa::mla_chunk_rows(B, H, max_len);

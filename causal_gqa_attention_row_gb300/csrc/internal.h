@@ -121,7 +121,7 @@ struct QkParams {
   void* v_pool;
   const void* q_weight;          // [d] of the element type, or NULL: no norm
   const void* k_weight;
-  const int32_t* positions;      // [B, T] (not PAGED)
+  const int32_t* positions;      // [B, T] (not PAGED), [N] with slots
   const float* freqs;            // [rot_dim / 2] float pairs (high, low part) of the frequencies
   const int32_t* tables;         // PAGED, from here on: as kv_append_paged_rows
   const int32_t* row_starts;
@@ -135,10 +135,48 @@ struct QkParams {
   float magnitude, eps;
   int parts, part_rows, first_part, lens_part;  // items per token, rows of one (set by the launcher)
   int mbps, bs, num_blocks;
+  const int64_t* slots;          // [N] pool slots (block * bs + row; below 0: none), instead of tables,
+                                 // row_starts and lengths; NULL: those
   int run_rows;                  // 0: only the lengths
   int lens_items;                // sequences whose length this launch advances (0 or B)
 };
 cudaError_t launch_qk_rows(const QkParams& p, int bf16, int paged, cudaStream_t st);
+
+// ---- a step's index arrays and accepted rows (plan_rows.cu, commit_rows.cu) ------
+// Parameters of kv_plan_rows (include/gqa_attn.h has the meaning of the arrays).
+struct PlanRows {
+  const int32_t *lens, *new_rows, *keep, *parents;
+  int32_t* tables;
+  const int32_t* held_in;
+  int32_t* held_out;
+  int32_t* free_list;
+  const int32_t* free_in;
+  int32_t *free_out, *row_starts, *positions;
+  int64_t* slots;
+  unsigned long long* mask;
+  unsigned* err;
+  int N, B, words, mbps, num_blocks, bs;
+  // set by the launcher
+  int per;                              // sequences of a CTA
+  int write_rows, write_state, report;  // what this launch writes (see there)
+};
+// Sequences of a call: their prefix sums stay in shared memory.
+constexpr int kPlanRowsMaxB = 16384;
+cudaError_t launch_plan_rows(PlanRows p, cudaStream_t st);
+
+// Parameters of kv_commit_rows, of up to kCommitLayers layers a launch.
+constexpr int kCommitLayers = 64;
+struct CommitRows {
+  void* k_pools[kCommitLayers];
+  void* v_pools[kCommitLayers];  // NULL: none
+  const int32_t *tables, *lens_in, *row_starts, *path, *n_path;
+  int32_t* lens_out;
+  unsigned* err;
+  int n_layers, B, max_path, mbps, num_blocks, bs, Hkv;
+  int k_bytes, v_bytes;          // of a row
+  int lens_only, lens_later;     // this launch writes the lengths alone; another launch does
+};
+cudaError_t launch_commit_rows(const CommitRows& p, cudaStream_t st);
 
 // The arms for the tensor-core prefill: window (<= 0: none), softcap * log2 e
 // (0: none), sink logits and ALiBi slopes ([H] fp32 on the device, natural

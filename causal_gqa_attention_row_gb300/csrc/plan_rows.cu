@@ -1,0 +1,326 @@
+// plan_rows.cu -- the index arrays of a step, from the requests' lengths: block tables that grow
+// from a list of free blocks and give back what they no longer need, the packed rows' starts,
+// positions and slots, and the masks of drafted trees.
+//
+//   need_b = max(ceil((len_b + new_b) / bs), keep_b),  give_b = max(0, held_b - need_b),
+//   take_b = max(0, need_b - held_b),  R = sum give
+//   b is served where take_b = 0 or take_0 + .. + take_b <= free + R
+//   the list is a stack: the R blocks given back go onto it, sequence by sequence, entries
+//   ascending; the t-th block taken is the one at free + R - 1 - t
+//
+// What it reads and writes is small (20 bytes a sequence, 12 and more a row), so what bounds it is
+// latency: one launch, and in it one chain of loads (the lengths, the block, the store). So no
+// CTA waits for another: each scans all lengths for itself (a thread takes four
+// sequences, 1024 of them a round) and then writes what is its sequences' own. A block that is
+// given back and taken in one call is not read from the list, where another CTA would be
+// writing it, but found at its place in the table that gives it back, by a search over the
+// prefix sums of give_b, which stay in shared memory. The list below `free` is only read, above
+// it only written. Sequences go round by grid x; where a sequence has many rows they are cut into
+// slices by grid y. A row's ancestors are indices that descend, so a thread that walks up from
+// its row writes the words of the mask from the highest to the lowest and holds one at a time.
+
+#include <atomic>
+#include <climits>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace gqa {
+namespace {
+
+constexpr int kPlanRowsThreads = 256;
+constexpr int kPer = 4;                             // sequences of a thread in a round
+constexpr int kRound = kPlanRowsThreads * kPer;
+
+// What sequence b brings.
+struct Req {
+  int len, rows, held, need;  // rows: those that count for the starts; need: held where nothing moves
+  bool ok;                    // its numbers are in range
+};
+__device__ __forceinline__ Req request(const PlanRows& p, int b) {
+  Req r;
+  r.len = __ldg(p.lens + b);
+  const int n = __ldg(p.new_rows + b);
+  r.held = p.held_in[b];  // (may be the array that the state is written to)
+  const int keep = p.keep ? __ldg(p.keep + b) : 0;
+  const long long want = (long long)r.len + n;
+  r.rows = n > 0 && n <= p.N ? n : 0;
+  r.ok = r.len >= 0 && n >= 0 && n <= p.N && want <= (long long)p.mbps * p.bs && r.held >= 0 && r.held <= p.mbps &&
+         keep >= 0 && keep <= r.held;
+  r.need = r.ok ? max((int)((want + p.bs - 1) / p.bs), keep) : r.held;
+  return r;
+}
+
+// Exclusive prefix sums of three values over the CTA and their totals. Ends with a barrier.
+__device__ __forceinline__ void scan3(long long (&v)[3], long long (&total)[3], long long (*sums)[kPlanRowsThreads / 32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x[3] = {v[0], v[1], v[2]};
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const long long y = __shfl_up_sync(0xffffffffu, x[k], off);
+      if (lane >= off) x[k] += y;
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sums[k][warp] = x[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanRowsThreads / 32; ++w) {
+      const long long s = sums[k][w];
+      if (w < warp) before += s;
+      all += s;
+    }
+    v[k] = before + x[k] - v[k];
+    total[k] = all;
+  }
+  __syncthreads();
+}
+
+// The mask of row i and its depth: up from the row, an ancestor at a time.
+__device__ __forceinline__ int walk_up(const PlanRows& p, long long start, int i) {
+  unsigned long long* out = p.mask + (start + i) * p.words;
+  int at = i, word = p.words - 1, depth = 0;
+  unsigned long long bits = 0;
+  while (true) {
+    while (word > at / 64) {  // (nothing further in this word)
+      out[word--] = bits;
+      bits = 0;
+    }
+    if (at < 64 * p.words) bits |= 1ull << (at & 63);
+    const int up = __ldg(p.parents + start + at);
+    if (up < 0 || up >= at) {
+      if (up != -1) raise_error(p.err, kErrBounds);
+      break;
+    }
+    at = up;
+    ++depth;
+  }
+  for (; word >= 0; --word) {
+    out[word] = bits;
+    bits = 0;
+  }
+  return depth;
+}
+
+__global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanRows p) {
+  __shared__ long long sums[3][kPlanRowsThreads / 32];
+  __shared__ long long at_first[3];  // rows, taken, given before this CTA's first sequence
+  __shared__ int taken_s;
+  extern __shared__ int give0[];     // [B + 1]
+  // launched as a programmatic dependent: the lengths may come from the kernel before this one
+  grid_dep_wait();
+  grid_dep_launch();
+  const int tid = threadIdx.x;
+  const int b_lo = (int)min((long long)blockIdx.x * p.per, (long long)p.B), b_hi = min(p.B, b_lo + p.per);
+  const int free_raw = __ldg(p.free_in), free = min(max(free_raw, 0), p.num_blocks);
+  // ---- all lengths
+  long long total[3] = {0, 0, 0};  // rows, taken (if all are served), given
+  bool bad = free_raw != free;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += kRound) {
+    const int b = b0 + tid * kPer;
+    int rows[kPer], take[kPer], give[kPer];
+    long long v[3] = {0, 0, 0}, sum[3];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      rows[k] = take[k] = give[k] = 0;
+      if (b + k < p.B) {
+        const Req r = request(p, b + k);
+        bad |= !r.ok;
+        rows[k] = r.rows;
+        take[k] = max(0, r.need - r.held);
+        give[k] = max(0, r.held - r.need);
+      }
+      v[0] += rows[k];
+      v[1] += take[k];
+      v[2] += give[k];
+    }
+    scan3(v, sum, sums);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] += total[k];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (b + k < p.B) give0[b + k] = (int)v[2];
+      if (b + k == b_lo && b_lo < b_hi)
+        for (int x = 0; x < 3; ++x) at_first[x] = v[x];
+      v[0] += rows[k];
+      v[1] += take[k];
+      v[2] += give[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) total[k] += sum[k];
+  }
+  if (tid == 0) {
+    give0[p.B] = (int)total[2];
+    taken_s = 0;
+  }
+  const int R = (int)total[2];
+  const long long room = (long long)free + R;  // blocks that can be taken
+  bad |= room > p.num_blocks || total[0] > p.N;
+  __syncthreads();
+  // ---- blocks that are taken: all that are wanted, or as many as the sequences served take
+  int taken = (int)min(total[1], room);
+  const bool keeper = p.write_state && blockIdx.x == 0 && blockIdx.y == 0;  // writes what the next step starts from
+  if (total[1] > room || keeper) {
+    long long before = 0;
+    int most = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += kRound) {
+      const int b = b0 + tid * kPer;
+      int take[kPer], need[kPer], held[kPer];
+      long long v[3] = {0, 0, 0}, sum[3];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        take[k] = need[k] = held[k] = 0;
+        if (b + k < p.B) {
+          const Req r = request(p, b + k);
+          need[k] = r.need;
+          held[k] = r.held;
+          take[k] = max(0, r.need - r.held);
+        }
+        v[1] += take[k];
+      }
+      scan3(v, sum, sums);  // (its barriers: everyone has read before anyone writes)
+      v[1] += before;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        v[1] += take[k];
+        const bool served = take[k] == 0 || v[1] <= room;
+        if (served && take[k]) most = (int)v[1];
+        if (keeper && b + k < p.B)
+          p.held_out[b + k] = served ? need[k] : held[k];
+      }
+      before += sum[1];
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if ((tid & 31) == 0) atomicMax(&taken_s, most);
+    __syncthreads();
+    taken = taken_s;
+  }
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (__syncthreads_or(bad) && tid == 0 && p.report) raise_error(p.err, kErrBounds);
+    if (keeper && tid == 0) {  // (every thread has read the count)
+      p.free_out[0] = (int)min(room - taken, (long long)p.num_blocks);
+      p.free_out[1] = (int)(total[1] - taken);
+    }
+  }
+  if (!p.write_rows) return;
+  // ---- this CTA's sequences
+  const int part = (int)blockIdx.y, parts = (int)gridDim.y;
+  const int step = parts * kPlanRowsThreads, first = part * kPlanRowsThreads + tid;
+  // the block at place `at` of the list with what is given back
+  const auto listed = [&](long long at) -> int {
+    if (at < free) return __ldg(p.free_list + at);
+    const int g = (int)(at - free);
+    int lo = 0, hi = p.B;  // give0[lo] <= g < give0[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (give0[mid] <= g) lo = mid;
+      else hi = mid;
+    }
+    const Req r = request(p, lo);
+    return __ldg(p.tables + (size_t)lo * p.mbps + r.need + (g - give0[lo]));
+  };
+  long long start = at_first[0], took = at_first[1];
+#pragma unroll 1
+  for (int b = b_lo; b < b_hi; ++b) {
+    const Req r = request(p, b);
+    const int take = max(0, r.need - r.held), give = max(0, r.held - r.need);
+    const bool served = r.ok && (take == 0 || took + take <= room);
+    int* table = p.tables + (size_t)b * p.mbps;
+    if (part == 0 && tid == 0) {
+      p.row_starts[b] = (int)min(start, (long long)INT_MAX);
+      if (b == p.B - 1) p.row_starts[p.B] = (int)min(start + r.rows, (long long)INT_MAX);
+    }
+    const auto block = [&](int k) {  // of the sequence's k-th block; -1: none
+      const int e = k < r.held ? __ldg(table + k) : listed(room - 1 - (took + (k - r.held)));
+      if (e >= 0 && e < p.num_blocks) return e;
+      raise_error(p.err, kErrBounds);
+      return -1;
+    };
+    // blocks given back, those of them that stay on the list
+    for (int k = first; k < give; k += step) {
+      const int g = give0[b] + k, e = __ldg(table + r.need + k);
+      if (e < 0 || e >= p.num_blocks) raise_error(p.err, kErrBounds);
+      if (free + (long long)g < room - taken && free + (long long)g < p.num_blocks) p.free_list[free + g] = e;
+    }
+    if (served)
+      for (int k = first; k < take; k += step) table[r.held + k] = block(r.held + k);
+    // rows
+    const int rows = (int)min((long long)r.rows, max(0ll, p.N - start));
+    for (int i = first; i < rows; i += step) {
+      long long slot = -1;
+      if (served) {
+        const int k = (r.len + i) / p.bs, e = block(k);
+        if (e >= 0) slot = (long long)e * p.bs + (r.len + i - k * p.bs);
+      }
+      p.slots[start + i] = slot;
+      int at = i;
+      if (p.parents) {
+        if (i >= 64 * p.words) raise_error(p.err, kErrBounds);
+        at = walk_up(p, start, i);
+      }
+      p.positions[start + i] = r.len + at;
+    }
+    start += r.rows;
+    took += take;
+  }
+  // ---- rows behind the last sequence
+  const long long stride = (long long)gridDim.x * step;
+  for (long long n = total[0] + (long long)blockIdx.x * step + first; n < p.N; n += stride) {
+    p.slots[n] = -1;
+    p.positions[n] = 0;
+    if (p.parents)
+      for (int w = 0; w < p.words; ++w) p.mask[n * p.words + w] = 0;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_plan_rows(PlanRows p, cudaStream_t st) {
+  const size_t smem = (size_t)(p.B + 1) * 4;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static std::atomic<unsigned long long> attr_done{0};  // per device
+  if (dev >= 64 || !(attr_done.load(std::memory_order_acquire) >> dev & 1ull)) {
+    const cudaError_t e = cudaFuncSetAttribute(plan_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (kPlanRowsMaxB + 1) * 4);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  // a CTA per sequence, up to four on each SM; slices of a sequence's rows where that leaves room
+  const int most = 4 * kDenseSms;
+  p.per = (p.B + most - 1) / most;
+  const int gx = (p.B + p.per - 1) / p.per;
+  const long long rows = (long long)p.N / p.B;
+  long long gy = (rows + kPlanRowsThreads - 1) / kPlanRowsThreads;
+  gy = gy < 1 ? 1 : gy > most / gx ? (most / gx < 1 ? 1 : most / gx) : gy;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)gx, (unsigned)gy);
+  cfg.blockDim = dim3(kPlanRowsThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // every CTA reads the blocks held and the count of free ones: written in the same launch only
+  // to other arrays, else by one CTA of a second one
+  const bool same = p.held_in == p.held_out || p.free_in == p.free_out;
+  p.write_rows = 1;
+  p.write_state = !same;
+  p.report = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_rows_kernel, p);
+  if (e != cudaSuccess || !same) return e;
+  p.write_rows = 0;
+  p.write_state = 1;
+  p.report = 0;
+  cfg.gridDim = dim3(1);
+  return cudaLaunchKernelEx(&cfg, plan_rows_kernel, p);
+}
+
+}  // namespace gqa

@@ -50,6 +50,10 @@ constexpr int kQkStages = 2;    // rounds in flight per warp (2 KB each)
 // adjacent pairs by whole chunks (or no rotation).
 enum { kTurnAny = 0, kTurnHalf = 1, kTurnAdjacent = 2 };
 
+// Where rows go: to the outputs, to the pool slots behind their sequence's rows, to pool slots that
+// are given.
+enum { kToOutputs = 0, kToSequences = 1, kToSlots = 2 };
+
 // 16 bytes from global to shared memory, asynchronously; each thread waits for its own.
 __device__ __forceinline__ void async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -150,8 +154,9 @@ __device__ __forceinline__ void advance_length(const QkParams& p, int b, int lan
 
 // L lanes per row: a power of two >= the row's chunk pairs. W tokens per warp, side by side (more
 // than one: each a whole token).
-template <typename ET, int L, int TURN, bool PAGED, int W>
+template <typename ET, int L, int TURN, int TO, int W>
 __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p) {
+  constexpr bool PAGED = TO != kToOutputs;
   constexpr int V = Elem<ET>::kPerChunk;  // elements of a 16-byte chunk
   constexpr int H2 = V / 2;
   constexpr int kSub = 32 / W;            // lanes of a token
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p
   // block row y: share y of the tokens' rows; PAGED: then the tokens' values (with a single
   // share they go with it: half as many warps wait for a position), then the lengths
   const int item = (int)(blockIdx.x * kQkWarps) + warp, part = (int)blockIdx.y + p.first_part;
-  if (PAGED && part == p.lens_part) {
+  if (TO == kToSequences && part == p.lens_part) {
     if (item < p.lens_items) advance_length(p, item, lane);
     return;
   }
@@ -247,7 +252,21 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p
   // ---- the token's position and, for the paged append, its slot
   int pos = 0;
   long long slot = 0;  // pool row of KV head 0: (block * Hkv) * bs + row
-  if (PAGED) {
+  if (TO == kToSlots) {
+    slot = __ldg(p.slots + tok);
+    pos = p.rot_dim ? __ldg(p.positions + tok) : 0;
+    if (slot >= (long long)p.num_blocks * p.bs) {
+      if (alive && sl == 0) raise_error(p.err, kErrBounds);
+      slot = -1;
+    }
+    alive = alive && slot >= 0;  // a row without a slot: left as it is
+    if (W == 1 ? !alive : !__any_sync(0xffffffffu, alive)) {
+      async_wait<0>();  // never exit with a copy in flight
+      return;
+    }
+    const long long blk = slot / p.bs;
+    slot = blk * p.Hkv * p.bs + (slot - blk * p.bs);
+  } else if (PAGED) {
     int len = 0, b = -1;
     long long row = 0;
     if (W == 1) {
@@ -284,6 +303,8 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p
     if (W == 1) alive = true;
     pos = alive ? (int)at : 0;
     slot = (long long)blk * p.Hkv * p.bs + at % p.bs;
+  }
+  if (PAGED) {
     if (values || p.parts == 1) {  // the values, copied as they are, four chunks in flight per lane
       const int cpv = p.dv / V, n = p.Hkv * cpv;
       for (int i0 = sl; alive && i0 < n; i0 += 4 * kSub) {
@@ -475,8 +496,9 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_rows_kernel(const QkParams p
   }
 }
 
-template <typename ET, int L, int TURN, bool PAGED, int W>
+template <typename ET, int L, int TURN, int TO, int W>
 cudaError_t launch_qk(QkParams p, cudaStream_t st) {
+  constexpr bool PAGED = TO != kToOutputs;
   const int n = p.run_rows ? (int)(((long long)p.N + W - 1) / W) : 0, lens = PAGED ? p.lens_items : 0;
   const int most = n > lens ? n : lens;
   if (most == 0) return cudaSuccess;
@@ -490,10 +512,10 @@ cudaError_t launch_qk(QkParams p, cudaStream_t st) {
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, qk_rows_kernel<ET, L, TURN, PAGED, W>, p);
+  return cudaLaunchKernelEx(&cfg, qk_rows_kernel<ET, L, TURN, TO, W>, p);
 }
 
-template <typename ET, int TURN, bool PAGED>
+template <typename ET, int TURN, int TO>
 cudaError_t dispatch_qk(QkParams p, cudaStream_t st) {
   constexpr int V = Elem<ET>::kPerChunk;
   const int cpr = p.d / V, np = p.rot_dim / 2 / V;
@@ -513,28 +535,30 @@ cudaError_t dispatch_qk(QkParams p, cudaStream_t st) {
   // of 64 7.8 and 8.8, 2,048 of 14 + 2 of 64 (256 warps for the GPU) 4.8 and 8.9. An append's rows
   // may be padding in good part (7,261 rows of 14 + 2 + 2 heads of 64, half of them padding: 9.7
   // and 10.4), so twice as many are asked for.
-  const bool side = p.parts == 1 && rounds <= 3 && p.N >= (PAGED ? 8 : 4) * 152 * (32 / L);
+  const bool side = p.parts == 1 && rounds <= 3 && p.N >= (TO != kToOutputs ? 8 : 4) * 152 * (32 / L);
   switch (L) {
-    case 4: return side ? launch_qk<ET, 4, TURN, PAGED, 8>(p, st) : launch_qk<ET, 4, TURN, PAGED, 1>(p, st);
-    case 8: return side ? launch_qk<ET, 8, TURN, PAGED, 4>(p, st) : launch_qk<ET, 8, TURN, PAGED, 1>(p, st);
-    case 16: return side ? launch_qk<ET, 16, TURN, PAGED, 2>(p, st) : launch_qk<ET, 16, TURN, PAGED, 1>(p, st);
-    default: return launch_qk<ET, 32, TURN, PAGED, 1>(p, st);
+    case 4: return side ? launch_qk<ET, 4, TURN, TO, 8>(p, st) : launch_qk<ET, 4, TURN, TO, 1>(p, st);
+    case 8: return side ? launch_qk<ET, 8, TURN, TO, 4>(p, st) : launch_qk<ET, 8, TURN, TO, 1>(p, st);
+    case 16: return side ? launch_qk<ET, 16, TURN, TO, 2>(p, st) : launch_qk<ET, 16, TURN, TO, 1>(p, st);
+    default: return launch_qk<ET, 32, TURN, TO, 1>(p, st);
   }
 }
 
-template <typename ET, bool PAGED>
+template <typename ET, int TO>
 cudaError_t dispatch_turn(const QkParams& p, cudaStream_t st) {
   constexpr int V = Elem<ET>::kPerChunk;
   const bool half = p.rot_dim && p.layout == 1;
-  if (p.rot_offset % V || (half ? p.rot_dim / 2 : p.rot_dim) % V) return dispatch_qk<ET, kTurnAny, PAGED>(p, st);
-  return half ? dispatch_qk<ET, kTurnHalf, PAGED>(p, st) : dispatch_qk<ET, kTurnAdjacent, PAGED>(p, st);
+  if (p.rot_offset % V || (half ? p.rot_dim / 2 : p.rot_dim) % V) return dispatch_qk<ET, kTurnAny, TO>(p, st);
+  return half ? dispatch_qk<ET, kTurnHalf, TO>(p, st) : dispatch_qk<ET, kTurnAdjacent, TO>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_qk_rows(const QkParams& p, int bf16, int paged, cudaStream_t st) {
-  if (bf16) return paged ? dispatch_turn<__nv_bfloat16, true>(p, st) : dispatch_turn<__nv_bfloat16, false>(p, st);
-  return paged ? dispatch_turn<float, true>(p, st) : dispatch_turn<float, false>(p, st);
+  if (p.slots) return bf16 ? dispatch_turn<__nv_bfloat16, kToSlots>(p, st) : dispatch_turn<float, kToSlots>(p, st);
+  if (bf16)
+    return paged ? dispatch_turn<__nv_bfloat16, kToSequences>(p, st) : dispatch_turn<__nv_bfloat16, kToOutputs>(p, st);
+  return paged ? dispatch_turn<float, kToSequences>(p, st) : dispatch_turn<float, kToOutputs>(p, st);
 }
 
 }  // namespace gqa

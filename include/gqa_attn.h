@@ -481,6 +481,91 @@ gqa_status kv_append_paged_rows(const gqa_heads* q, const gqa_heads* k_new, cons
                                 int d_v, const void* q_weight, const void* k_weight, float eps, const gqa_rope* rope,
                                 gqa_dtype dt, void* stream);
 
+/* ---- a step that verifies drafted tokens ---------------------------------------
+ * A sequence brings a tree of drafted rows behind the rows that it holds: row i of the tree hangs
+ * on row parents[i] of it, or on the history (-1). It lies in the cache behind the history, in the
+ * order of the rows, stands at the position of its depth, and sees the history, its ancestors and
+ * itself. kv_plan_rows makes the step's index arrays (the blocks too), kv_append_slots writes the
+ * rows, attn_tree_paged is their attention, and kv_commit_rows keeps those of the path that was
+ * accepted. A step of plain rows (one each, or chunks of prompts) is the case without parents.
+ * The rows of all sequences lie packed, as for kv_append_paged_rows; `position_offset` and
+ * `seq_lens` below are the rows present before the step's.
+ */
+
+/*
+ * The index arrays of a step, from the requests' lengths.
+ *
+ *   seq_lens     int32 [B]: rows present; new_rows int32 [B]: rows that the step adds
+ *   block_tables int32 [B, max_blocks_per_seq], updated in place; blocks_in int32 [B]: entries of a
+ *                row that are in use, blocks_out int32 [B] (may be the array blocks_in): afterwards
+ *   keep_blocks  int32 [B] or NULL (zeros): the first so many entries of a row in use are never given back
+ *                (a prefix that other rows of the table name too), 0 .. blocks_in[b]
+ *   free_list    int32 [num_blocks], updated in place: a stack of the free blocks, of which there are
+ *                free_in[0] (int32 [1]); free_out int32 [2]: how many there are afterwards (free_out may be
+ *                the array free_in, if it has two entries), and how many were wanting
+ * Sequence b needs max(ceil((seq_lens[b] + new_rows[b]) / block_size), keep_blocks[b]) blocks. Blocks
+ * past that go back onto the stack (sequence by sequence, entries ascending), then those that are
+ * missing are taken off it, in the order of the sequences, until one cannot be served: it and later
+ * ones that need blocks get none, keep what they have, and their rows have no slot. A finished request
+ * (seq_lens 0, new_rows 0) gives its blocks back. Entries behind blocks_out[b] and stack places behind
+ * free_out[0] hold whatever they held, so that the same call again (with arrays of its own for
+ * blocks_out and free_out) gives the same.
+ *   row_starts   int32 [B + 1]: the prefix sums of new_rows
+ *   positions    int32 [N]: seq_lens[b] + i for row i of sequence b; with parents, + its depth
+ *   slots        int64 [N]: block * block_size + row in the block; -1 for a row without one
+ *   parents      int32 [N] or NULL: each packed row's parent in its tree, -1 .. its own index - 1
+ *   tree_mask    uint64 [N, mask_words] (with parents): bit j of row i: row j of the sequence is
+ *                row i or an ancestor of it
+ * Rows behind the last sequence get position 0, slot -1 and an empty mask. Numbers out of range
+ * (a length or count below 0, more rows than N or than a table row or a mask can name, blocks_in or keep_blocks
+ * out of range, a parent that does not precede its row, an entry that is no block, more blocks free than there
+ * are) set the device error word: such a sequence keeps its blocks and its rows have no slot; a row with a bad
+ * parent counts as hanging on the history. B is at most 16384, B * max_blocks_per_seq at most INT_MAX;
+ * B = 0 does nothing. No workspace.
+ */
+gqa_status kv_plan_rows(const int32_t* seq_lens, const int32_t* new_rows, int32_t* block_tables,
+                        const int32_t* blocks_in, int32_t* blocks_out, const int32_t* keep_blocks, int32_t* free_list,
+                        const int32_t* free_in, int32_t* free_out, int32_t* row_starts, int32_t* positions,
+                        int64_t* slots, const int32_t* parents, uint64_t* tree_mask, int mask_words, int N, int B,
+                        int max_blocks_per_seq, int num_blocks, int block_size, void* stream);
+
+/*
+ * kv_append_paged_rows with each row's position and slot given: norm and rotation as there, keys and
+ * values to slot slots[n] of the pools.
+ *
+ *   q, q_out, k_new, v_new, pools, norm, rotation, N  as for kv_append_paged_rows
+ *   positions  int32 [N]: what a row is turned by (NULL without a rotation)
+ *   slots      int64 [N]: block * block_size + row in the block. Below 0: nothing of the row is
+ *              written. At or past num_blocks * block_size: neither, and the device error word is set.
+ * Two rows must not have one slot. No workspace.
+ */
+gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa_heads* v_new, const gqa_heads* q_out,
+                           void* k_pool, void* v_pool, const int64_t* slots, const int32_t* positions, int N,
+                           int num_blocks, int block_size, int H, int Hkv, int d_k, int d_v, const void* q_weight,
+                           const void* k_weight, float eps, const gqa_rope* rope, gqa_dtype dt, void* stream);
+
+/*
+ * Keeps the accepted rows of each sequence's drafted ones: row seq_lens_in[b] + path[b][j] of the
+ * cache moves to row seq_lens_in[b] + j, in the pools of all layers, and seq_lens_out[b] =
+ * seq_lens_in[b] + n_path[b].
+ *
+ *   k_pools, v_pools  n_layers pools each (arrays on the host, read during the call, of device
+ *               pointers), [num_blocks, Hkv, block_size, d_k] and [.., d_v]; v_pools NULL: there are
+ *               none (a cache of one row a position, as the latent one, with Hkv = 1)
+ *   block_tables, row_starts  as for the step; sequence b drafted row_starts[b + 1] - row_starts[b] rows
+ *   path        int32 [B, max_path]: the accepted rows' indices among them, ascending, n_path[b] of them
+ *   n_path      int32 [B], 0 .. max_path
+ *   seq_lens_in int32 [B], seq_lens_out int32 [B] (may be the same array, at the cost of a second launch)
+ * A path that does not ascend or leaves the drafted rows, a length out of range, or a table entry that
+ * is no block leaves the sequence as it is (seq_lens_out[b] = seq_lens_in[b]) and sets the device error
+ * word. Two sequences must not name one block for the rows that move. d_k and d_v multiples of 8, at
+ * most 1024. No workspace.
+ */
+gqa_status kv_commit_rows(void* const* k_pools, void* const* v_pools, int n_layers, const int32_t* block_tables,
+                          const int32_t* seq_lens_in, const int32_t* row_starts, const int32_t* path,
+                          const int32_t* n_path, int32_t* seq_lens_out, int B, int max_path, int max_blocks_per_seq,
+                          int num_blocks, int block_size, int Hkv, int d_k, int d_v, gqa_dtype dt, void* stream);
+
 /* Bytes of workspace attn_decode_contig / attn_decode_paged need for B
  * sequences of at most max_len_upper_bound rows (0 when no sequence that long
  * is split). With S = ceil(max_len_upper_bound / 2048) splits and U = B*H*S:
