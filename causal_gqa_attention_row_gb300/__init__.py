@@ -29,7 +29,8 @@ EXPORTS = ("attn_prefill_causal", "attn_decode_contig", "attn_decode_paged", "kv
            "attn_decode_mla_absorbed_workspace_bytes", "mla_unabsorb_out", "attn_decode_mla_absorbed_paged",
            "attn_rope_interleaved_qk", "gqa_rope_frequencies", "attn_qk_norm_rope", "kv_append_paged_rows",
            "attn_decode_shared_prefix", "attn_decode_shared_prefix_workspace_bytes", "attn_cross",
-           "attn_cross_workspace_bytes", "kv_plan_rows", "kv_append_slots", "kv_commit_rows")
+           "attn_cross_workspace_bytes", "kv_plan_rows", "kv_append_slots", "kv_commit_rows",
+           "attn_tree_paged", "attn_tree_paged_workspace_bytes")
 
 
 class GqaArms(ctypes.Structure):
@@ -108,6 +109,7 @@ def load(path: str = None):
         "kv_append_paged_rows": [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P, F, P, I, P],
         "kv_plan_rows": [P] * 14 + [I] * 6 + [P],
         "kv_append_slots": [P] * 8 + [I] * 7 + [P, P, F, P, I, P],
+        "attn_tree_paged": [P] * 8 + [I] * 11 + [F, I, P, S, P, P],
         "kv_commit_rows": [P, P, I] + [P] * 6 + [I] * 8 + [I, P],
     }
     for name, args in sig.items():
@@ -122,6 +124,8 @@ def load(path: str = None):
     lib.attn_decode_shared_prefix_workspace_bytes.restype = S
     lib.attn_cross_workspace_bytes.argtypes = [I] * 8
     lib.attn_cross_workspace_bytes.restype = S
+    lib.attn_tree_paged_workspace_bytes.argtypes = [I] * 9
+    lib.attn_tree_paged_workspace_bytes.restype = S
     lib.gqa_status_string.argtypes = [I]
     lib.gqa_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -627,6 +631,47 @@ def kv_append_slots(q, k_new, v_new, q_out, k_pool, v_pool, slots, positions=Non
         _i32(positions), N, nb, bs, H, Hkv, dk, dv, _weight(q_weight, dk), _weight(k_weight, dk), float(eps), _ref(rope),
         _dtype(q, k_new, v_new, q_out, k_pool, v_pool, q_weight, k_weight), _stream(stream)), "kv_append_slots")
     return q_out
+
+
+def attn_tree_paged_workspace_bytes(N, B, max_rows, max_len, H, Hkv, d_k, d_v, dtype=torch.bfloat16):
+    return int(load().attn_tree_paged_workspace_bytes(N, B, max_rows, max_len, H, Hkv, d_k, d_v,
+                                                      BF16 if dtype == torch.bfloat16 else F32))
+
+
+def tree_workspace(N, B, max_rows, H, Hkv, d_k, d_v, max_len, dtype=torch.bfloat16, device="cuda"):
+    """A workspace tensor of the size attn_tree_paged needs (max_len: rows a table row can name); it does for smaller
+    N, B, max_rows and max_len too."""
+    return torch.empty(attn_tree_paged_workspace_bytes(N, B, max_rows, max_len, H, Hkv, d_k, d_v, dtype), dtype=torch.uint8,
+                       device=device)
+
+
+def attn_tree_paged(q, k_pool, v_pool, block_tables, position_offset, row_starts, tree_mask, out, attention_scale, max_rows,
+                    workspace, stream=None, window=0, softcap=0.0, sinks=None, alibi_slopes=None):
+    """Attention of drafted rows over the paged pool: rows row_starts[b] .. row_starts[b + 1] - 1 (int32 [B + 1], at most
+    max_rows each) of q [N, H, dk] are sequence b's, lie in its cache behind position_offset[b] rows of history (int32
+    [B] or None), and see that history and the drafted rows whose bits tree_mask int64 [N, words] sets (None: a chain,
+    row i sees rows 0 .. i). pools [num_blocks, Hkv, bs, d]; block_tables int32 [B, mbps]; out [N, H, dv]; workspace from
+    tree_workspace; window / softcap / sinks / alibi_slopes: the arms (`gqa_arms`)."""
+    N, H, dk = q.shape
+    nb, Hkv, bs, dv = v_pool.shape
+    B, mbps = block_tables.shape
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != N:
+            raise ValueError("tree_mask must be [N, words]")
+        words = tree_mask.shape[1]
+    if (k_pool.shape != (nb, Hkv, bs, dk) or out.shape != (N, H, dv) or row_starts.numel() != B + 1 or
+            (position_offset is not None and position_offset.numel() != B)):
+        raise ValueError("q, the pools, the tables, the lengths, row_starts and out do not agree")
+    _here(q, k_pool, v_pool, block_tables, position_offset, row_starts, tree_mask, out, workspace, sinks, alibi_slopes)
+    if any(x is not None and x.numel() != H for x in (sinks, alibi_slopes)):
+        raise ValueError("sinks and alibi_slopes must be float32 [H]")
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().attn_tree_paged(
+        _p(q), _p(k_pool), _p(v_pool), _i32(block_tables), _i32(position_offset), _i32(row_starts), _i64(tree_mask), _p(out),
+        N, B, int(max_rows), words, mbps, nb, bs, H, Hkv, dk, dv, float(attention_scale), _dtype(q, k_pool, v_pool, out),
+        _p(workspace), ws, _arms(window, softcap, sinks, alibi_slopes), _stream(stream)), "attn_tree_paged")
+    return out
 
 
 def kv_commit_rows(k_pools, v_pools, block_tables, seq_lens_in, row_starts, path, n_path, seq_lens_out, stream=None):

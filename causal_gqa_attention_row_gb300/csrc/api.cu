@@ -905,7 +905,8 @@ gqa_status kv_plan_rows(const int32_t* seq_lens, const int32_t* new_rows, int32_
   if (N < 0 || B < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || block_size <= 0 ||
       (long long)max_blocks_per_seq * block_size > INT_MAX / 2 || (long long)B * max_blocks_per_seq > INT_MAX)
     return GQA_ERR_INVALID_ARG;
-  if ((parents == nullptr) != (tree_mask == nullptr) || (parents != nullptr) != (mask_words > 0)) return GQA_ERR_INVALID_ARG;
+  if (mask_words < 0 || (N > 0 && ((parents == nullptr) != (tree_mask == nullptr) || (parents != nullptr) != (mask_words > 0))))
+    return GQA_ERR_INVALID_ARG;
   if (B > gqa::kPlanRowsMaxB) return GQA_ERR_UNSUPPORTED;
   if (B == 0) return GQA_OK;
   if (!seq_lens || !new_rows || !block_tables || !blocks_in || !blocks_out || !free_list || !free_in || !free_out ||
@@ -919,7 +920,7 @@ gqa_status kv_plan_rows(const int32_t* seq_lens, const int32_t* new_rows, int32_
   p.lens = seq_lens;
   p.new_rows = new_rows;
   p.keep = keep_blocks;
-  p.parents = parents;
+  p.parents = N > 0 ? parents : nullptr;
   p.tables = block_tables;
   p.held_in = blocks_in;
   p.held_out = blocks_out;
@@ -977,6 +978,184 @@ gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa
   p.num_blocks = num_blocks;
   p.run_rows = 1;
   return from_cuda(gqa::launch_qk_rows(p, bf16, 1, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- attn_tree_paged ----------------------------------------------------------------
+namespace {
+
+// How a call's rows are tiled, on the tensor cores or on the SIMT kernel, and its workspace: the line's
+// length and slots, the sequences' records, the rows' sequences, the partial results.
+struct TreeLayout {
+  int GH, RPT, R, n_hchunks, heads, slots;
+  long long items;  // at most, of a launch
+  size_t rec, row_seq, partial, bytes;
+};
+
+bool tree_layout(int N, int B, int max_rows, int max_len, int H, int Hkv, int d_k, int d_v, int bf16, bool tc,
+                 TreeLayout* t) {
+  *t = TreeLayout{};
+  const int G = H / Hkv, most = tc ? 128 : gqa::tree_rows_tile();
+  if (max_rows > N) max_rows = N;
+  if (tc) {
+    t->slots = gqa::dense_tc_slots(d_k);
+  } else {
+    const int ctas = gqa::tree_rows_ctas(bf16, d_k, d_v);
+    if (!ctas) return false;
+    t->slots = ctas * gqa::kDenseSms;
+  }
+  t->GH = G < most ? G : most;
+  while (G % t->GH) --t->GH;
+  t->RPT = most / t->GH < max_rows ? most / t->GH : max_rows;
+  t->R = (t->GH * t->RPT + 3) / 4 * 4;  // a whole number of 16-byte steps per part
+  t->n_hchunks = G / t->GH;
+  t->heads = Hkv * t->n_hchunks;
+  // row tiles: one of each sequence with rows, and as many more as whole ones fit
+  const int seqs = B < gqa::kTreeSeqs ? B : gqa::kTreeSeqs;
+  const long long tiles = (long long)(seqs < N ? seqs : N) + (max_rows > t->RPT ? N / t->RPT : 0);
+  t->items = tiles * t->heads;
+  const long long steps = t->items * (max_len / 128 + 3);
+  if (steps < t->slots) t->slots = (int)steps;
+  const size_t parts = (size_t)t->items + (size_t)t->slots;
+  size_t at = 256;
+  const auto take = [&](size_t n) {
+    const size_t a = at;
+    at += gqa::round_up256(n);
+    return a;
+  };
+  t->rec = take((size_t)seqs * sizeof(gqa::TreeRec));
+  t->row_seq = take((size_t)N * 4);
+  t->partial = take(parts * gqa::dense_part_floats(t->R, d_v) * 4);
+  t->bytes = at;
+  return true;
+}
+
+}  // namespace
+
+size_t attn_tree_paged_workspace_bytes(int N, int B, int max_rows, int max_len, int H, int Hkv, int d_k, int d_v,
+                                       gqa_dtype dt) {
+  const int bf16 = dtype_flag(dt);
+  if (bf16 < 0 || N <= 0 || B <= 0 || max_rows <= 0 || max_len <= 0 || !heads_ok(H, Hkv) || !width_ok(d_k) ||
+      !width_ok(d_v))
+    return 0;
+  // a call with ALiBi slopes, say, runs on the SIMT kernel; fewer rows of a sequence may make larger
+  // tiles of more heads' rows, never more of them
+  size_t most = 0;
+  for (int tc = 0; tc < 2; ++tc) {
+    TreeLayout t;
+    if ((!tc || gqa::dense_tc_supported(bf16, d_k, d_v)) &&
+        tree_layout(N, B, max_rows, max_len, H, Hkv, d_k, d_v, bf16, tc, &t) && t.bytes > most)
+      most = t.bytes;
+  }
+  return most;
+}
+
+gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool, const int32_t* block_tables,
+                           const int32_t* position_offset, const int32_t* row_starts, const uint64_t* tree_mask,
+                           void* out, int N, int B, int max_rows, int mask_words, int max_blocks_per_seq, int num_blocks,
+                           int block_size, int H, int Hkv, int d_k, int d_v, float attention_scale, gqa_dtype dt,
+                           void* workspace, size_t workspace_bytes, const gqa_arms* arms, void* stream) {
+  const int bf16 = dtype_flag(dt);
+  if (bf16 < 0 || N < 0 || B < 0 || max_rows <= 0 || mask_words < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 ||
+      block_size <= 0 || !heads_ok(H, Hkv) || !width_ok(d_k) || !width_ok(d_v) || !std::isfinite(attention_scale))
+    return GQA_ERR_INVALID_ARG;
+  if ((long long)max_blocks_per_seq * block_size > INT_MAX / 2 || (long long)N * H > INT_MAX) return GQA_ERR_INVALID_ARG;
+  if (mask_words > 0 && (long long)mask_words * 64 < max_rows) return GQA_ERR_INVALID_ARG;
+  if (B == 0 || N == 0) return GQA_OK;
+  if ((tree_mask == nullptr) != (mask_words == 0)) return GQA_ERR_INVALID_ARG;
+  if (!q || !k_pool || !v_pool || !block_tables || !row_starts || !out) return GQA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || !aligned_to(tree_mask, 8))
+    return GQA_ERR_INVALID_ARG;
+  gqa::RowsParams arm{};  // (the arms in the kernels' units)
+  bool arms_on;
+  const gqa_status sa = apply_arms(arm, arms, &arms_on);
+  if (sa != GQA_OK) return sa;
+  const bool tc = gqa::dense_tc_supported(bf16, d_k, d_v, block_size) && attention_scale > 0.f && !arm.alibi;
+  const int capacity = max_blocks_per_seq * block_size;
+  TreeLayout t;
+  if (!tree_layout(N, B, max_rows, capacity, H, Hkv, d_k, d_v, bf16, tc, &t)) return GQA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < t.bytes) return GQA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return GQA_ERR_INVALID_ARG;
+  // places on the line, and partial results in 16-byte steps, are counted in 32 bits
+  if (t.items > INT_MAX / (capacity / 128 + 3) || (t.bytes - t.partial) / 16 > (size_t)INT_MAX) return GQA_ERR_INVALID_ARG;
+  unsigned* err = error_word();
+  if (!err) return GQA_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+
+  gqa::TreeParams p{};
+  p.w.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+  p.w.N = N;
+  p.w.max_rows = max_rows;
+  p.w.words = mask_words;
+  p.w.heads = t.heads;
+  p.w.GH = t.GH;
+  p.w.RPT = t.RPT;
+  p.w.R = t.R;
+  p.w.capacity = capacity;
+  p.w.bs = block_size;
+  p.w.window = arm.window;
+  p.w.slots = t.slots;
+  p.w.rec = reinterpret_cast<gqa::TreeRec*>(ws + t.rec);
+  p.w.row_seq = reinterpret_cast<int*>(ws + t.row_seq);
+  p.w.line = reinterpret_cast<int*>(ws);
+  p.w.err = err;
+  p.q = q;
+  p.k = k_pool;
+  p.v = v_pool;
+  p.out = out;
+  p.partial = reinterpret_cast<float*>(ws + t.partial);
+  p.H = H;
+  p.G = H / Hkv;
+  p.n_hchunks = t.n_hchunks;
+  p.Hkv = Hkv;
+  p.mbps = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.dk = d_k;
+  p.dv = d_v;
+  p.qscale = attention_scale * gqa::kLog2e;
+  p.softcap2 = arm.softcap2;
+  p.sinks = arm.sinks;
+  p.alibi = arm.alibi;
+  p.check = tc;
+  for (int b0 = 0; b0 < B; b0 += gqa::kTreeSeqs) {
+    p.w.B = B - b0 < gqa::kTreeSeqs ? B - b0 : gqa::kTreeSeqs;
+    p.w.row_starts = row_starts + b0;
+    p.w.offsets = position_offset ? position_offset + b0 : nullptr;
+    p.tables = block_tables + (size_t)b0 * max_blocks_per_seq;
+    cudaError_t e;
+    if (tc) {
+      gqa::DenseParams d{};
+      d.H = H;
+      d.Hkv = Hkv;
+      d.G = p.G;
+      d.GH = t.GH;
+      d.RPT = t.RPT;
+      d.n_hchunks = t.n_hchunks;
+      d.n_i = N;
+      d.S_kv = capacity;
+      d.own_rows = t.R;
+      d.tables = p.tables;
+      d.mbps = max_blocks_per_seq;
+      d.bs = block_size;
+      d.num_blocks = num_blocks;
+      d.partial = p.partial;
+      d.out = static_cast<__nv_bfloat16*>(out);
+      d.qscale = p.qscale;
+      d.err = err;
+      d.debug_withhold = g_withhold_first_tile;
+      d.window = arm.window;
+      d.cap_out = arm.softcap2;
+      d.cap_in = arm.softcap2 > 0.f ? d.qscale / arm.softcap2 : 0.f;
+      d.tree = p.w;
+      e = gqa::launch_dense_tc(q, k_pool, v_pool, d, 1, d_k, d_v, arm.window > 0 || arm.softcap2 > 0.f, st);
+    } else {
+      e = gqa::launch_tree_rows(p, bf16, st);
+    }
+    if (e != cudaSuccess) return from_cuda(e);
+    e = gqa::launch_tree_combine(p, bf16, st);
+    if (e != cudaSuccess) return from_cuda(e);
+  }
+  return GQA_OK;
 }
 
 gqa_status kv_commit_rows(void* const* k_pools, void* const* v_pools, int n_layers, const int32_t* block_tables,

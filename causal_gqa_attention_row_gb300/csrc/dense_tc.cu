@@ -59,6 +59,7 @@
 
 #include "attn_tc.cuh"
 #include "tmap.h"
+#include "tree_part.cuh"
 
 namespace gqa {
 namespace {
@@ -132,12 +133,29 @@ __device__ __forceinline__ DenseUnit cross_unit(const DenseParams& p, int x, int
 
 __device__ __forceinline__ int unit_tiles(const DenseUnit& u) { return (u.key1 - u.key0 + kBN - 1) / kBN; }
 
-template <int DK, int DV, bool ARMS, bool PAGED>
+// What the keys of a unit are: an encoder's, a pool's behind the shared prefixes' plan, a pool's with drafted rows.
+enum { kKeysContig = 0, kKeysShared = 1, kKeysTree = 2 };
+
+// The mask of a row's 128 keys from j0 on, of which some are drafted rows.
+template <bool ARMS>
+__device__ __noinline__ uint4 tree_mask_of(const DenseParams& p, const TreeSeq* s, int row, int n, int j0, int depth) {
+  const int o = j0 - s->hist, i = row - s->row0;
+  uint32_t m[4];
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    m[c] = tree_bits(p.tree, row, i, n, o + 32 * c);
+    if (ARMS && p.window > 0) m[c] = tree_window(p.tree, m[c], s->row0, n, o + 32 * c, depth);
+  }
+  return make_uint4(m[0], m[1], m[2], m[3]);
+}
+
+template <int DK, int DV, bool ARMS, int KEYS>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_o, const DenseParams p) {
   using C = DenseCfg<DK, DV>;
+  constexpr bool PAGED = KEYS != kKeysContig, TREE = KEYS == kKeysTree;
   constexpr int kTileK = C::kTileK, kTileV = C::kTileV, kStages = C::kStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -182,7 +200,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the plan's units, the lengths and everything else may come from the kernel before
   grid_dep_wait();
   grid_dep_launch();  // the next launch may start setting up on the SMs this grid frees
-  const int n_units = PAGED ? __ldcg(p.units_listed) : p.n_units;
+  // drafted rows: the line of all work, in the room that output tiles do not need here
+  TreeSeq* tree_seq = reinterpret_cast<TreeSeq*>(smem + C::kOffOut);
+  if (TREE) tree_line<kThreads>(p.tree, tree_seq, (int)blockIdx.x, (int)gridDim.x);
+  const int n_units = TREE ? 0 : PAGED ? __ldcg(p.units_listed) : p.n_units;
   const int slots = (int)gridDim.x * C::kHalves;
 
   if (warp >= kProducerWarp) {
@@ -204,6 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int next_x = (int)blockIdx.x + (int)gridDim.x * w, ahead = 1;  // steps done: 1 number, 2 record, 3 entry
       DenseUnit next_u = {};
       int next_e = 0;
+      TreeWalk walk = {};
+      if (TREE) walk = tree_walk(p.tree, tree_seq, next_x);
       // paged: lane y < per brings block y of a tile and holds its table entry
       const int per = PAGED ? kBN / p.bs : 1;
       const int my_block = lane % per;
@@ -215,16 +238,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const auto fetch_ahead = [&] {
         if (ahead == 0) {
-          if (PAGED) {
+          if (TREE) {
+          } else if (PAGED) {
             if (lane == 0) next_x = slots + atomicAdd(p.ticket, 1);
           } else {
             next_x += slots;
           }
           ahead = 1;
         } else if (ahead == 1) {
-          if (PAGED) next_x = __shfl_sync(0xffffffffu, next_x, 0);
+          if (PAGED && !TREE) next_x = __shfl_sync(0xffffffffu, next_x, 0);
           next_u = DenseUnit{};
-          if (next_x < n_units) {
+          TreeUnit t;
+          if (TREE) {
+            if (tree_next(p.tree, tree_seq, walk, t)) {
+              const int i0 = t.tile * p.RPT, part = (int)(dense_part_floats(p.own_rows, DV) / 4);
+              next_u = {t.row0 + i0, min(p.RPT, t.n - i0), t.hc * p.GH, t.b, t.key0, t.key1, t.index * part, 0};
+            }
+          } else if (next_x < n_units) {
             if (PAGED) {
               const int4 a = __ldcg(reinterpret_cast<const int4*>(p.units + next_x));
               const int4 c = __ldcg(reinterpret_cast<const int4*>(p.units + next_x) + 1);
@@ -361,7 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_i = hb.unit[us].n_i, keys = hb.unit[us].key1 - hb.unit[us].key0;
         // keys at the start of a sequence's own, on the first one's block, that its window hides
         int hidden = 0;
-        if (ARMS && p.window > 0 && hb.unit[us].batch_or_own)
+        if (ARMS && TREE && p.window > 0 && n_i > 0)
+          hidden = first_visible_key(tree_seq[hb.unit[us].seq].hist, p.window) - hb.unit[us].key0;
+        else if (ARMS && !TREE && p.window > 0 && hb.unit[us].batch_or_own)
           hidden = first_visible_key(__ldg(p.seq_lens + hb.unit[us].seq) - 1, p.window) - hb.unit[us].key0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&hb.unit_free[us]);
@@ -474,17 +506,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       float th;  // the reference max moves when a score passes it by this much
       float alibi2 = 0.f;
       bool warp_live;
+      int depth = 0, tree_n = 0;  // drafted rows: those that this row sees, and the sequence's
       {
         const int rows = u.n_i * p.GH;  // rows of the tile in use
         warp_live = quarter * 32 < rows;
         lim = u.key1;
-        if (ARMS) {  // a row is a sequence of its own length; its position is its last key's
+        if (TREE) {
+          const TreeSeq& s = tree_seq[u.seq];
+          tree_n = __ldg(p.tree.row_starts + u.seq + 1) - s.row0;
+          if (ARMS && p.window > 0 && warp_live) {
+            const int row = u.i0 + min(r, rows - 1) / p.GH;
+            depth = tree_depth(p.tree, row, row - s.row0, tree_n);
+            lo_key = min(first_visible_key(s.hist + depth - 1, p.window), s.hist);  // (drafted rows: by their masks)
+          }
+        } else if (ARMS) {  // a row is a sequence of its own length; its position is its last key's
           pos = __ldg(p.seq_lens + u.i0 + min(r, rows - 1) / p.GH) - 1;
           if (u.batch_or_own) lo_key = first_visible_key(pos, p.window);
         }
         // a padding row beside live ones needs no mask and never moves its reference: whatever
         // it holds stays in its own row
         if (r >= rows) lim = INT_MAX;
+        if (TREE && r >= rows) lo_key = 0;
         th = r < rows ? kRescaleLog2 / qs : INFINITY;
         if (ARMS && p.alibi) alibi2 = __ldg(p.alibi + u.head0 + min(r, rows - 1) % p.GH) * kLog2e;
       }
@@ -492,6 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l_run = 0.f;  // the row sum of p, against m_ref
       for (int k = 0; k < tiles; ++k, ++t_all) {
         const int j0 = key0 + k * kBN;  // the tile's first key
+        bool drafted = false;           // some of the tile's keys are
+        uint4 seen = make_uint4(~0u, ~0u, ~0u, ~0u);
+        if (TREE) {
+          const TreeSeq* s = tree_seq + u.seq;
+          drafted = j0 + kBN > s->hist;
+          if (drafted && lim != INT_MAX) seen = tree_mask_of<ARMS>(p, s, u.i0 + r / p.GH, tree_n, j0, depth);
+        }
         if (!warp_wait_tc(&hb.s_full, t_all & 1, bars, p.err)) {
           alive = false;
           break;
@@ -560,8 +609,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // keys that some row of the warp does not see weigh zero for it
-        if (__any_sync(0xffffffffu, j0 > lim - kBN || (ARMS && j0 < lo_key))) {
-          const int end = lim - j0, begin = ARMS ? lo_key - j0 : 0;
+        if (TREE && drafted) {
+          const uint32_t m[4] = {seen.x, seen.y, seen.z, seen.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(m[c] >> e & 1u)) sv[c][e] = __float_as_uint(-INFINITY);
+        }
+        if (__any_sync(0xffffffffu, (!TREE && j0 > lim - kBN) || (ARMS && j0 < lo_key))) {
+          const int end = TREE ? kBN : lim - j0, begin = ARMS ? lo_key - j0 : 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -658,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int at = u.part;
       if (PAGED || at >= 0) {
         if (warp_live) {
-          const int rows = u.n_i * p.GH, R = PAGED && u.batch_or_own ? p.own_rows : kBM;
+          const int rows = u.n_i * p.GH, R = TREE || (PAGED && u.batch_or_own) ? p.own_rows : kBM;
           float* part = p.partial + (size_t)at * 4;
 #pragma unroll 1
           for (int cc = 0; cc < DV / 32; ++cc) {
@@ -877,7 +934,7 @@ bool make_pool_map(CUtensorMap* m, const void* base, int d, const DenseParams& p
   return make_tmap_bf16(m, base, dims, strides, box);
 }
 
-template <int DK, int DV, bool ARMS, bool PAGED>
+template <int DK, int DV, bool ARMS, int KEYS>
 cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtensorMap& tk, const CUtensorMap& tv,
                      const CUtensorMap& to, const DenseParams& p, cudaStream_t st) {
   using C = DenseCfg<DK, DV>;
@@ -888,14 +945,15 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtens
     // The register hand-over inside the kernel assumes exactly kLaunchRegs per
     // thread at launch; a build with any other allocation is refused.
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, dense_tc_kernel<DK, DV, ARMS, PAGED>);
+    cudaError_t e = cudaFuncGetAttributes(&fa, dense_tc_kernel<DK, DV, ARMS, KEYS>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
-    e = cudaFuncSetAttribute(dense_tc_kernel<DK, DV, ARMS, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    e = cudaFuncSetAttribute(dense_tc_kernel<DK, DV, ARMS, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
   }
-  const int grid = p.units || p.n_units > kDenseSms ? kDenseSms : p.n_units;
+  const int n = KEYS == kKeysTree ? p.tree.slots : KEYS == kKeysShared ? kDenseSms : p.n_units;
+  const int grid = n < kDenseSms ? n : kDenseSms;
   if (grid <= 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -905,16 +963,19 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtens
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dense_tc_kernel<DK, DV, ARMS, PAGED>, tq, tq1, tk, tv, to, p);
+  return cudaLaunchKernelEx(&cfg, dense_tc_kernel<DK, DV, ARMS, KEYS>, tq, tq1, tk, tv, to, p);
 }
 
-// (the arms belong to the shared-prefix step, which is paged)
+// (the arms belong to the paged steps)
 template <int DK, int DV>
 cudaError_t launch_w(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtensorMap& tk, const CUtensorMap& tv,
                      const CUtensorMap& to, const DenseParams& p, bool arms, cudaStream_t st) {
-  if (!p.tables) return launch_d<DK, DV, false, false>(tq, tq1, tk, tv, to, p, st);
-  return arms ? launch_d<DK, DV, true, true>(tq, tq1, tk, tv, to, p, st)
-              : launch_d<DK, DV, false, true>(tq, tq1, tk, tv, to, p, st);
+  if (!p.tables) return launch_d<DK, DV, false, kKeysContig>(tq, tq1, tk, tv, to, p, st);
+  if (p.tree.row_starts)
+    return arms ? launch_d<DK, DV, true, kKeysTree>(tq, tq1, tk, tv, to, p, st)
+                : launch_d<DK, DV, false, kKeysTree>(tq, tq1, tk, tv, to, p, st);
+  return arms ? launch_d<DK, DV, true, kKeysShared>(tq, tq1, tk, tv, to, p, st)
+              : launch_d<DK, DV, false, kKeysShared>(tq, tq1, tk, tv, to, p, st);
 }
 
 }  // namespace

@@ -201,6 +201,25 @@ cudaError_t launch_prefill_tc(const void* q, const void* k, const void* v, void*
 bool prefill_tc_supported(int bf16, int dk, int dv, int bs = 0, int mbps = 0);
 
 // ---- attention without a causal rule on tcgen05 (dense_tc.cu) -----------------
+// How the attention of drafted rows is cut into work (tree_part.cuh).
+constexpr int kTreeSeqs = 1000;  // sequences of a launch: their table stays in shared memory
+struct alignas(16) TreeRec {     // what the join reads of a sequence
+  int row0, n, cost0, item0;     // n 0: nothing to join (no rows, or numbers out of range)
+  int hist, pad[3];
+};
+struct TreeWork {
+  const int32_t *row_starts, *offsets;
+  const unsigned long long* mask;  // [N, words], or NULL: every row sees those up to its own
+  int N, B, max_rows, words;
+  int heads, GH, RPT, R;           // KV heads times head chunks; heads and rows of a tile; rows of a partial result
+  int capacity, bs, window;
+  int slots;
+  TreeRec* rec;                    // [B]
+  int* row_seq;                    // [N]
+  int* line;                       // its length, and the slots that it is cut for
+  unsigned* err;
+};
+
 // One unit of work: rows i0 .. i0 + n_i - 1 of heads head0 .. head0 + GH - 1 against keys
 // key0 .. key1 - 1 of sequence seq (key0 a multiple of the pool's block size). part: where
 // the partial result goes, in 16-byte steps from DenseParams::partial (-1: final results);
@@ -239,6 +258,8 @@ struct DenseParams {
   int window;              // the arms, as for the tensor-core prefill
   float cap_in, cap_out;
   const float* alibi;
+  // drafted rows: units from the line, a mask per row; q and out [N, H, d]
+  TreeWork tree;
 };
 
 // Heads of a group per row tile (the largest divisor of G that is at most 128) and
@@ -304,6 +325,27 @@ struct SharedPlan {
   unsigned* err;
 };
 cudaError_t launch_shared_plan(const SharedPlan& s, cudaStream_t st);
+
+// ---- attention of drafted rows (attn_tree_paged) ---------------------------------
+// On the tensor cores (dense_tc.cu; launch_dense_tc with p.tree.row_starts set), or on the SIMT kernel
+// (tree_rows.cu) for every other type, width and block size; both leave partial results of R rows, which
+// launch_tree_combine joins.
+struct TreeParams {
+  TreeWork w;
+  const void *q, *k, *v;           // [N, H, d_k], pools
+  void* out;                       // [N, H, d_v]
+  const int32_t* tables;
+  float* partial;
+  int H, G, n_hchunks, Hkv, mbps, num_blocks, dk, dv;
+  float qscale;                    // attention_scale * log2(e)
+  float softcap2;                  // softcap * log2(e), 0: none
+  const float *sinks, *alibi;
+  int check;                       // the join looks for values that rows do not see but the products mixed in
+};
+int tree_rows_ctas(int bf16, int dk, int dv);  // of the SIMT kernel an SM (0: width not taken)
+int tree_rows_tile();                          // rows (times heads) of its tile
+cudaError_t launch_tree_rows(const TreeParams& p, int bf16, cudaStream_t st);
+cudaError_t launch_tree_combine(const TreeParams& p, int bf16, cudaStream_t st);
 
 // Absorbed MLA decode on tcgen05 (bf16, d_c = 512, d_r = 64): attention of
 // q_abs [B, H, d_c + d_r] over the latent rows [B, max_len, d_c + d_r] (value =

@@ -545,6 +545,44 @@ gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa
                            const void* k_weight, float eps, const gqa_rope* rope, gqa_dtype dt, void* stream);
 
 /*
+ * Attention of drafted rows against the paged pool, which holds them already behind their sequence's history:
+ * every row sees the whole history and, among the drafted rows of its sequence, those that its mask names.
+ *
+ *   q  [N, H, d_k], out [N, H, d_v]: the rows of all sequences, packed
+ *   k_pool, v_pool, block_tables  as for attn_decode_paged
+ *   position_offset  int32 [B]: rows of history, or NULL for all zeros; drafted row j of sequence b is row
+ *               position_offset[b] + j of its cache
+ *   row_starts  int32 [B + 1], ascending: rows row_starts[b] .. row_starts[b + 1] - 1 are sequence b's, at
+ *               most max_rows of them, or none; rows outside every sequence are left as they are
+ *   tree_mask   uint64 [N, mask_words]: bit j of a row: it sees drafted row j of its sequence (its own bit
+ *               too: a row does not see itself otherwise); bits past the sequence's rows mean nothing. Any set of
+ *               rows will do. mask_words * 64 >= max_rows. NULL (mask_words 0): a chain, row i sees rows 0 .. i
+ *   arms        as for attn_decode_paged_ex, or NULL. A drafted row's position, by which the window and the
+ *               ALiBi slopes go, is position_offset[b] + (drafted rows that it sees, at least 1) - 1: its depth
+ *               in a tree. A window hides drafted rows too.
+ * A row that sees no key gets zeros; a key that scores -infinity weighs zero. What a row does not see does
+ * not reach it, whatever the slot holds, an infinity or NaN included. Sequences with lengths out of range or more
+ * rows than max_rows set the device error word, and their rows are left as they are.
+ * bf16 with (d_k, d_v) = (64, 64), (128, 128) or (192, 128), block_size a multiple of 8 dividing 128,
+ * attention_scale > 0 and no ALiBi slopes runs on the tcgen05 tensor-core kernel (the probabilities rounded to
+ * bf16 for the product with V), every other case on a SIMT kernel of fp32 arithmetic. How a sequence's keys are
+ * split depends on the batch, so the last bits of its results do too; repeated calls give the same bits.
+ * workspace: at least attn_tree_paged_workspace_bytes(..) bytes, 16-byte aligned, always needed; calls
+ * whose kernels may overlap must not share one. The size does for smaller N, B, max_rows and max_len too.
+ * H / GH * (N / RPT + B) * (max_blocks_per_seq * block_size / 128 + 3), with GH * RPT = 64 to 128 heads times
+ * rows, is at most INT_MAX.
+ */
+gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool, const int32_t* block_tables,
+                           const int32_t* position_offset, const int32_t* row_starts, const uint64_t* tree_mask,
+                           void* out, int N, int B, int max_rows, int mask_words, int max_blocks_per_seq, int num_blocks,
+                           int block_size, int H, int Hkv, int d_k, int d_v, float attention_scale, gqa_dtype dt,
+                           void* workspace, size_t workspace_bytes, const gqa_arms* arms, void* stream);
+/* For up to N rows of B sequences, max_rows of one, and max_len keys (history and drafted rows) of one; 0 for
+ * arguments that attn_tree_paged refuses. Host only; launches nothing. */
+size_t attn_tree_paged_workspace_bytes(int N, int B, int max_rows, int max_len, int H, int Hkv, int d_k, int d_v,
+                                       gqa_dtype dt);
+
+/*
  * Keeps the accepted rows of each sequence's drafted ones: row seq_lens_in[b] + path[b][j] of the
  * cache moves to row seq_lens_in[b] + j, in the pools of all layers, and seq_lens_out[b] =
  * seq_lens_in[b] + n_path[b].

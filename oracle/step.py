@@ -96,7 +96,8 @@ def attend(q, k, v, hist, seen, scale, window=0, softcap=0.0, sinks=None, slopes
             kh, vh = k[h // G][idx], v[h // G][idx]
             with np.errstate(invalid="ignore", over="ignore"):
                 s = scale * (kh @ q[i, h])
-                reach[i, h, 0] = scale * (np.abs(kh) @ np.abs(q[i, h])).max()
+                far = scale * (np.abs(kh) @ np.abs(q[i, h]))
+                reach[i, h, 0] = far[s != -math.inf].max(initial=0.0)  # (a key that scores -infinity weighs zero, exactly)
                 if softcap > 0:
                     s = softcap * np.tanh(s / softcap)
                 if slopes is not None:

@@ -1,6 +1,7 @@
 """Host-side refusals of the calls of a step that verifies drafted tokens (CPU): each fails a check
 before any launch."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -99,3 +100,50 @@ def test_binding_checks(g):
         g.kv_commit_rows([pool, pool], [pool], i(2, 8), i(2), i(3), i(2, 4), i(2), i(2))
     with pytest.raises(ValueError):  # pools of two shapes
         g.kv_commit_rows([pool, pool[:4]], None, i(2, 8), i(2), i(3), i(2, 4), i(2), i(2))
+
+
+def tree(g, q=P, k=P, v=P, tab=P, off=P, starts=P, mask=P, out=P, n=20, B=4, most=8, words=1, mbps=8, nb=50, bs=16, H=8, Hkv=2,
+         dk=128, dv=128, scale=0.1, dt=1, ws=P, size=1 << 40, arms=N):
+    a = N if arms is N else ctypes.byref(g.GqaArms(*arms))
+    return g.load().attn_tree_paged(q, k, v, tab, off, starts, mask, out, n, B, most, words, mbps, nb, bs, H, Hkv, dk, dv, scale,
+                                    dt, ws, size, a, N)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dt=5), INV), (dict(n=-1), INV), (dict(B=-1), INV), (dict(most=0), INV), (dict(words=-1), INV), (dict(mbps=0), INV),
+    (dict(nb=0), INV), (dict(bs=0), INV), (dict(H=7), INV), (dict(dk=100), INV), (dict(dv=0), INV), (dict(mbps=1 << 20, bs=1 << 20), INV),
+    (dict(n=1 << 30), INV), (dict(scale=float("nan")), INV), (dict(scale=float("inf")), INV), (dict(mask=N), INV), (dict(words=0), INV),
+    (dict(most=65), INV), (dict(q=N), INV), (dict(k=N), INV), (dict(v=N), INV), (dict(tab=N), INV), (dict(starts=N), INV),
+    (dict(out=N), INV), (dict(q=24), INV), (dict(out=40), INV), (dict(mask=20), INV), (dict(ws=N), 4), (dict(size=1000), 4), (dict(ws=24), INV),
+    (dict(arms=(0, float("nan"), N, N)), INV), (dict(arms=(0, 0.0, 18, N)), INV), (dict(dk=40, dv=40), UNSUP),
+    (dict(n=4000, B=1000, mbps=1 << 25), INV),
+])
+def test_tree_refusals(g, kw, want):
+    assert tree(g, **kw) == want
+
+
+def test_tree_of_nothing_and_its_workspace(g):
+    assert tree(g, B=0, q=N, ws=N) == 0 and tree(g, n=0, q=N, ws=N) == 0
+    f = g.attn_tree_paged_workspace_bytes
+    assert f(0, 4, 8, 128, 8, 2, 128, 128) == 0 and f(20, 4, 8, 128, 8, 3, 128, 128) == 0
+    need = f(20, 4, 8, 128, 8, 2, 128, 128, torch.float32)
+    assert tree(g, dt=0, size=need - 1) == 4
+    # a workspace does for everything smaller
+
+    r = random.Random(1)
+    for _ in range(300):
+        H, Hkv = r.choice([(8, 2), (14, 2), (4, 4), (130, 1), (64, 1)])
+        d, dt = r.choice([(64, torch.bfloat16), (128, torch.bfloat16), (32, torch.bfloat16), (64, torch.float32), (256, torch.float32)])
+        big = (r.randint(1, 5000), r.randint(1, 3000), r.randint(1, 300), r.randint(1, 9000))
+        small = tuple(r.randint(1, x) for x in big)
+        assert f(*small, H, Hkv, d, d, dt) <= f(*big, H, Hkv, d, d, dt), (small, big, H, Hkv, d, dt)
+
+
+def test_tree_binding_checks(g):
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    pool, q = torch.zeros(5, 2, 16, 64), torch.zeros(6, 4, 64)
+    mask = torch.zeros(6, 1, dtype=torch.int64)
+    for kw in (dict(mask=mask[:5]), dict(mask=mask[:, 0]), dict(out=q[:5]), dict(starts=i(2)), dict(off=i(3))):
+        a = dict(dict(mask=mask, out=q, starts=i(3), off=i(2)), **kw)
+        with pytest.raises(ValueError):
+            g.attn_tree_paged(q, pool, pool, i(2, 8), a["off"], a["starts"], a["mask"], a["out"], 0.1, 4, None)

@@ -121,6 +121,15 @@ def test_trees(gpu_lib, B, rows, words, roots, pad):
     verify(c, got, par, words)
 
 
+def test_a_step_without_rows(gpu_lib):
+    """Blocks go back, trees of no rows and all."""
+    g = gpu_lib
+    c = case(20, 300, 0, 16, seed=2, finished=0.5)
+    got, _ = run(g, c, np.zeros(0), 1)
+    assert g.attn_get_device_error() == g.OK
+    verify(c, got)
+
+
 def test_chain_of_one_tree(gpu_lib):
     """Every row on the one before: the longest walk, every bit below a row's own."""
     g = gpu_lib
