@@ -983,12 +983,12 @@ gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa
 // ---- attn_tree_paged ----------------------------------------------------------------
 namespace {
 
-// How a call's rows are tiled, on the tensor cores or on the SIMT kernel, and its workspace: the line's
-// length and slots, the sequences' records, the rows' sequences, the partial results.
+// How a call's rows are tiled, on the tensor cores or on the SIMT kernel, and its workspace: the number of row
+// tiles, their records, the partial results.
 struct TreeLayout {
-  int GH, RPT, R, n_hchunks, heads, slots;
-  long long items;  // at most, of a launch
-  size_t rec, row_seq, partial, bytes;
+  int GH, RPT, R, n_hchunks, heads, slots, pair_slots;
+  long long items;  // row tiles of all heads, at most, of a launch
+  size_t rec, partial, bytes;
 };
 
 bool tree_layout(int N, int B, int max_rows, int max_len, int H, int Hkv, int d_k, int d_v, int bf16, bool tc,
@@ -1015,15 +1015,18 @@ bool tree_layout(int N, int B, int max_rows, int max_len, int H, int Hkv, int d_
   t->items = tiles * t->heads;
   const long long steps = t->items * (max_len / 128 + 3);
   if (steps < t->slots) t->slots = (int)steps;
-  const size_t parts = (size_t)t->items + (size_t)t->slots;
+  // (pairs where a sequence can have two row tiles and a CTA has two halves)
+  const bool pairs = tc && max_rows > t->RPT && gqa::dense_tc_slots(d_k) == 2 * gqa::kDenseSms;
+  t->pair_slots = !pairs ? 0 : steps < gqa::kDenseSms ? (int)steps : gqa::kDenseSms;
+  // (tree_part.cuh) a part for each item and slot of both lines; a pair's two are two of the items
+  const size_t parts = (size_t)t->items + (size_t)t->slots + 2 * (size_t)t->pair_slots;
   size_t at = 256;
   const auto take = [&](size_t n) {
     const size_t a = at;
     at += gqa::round_up256(n);
     return a;
   };
-  t->rec = take((size_t)seqs * sizeof(gqa::TreeRec));
-  t->row_seq = take((size_t)N * 4);
+  t->rec = take((size_t)t->items * sizeof(gqa::TreeRec));
   t->partial = take(parts * gqa::dense_part_floats(t->R, d_v) * 4);
   t->bytes = at;
   return true;
@@ -1095,8 +1098,9 @@ gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool
   p.w.bs = block_size;
   p.w.window = arm.window;
   p.w.slots = t.slots;
+  p.w.pair_slots = t.pair_slots;
+  p.tiles = (int)t.items;
   p.w.rec = reinterpret_cast<gqa::TreeRec*>(ws + t.rec);
-  p.w.row_seq = reinterpret_cast<int*>(ws + t.row_seq);
   p.w.line = reinterpret_cast<int*>(ws);
   p.w.err = err;
   p.q = q;

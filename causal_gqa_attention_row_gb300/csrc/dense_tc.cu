@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       DenseUnit next_u = {};
       int next_e = 0;
       TreeWalk walk = {};
-      if (TREE) walk = tree_walk(p.tree, tree_seq, next_x);
+      int tree_line_no = 0;  // pairs of row tiles first, then single ones
+      if (TREE) walk = tree_walk(p.tree, tree_seq, 0, (int)blockIdx.x);
       // paged: lane y < per brings block y of a tile and holds its table entry
       const int per = PAGED ? kBN / p.bs : 1;
       const int my_block = lane % per;
@@ -250,7 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           next_u = DenseUnit{};
           TreeUnit t;
           if (TREE) {
-            if (tree_next(p.tree, tree_seq, walk, t)) {
+            bool some = tree_next(p.tree, tree_seq, tree_line_no, w, walk, t);
+            if (!some && tree_line_no == 0) {
+              walk = tree_walk(p.tree, tree_seq, tree_line_no = 1, next_x);
+              some = tree_next(p.tree, tree_seq, 1, w, walk, t);
+            }
+            if (some) {
               const int i0 = t.tile * p.RPT, part = (int)(dense_part_floats(p.own_rows, DV) / 4);
               next_u = {t.row0 + i0, min(p.RPT, t.n - i0), t.hc * p.GH, t.b, t.key0, t.key1, t.index * part, 0};
             }
@@ -952,7 +958,7 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtens
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
   }
-  const int n = KEYS == kKeysTree ? p.tree.slots : KEYS == kKeysShared ? kDenseSms : p.n_units;
+  const int n = KEYS == kKeysTree ? max(p.tree.slots, p.tree.pair_slots) : KEYS == kKeysShared ? kDenseSms : p.n_units;
   const int grid = n < kDenseSms ? n : kDenseSms;
   if (grid <= 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};

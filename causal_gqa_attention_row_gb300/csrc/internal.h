@@ -202,10 +202,10 @@ bool prefill_tc_supported(int bf16, int dk, int dv, int bs = 0, int mbps = 0);
 
 // ---- attention without a causal rule on tcgen05 (dense_tc.cu) -----------------
 // How the attention of drafted rows is cut into work (tree_part.cuh).
-constexpr int kTreeSeqs = 1000;  // sequences of a launch: their table stays in shared memory
-struct alignas(16) TreeRec {     // what the join reads of a sequence
-  int row0, n, cost0, item0;     // n 0: nothing to join (no rows, or numbers out of range)
-  int hist, pad[3];
+constexpr int kTreeSeqs = 640;  // sequences of a launch: their table stays in shared memory
+struct alignas(16) TreeRec {    // what the join reads of a row tile
+  int row, n, hc, b;            // its first packed row, its drafted rows; KV head and head chunk; sequence
+  int part, parts, stride, hist;  // its partial results: part, part + stride, ..
 };
 struct TreeWork {
   const int32_t *row_starts, *offsets;
@@ -213,10 +213,9 @@ struct TreeWork {
   int N, B, max_rows, words;
   int heads, GH, RPT, R;           // KV heads times head chunks; heads and rows of a tile; rows of a partial result
   int capacity, bs, window;
-  int slots;
-  TreeRec* rec;                    // [B]
-  int* row_seq;                    // [N]
-  int* line;                       // its length, and the slots that it is cut for
+  int slots, pair_slots;           // pieces of the line of single tiles, and of pairs (0: no pairs)
+  TreeRec* rec;                    // of each row tile
+  int* line;                       // [0] the row tiles
   unsigned* err;
 };
 
@@ -341,6 +340,7 @@ struct TreeParams {
   float softcap2;                  // softcap * log2(e), 0: none
   const float *sinks, *alibi;
   int check;                       // the join looks for values that rows do not see but the products mixed in
+  int tiles;                       // row tiles, at most
 };
 int tree_rows_ctas(int bf16, int dk, int dv);  // of the SIMT kernel an SM (0: width not taken)
 int tree_rows_tile();                          // rows (times heads) of its tile

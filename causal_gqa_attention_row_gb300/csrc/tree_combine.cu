@@ -1,18 +1,20 @@
 // tree_combine.cu -- joins the partial results of drafted rows (tree_part.cuh), in the order of their slots:
 //   M = max m_s (and the sink logit),  out = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s
 //
-// A CTA takes rows (drafted row, head) of one head chunk, next to one another in the parts, rows along the
-// lanes; rows by d_v / 4 threads of four columns by `shares` of the parts (several where few rows
-// would leave SMs without work), four parts at a time, the shares joined at the end in their order. Three
-// trips to memory bound it: which sequence the row is of, that sequence's place on the line, the parts.
+// A CTA takes rows of one row tile (drafted row, head), next to one another in the parts, rows along the
+// lanes: rows by d_v / 4 threads of four columns by `shares` of the parts (several where few rows
+// would leave SMs without work), four parts at a time, the shares joined at the end in their order; where a tile
+// has one or two parts, two groups of rows at a time instead. Latency bounds it, so a CTA goes on
+// through its tile's rows: one trip to memory for the tile's record, which the kernel before has written, then one
+// for each two groups. (A CTA for each group of eight rows took 84 us for 2,059 rows of 32 heads; with a row's place
+// worked out here, by two 64-bit divisions a thread, 116.)
 //
 // Values that a row does not see. A product with V on the tensor cores mixes all keys of a tile, and 0 * NaN is
 // NaN: an infinity or NaN in one drafted row's value (or in a history row that the window has left for
 // some rows) would reach rows that do not see it. That cannot happen without a result that is not
-// finite, so a CTA that finds one looks at the values that its row does not see, and if one of them is not finite
-// works the row out again from the keys that it does see, a warp a key. (Checked per row here it
-// costs a vote; values looked over in every tile by the kernel itself took its MMA warp half a
-// tile's time.)
+// finite, so a CTA that has written one looks at the values that its row does not see, and if one of them is not finite
+// works the row out again from the keys that it does see, a warp a key. (Looking over
+// the values of every tile with drafted rows would have cost all calls.)
 
 #include <atomic>
 
@@ -24,6 +26,7 @@ namespace gqa {
 namespace {
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinCtas = 8;  // an SM, about, that a tile's rows are cut for
 
 __device__ __forceinline__ float exp2_of(float x) {
   float y;
@@ -127,97 +130,45 @@ template <typename ET, bool CHECK>
 __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const __grid_constant__ TreeParams p, int shares) {
   __shared__ float4 acc_s[kJoinThreads];
   __shared__ float2 md_s[kJoinThreads];
-  __shared__ int again_s[kJoinThreads / 4];
+  __shared__ uint32_t again_s[4];  // rows of the tile (at most 128) to be worked out again
   grid_dep_wait();
   const TreeWork& w = p.w;
   const int dv = p.dv, rows_here = 1024 / dv / shares;  // powers of two, as dv is
   const int tid = threadIdx.x, rr = tid & (rows_here - 1), c = tid / rows_here % (dv / 4);
   const int share = tid / (kJoinThreads / shares);
-  const long long per_chunk = ((long long)w.N * w.GH + rows_here - 1) / rows_here;
-  const int chunk = (int)(blockIdx.x / per_chunk);  // KV head and head chunk
-  const long long x = (long long)(blockIdx.x % per_chunk) * rows_here + rr;
-  if (CHECK && tid < rows_here) again_s[tid] = 0;
-  // ---- the row's place on the line
-  bool live = x < (long long)w.N * w.GH;
-  const int row = live ? (int)(x / w.GH) : 0, g = live ? (int)(x - (long long)row * w.GH) : 0, h = chunk * w.GH + g;
-  const int C = __ldcg(w.line), S = __ldcg(w.line + 1);
-  const int b = live ? __ldcg(w.row_seq + row) : -1;
-  live = live && b >= 0 && b < w.B;
-  int4 rec = make_int4(0, 0, 0, 0);
-  int hist = 0;
-  if (live) {
-    rec = __ldcg(reinterpret_cast<const int4*>(w.rec + b));
-    hist = __ldcg(&w.rec[b].hist);
-  }
-  const int i = row - rec.x, n = rec.y;
-  live = live && n > 0 && i >= 0 && i < n && C > 0;
-  int first = 0, total = 0, in_tile = 0;
-  const float* U = p.partial;
-  const size_t part = dense_part_floats(w.R, dv);
-  if (live) {
-    const TreeShape s = tree_shape(w, n, hist);
-    const int tile = i / w.RPT, item = chunk * s.tiles + tile, at = rec.z + item * (s.T + 1);
-    first = tree_slot_of(C, S, at + 1);
-    total = tree_slot_of(C, S, at + s.T) - first + 1;
-    in_tile = (i - tile * w.RPT) * w.GH + g;
-    U = p.partial + (size_t)(rec.w + item + first) * part;
-  }
-  const float z2 = p.sinks && live ? __ldg(p.sinks + h) * kLog2e : -INFINITY;
-  float M = share == 0 ? z2 : -INFINITY, den = M != -INFINITY ? 1.f : 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-  for (int s0 = 4 * share; s0 < total; s0 += 4 * shares) {
-    float4 o[4];
-    float m[4], l[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      m[t] = -INFINITY;
-      l[t] = 0.f;
-      o[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s0 + t < total) {
-        const float* u = U + (size_t)(s0 + t) * part;
-        m[t] = __ldcg(u + (size_t)w.R * dv + in_tile);
-        l[t] = __ldcg(u + (size_t)w.R * dv + w.R + in_tile);
-        o[t] = __ldcg(reinterpret_cast<const float4*>(u) + (size_t)c * w.R + in_tile);
-      }
+  const int tiles = __ldcg(w.line);
+  const int4 r0 = __ldcg(reinterpret_cast<const int4*>(w.rec + blockIdx.x));
+  const int4 r1 = __ldcg(reinterpret_cast<const int4*>(w.rec + blockIdx.x) + 1);
+  if ((int)blockIdx.x >= tiles) return;  // as many row tiles as there may be are launched
+  const int rows = r0.y * w.GH, total = r1.y;
+  const size_t part = dense_part_floats(w.R, dv), next = part * r1.z;
+  const float* parts = p.partial + part * r1.x;
+  // part s of row x: its maximum, sum and this thread's columns
+  const auto fetch = [&](int s, int x, float& m, float& l, float4& o) {
+    m = -INFINITY;
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s < total && x < rows) {
+      const float* u = parts + s * next;
+      m = __ldcg(u + w.R * dv + x);
+      l = __ldcg(u + w.R * dv + w.R + x);
+      o = __ldcg(reinterpret_cast<const float4*>(u) + c * w.R + x);
     }
-    const float Mn = fmaxf(fmaxf(fmaxf(M, m[0]), fmaxf(m[1], m[2])), m[3]);
-    const float f = M == -INFINITY ? 0.f : exp2_of(M - Mn);
-    den = den == 0.f ? 0.f : den * f;
-    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-    M = Mn;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      if (l[t] == 0.f) continue;  // no visible key, whatever m and o hold (a NaN in l goes through)
-      const float f2 = exp2_of(m[t] - M);
-      den = fmaf(f2, l[t], den);
-      acc.x = fmaf(f2, o[t].x, acc.x);
-      acc.y = fmaf(f2, o[t].y, acc.y);
-      acc.z = fmaf(f2, o[t].z, acc.z);
-      acc.w = fmaf(f2, o[t].w, acc.w);
-    }
-  }
-  if (shares > 1) {
-    md_s[tid] = make_float2(M, den);
-    acc_s[tid] = acc;
-    __syncthreads();
-    if (share == 0)
-      for (int k = 1; k < shares; ++k) {
-        const float2 md = md_s[tid + k * (kJoinThreads / shares)];
-        const float4 a = acc_s[tid + k * (kJoinThreads / shares)];
-        if (md.y == 0.f) continue;
-        const float Mn = fmaxf(M, md.x), f = den == 0.f ? 0.f : exp2_of(M - Mn), f2 = exp2_of(md.x - Mn);
-        den = fmaf(f2, md.y, den == 0.f ? 0.f : den * f);
-        acc = make_float4(fmaf(f2, a.x, acc.x * f), fmaf(f2, a.y, acc.y * f), fmaf(f2, a.z, acc.z * f),
-                          fmaf(f2, a.w, acc.w * f));
-        M = Mn;
-      }
-  }
-  bool again = false;
-  if (live && share == 0) {
+  };
+  const auto join = [](float m, float l, float4 o, float M, float& den, float4& acc) {
+    if (l == 0.f) return;  // no visible key, whatever m and o hold (a NaN in l goes through)
+    const float f = exp2_of(m - M);
+    den = fmaf(f, l, den);
+    acc = make_float4(fmaf(f, o.x, acc.x), fmaf(f, o.y, acc.y), fmaf(f, o.z, acc.z), fmaf(f, o.w, acc.w));
+  };
+  const auto head_of = [&](int x) { return r0.z * w.GH + x % w.GH; };
+  const auto sink_of = [&](int x) { return p.sinks && x < rows ? __ldg(p.sinks + head_of(x)) * kLog2e : -INFINITY; };
+  // row x's output; whether it is not finite
+  const auto finish = [&](int x, float den, float4 acc) {
+    if (x >= rows) return false;
     const float inv = den != 0.f ? 1.f / den : 0.f;
     const float4 y = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    ET* to = static_cast<ET*>(p.out) + ((size_t)row * p.H + h) * dv + 4 * c;
+    ET* to = static_cast<ET*>(p.out) + ((size_t)(r0.x + x / w.GH) * p.H + head_of(x)) * dv + 4 * c;
     if constexpr (sizeof(ET) == 2) {
       const __nv_bfloat162 a = __floats2bfloat162_rn(y.x, y.y), z = __floats2bfloat162_rn(y.z, y.w);
       *reinterpret_cast<uint2*>(to) =
@@ -225,27 +176,91 @@ __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const __grid
     } else {
       *reinterpret_cast<float4*>(to) = y;
     }
-    again = CHECK && !(finite4(y) && finite4(acc));
-  }
+    return CHECK && !(finite4(y) && finite4(acc));
+  };
   if (CHECK) {
-    if (!__syncthreads_or(again)) return;
-    if (again) again_s[rr] = 1;
-    for (int k = 0; k < rows_here; ++k) {
-      __syncthreads();  // (the rows are marked; shared memory is free)
-      if (!again_s[k]) continue;
-      const long long xk = (long long)(blockIdx.x % per_chunk) * rows_here + k;
-      Row r;
-      r.row = (int)(xk / w.GH);
-      const int bk = __ldcg(w.row_seq + r.row);
-      const int4 q = __ldcg(reinterpret_cast<const int4*>(w.rec + bk));
-      r.row0 = q.x;
-      r.i = r.row - q.x;
-      r.n = q.y;
-      r.hist = __ldcg(&w.rec[bk].hist);
-      r.depth = tree_depth(w, r.row, r.i, r.n);
-      row_again(p, bk, r, chunk * w.GH + (int)(xk - (long long)r.row * w.GH), reinterpret_cast<float*>(acc_s), md_s);
+    if (tid < 4) again_s[tid] = 0;
+    __syncthreads();
+  }
+  const auto mark = [&](int x, bool again) {
+    if (CHECK && again) atomicOr(&again_s[x >> 5], 1u << (x & 31));
+  };
+  const int step = (int)gridDim.y * rows_here;
+  if (shares == 1 && total <= 2) {
+#pragma unroll 1
+    for (int x0 = (int)blockIdx.y * rows_here; x0 < rows; x0 += 2 * step) {
+      float m[2][2], l[2][2];
+      float4 o[2][2];
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) fetch(s, x0 + v * step + rr, m[v][s], l[v][s], o[v][s]);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const int x = x0 + v * step + rr;
+        const float z2 = sink_of(x), M = fmaxf(z2, fmaxf(m[v][0], m[v][1]));
+        float den = z2 != -INFINITY ? exp2_of(z2 - M) : 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        join(m[v][0], l[v][0], o[v][0], M, den, acc);
+        join(m[v][1], l[v][1], o[v][1], M, den, acc);
+        mark(x, finish(x, den, acc));
+      }
     }
   }
+#pragma unroll 1
+  for (int x0 = (int)blockIdx.y * rows_here; x0 < rows && !(shares == 1 && total <= 2); x0 += step) {
+    const int x = x0 + rr;
+    const float z2 = sink_of(x);
+    float M = share == 0 ? z2 : -INFINITY, den = M != -INFINITY ? 1.f : 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int s0 = 4 * share; s0 < total; s0 += 4 * shares) {
+      float4 o[4];
+      float m[4], l[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) fetch(s0 + t, x, m[t], l[t], o[t]);
+      const float Mn = fmaxf(fmaxf(fmaxf(M, m[0]), fmaxf(m[1], m[2])), m[3]);
+      const float f = M == -INFINITY ? 0.f : exp2_of(M - Mn);
+      den = den == 0.f ? 0.f : den * f;
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+      M = Mn;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) join(m[t], l[t], o[t], M, den, acc);
+    }
+    if (shares > 1) {
+      md_s[tid] = make_float2(M, den);
+      acc_s[tid] = acc;
+      __syncthreads();
+      if (share == 0)
+        for (int k = 1; k < shares; ++k) {
+          const float2 md = md_s[tid + k * (kJoinThreads / shares)];
+          const float4 a = acc_s[tid + k * (kJoinThreads / shares)];
+          if (md.y == 0.f) continue;
+          const float Mn = fmaxf(M, md.x), f = den == 0.f ? 0.f : exp2_of(M - Mn), f2 = exp2_of(md.x - Mn);
+          den = fmaf(f2, md.y, den == 0.f ? 0.f : den * f);
+          acc = make_float4(fmaf(f2, a.x, acc.x * f), fmaf(f2, a.y, acc.y * f), fmaf(f2, a.z, acc.z * f),
+                            fmaf(f2, a.w, acc.w * f));
+          M = Mn;
+        }
+      __syncthreads();
+    }
+    if (share == 0) mark(x, finish(x, den, acc));
+  }
+  if (!CHECK) return;
+  __syncthreads();
+  for (int k = 0; k < 4; ++k)
+    for (uint32_t left = again_s[k]; left; left &= left - 1) {  // (the same for all threads)
+      const int x = 32 * k + __ffs(left) - 1;
+      Row r;
+      r.row = r0.x + x / w.GH;
+      r.row0 = __ldg(w.row_starts + r0.w);
+      r.i = r.row - r.row0;
+      r.n = __ldg(w.row_starts + r0.w + 1) - r.row0;
+      r.hist = r1.w;
+      r.depth = tree_depth(w, r.row, r.i, r.n);
+      row_again(p, r0.w, r, head_of(x), reinterpret_cast<float*>(acc_s), md_s);
+      __syncthreads();
+    }
 }
 
 }  // namespace
@@ -265,19 +280,19 @@ cudaError_t launch_tree_combine(const TreeParams& p, int bf16, cudaStream_t st) 
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
   }
+  // few rows: fewer of a CTA, by more shares of their parts; many: a CTA goes through more of its tile's
   int rows_here = 1024 / p.dv, shares = 1;
-  const auto blocks_of = [&](int rows) {
-    return (long long)p.w.heads * (((long long)p.w.N * p.w.GH + rows - 1) / rows);
-  };
+  const auto blocks_of = [&](int rows) { return (long long)p.tiles * ((p.w.R + rows - 1) / rows); };
   while (rows_here > 1 && shares < 8 && blocks_of(rows_here / 2) <= 2 * kDenseSms) {
     rows_here /= 2;
     shares *= 2;
   }
-  const long long blocks = blocks_of(rows_here);
-  if (blocks <= 0) return cudaSuccess;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int groups = (p.w.R + rows_here - 1) / rows_here;
+  const long long want = (kJoinCtas * (long long)kDenseSms + p.tiles - 1) / (p.tiles > 0 ? p.tiles : 1);
+  const int split = want < groups ? (int)want : groups;
+  if (p.tiles <= 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)p.tiles, (unsigned)split);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};

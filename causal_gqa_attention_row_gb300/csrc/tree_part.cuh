@@ -7,10 +7,16 @@
 // as many equal pieces as there are slots (CTAs, or halves of one); a slot walks its piece, a unit
 // for each item that it meets. So all slots have the same work whatever the lengths are, an item
 // has as many units as pieces touch its tiles, and neither a list of units nor a launch to make
-// one is needed: a CTA sums up the lengths for itself (1 to 2 us; the planner of the shared
-// prefixes, a launch of its own, takes 8). From one unit to the next in a walk the item or the
-// slot moves on by one, so item + slot numbers the units without a gap that matters, and the place
-// of a unit's partial result follows from it.
+// one is needed: a CTA sums up the lengths for itself (the planner of the shared prefixes, a
+// launch of its own, takes 8 us). From one unit to the next in a walk the item or the slot moves
+// on by one, so item + slot numbers the units without a gap that matters, and the place of a
+// unit's partial result follows from it.
+//
+// There are two lines. Where a sequence has two row tiles or more (of the same heads), pairs of them lie on the
+// first, cut for the CTAs: the halves of a CTA take a tile each of the same keys at the same time, so
+// that the second finds them in L2. (As items of their own, 8 sequences of two row tiles behind 24,600 keys
+// read every key twice from HBM: 257 us.) Single row tiles lie on the second, cut for all the
+// halves. Every slot has its piece of both.
 #pragma once
 
 #include "common.cuh"
@@ -18,11 +24,11 @@
 
 namespace gqa {
 
-// A sequence in shared memory; entry B closes the line.
-struct alignas(16) TreeSeq {
-  int cost0, item0, row0, hist;
+// A sequence in shared memory; entry B closes the lines. [0] the line of pairs, [1] that of single tiles.
+struct alignas(8) TreeSeq {
+  int cost0[2], item0[2], row0, hist;
 };
-static_assert(sizeof(TreeSeq) * (kTreeSeqs + 1) + 12 * 8 <= 16384, "the sequences' table and the scan's sums");
+static_assert(sizeof(TreeSeq) * (kTreeSeqs + 1) + 12 * 16 <= 16384, "the sequences' table and the scan's sums");
 
 // Row tiles, key tiles and the first key (on a block's boundary) of a sequence of n > 0 rows behind hist.
 struct TreeShape {
@@ -35,22 +41,32 @@ __device__ __forceinline__ TreeShape tree_shape(const TreeWork& w, int n, int hi
   s.T = (hist + n - s.key0 + 127) / 128;
   return s;
 }
+// Items of each of its head chunks on line x.
+__device__ __forceinline__ int tree_items(const TreeWork& w, int tiles, int x) {
+  return x == 0 ? (w.pair_slots ? tiles >> 1 : 0) : w.pair_slots ? tiles & 1 : tiles;
+}
+__device__ __forceinline__ int tree_slots(const TreeWork& w, int x) { return x == 0 ? w.pair_slots : w.slots; }
 
-// The line, by all THREADS of a CTA; `seq` (and the sums behind it) in shared memory. Ends with a barrier. CTA
+// The slot whose piece holds place x of a line of length C cut for S.
+__device__ __forceinline__ int tree_slot_of(int C, int S, int x) {
+  return (int)((((long long)x + 1) * S - 1) / C);
+}
+
+// The lines, by all THREADS of a CTA; `seq` (and the sums behind it) in shared memory. Ends with a barrier. CTA
 // `cta` of `ctas` also writes its share of what the join reads, and CTA 0 reports lengths out of range.
 template <int THREADS>
 __device__ void tree_line(const TreeWork& w, TreeSeq* seq, int cta, int ctas) {
   constexpr int kWarps = THREADS / 32, kEach = (kTreeSeqs + THREADS - 1) / THREADS;
-  int2* sums = reinterpret_cast<int2*>(seq + kTreeSeqs + 1);
+  int4* sums = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(seq + kTreeSeqs + 1) + 15) & ~uintptr_t(15));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   TreeSeq mine[kEach];
   int n_of[kEach];
-  int cost = 0, items = 0;
+  int4 sum = make_int4(0, 0, 0, 0);  // costs, items
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     const int b = tid * kEach + k;
-    mine[k] = TreeSeq{0, 0, 0, 0};
+    mine[k] = TreeSeq{};
     n_of[k] = 0;
     if (b < w.B) {
       const int s0 = __ldg(w.row_starts + b), s1 = __ldg(w.row_starts + b + 1), hist = w.offsets ? __ldg(w.offsets + b) : 0;
@@ -64,73 +80,87 @@ __device__ void tree_line(const TreeWork& w, TreeSeq* seq, int cta, int ctas) {
   }
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    mine[k].cost0 = cost;
-    mine[k].item0 = items;
+    mine[k].cost0[0] = sum.x;
+    mine[k].cost0[1] = sum.y;
+    mine[k].item0[0] = sum.z;
+    mine[k].item0[1] = sum.w;
     if (n_of[k] > 0) {
       const TreeShape s = tree_shape(w, n_of[k], mine[k].hist);
-      items += w.heads * s.tiles;
-      cost += w.heads * s.tiles * (s.T + 1);
+      const int pairs = w.heads * tree_items(w, s.tiles, 0), singles = w.heads * tree_items(w, s.tiles, 1);
+      sum.x += pairs * (s.T + 1);
+      sum.y += singles * (s.T + 1);
+      sum.z += pairs;
+      sum.w += singles;
     }
   }
-  int2 x = make_int2(cost, items);
+  int4 x = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int a = __shfl_up_sync(0xffffffffu, x.x, off), b = __shfl_up_sync(0xffffffffu, x.y, off);
-    if (lane >= off) {
-      x.x += a;
-      x.y += b;
-    }
+    const int c = __shfl_up_sync(0xffffffffu, x.z, off), d = __shfl_up_sync(0xffffffffu, x.w, off);
+    if (lane >= off) x = make_int4(x.x + a, x.y + b, x.z + c, x.w + d);
   }
   if (lane == 31) sums[warp] = x;
   bad = __syncthreads_or(bad);
-  int2 before = make_int2(0, 0), all = make_int2(0, 0);
+  int4 before = make_int4(x.x - sum.x, x.y - sum.y, x.z - sum.z, x.w - sum.w), all = make_int4(0, 0, 0, 0);
 #pragma unroll
   for (int v = 0; v < kWarps; ++v) {
-    const int2 s = sums[v];
-    if (v < warp) {
-      before.x += s.x;
-      before.y += s.y;
-    }
-    all.x += s.x;
-    all.y += s.y;
+    const int4 s = sums[v];
+    if (v < warp) before = make_int4(before.x + s.x, before.y + s.y, before.z + s.z, before.w + s.w);
+    all = make_int4(all.x + s.x, all.y + s.y, all.z + s.z, all.w + s.w);
   }
-  before.x += x.x - cost;
-  before.y += x.y - items;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     const int b = tid * kEach + k;
-    mine[k].cost0 += before.x;
-    mine[k].item0 += before.y;
+    mine[k].cost0[0] += before.x;
+    mine[k].cost0[1] += before.y;
+    mine[k].item0[0] += before.z;
+    mine[k].item0[1] += before.w;
     if (b < w.B) seq[b] = mine[k];
-    if (b % ctas == cta && b < w.B) {
-      int4* rec = reinterpret_cast<int4*>(w.rec + b);
-      rec[0] = make_int4(mine[k].row0, n_of[k], mine[k].cost0, mine[k].item0);
-      rec[1] = make_int4(mine[k].hist, 0, 0, 0);
-    }
   }
   if (tid == 0) {
-    seq[w.B] = TreeSeq{all.x, all.y, 0, 0};
+    seq[w.B] = TreeSeq{{all.x, all.y}, {all.z, all.w}, 0, 0};
     if (cta == 0) {
-      w.line[0] = all.x;
-      w.line[1] = min(w.slots, all.x);
+      w.line[0] = 2 * all.z + all.w;  // row tiles
       if (bad) raise_error(w.err, kErrBounds);
     }
   }
   __syncthreads();
-  // which sequence a row is of: a hint that the join checks, since nothing is written for rows outside
+  // ---- what the join reads of this CTA's sequences: for each row tile its rows and its parts
   for (int b = cta; b < w.B; b += ctas) {
-    if ((b + 1 < w.B ? seq[b + 1].item0 : all.y) == seq[b].item0) continue;
-    const int s0 = seq[b].row0, n = __ldg(w.row_starts + b + 1) - s0;
-    for (int i = tid; i < n; i += THREADS) w.row_seq[s0 + i] = b;
+    const TreeSeq q = seq[b];
+    const int first = 2 * q.item0[0] + q.item0[1], tiles_all = 2 * seq[b + 1].item0[0] + seq[b + 1].item0[1] - first;
+    if (tiles_all == 0) continue;
+    const int n = __ldg(w.row_starts + b + 1) - q.row0;
+    const TreeShape s = tree_shape(w, n, q.hist);
+    for (int e = tid; e < tiles_all; e += THREADS) {
+      const int hc = e / s.tiles, tile = e - hc * s.tiles, paired = 2 * tree_items(w, s.tiles, 0);
+      const int x = tile >= paired, each = tree_items(w, s.tiles, x);
+      const int in = hc * each + (x ? tile - paired : tile >> 1);  // of the sequence's items on line x
+      const int C = x ? all.y : all.x, S = min(tree_slots(w, x), C), at = q.cost0[x] + in * (s.T + 1);
+      const int s0 = tree_slot_of(C, S, at + 1), s1 = tree_slot_of(C, S, at + s.T);
+      TreeRec r;
+      r.row = q.row0 + tile * w.RPT;
+      r.n = min(w.RPT, n - tile * w.RPT);
+      r.hc = hc;
+      r.b = b;
+      r.parts = s1 - s0 + 1;
+      r.stride = x ? 1 : 2;
+      r.part = x ? 2 * (all.z + w.pair_slots) + q.item0[1] + in + s0 : 2 * (q.item0[0] + in + s0) + (tile & 1);
+      r.hist = q.hist;
+      int4* to = reinterpret_cast<int4*>(w.rec + first + e);
+      to[0] = make_int4(r.row, r.n, r.hc, r.b);
+      to[1] = make_int4(r.part, r.parts, r.stride, r.hist);
+    }
   }
 }
 
-// A slot's walk along its piece of the line.
+// A slot's walk along its piece of line x.
 struct TreeWalk {
   int at, end, slot;
 };
-__device__ __forceinline__ TreeWalk tree_walk(const TreeWork& w, const TreeSeq* seq, int slot) {
-  const int C = seq[w.B].cost0, S = min(w.slots, C);
+__device__ __forceinline__ TreeWalk tree_walk(const TreeWork& w, const TreeSeq* seq, int x, int slot) {
+  const int C = seq[w.B].cost0[x], S = min(tree_slots(w, x), C);
   TreeWalk k;
   k.slot = slot;
   k.at = slot < S ? (int)((long long)C * slot / S) : 0;
@@ -138,17 +168,17 @@ __device__ __forceinline__ TreeWalk tree_walk(const TreeWork& w, const TreeSeq* 
   return k;
 }
 
-// The next unit of a walk; false at its end.
+// The next unit of a walk along line x; false at its end. half: the tile of a pair that is wanted.
 struct TreeUnit {
   int b, hc, tile, row0, n, hist;  // hc: KV head and head chunk; the sequence's rows row0 .. row0 + n - 1
   int key0, key1, index;
 };
-__device__ __forceinline__ bool tree_next(const TreeWork& w, const TreeSeq* seq, TreeWalk& k, TreeUnit& u) {
+__device__ __forceinline__ bool tree_next(const TreeWork& w, const TreeSeq* seq, int x, int half, TreeWalk& k, TreeUnit& u) {
   while (k.at < k.end) {
     int lo = 0, hi = w.B;  // the last sequence that starts at or before `at`
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (seq[mid].cost0 <= k.at) lo = mid;
+      if (seq[mid].cost0[x] <= k.at) lo = mid;
       else hi = mid;
     }
     const TreeSeq q = seq[lo];
@@ -157,23 +187,20 @@ __device__ __forceinline__ bool tree_next(const TreeWork& w, const TreeSeq* seq,
     u.hist = q.hist;
     u.n = __ldg(w.row_starts + lo + 1) - q.row0;
     const TreeShape s = tree_shape(w, u.n, q.hist);
-    const int r = k.at - q.cost0, item = r / (s.T + 1), off = r - item * (s.T + 1);
+    const int r = k.at - q.cost0[x], item = r / (s.T + 1), off = r - item * (s.T + 1);
     const int to = min(s.T + 1, off + k.end - k.at);
     k.at += to - off;
     if (to <= 1) continue;  // (the item's first step alone)
-    u.hc = item / s.tiles;
-    u.tile = item - u.hc * s.tiles;
+    const int each = tree_items(w, s.tiles, x);
+    u.hc = item / each;
+    u.tile = x ? 2 * tree_items(w, s.tiles, 0) + item - u.hc * each : 2 * (item - u.hc * each) + half;
     u.key0 = s.key0 + max(off - 1, 0) * 128;
     u.key1 = min(s.key0 + (to - 1) * 128, q.hist + u.n);
-    u.index = q.item0 + item + k.slot;
+    const int at = q.item0[x] + item + k.slot;
+    u.index = x ? 2 * (seq[w.B].item0[0] + w.pair_slots) + at : 2 * at + half;
     return true;
   }
   return false;
-}
-
-// The slot whose piece holds place x of the line.
-__device__ __forceinline__ int tree_slot_of(int C, int S, int x) {
-  return (int)((((long long)x + 1) * S - 1) / C);
 }
 
 // Drafted rows that row i (of n, packed row `row`) sees: bits o .. o + 31 of its mask. Bits below 0 stand

@@ -64,11 +64,11 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<ET, DK, DV>::kCtas)
   grid_dep_wait();
   grid_dep_launch();
   tree_line<kTreeThreads>(w, seq, (int)blockIdx.x, (int)gridDim.x);
-  TreeWalk walk = tree_walk(w, seq, (int)blockIdx.x);
+  TreeWalk walk = tree_walk(w, seq, 1, (int)blockIdx.x);
   const bool placed = w.window > 0 || p.alibi;  // positions matter
   const float cap_k = p.softcap2 > 0.f ? 2.8853900817779268f / p.softcap2 : 0.f;  // 2 log2(e) / cap
   TreeUnit u;
-  while (tree_next(w, seq, walk, u)) {
+  while (tree_next(w, seq, 1, 0, walk, u)) {
     const int i0 = u.tile * w.RPT, n_i = min(w.RPT, u.n - i0), rows = n_i * w.GH, head0 = u.hc * w.GH;
     const int kvh = head0 / p.G, n_tiles = (u.key1 - u.key0 + kTreeKeys - 1) / kTreeKeys;
     const bool busy = (tid >> 5) * 8 < rows;  // this warp's eight rows
