@@ -270,13 +270,12 @@ cudaError_t launch_tree_combine(const TreeParams& p, int bf16, cudaStream_t st) 
   cudaGetDevice(&dev);
   static std::atomic<unsigned long long> attr_done{0};  // per device
   if (dev >= 64 || !(attr_done.load(std::memory_order_acquire) >> dev & 1ull)) {
-    // (the whole L1: see dense_combine_kernel)
-    const auto full = [](const void* k) {
-      return cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1);
-    };
-    cudaError_t e = full(reinterpret_cast<const void*>(tree_combine_kernel<__nv_bfloat16, true>));
-    if (e == cudaSuccess) e = full(reinterpret_cast<const void*>(tree_combine_kernel<__nv_bfloat16, false>));
-    if (e == cudaSuccess) e = full(reinterpret_cast<const void*>(tree_combine_kernel<float, false>));
+    // Shared memory for eight CTAs an SM and the rest for L1: the kernel before leaves 28 KB for that (see
+    // dense_combine_kernel), but asking for all of it leaves room for one CTA (2,059 rows of 32 heads: 37 us).
+    const auto share = [](const void* k) { return cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 28); };
+    cudaError_t e = share(reinterpret_cast<const void*>(tree_combine_kernel<__nv_bfloat16, true>));
+    if (e == cudaSuccess) e = share(reinterpret_cast<const void*>(tree_combine_kernel<__nv_bfloat16, false>));
+    if (e == cudaSuccess) e = share(reinterpret_cast<const void*>(tree_combine_kernel<float, false>));
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
   }
