@@ -97,6 +97,9 @@ struct HalfBars {
 };
 struct DenseBars {
   HalfBars half[2];
+  // pairs of row tiles: the stages of both halves as one ring, a tile for both
+  uint64_t pair_k_full[2 * kDenseStagesMax], pair_k_empty[2 * kDenseStagesMax];
+  uint64_t pair_v_full[2 * kDenseStagesMax], pair_v_empty[2 * kDenseStagesMax];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -133,8 +136,10 @@ __device__ __forceinline__ DenseUnit cross_unit(const DenseParams& p, int x, int
 
 __device__ __forceinline__ int unit_tiles(const DenseUnit& u) { return (u.key1 - u.key0 + kBN - 1) / kBN; }
 
-// What the keys of a unit are: an encoder's, a pool's behind the shared prefixes' plan, a pool's with drafted rows.
-enum { kKeysContig = 0, kKeysShared = 1, kKeysTree = 2 };
+// What the keys of a unit are: an encoder's, a pool's behind the shared prefixes' plan, a pool's with drafted rows, of
+// which no sequence has more than a row tile, or some may. (With the pairs' ring in the code of every call its
+// control warps took 4% longer: 2,059 rows of 64 sequences 158 us, so 164.)
+enum { kKeysContig = 0, kKeysShared = 1, kKeysTree = 2, kKeysTreePairs = 3 };
 
 // The mask of a row's 128 keys from j0 on, of which some are drafted rows.
 template <bool ARMS>
@@ -155,7 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_o, const DenseParams p) {
   using C = DenseCfg<DK, DV>;
-  constexpr bool PAGED = KEYS != kKeysContig, TREE = KEYS == kKeysTree;
+  constexpr bool PAGED = KEYS != kKeysContig, TREE = KEYS == kKeysTree || KEYS == kKeysTreePairs;
+  constexpr bool PAIRS = KEYS == kKeysTreePairs;
+  constexpr int kRing = C::kHalves * C::kStages;
   constexpr int kTileK = C::kTileK, kTileV = C::kTileV, kStages = C::kStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -183,6 +190,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&h.mma_final, 1);
       mbar_init(&h.out_turn, 4);
     }
+    if (PAIRS)
+      for (int s = 0; s < kRing; ++s) {
+        mbar_init(&bars->pair_k_full[s], 1);
+        mbar_init(&bars->pair_k_empty[s], 2);  // the MMA warps of both halves
+        mbar_init(&bars->pair_v_full[s], 1);
+        mbar_init(&bars->pair_v_empty[s], 2);
+      }
     bars->abort_flag = 0;
     fence_barrier_init();
     tc::prefetch_tmap(&tm_q);
@@ -202,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch();  // the next launch may start setting up on the SMs this grid frees
   // drafted rows: the line of all work, in the room that output tiles do not need here
   TreeSeq* tree_seq = reinterpret_cast<TreeSeq*>(smem + C::kOffOut);
-  if (TREE) tree_line<kThreads>(p.tree, tree_seq, (int)blockIdx.x, (int)gridDim.x);
+  if (TREE) tree_line<kThreads>(p.tree, tree_seq, (int)blockIdx.x);
   const int n_units = TREE ? 0 : PAGED ? __ldcg(p.units_listed) : p.n_units;
   const int slots = (int)gridDim.x * C::kHalves;
 
@@ -217,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 0;        // units so far
       int t_all = 0;    // tiles so far
       int k_sent = 0, v_sent = 0;        // K and V tiles requested
+      int t_pair = 0, pair_sent = 0;     // tiles of pairs so far (before any other), those requested here
       int last_q[2] = {-1, -1};          // the last unit of each parity, if a Q copy was requested for it
       bool alive = true;
       // The units of a plan differ in length: the first of each half is its slot, the others
@@ -226,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       DenseUnit next_u = {};
       int next_e = 0;
       TreeWalk walk = {};
-      int tree_line_no = 0;  // pairs of row tiles first, then single ones
-      if (TREE) walk = tree_walk(p.tree, tree_seq, 0, (int)blockIdx.x);
+      int tree_line_no = PAIRS ? 0 : 1;  // pairs of row tiles first, then single ones
+      if (TREE) walk = tree_walk(p.tree, tree_seq, tree_line_no, PAIRS ? (int)blockIdx.x : next_x);
       // paged: lane y < per brings block y of a tile and holds its table entry
       const int per = PAGED ? kBN / p.bs : 1;
       const int my_block = lane % per;
@@ -252,13 +267,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           TreeUnit t;
           if (TREE) {
             bool some = tree_next(p.tree, tree_seq, tree_line_no, w, walk, t);
-            if (!some && tree_line_no == 0) {
+            if (PAIRS && !some && tree_line_no == 0) {
               walk = tree_walk(p.tree, tree_seq, tree_line_no = 1, next_x);
               some = tree_next(p.tree, tree_seq, 1, w, walk, t);
             }
             if (some) {
               const int i0 = t.tile * p.RPT, part = (int)(dense_part_floats(p.own_rows, DV) / 4);
-              next_u = {t.row0 + i0, min(p.RPT, t.n - i0), t.hc * p.GH, t.b, t.key0, t.key1, t.index * part, 0};
+              next_u = {t.row0 + i0, min(p.RPT, t.n - i0), t.hc * p.GH, t.b, t.key0, t.key1, t.index * part, tree_line_no == 0};
             }
           } else if (next_x < n_units) {
             if (PAGED) {
@@ -275,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // its Q and (contiguous) first K and V tiles on their way to L2: units that end
           // together would all wait for HBM at their next one's start
           if (next_u.n_i && next_u.key1 > next_u.key0) {
-            const int own = PAGED && next_u.batch_or_own, seq = PAGED ? 0 : next_u.batch_or_own;
+            const int own = PAGED && !TREE && next_u.batch_or_own, seq = PAGED ? 0 : next_u.batch_or_own;
             if (lane < C::kCBK)
               tc::tma_prefetch_4d(own ? &tm_q1 : &tm_q, lane * 64, next_u.head0, next_u.i0, seq);
             if (!PAGED && lane < C::kCBK)
@@ -298,10 +313,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // last S of the previous unit is done
         bool ok = true;
         if (n >= 2) ok = warp_wait_tc(&hb.unit_free[us], ((n >> 1) - 1) & 1, bars, p.err);
+        const bool pair = PAIRS && u.n_i > 0 && u.batch_or_own;
+        if (PAIRS && t_pair > 0 && t_all == 0) {
+          if (pair) {
+            ok = ok && warp_wait_tc(&bars->pair_k_empty[(t_pair - 1) % kRing], ((t_pair - 1) / kRing) & 1, bars, p.err);
+          } else {  // the pairs are over: this half has its stages for itself once both have done with the ring
+            for (int s = 0; ok && s < kRing; ++s) {
+              const int last = (t_pair - 1 - s) / kRing;  // phase of the stage's last tile
+              if (t_pair > s) ok = warp_wait_tc(&bars->pair_k_empty[s], last & 1, bars, p.err);
+              if (ok && t_pair > s) ok = warp_wait_tc(&bars->pair_v_empty[s], last & 1, bars, p.err);
+            }
+          }
+        }
         if (ok && t_all > 0)
           ok = warp_wait_tc(&hb.k_empty[(t_all - 1) % kStages], ((t_all - 1) / kStages) & 1, bars, p.err);
         if (!ok) break;
-        const bool small = PAGED && u.batch_or_own;
+        const bool small = PAGED && !TREE && u.batch_or_own;
         if (lane == 0) {
           hb.unit[us] = u;
           if (tiles > 0)
@@ -317,8 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tiles > 0 && lane < C::kCBK)
           tc::tma_load_4d(sm + lane * kBlk, small ? &tm_q1 : &tm_q, lane * 64, u.head0, u.i0,
                           PAGED ? 0 : u.batch_or_own, &hb.q_full[us]);
-        for (int j = 0; j < tiles; ++j, ++t_all) {
-          const int st = t_all % kStages;
+        for (int j = 0; j < tiles; ++j) {
+          const int st = pair ? t_pair % kRing : t_all % kStages;
           // a block that holds no key, or whose entry is out of range (flagged), loads from
           // past the end of the pool: the TMA engine fills it with zeros
           int blk = e;
@@ -331,16 +358,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {  // the K tile, then the V tile
+            if (pair && kv != w) continue;  // (of a pair the first half's producer brings K, the second's V)
             uint64_t* full = kv ? &hb.v_full[st] : &hb.k_full[st];
-            if (t_all >= kStages) {
+            if (pair) {
+              full = kv ? &bars->pair_v_full[st] : &bars->pair_k_full[st];
+              if (t_pair >= kRing)
+                ok = warp_wait_tc(kv ? &bars->pair_v_empty[st] : &bars->pair_k_empty[st], (t_pair / kRing - 1) & 1, bars, p.err);
+              if (!ok) break;
+            } else if (t_all >= kStages) {
               ok = warp_wait_tc(kv ? &hb.v_empty[st] : &hb.k_empty[st], (t_all / kStages - 1) & 1, bars, p.err);
               if (!ok) break;
             }
             // test hook: withheld, the first K tile is never requested (nothing is left in
             // flight), so the first wait on it runs into its bound and the half gives up
-            if (p.debug_withhold && t_all == 0 && !kv) continue;
+            if (p.debug_withhold && t_all + t_pair == 0 && !kv) continue;
             const int ncb = kv ? C::kCBV : C::kCBK;
             unsigned char* dst = sm + (kv ? C::kOffV + st * kTileV : C::kOffK + st * kTileK);
+            if (pair)
+              dst = smem + st % C::kHalves * C::kHalfBytes +
+                    (kv ? C::kOffV + st / C::kHalves * kTileV : C::kOffK + st / C::kHalves * kTileK);
             const CUtensorMap* tm = kv ? &tm_v : &tm_k;
             if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(ncb * kBlk));
             __syncwarp();
@@ -350,12 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::tma_load_4d(dst + lane * p.bs * 128 * ncb, tm, 0, 0, 0, (blk * p.Hkv + kvh) * (p.bs / 8), full);
             }
             __syncwarp();
-            (kv ? v_sent : k_sent) = t_all + 1;
+            (pair ? pair_sent : kv ? v_sent : k_sent) = (pair ? t_pair : t_all) + 1;
           }
           if (!ok) {
             alive = false;
             break;
           }
+          ++(pair ? t_pair : t_all);
           fetch_ahead();  // one step a tile
         }
       }
@@ -366,8 +403,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (last_q[s] >= 0) landed &= mbar_wait(&hb.q_full[s], (last_q[s] >> 1) & 1);
         for (int s = 0; s < kStages; ++s) {
           const int k_last = (k_sent - 1 - s) / kStages, v_last = (v_sent - 1 - s) / kStages;  // phase of the last tile
-          if (k_sent > s && !(p.debug_withhold && k_last == 0 && s == 0)) landed &= mbar_wait(&hb.k_full[s], k_last & 1);
+          if (k_sent > s && !(p.debug_withhold && t_pair == 0 && k_last == 0 && s == 0)) landed &= mbar_wait(&hb.k_full[s], k_last & 1);
           if (v_sent > s) landed &= mbar_wait(&hb.v_full[s], v_last & 1);
+        }
+        for (int s = 0; PAIRS && s < kRing; ++s) {
+          const int last = (pair_sent - 1 - s) / kRing;
+          if (pair_sent > s && !(p.debug_withhold && w == 0 && last == 0 && s == 0))
+            landed &= mbar_wait(w ? &bars->pair_v_full[s] : &bars->pair_k_full[s], last & 1);
         }
         if (!landed) raise_error(p.err, kErrTimeout);
       }
@@ -390,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kLag = C::kAlias ? 0 : 1;
       bool ok = true;
       int t_all = 0;  // tiles before this unit
+      int t_pair = 0;  // those of pairs, which come first
       for (int n = 0; ok; ++n) {
         const int us = n & 1;
         ok = warp_wait_tc(&hb.q_full[us], (n >> 1) & 1, bars, p.err);
@@ -401,24 +444,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           hidden = first_visible_key(tree_seq[hb.unit[us].seq].hist, p.window) - hb.unit[us].key0;
         else if (ARMS && !TREE && p.window > 0 && hb.unit[us].batch_or_own)
           hidden = first_visible_key(__ldg(p.seq_lens + hb.unit[us].seq) - 1, p.window) - hb.unit[us].key0;
+        const bool pair = PAIRS && n_i > 0 && hb.unit[us].batch_or_own;
         __syncwarp();
         if (lane == 0) mbar_arrive(&hb.unit_free[us]);
         if (n_i == 0) break;
         const int tiles = (keys + kBN - 1) / kBN;
+        if (pair) t_pair = t_all + tiles;
+        // stage and phase of tile t, and where its K and V lie
+        const auto stage = [&](int t) { return pair ? t % kRing : (t - t_pair) % kStages; };
+        const auto phase = [&](int t) { return (pair ? t / kRing : (t - t_pair) / kStages) & 1; };
+        const auto at_k = [&](int st) {
+          return pair ? smem + st % C::kHalves * C::kHalfBytes + C::kOffK + st / C::kHalves * kTileK : sm + C::kOffK + st * kTileK;
+        };
+        const auto at_v = [&](int st) {
+          return pair ? smem + st % C::kHalves * C::kHalfBytes + C::kOffV + st / C::kHalves * kTileV : sm + C::kOffV + st * kTileV;
+        };
 #pragma unroll 1
         for (int i = 0; ok && i < tiles + kLag && tiles > 0; ++i) {
           if (i < tiles) {  // S = Q K^T of tile i
-            const int t = t_all + i, st = t % kStages;
+            const int t = t_all + i, st = stage(t);
             // its columns are free once the previous tile's S is in registers (d_v = 64), or its
             // PV has read the P that lies over them (d_v = 128)
             if (t > 0) ok = warp_wait_tc(C::kAlias ? &hb.o_done : &hb.s_free, (t - 1) & 1, bars, p.err);
-            ok = ok && warp_wait_tc(&hb.k_full[st], (t / kStages) & 1, bars, p.err);
+            ok = ok && warp_wait_tc(pair ? &bars->pair_k_full[st] : &hb.k_full[st], phase(t), bars, p.err);
             if (!ok) break;
             tc::fence_after_sync();
             // (the descriptors are built here from the buffers' addresses: as loop invariants
             // all of them were kept, in more registers than the control warps have)
             const uint64_t dQ = kHiQ | fresh(smem_u32(sm) >> 4);
-            const uint64_t dK = kHiK | fresh(smem_u32(sm + C::kOffK + st * kTileK) >> 4);
+            const uint64_t dK = kHiK | fresh(smem_u32(at_k(st)) >> 4);
             if (tc::elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < DK / 16; ++kk) {
@@ -426,20 +480,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::mma_f16_ss(dS0, dQ + (at >> 4), dK + (at_k >> 4), idS, kk > 0);
               }
               tc::mma_commit(&hb.s_full);
-              tc::mma_commit(&hb.k_empty[st]);  // the K stage is free once S is done
+              tc::mma_commit(pair ? &bars->pair_k_empty[st] : &hb.k_empty[st]);  // the K stage is free once S is done
             }
             __syncwarp();
           }
           const int k = i - kLag;
           if (k >= 0) {  // O += P V of tile k
-            const int t = t_all + k, st = t % kStages;
-            ok = warp_wait_tc(&hb.v_full[st], (t / kStages) & 1, bars, p.err);
+            const int t = t_all + k, st = stage(t);
+            ok = warp_wait_tc(pair ? &bars->pair_v_full[st] : &hb.v_full[st], phase(t), bars, p.err);
             if (!ok) break;
             // zeros for the rows behind the last key and for those before the first one that the row
             // sees (the swizzle moves chunks within a row only)
             const int valid = keys - k * kBN, skip = ARMS ? hidden - k * kBN : 0;
             if (valid < kBN || (ARMS && skip > 0)) {
-              unsigned char* dst = sm + C::kOffV + st * kTileV + lane / 8 % C::kCBV * kNextCols + lane % 8 * 16;
+              unsigned char* dst = at_v(st) + lane / 8 % C::kCBV * kNextCols + lane % 8 * 16;
 #pragma unroll 1
               for (int row = (ARMS && skip > 0 ? 0 : valid) + lane / (8 * C::kCBV); row < kBN; row += 4 / C::kCBV)
                 if (!ARMS || row >= valid || row < skip)
@@ -450,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = warp_wait_tc(C::kAlias ? &hb.p_half : &hb.p_full, t & 1, bars, p.err);
             if (!ok) break;
             tc::fence_after_sync();
-            const uint64_t dV = kHiV | fresh(smem_u32(sm + C::kOffV + st * kTileV) >> 4);
+            const uint64_t dV = kHiV | fresh(smem_u32(at_v(st)) >> 4);
             constexpr int kSteps = kBN / 16, kTurn = C::kAlias ? kSteps / 2 : kSteps;
 #pragma unroll
             for (int k0 = 0; k0 < kSteps; k0 += kTurn) {
@@ -465,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tc::mma_f16_ts(dO, tP0 + kk * 8, dV + kk * (kNextRowsV >> 3), idO, (k > 0 || kk > 0));
                 if (k0 + kTurn == kSteps) {
                   tc::mma_commit(&hb.o_done);
-                  tc::mma_commit(&hb.v_empty[st]);
+                  tc::mma_commit(pair ? &bars->pair_v_empty[st] : &hb.v_empty[st]);
                 }
               }
               __syncwarp();
@@ -496,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_addr + C::col_o(wg);
     const uint32_t tP = tmem + lane_addr + C::col_p(wg);
     const float2 qs2 = make_float2(qs, qs);
+    if (TREE) tree_publish(p.tree, tree_seq, (int)blockIdx.x, (int)gridDim.x, (int)threadIdx.x, 128 * kWG);
     bool alive = wg < C::kHalves;
     int t_all = 0;  // tiles so far: the phase of every barrier of the tile loop
     int turn = 0;   // steps of output tiles so far: the phase of out_turn
@@ -958,7 +1013,7 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtens
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
   }
-  const int n = KEYS == kKeysTree ? max(p.tree.slots, p.tree.pair_slots) : KEYS == kKeysShared ? kDenseSms : p.n_units;
+  const int n = KEYS >= kKeysTree ? max(p.tree.slots, p.tree.pair_slots) : KEYS == kKeysShared ? kDenseSms : p.n_units;
   const int grid = n < kDenseSms ? n : kDenseSms;
   if (grid <= 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
@@ -977,6 +1032,11 @@ template <int DK, int DV>
 cudaError_t launch_w(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtensorMap& tk, const CUtensorMap& tv,
                      const CUtensorMap& to, const DenseParams& p, bool arms, cudaStream_t st) {
   if (!p.tables) return launch_d<DK, DV, false, kKeysContig>(tq, tq1, tk, tv, to, p, st);
+  if constexpr (DenseCfg<DK, DV>::kHalves == 2) {
+    if (p.tree.pair_slots)
+      return arms ? launch_d<DK, DV, true, kKeysTreePairs>(tq, tq1, tk, tv, to, p, st)
+                  : launch_d<DK, DV, false, kKeysTreePairs>(tq, tq1, tk, tv, to, p, st);
+  }
   if (p.tree.row_starts)
     return arms ? launch_d<DK, DV, true, kKeysTree>(tq, tq1, tk, tv, to, p, st)
                 : launch_d<DK, DV, false, kKeysTree>(tq, tq1, tk, tv, to, p, st);

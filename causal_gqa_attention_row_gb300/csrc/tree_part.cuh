@@ -52,10 +52,10 @@ __device__ __forceinline__ int tree_slot_of(int C, int S, int x) {
   return (int)((((long long)x + 1) * S - 1) / C);
 }
 
-// The lines, by all THREADS of a CTA; `seq` (and the sums behind it) in shared memory. Ends with a barrier. CTA
-// `cta` of `ctas` also writes its share of what the join reads, and CTA 0 reports lengths out of range.
+// The lines, by all THREADS of a CTA; `seq` (and the sums behind it) in shared memory. Ends with a barrier. CTA 0
+// reports lengths out of range.
 template <int THREADS>
-__device__ void tree_line(const TreeWork& w, TreeSeq* seq, int cta, int ctas) {
+__device__ void tree_line(const TreeWork& w, TreeSeq* seq, int cta) {
   constexpr int kWarps = THREADS / 32, kEach = (kTreeSeqs + THREADS - 1) / THREADS;
   int4* sums = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(seq + kTreeSeqs + 1) + 15) & ~uintptr_t(15));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -126,18 +126,22 @@ __device__ void tree_line(const TreeWork& w, TreeSeq* seq, int cta, int ctas) {
     }
   }
   __syncthreads();
-  // ---- what the join reads of this CTA's sequences: for each row tile its rows and its parts
+}
+
+// What the join reads: for each row tile of this CTA's share of the sequences its rows and its parts. By `threads`
+// threads of the CTA that have nothing else to do yet (before the first load it took 1 us of the call).
+__device__ __forceinline__ void tree_publish(const TreeWork& w, const TreeSeq* seq, int cta, int ctas, int tid, int threads) {
   for (int b = cta; b < w.B; b += ctas) {
     const TreeSeq q = seq[b];
     const int first = 2 * q.item0[0] + q.item0[1], tiles_all = 2 * seq[b + 1].item0[0] + seq[b + 1].item0[1] - first;
     if (tiles_all == 0) continue;
     const int n = __ldg(w.row_starts + b + 1) - q.row0;
     const TreeShape s = tree_shape(w, n, q.hist);
-    for (int e = tid; e < tiles_all; e += THREADS) {
+    for (int e = tid; e < tiles_all; e += threads) {
       const int hc = e / s.tiles, tile = e - hc * s.tiles, paired = 2 * tree_items(w, s.tiles, 0);
       const int x = tile >= paired, each = tree_items(w, s.tiles, x);
       const int in = hc * each + (x ? tile - paired : tile >> 1);  // of the sequence's items on line x
-      const int C = x ? all.y : all.x, S = min(tree_slots(w, x), C), at = q.cost0[x] + in * (s.T + 1);
+      const int C = seq[w.B].cost0[x], S = min(tree_slots(w, x), C), at = q.cost0[x] + in * (s.T + 1);
       const int s0 = tree_slot_of(C, S, at + 1), s1 = tree_slot_of(C, S, at + s.T);
       TreeRec r;
       r.row = q.row0 + tile * w.RPT;
@@ -146,7 +150,7 @@ __device__ void tree_line(const TreeWork& w, TreeSeq* seq, int cta, int ctas) {
       r.b = b;
       r.parts = s1 - s0 + 1;
       r.stride = x ? 1 : 2;
-      r.part = x ? 2 * (all.z + w.pair_slots) + q.item0[1] + in + s0 : 2 * (q.item0[0] + in + s0) + (tile & 1);
+      r.part = x ? 2 * (seq[w.B].item0[0] + w.pair_slots) + q.item0[1] + in + s0 : 2 * (q.item0[0] + in + s0) + (tile & 1);
       r.hist = q.hist;
       int4* to = reinterpret_cast<int4*>(w.rec + first + e);
       to[0] = make_int4(r.row, r.n, r.hc, r.b);
@@ -163,8 +167,10 @@ __device__ __forceinline__ TreeWalk tree_walk(const TreeWork& w, const TreeSeq* 
   const int C = seq[w.B].cost0[x], S = min(tree_slots(w, x), C);
   TreeWalk k;
   k.slot = slot;
-  k.at = slot < S ? (int)((long long)C * slot / S) : 0;
-  k.end = slot < S ? (int)((long long)C * (slot + 1) / S) : 0;
+  // C * slot / S in 32 bits (by 64-bit divisions a walk began 0.5 us later)
+  const int each = S > 0 ? C / S : 0, rest = C - each * S;
+  k.at = slot < S ? each * slot + rest * slot / S : 0;
+  k.end = slot < S ? each * (slot + 1) + rest * (slot + 1) / S : 0;
   return k;
 }
 

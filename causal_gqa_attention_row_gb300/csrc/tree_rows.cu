@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<ET, DK, DV>::kCtas)
   const TreeWork& w = p.w;
   grid_dep_wait();
   grid_dep_launch();
-  tree_line<kTreeThreads>(w, seq, (int)blockIdx.x, (int)gridDim.x);
+  tree_line<kTreeThreads>(w, seq, (int)blockIdx.x);
+  tree_publish(w, seq, (int)blockIdx.x, (int)gridDim.x, tid, kTreeThreads);
   TreeWalk walk = tree_walk(w, seq, 1, (int)blockIdx.x);
   const bool placed = w.window > 0 || p.alibi;  // positions matter
   const float cap_k = p.softcap2 > 0.f ? 2.8853900817779268f / p.softcap2 : 0.f;  // 2 log2(e) / cap
