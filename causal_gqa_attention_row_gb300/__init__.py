@@ -571,10 +571,30 @@ def kv_append_paged_rows(q, k_new, v_new, q_out, k_pool, v_pool, block_tables, r
     return q_out
 
 
-def _i64(t):
-    if t is not None and t.dtype != torch.int64:
-        raise TypeError("slots and tree masks must be int64")
-    return _p(t)
+# The calls of a step that verifies drafted tokens take ten tensors and more, and the small ones last 3 to 12 us on
+# the GPU: their arguments are looked at once each, and go as plain numbers (with the helpers above, which build an
+# object for each pointer, kv_plan_rows took 12 us of a Grace core).
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _at(t, dev, dtype):
+    """The address of a contiguous tensor of the given type on device `dev`; None stays None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"expected a tensor of {dtype}, got {t.dtype}")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("tensors must be contiguous and live on the current CUDA device")
+    return t.data_ptr()
+
+
+def _number(dtype):
+    if dtype is _BF16:
+        return BF16
+    if dtype is _F32:
+        return F32
+    raise TypeError(f"unsupported dtype {dtype}")
 
 
 def kv_plan_rows(seq_lens, new_rows, block_tables, blocks_in, blocks_out, free_list, free_in, free_out, row_starts, positions,
@@ -595,15 +615,17 @@ def kv_plan_rows(seq_lens, new_rows, block_tables, blocks_in, blocks_out, free_l
         if tree_mask.dim() != 2 or tree_mask.shape[0] != N or parents.numel() != N:
             raise ValueError("parents must be [N] and tree_mask [N, words]")
         words = tree_mask.shape[1]
-    if (any(x is not None and x.numel() != B for x in (seq_lens, new_rows, blocks_in, blocks_out, keep_blocks)) or
-            row_starts.numel() != B + 1 or slots.numel() != N or free_in.numel() < 1 or free_out.numel() != 2):
+    if (seq_lens.numel() != B or new_rows.numel() != B or blocks_in.numel() != B or blocks_out.numel() != B or
+            (keep_blocks is not None and keep_blocks.numel() != B) or row_starts.numel() != B + 1 or slots.numel() != N or
+            free_in.numel() < 1 or free_out.numel() != 2):
         raise ValueError("the lengths, the blocks, row_starts, positions, slots and the list's counts do not agree")
-    _here(seq_lens, new_rows, block_tables, blocks_in, blocks_out, keep_blocks, free_list, free_in, free_out, row_starts,
-          positions, slots, parents, tree_mask)
+    dev = torch.cuda.current_device()
     _check(load().kv_plan_rows(
-        _i32(seq_lens), _i32(new_rows), _i32(block_tables), _i32(blocks_in), _i32(blocks_out), _i32(keep_blocks),
-        _i32(free_list), _i32(free_in), _i32(free_out), _i32(row_starts), _i32(positions), _i64(slots), _i32(parents),
-        _i64(tree_mask), words, N, B, mbps, free_list.numel(), int(block_size), _stream(stream)), "kv_plan_rows")
+        _at(seq_lens, dev, _I32), _at(new_rows, dev, _I32), _at(block_tables, dev, _I32), _at(blocks_in, dev, _I32),
+        _at(blocks_out, dev, _I32), _at(keep_blocks, dev, _I32), _at(free_list, dev, _I32), _at(free_in, dev, _I32),
+        _at(free_out, dev, _I32), _at(row_starts, dev, _I32), _at(positions, dev, _I32), _at(slots, dev, _I64),
+        _at(parents, dev, _I32), _at(tree_mask, dev, _I64), words, N, B, mbps, free_list.numel(), block_size,
+        _raw_stream(dev) if stream is None else stream.cuda_stream), "kv_plan_rows")
 
 
 def kv_append_slots(q, k_new, v_new, q_out, k_pool, v_pool, slots, positions=None, rope=None, q_weight=None, k_weight=None,
@@ -611,9 +633,9 @@ def kv_append_slots(q, k_new, v_new, q_out, k_pool, v_pool, slots, positions=Non
     """kv_append_paged_rows with each row's place given: row n is turned by positions[n] (int32 [N]) and its key
     and value go to slot slots[n] = block * bs + row of the pools (int64 [N]; below 0: the row is left out)."""
     N, Hkv, dk = k_new.shape
-    nb, _, bs, dv = v_pool.shape
+    nb, pool_heads, bs, dv = v_pool.shape
     H = 0
-    if v_new.shape != (N, Hkv, dv) or k_pool.shape != (nb, Hkv, bs, dk) or v_pool.shape[1] != Hkv:
+    if v_new.shape != (N, Hkv, dv) or k_pool.shape != (nb, Hkv, bs, dk) or pool_heads != Hkv:
         raise ValueError("k_new, v_new and the pools do not agree")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
@@ -621,21 +643,29 @@ def kv_append_slots(q, k_new, v_new, q_out, k_pool, v_pool, slots, positions=Non
         H = q.shape[1]
         if q.shape != (N, H, dk) or q_out.shape != (N, H, dk):
             raise ValueError("q and q_out must both be [N, H, dk]")
+        _writes_once(q_out)
     if slots.numel() != N or (positions is not None and positions.numel() != N):
         raise ValueError("slots and positions must be [N]")
-    _here(q, k_new, v_new, q_out, k_pool, v_pool, slots, positions, q_weight, k_weight,
-          rope.table if rope is not None else None)
-    _writes_once(q_out)
+    if (q_weight is not None and q_weight.shape != (dk,)) or (k_weight is not None and k_weight.shape != (dk,)):
+        raise ValueError(f"a norm weight must be [{dk}]")
+    dev = torch.cuda.current_device()
+    dt = k_new.dtype
+    for t in (q, k_new, v_new, q_out):
+        if t is not None and (t.dtype is not dt or t.get_device() != dev):
+            raise (TypeError("tensors must share one dtype") if t.dtype is not dt else
+                   ValueError("tensors must live on the current CUDA device"))
+    if rope is not None:
+        _here(rope.table)
     _check(load().kv_append_slots(
-        _view(q, 3), _view(k_new, 3), _view(v_new, 3), _view(q_out, 3), _p(k_pool), _p(v_pool), _i64(slots),
-        _i32(positions), N, nb, bs, H, Hkv, dk, dv, _weight(q_weight, dk), _weight(k_weight, dk), float(eps), _ref(rope),
-        _dtype(q, k_new, v_new, q_out, k_pool, v_pool, q_weight, k_weight), _stream(stream)), "kv_append_slots")
+        _view(q, 3), _view(k_new, 3), _view(v_new, 3), _view(q_out, 3), _at(k_pool, dev, dt), _at(v_pool, dev, dt),
+        _at(slots, dev, _I64), _at(positions, dev, _I32), N, nb, bs, H, Hkv, dk, dv, _at(q_weight, dev, dt),
+        _at(k_weight, dev, dt), eps, _ref(rope), _number(dt), _raw_stream(dev) if stream is None else stream.cuda_stream),
+           "kv_append_slots")
     return q_out
 
 
 def attn_tree_paged_workspace_bytes(N, B, max_rows, max_len, H, Hkv, d_k, d_v, dtype=torch.bfloat16):
-    return int(load().attn_tree_paged_workspace_bytes(N, B, max_rows, max_len, H, Hkv, d_k, d_v,
-                                                      BF16 if dtype == torch.bfloat16 else F32))
+    return int(load().attn_tree_paged_workspace_bytes(N, B, max_rows, max_len, H, Hkv, d_k, d_v, _number(dtype)))
 
 
 def tree_workspace(N, B, max_rows, H, Hkv, d_k, d_v, max_len, dtype=torch.bfloat16, device="cuda"):
@@ -663,14 +693,23 @@ def attn_tree_paged(q, k_pool, v_pool, block_tables, position_offset, row_starts
     if (k_pool.shape != (nb, Hkv, bs, dk) or out.shape != (N, H, dv) or row_starts.numel() != B + 1 or
             (position_offset is not None and position_offset.numel() != B)):
         raise ValueError("q, the pools, the tables, the lengths, row_starts and out do not agree")
-    _here(q, k_pool, v_pool, block_tables, position_offset, row_starts, tree_mask, out, workspace, sinks, alibi_slopes)
-    if any(x is not None and x.numel() != H for x in (sinks, alibi_slopes)):
-        raise ValueError("sinks and alibi_slopes must be float32 [H]")
-    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    dev = torch.cuda.current_device()
+    arms = None
+    if window or softcap or sinks is not None or alibi_slopes is not None:
+        _here(sinks, alibi_slopes)
+        if any(x is not None and x.numel() != H for x in (sinks, alibi_slopes)):
+            raise ValueError("sinks and alibi_slopes must be float32 [H]")
+        arms = _arms(window, softcap, sinks, alibi_slopes)
+    dt, ws = q.dtype, 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("tensors must be contiguous and live on the current CUDA device")
+        ws = workspace.numel() * workspace.element_size()
     _check(load().attn_tree_paged(
-        _p(q), _p(k_pool), _p(v_pool), _i32(block_tables), _i32(position_offset), _i32(row_starts), _i64(tree_mask), _p(out),
-        N, B, int(max_rows), words, mbps, nb, bs, H, Hkv, dk, dv, float(attention_scale), _dtype(q, k_pool, v_pool, out),
-        _p(workspace), ws, _arms(window, softcap, sinks, alibi_slopes), _stream(stream)), "attn_tree_paged")
+        _at(q, dev, dt), _at(k_pool, dev, dt), _at(v_pool, dev, dt), _at(block_tables, dev, _I32),
+        _at(position_offset, dev, _I32), _at(row_starts, dev, _I32), _at(tree_mask, dev, _I64), _at(out, dev, dt), N, B, max_rows,
+        words, mbps, nb, bs, H, Hkv, dk, dv, attention_scale, _number(dt), None if workspace is None else workspace.data_ptr(),
+        ws, arms, _raw_stream(dev) if stream is None else stream.cuda_stream), "attn_tree_paged")
     return out
 
 
@@ -679,23 +718,32 @@ def kv_commit_rows(k_pools, v_pools, block_tables, seq_lens_in, row_starts, path
     (k_pools, v_pools: a tensor [num_blocks, Hkv, bs, d] each layer; v_pools None: keys alone) and sets
     seq_lens_out[b] = seq_lens_in[b] + n_path[b] (may be the same tensor). path int32 [B, max_path], ascending
     indices among the row_starts[b + 1] - row_starts[b] drafted rows; n_path int32 [B]."""
-    k_pools, v_pools = list(k_pools), None if v_pools is None else list(v_pools)
+    layers = len(k_pools)
     B, mbps = block_tables.shape
-    if not k_pools or (v_pools is not None and len(v_pools) != len(k_pools)):
+    if not layers or (v_pools is not None and len(v_pools) != layers):
         raise ValueError("a pool of keys, and with values one of those, for each layer")
-    nb, Hkv, bs, dk = k_pools[0].shape
-    dv = v_pools[0].shape[-1] if v_pools is not None else 0
-    if (any(x.shape != (nb, Hkv, bs, dk) for x in k_pools) or
-            any(x.shape != (nb, Hkv, bs, dv) for x in v_pools or ()) or path.dim() != 2 or path.shape[0] != B or
-            row_starts.numel() != B + 1 or any(x.numel() != B for x in (seq_lens_in, n_path, seq_lens_out))):
+    k_shape, dt = k_pools[0].shape, k_pools[0].dtype
+    nb, Hkv, bs, dk = k_shape
+    v_shape = k_shape if v_pools is None else v_pools[0].shape
+    dv = 0 if v_pools is None else v_shape[3]
+    if (v_shape[:3] != k_shape[:3] or len(v_shape) != 4 or path.dim() != 2 or path.shape[0] != B or row_starts.numel() != B + 1 or
+            seq_lens_in.numel() != B or n_path.numel() != B or seq_lens_out.numel() != B):
         raise ValueError("the pools, the tables, the lengths and the paths do not agree")
-    _here(block_tables, seq_lens_in, row_starts, path, n_path, seq_lens_out, *k_pools, *(v_pools or ()))
-    dt = _dtype(*k_pools, *(v_pools or ()))
-    pointers = ctypes.c_void_p * len(k_pools)
+    if any(x.shape != k_shape for x in k_pools) or any(x.shape != v_shape for x in v_pools or ()):
+        raise ValueError("the layers' pools must be alike")
+    dev = torch.cuda.current_device()
+
+    def addresses(pools):
+        for x in pools:
+            if x.dtype is not dt or x.get_device() != dev or not x.is_contiguous():
+                raise ValueError("pools must share one dtype, be contiguous and live on the current CUDA device")
+        return (ctypes.c_void_p * layers)(*[x.data_ptr() for x in pools])
+
     _check(load().kv_commit_rows(
-        pointers(*[_p(x).value for x in k_pools]), None if v_pools is None else pointers(*[_p(x).value for x in v_pools]),
-        len(k_pools), _i32(block_tables), _i32(seq_lens_in), _i32(row_starts), _i32(path), _i32(n_path), _i32(seq_lens_out),
-        B, path.shape[1], mbps, nb, bs, Hkv, dk, dv, dt, _stream(stream)), "kv_commit_rows")
+        addresses(k_pools), None if v_pools is None else addresses(v_pools), layers, _at(block_tables, dev, _I32),
+        _at(seq_lens_in, dev, _I32), _at(row_starts, dev, _I32), _at(path, dev, _I32), _at(n_path, dev, _I32),
+        _at(seq_lens_out, dev, _I32), B, path.shape[1], mbps, nb, bs, Hkv, dk, dv, _number(dt),
+        _raw_stream(dev) if stream is None else stream.cuda_stream), "kv_commit_rows")
 
 
 def attn_get_device_error(stream=None):

@@ -1013,7 +1013,7 @@ bool tree_layout(int N, int B, int max_rows, int max_len, int H, int Hkv, int d_
   const int seqs = B < gqa::kTreeSeqs ? B : gqa::kTreeSeqs;
   const long long tiles = (long long)(seqs < N ? seqs : N) + (max_rows > t->RPT ? N / t->RPT : 0);
   t->items = tiles * t->heads;
-  const long long steps = t->items * (max_len / 128 + 3);
+  const long long steps = t->items * (max_len / (tc ? 128 : 64) + 3);
   if (steps < t->slots) t->slots = (int)steps;
   // (pairs where a sequence can have two row tiles and a CTA has two halves)
   const bool pairs = tc && max_rows > t->RPT && gqa::dense_tc_slots(d_k) == 2 * gqa::kDenseSms;
@@ -1045,7 +1045,7 @@ size_t attn_tree_paged_workspace_bytes(int N, int B, int max_rows, int max_len, 
   size_t most = 0;
   for (int tc = 0; tc < 2; ++tc) {
     TreeLayout t;
-    if ((!tc || gqa::dense_tc_supported(bf16, d_k, d_v)) &&
+    if ((!tc || gqa::tree_tc_supported(bf16, d_k, d_v)) &&
         tree_layout(N, B, max_rows, max_len, H, Hkv, d_k, d_v, bf16, tc, &t) && t.bytes > most)
       most = t.bytes;
   }
@@ -1072,14 +1072,14 @@ gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool
   bool arms_on;
   const gqa_status sa = apply_arms(arm, arms, &arms_on);
   if (sa != GQA_OK) return sa;
-  const bool tc = gqa::dense_tc_supported(bf16, d_k, d_v, block_size) && attention_scale > 0.f && !arm.alibi;
+  const bool tc = gqa::tree_tc_supported(bf16, d_k, d_v, block_size) && attention_scale > 0.f && !arm.alibi;
   const int capacity = max_blocks_per_seq * block_size;
   TreeLayout t;
   if (!tree_layout(N, B, max_rows, capacity, H, Hkv, d_k, d_v, bf16, tc, &t)) return GQA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < t.bytes) return GQA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return GQA_ERR_INVALID_ARG;
   // places on the line, and partial results in 16-byte steps, are counted in 32 bits
-  if (t.items > INT_MAX / (capacity / 128 + 3) || (t.bytes - t.partial) / 16 > (size_t)INT_MAX) return GQA_ERR_INVALID_ARG;
+  if (t.items > INT_MAX / (capacity / (tc ? 128 : 64) + 3) || (t.bytes - t.partial) / 16 > (size_t)INT_MAX) return GQA_ERR_INVALID_ARG;
   unsigned* err = error_word();
   if (!err) return GQA_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1097,6 +1097,7 @@ gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool
   p.w.capacity = capacity;
   p.w.bs = block_size;
   p.w.window = arm.window;
+  p.w.step_log2 = tc ? 7 : 6;
   p.w.slots = t.slots;
   p.w.pair_slots = t.pair_slots;
   p.tiles = (int)t.items;

@@ -1,5 +1,5 @@
 // dense_tc.cu -- attention without a causal rule on the tcgen05 tensor cores
-// (bf16; (d_k, d_v) = (64, 64), (128, 128) or (192, 128)): rows that all see the same
+// (bf16; (d_k, d_v) = (64, 64), (128, 128) or (192, 128), drafted rows (256, 256) too): rows that all see the same
 // keys, as decoder rows against an encoder's states (attn_cross), the decode rows of
 // sequences that share a prefix against that prefix, and a sequence's decode row against
 // its own keys (attn_decode_shared_prefix).
@@ -71,7 +71,7 @@ struct DenseCfg {
   static constexpr int kTileK = kCBK * kBlk, kTileV = kCBV * kBlk;
   static constexpr bool kAlias = DV > 64;  // P over the first 64 columns of S
   static constexpr int kHalves = DK > 128 ? 1 : 2;
-  static constexpr int kStages = DK > 128 ? 2 : DK > 64 ? 1 : 2;  // K and V stages of a half
+  static constexpr int kStages = DK > 192 ? 1 : DK > 128 ? 2 : DK > 64 ? 1 : 2;  // K and V stages of a half
   __host__ __device__ static constexpr uint32_t col_s(int w) { return kAlias ? (128 + DV) * w : 128 * w; }
   __host__ __device__ static constexpr uint32_t col_o(int w) { return kAlias ? (128 + DV) * w + 128 : 256 + 64 * w; }
   __host__ __device__ static constexpr uint32_t col_p(int w) { return kAlias ? (128 + DV) * w : 384 + 64 * w; }
@@ -1051,6 +1051,10 @@ bool dense_tc_supported(int bf16, int dk, int dv, int bs) {
   return bf16 == 1 && widths && (bs == 0 || (bs % 8 == 0 && kBN % bs == 0));
 }
 
+bool tree_tc_supported(int bf16, int dk, int dv, int bs) {
+  return dense_tc_supported(bf16, dk == 256 && dv == 256 ? 128 : dk, dk == 256 && dv == 256 ? 128 : dv, bs);
+}
+
 int dense_tc_slots(int dk) { return dk > 128 ? kDenseSms : 2 * kDenseSms; }
 
 void dense_rows(int G, int* GH, int* RPT) {
@@ -1064,19 +1068,26 @@ void dense_rows(int G, int* GH, int* RPT) {
 // [n_b, Hkv, S_kv, d] (p.tables NULL) or pools [num_blocks, Hkv, bs, d].
 cudaError_t launch_dense_tc(const void* q, const void* k, const void* v, const DenseParams& p, int n_b, int dk, int dv,
                             bool arms, cudaStream_t st) {
-  if (!dense_tc_supported(1, dk, dv, p.tables ? p.bs : 0) || !(p.qscale > 0.f)) return cudaErrorNotSupported;
+  const bool tree = p.tree.row_starts != nullptr;
+  if (!(tree ? tree_tc_supported : dense_tc_supported)(1, dk, dv, p.tables ? p.bs : 0) || !(p.qscale > 0.f))
+    return cudaErrorNotSupported;
   CUtensorMap tq, tq1, tk, tv, to;
   if (!make_map(&tq, q, dk, p.H, p.n_i, n_b, p.GH, p.RPT)) return cudaErrorInvalidValue;
-  if (!make_map(&tq1, q, dk, p.H, p.n_i, n_b, p.GH, 1)) return cudaErrorInvalidValue;
+  if (tree) tq1 = tq;  // (drafted rows: not used)
+  else if (!make_map(&tq1, q, dk, p.H, p.n_i, n_b, p.GH, 1)) return cudaErrorInvalidValue;
   if (p.tables) {
     if (!make_pool_map(&tk, k, dk, p) || !make_pool_map(&tv, v, dv, p)) return cudaErrorInvalidValue;
   } else {
     if (!make_map(&tk, k, dk, p.S_kv, p.Hkv, n_b, kBN, 1)) return cudaErrorInvalidValue;
     if (!make_map(&tv, v, dv, p.S_kv, p.Hkv, n_b, kBN, 1)) return cudaErrorInvalidValue;
   }
-  if (!make_map(&to, p.out, dv, p.H, p.n_i, n_b, p.GH, p.RPT)) return cudaErrorInvalidValue;
+  if (tree) to = tq;  // (nor this: the join writes the output)
+  else if (!make_map(&to, p.out, dv, p.H, p.n_i, n_b, p.GH, p.RPT)) return cudaErrorInvalidValue;
   if (dk == 64) return launch_w<64, 64>(tq, tq1, tk, tv, to, p, arms, st);
   if (dk == 128) return launch_w<128, 128>(tq, tq1, tk, tv, to, p, arms, st);
+  if (dk == 256)  // (drafted rows alone)
+    return arms ? launch_d<256, 256, true, kKeysTree>(tq, tq1, tk, tv, to, p, st)
+                : launch_d<256, 256, false, kKeysTree>(tq, tq1, tk, tv, to, p, st);
   return launch_w<192, 128>(tq, tq1, tk, tv, to, p, arms, st);
 }
 

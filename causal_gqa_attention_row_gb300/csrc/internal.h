@@ -213,6 +213,7 @@ struct TreeWork {
   int N, B, max_rows, words;
   int heads, GH, RPT, R;           // KV heads times head chunks; heads and rows of a tile; rows of a partial result
   int capacity, bs, window;
+  int step_log2;                   // keys of a tile
   int slots, pair_slots;           // pieces of the line of single tiles, and of pairs (0: no pairs)
   TreeRec* rec;                    // of each row tile
   int* line;                       // [0] the row tiles
@@ -265,6 +266,7 @@ struct DenseParams {
 // rows i per tile.
 void dense_rows(int G, int* GH, int* RPT);
 bool dense_tc_supported(int bf16, int dk, int dv, int bs = 0);
+bool tree_tc_supported(int bf16, int dk, int dv, int bs = 0);  // of drafted rows: (256, 256) too
 // Units that the SMs work on at a time.
 int dense_tc_slots(int dk);
 cudaError_t launch_dense_tc(const void* q, const void* k, const void* v, const DenseParams& p, int n_b, int dk, int dv,

@@ -293,8 +293,8 @@ cudaError_t launch_plan_rows(PlanRows p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
   }
-  // a CTA per sequence, up to four on each SM; slices of a sequence's rows where that leaves room
-  const int most = 4 * kDenseSms;
+  // a CTA per sequence, up to eight on each SM; slices of a sequence's rows where that leaves room
+  const int most = 8 * kDenseSms;
   p.per = (p.B + most - 1) / most;
   const int gx = (p.B + p.per - 1) / p.per;
   const long long rows = (long long)p.N / p.B;

@@ -75,7 +75,7 @@ __device__ __noinline__ void row_again(const TreeParams& p, int b, const Row& r,
   for (int key = first + warp; key < own; key += kJoinThreads / 32) look(key);
   for (int key = r.hist + warp; key < end; key += kJoinThreads / 32) look(key);
   if (!__syncthreads_or(bad)) return;
-  constexpr int kMost = 6;  // columns of a lane: d_k at most 192 on the tensor cores
+  constexpr int kMost = 8;  // columns of a lane
   float q[kMost], o[kMost], m = -INFINITY, l = 0.f;
   const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)r.row * p.H + h) * dk;
 #pragma unroll
@@ -128,7 +128,7 @@ __device__ __noinline__ void row_again(const TreeParams& p, int b, const Row& r,
 // CHECK: the parts come from the tensor cores (above).
 template <typename ET, bool CHECK>
 __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const __grid_constant__ TreeParams p, int shares) {
-  __shared__ float4 acc_s[kJoinThreads];
+  __shared__ float4 acc_s[CHECK ? 2 * kJoinThreads : kJoinThreads];  // (row_again: eight rows of up to 256 columns)
   __shared__ float2 md_s[kJoinThreads];
   __shared__ uint32_t again_s[4];  // rows of the tile (at most 128) to be worked out again
   grid_dep_wait();

@@ -2,7 +2,7 @@
 // (dense_tc.cu, tree_rows.cu) and the one that joins their partial results (tree_combine.cu).
 //
 // An item is a row tile of a sequence (up to RPT of its drafted rows, GH heads of one KV head) with
-// all of the sequence's keys, T key tiles of 128. Items lie one after another on a line, each
+// all of the sequence's keys, T key tiles of 128 (SIMT: 64). Items lie one after another on a line, each
 // T + 1 long: a step for what a unit takes beside its tiles, then its tiles. The line is cut into
 // as many equal pieces as there are slots (CTAs, or halves of one); a slot walks its piece, a unit
 // for each item that it meets. So all slots have the same work whatever the lengths are, an item
@@ -38,7 +38,7 @@ __device__ __forceinline__ TreeShape tree_shape(const TreeWork& w, int n, int hi
   TreeShape s;
   s.key0 = first_visible_key(hist, w.window) / w.bs * w.bs;
   s.tiles = (n + w.RPT - 1) / w.RPT;
-  s.T = (hist + n - s.key0 + 127) / 128;
+  s.T = (hist + n - s.key0 + (1 << w.step_log2) - 1) >> w.step_log2;
   return s;
 }
 // Items of each of its head chunks on line x.
@@ -200,8 +200,8 @@ __device__ __forceinline__ bool tree_next(const TreeWork& w, const TreeSeq* seq,
     const int each = tree_items(w, s.tiles, x);
     u.hc = item / each;
     u.tile = x ? 2 * tree_items(w, s.tiles, 0) + item - u.hc * each : 2 * (item - u.hc * each) + half;
-    u.key0 = s.key0 + max(off - 1, 0) * 128;
-    u.key1 = min(s.key0 + (to - 1) * 128, q.hist + u.n);
+    u.key0 = s.key0 + (max(off - 1, 0) << w.step_log2);
+    u.key1 = min(s.key0 + ((to - 1) << w.step_log2), q.hist + u.n);
     const int at = q.item0[x] + item + k.slot;
     u.index = x ? 2 * (seq[w.B].item0[0] + w.pair_slots) + at : 2 * at + half;
     return true;

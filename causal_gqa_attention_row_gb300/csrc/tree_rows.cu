@@ -249,21 +249,26 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<ET, DK, DV>::kCtas)
               }
           }
         } else {
+const int some = min(kTreeKeys, u.key1 - j0);  // (the last tile's keys)
 #pragma unroll 1
-          for (int k = 0; k < kTreeKeys; ++k) {
-            float e[4];
+          for (int k = 0; k < some; k += 4) {
+            float4 pr[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = sp[(ty * 4 + i) * kPStride + k];
+            for (int i = 0; i < 4; ++i) pr[i] = *reinterpret_cast<const float4*>(sp + (ty * 4 + i) * kPStride + k);
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-              const float4 v = *reinterpret_cast<const float4*>(skv + k * C::kStride + tx * 4 + 64 * c);
+            for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (e[i] != 0.f) {
-                  o[i][c][0] = __ffma2_rn(make_float2(e[i], e[i]), make_float2(v.x, v.y), o[i][c][0]);
-                  o[i][c][1] = __ffma2_rn(make_float2(e[i], e[i]), make_float2(v.z, v.w), o[i][c][1]);
+              for (int c = 0; c < kCols; ++c) {
+                const float4 v = *reinterpret_cast<const float4*>(skv + (k + kk) * C::kStride + tx * 4 + 64 * c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float e = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
+                  if (e != 0.f) {
+                    o[i][c][0] = __ffma2_rn(make_float2(e, e), make_float2(v.x, v.y), o[i][c][0]);
+                    o[i][c][1] = __ffma2_rn(make_float2(e, e), make_float2(v.z, v.w), o[i][c][1]);
+                  }
                 }
-            }
+              }
           }
         }
       }

@@ -563,13 +563,13 @@ gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa
  * A row that sees no key gets zeros; a key that scores -infinity weighs zero. What a row does not see does
  * not reach it, whatever the slot holds, an infinity or NaN included. Sequences with lengths out of range or more
  * rows than max_rows set the device error word, and their rows are left as they are.
- * bf16 with (d_k, d_v) = (64, 64), (128, 128) or (192, 128), block_size a multiple of 8 dividing 128,
+ * bf16 with (d_k, d_v) = (64, 64), (128, 128), (192, 128) or (256, 256), block_size a multiple of 8 dividing 128,
  * attention_scale > 0 and no ALiBi slopes runs on the tcgen05 tensor-core kernel (the probabilities rounded to
  * bf16 for the product with V), every other case on a SIMT kernel of fp32 arithmetic. How a sequence's keys are
  * split depends on the batch, so the last bits of its results do too; repeated calls give the same bits.
  * workspace: at least attn_tree_paged_workspace_bytes(..) bytes, 16-byte aligned, always needed; calls
  * whose kernels may overlap must not share one. The size does for smaller N, B, max_rows and max_len too.
- * H / GH * (N / RPT + B) * (max_blocks_per_seq * block_size / 128 + 3), with GH * RPT = 64 to 128 heads times
+ * H / GH * (N / RPT + B) * (max_blocks_per_seq * block_size / 64 + 3), with GH * RPT = 64 to 128 heads times
  * rows, is at most INT_MAX.
  */
 gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool, const int32_t* block_tables,

@@ -113,7 +113,7 @@ SHAPES = [
 ]
 
 
-@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (192, 128)], ids=str)
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (192, 128), (256, 256)], ids=str)
 @pytest.mark.parametrize("shape", SHAPES, ids=range(len(SHAPES)))
 def test_tensor_cores(gpu_lib, dims, shape):
     g = gpu_lib
@@ -128,7 +128,7 @@ def test_tensor_cores(gpu_lib, dims, shape):
 
 @pytest.mark.parametrize("dt,dims,bs", [(F32, (16, 16), 16), (F32, (32, 32), 8), (F32, (64, 64), 16), (F32, (128, 128), 12),
                                         (F32, (192, 128), 16), (F32, (256, 256), 32), (BF16, (16, 16), 16), (BF16, (32, 32), 1),
-                                        (BF16, (64, 64), 12), (BF16, (128, 128), 256), (BF16, (192, 128), 4), (BF16, (256, 256), 16)], ids=str)
+                                        (BF16, (64, 64), 12), (BF16, (128, 128), 256), (BF16, (192, 128), 4), (BF16, (256, 256), 24)], ids=str)
 @pytest.mark.parametrize("rows,hist,H,Hkv", [([5, 0, 1], [63, 9, 0], 6, 2), ([70, 9, 33], [130, 700, 64], 4, 1),
                                              ([3], [1500], 100, 1)])
 def test_simt(gpu_lib, dt, dims, bs, rows, hist, H, Hkv):
@@ -141,7 +141,7 @@ def test_simt(gpu_lib, dt, dims, bs, rows, hist, H, Hkv):
     assert torch.equal(out, run(g, c, scale, fill=0))
 
 
-PATHS = [(BF16, 64), (BF16, 128), (F32, 64)]
+PATHS = [(BF16, 64), (BF16, 128), (BF16, 256), (F32, 64)]
 
 
 @pytest.mark.parametrize("dt,d", PATHS)
