@@ -157,7 +157,7 @@ struct PlanRows {
   unsigned* err;
   int N, B, words, mbps, num_blocks, bs;
   // set by the launcher
-  int per;                              // sequences of a CTA
+  int per, lanes;                       // sequences of a CTA, threads of a sequence
   int write_rows, write_state, report;  // what this launch writes (see there)
 };
 // Sequences of a call: their prefix sums stay in shared memory.

@@ -11,12 +11,13 @@
 // What it reads and writes is small (20 bytes a sequence, 12 and more a row), so what bounds it is
 // latency: one launch, and in it one chain of loads (the lengths, the block, the store). So no
 // CTA waits for another: each scans all lengths for itself (a thread takes four
-// sequences, 1024 of them a round) and then writes what is its sequences' own. A block that is
+// sequences, 1024 of them a round) and then writes what is its sequences' own, a warp or
+// more for each (a CTA for each sequence had 794 of them of seven rows scan all lengths 794 times:
+// 11 to 13 us). A block that is
 // given back and taken in one call is not read from the list, where another CTA would be
 // writing it, but found at its place in the table that gives it back, by a search over the
 // prefix sums of give_b, which stay in shared memory. The list below `free` is only read, above
-// it only written. Sequences go round by grid x; where a sequence has many rows they are cut into
-// slices by grid y. A row's ancestors are indices that descend, so a thread that walks up from
+// it only written. Where a sequence has many rows they are cut into slices by grid y. A row's ancestors are indices that descend, so a thread that walks up from
 // its row writes the words of the mask from the highest to the lowest and holds one at a time.
 
 #include <atomic>
@@ -51,33 +52,32 @@ __device__ __forceinline__ Req request(const PlanRows& p, int b) {
   return r;
 }
 
-// Exclusive prefix sums of three values over the CTA and their totals. Ends with a barrier.
-__device__ __forceinline__ void scan3(long long (&v)[3], long long (&total)[3], long long (*sums)[kPlanRowsThreads / 32]) {
+// What a scan sums: rows, blocks wanted, blocks given back.
+struct Sums {
+  long long rows;
+  int take, give;
+};
+// Exclusive prefix sums over the CTA and their totals. Ends with a barrier.
+__device__ __forceinline__ void scan(Sums& v, Sums& total, Sums* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x[3] = {v[0], v[1], v[2]};
+  Sums x = v;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1)
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const long long y = __shfl_up_sync(0xffffffffu, x[k], off);
-      if (lane >= off) x[k] += y;
-    }
-  if (lane == 31)
-#pragma unroll
-    for (int k = 0; k < 3; ++k) sums[k][warp] = x[k];
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    long long before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanRowsThreads / 32; ++w) {
-      const long long s = sums[k][w];
-      if (w < warp) before += s;
-      all += s;
-    }
-    v[k] = before + x[k] - v[k];
-    total[k] = all;
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long r = __shfl_up_sync(0xffffffffu, x.rows, off);
+    const int t = __shfl_up_sync(0xffffffffu, x.take, off), g = __shfl_up_sync(0xffffffffu, x.give, off);
+    if (lane >= off) x = Sums{x.rows + r, x.take + t, x.give + g};
   }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  Sums before = {0, 0, 0};
+  total = Sums{0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < kPlanRowsThreads / 32; ++w) {
+    const Sums s = sums[w];
+    if (w < warp) before = Sums{before.rows + s.rows, before.take + s.take, before.give + s.give};
+    total = Sums{total.rows + s.rows, total.take + s.take, total.give + s.give};
+  }
+  v = Sums{before.rows + x.rows - v.rows, before.take + x.take - v.take, before.give + x.give - v.give};
   __syncthreads();
 }
 
@@ -108,10 +108,11 @@ __device__ __forceinline__ int walk_up(const PlanRows& p, long long start, int i
 }
 
 __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanRows p) {
-  __shared__ long long sums[3][kPlanRowsThreads / 32];
-  __shared__ long long at_first[3];  // rows, taken, given before this CTA's first sequence
+  __shared__ Sums sums[kPlanRowsThreads / 32];
   __shared__ int taken_s;
-  extern __shared__ int give0[];     // [B + 1]
+  extern __shared__ __align__(16) unsigned char dyn[];
+  Sums* first = reinterpret_cast<Sums*>(dyn);       // before each of this CTA's sequences
+  int* give0 = reinterpret_cast<int*>(first + p.per);  // [B + 1]
   // launched as a programmatic dependent: the lengths may come from the kernel before this one
   grid_dep_wait();
   grid_dep_launch();
@@ -119,61 +120,49 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
   const int b_lo = (int)min((long long)blockIdx.x * p.per, (long long)p.B), b_hi = min(p.B, b_lo + p.per);
   const int free_raw = __ldg(p.free_in), free = min(max(free_raw, 0), p.num_blocks);
   // ---- all lengths
-  long long total[3] = {0, 0, 0};  // rows, taken (if all are served), given
+  Sums total = {0, 0, 0};  // (blocks wanted, whether served or not)
   bool bad = free_raw != free;
 #pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += kRound) {
     const int b = b0 + tid * kPer;
-    int rows[kPer], take[kPer], give[kPer];
-    long long v[3] = {0, 0, 0}, sum[3];
+    Sums of[kPer], v = {0, 0, 0}, sum;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      rows[k] = take[k] = give[k] = 0;
+      of[k] = Sums{0, 0, 0};
       if (b + k < p.B) {
         const Req r = request(p, b + k);
         bad |= !r.ok;
-        rows[k] = r.rows;
-        take[k] = max(0, r.need - r.held);
-        give[k] = max(0, r.held - r.need);
+        of[k] = Sums{r.rows, max(0, r.need - r.held), max(0, r.held - r.need)};
       }
-      v[0] += rows[k];
-      v[1] += take[k];
-      v[2] += give[k];
+      v = Sums{v.rows + of[k].rows, v.take + of[k].take, v.give + of[k].give};
     }
-    scan3(v, sum, sums);
-#pragma unroll
-    for (int k = 0; k < 3; ++k) v[k] += total[k];
+    scan(v, sum, sums);
+    v = Sums{v.rows + total.rows, v.take + total.take, v.give + total.give};
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      if (b + k < p.B) give0[b + k] = (int)v[2];
-      if (b + k == b_lo && b_lo < b_hi)
-        for (int x = 0; x < 3; ++x) at_first[x] = v[x];
-      v[0] += rows[k];
-      v[1] += take[k];
-      v[2] += give[k];
+      if (b + k < p.B) give0[b + k] = v.give;
+      if (b + k >= b_lo && b + k < b_hi) first[b + k - b_lo] = v;
+      v = Sums{v.rows + of[k].rows, v.take + of[k].take, v.give + of[k].give};
     }
-#pragma unroll
-    for (int k = 0; k < 3; ++k) total[k] += sum[k];
+    total = Sums{total.rows + sum.rows, total.take + sum.take, total.give + sum.give};
   }
   if (tid == 0) {
-    give0[p.B] = (int)total[2];
+    give0[p.B] = total.give;
     taken_s = 0;
   }
-  const int R = (int)total[2];
-  const long long room = (long long)free + R;  // blocks that can be taken
-  bad |= room > p.num_blocks || total[0] > p.N;
+  const long long room = (long long)free + total.give;  // blocks that can be taken
+  bad |= room > p.num_blocks || total.rows > p.N;
   __syncthreads();
   // ---- blocks that are taken: all that are wanted, or as many as the sequences served take
-  int taken = (int)min(total[1], room);
+  int taken = (int)min((long long)total.take, room);
   const bool keeper = p.write_state && blockIdx.x == 0 && blockIdx.y == 0;  // writes what the next step starts from
-  if (total[1] > room || keeper) {
-    long long before = 0;
-    int most = 0;
+  if (total.take > room || keeper) {
+    int before = 0, most = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += kRound) {
       const int b = b0 + tid * kPer;
       int take[kPer], need[kPer], held[kPer];
-      long long v[3] = {0, 0, 0}, sum[3];
+      Sums v = {0, 0, 0}, sum;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         take[k] = need[k] = held[k] = 0;
@@ -183,19 +172,18 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
           held[k] = r.held;
           take[k] = max(0, r.need - r.held);
         }
-        v[1] += take[k];
+        v.take += take[k];
       }
-      scan3(v, sum, sums);  // (its barriers: everyone has read before anyone writes)
-      v[1] += before;
+      scan(v, sum, sums);  // (its barriers: everyone has read before anyone writes)
+      v.take += before;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        v[1] += take[k];
-        const bool served = take[k] == 0 || v[1] <= room;
-        if (served && take[k]) most = (int)v[1];
-        if (keeper && b + k < p.B)
-          p.held_out[b + k] = served ? need[k] : held[k];
+        v.take += take[k];
+        const bool served = take[k] == 0 || v.take <= room;
+        if (served && take[k]) most = v.take;
+        if (keeper && b + k < p.B) p.held_out[b + k] = served ? need[k] : held[k];
       }
-      before += sum[1];
+      before += sum.take;
     }
     most = __reduce_max_sync(0xffffffffu, most);
     if ((tid & 31) == 0) atomicMax(&taken_s, most);
@@ -206,13 +194,13 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
     if (__syncthreads_or(bad) && tid == 0 && p.report) raise_error(p.err, kErrBounds);
     if (keeper && tid == 0) {  // (every thread has read the count)
       p.free_out[0] = (int)min(room - taken, (long long)p.num_blocks);
-      p.free_out[1] = (int)(total[1] - taken);
+      p.free_out[1] = total.take - taken;
     }
   }
   if (!p.write_rows) return;
-  // ---- this CTA's sequences
-  const int part = (int)blockIdx.y, parts = (int)gridDim.y;
-  const int step = parts * kPlanRowsThreads, first = part * kPlanRowsThreads + tid;
+  // ---- this CTA's sequences, `lanes` threads each
+  const int lanes = p.lanes, part = (int)blockIdx.y, parts = (int)gridDim.y;
+  const int step = parts * lanes, at0 = part * lanes + tid % lanes;
   // the block at place `at` of the list with what is given back
   const auto listed = [&](long long at) -> int {
     if (at < free) return __ldg(p.free_list + at);
@@ -226,34 +214,35 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
     const Req r = request(p, lo);
     return __ldg(p.tables + (size_t)lo * p.mbps + r.need + (g - give0[lo]));
   };
-  long long start = at_first[0], took = at_first[1];
 #pragma unroll 1
-  for (int b = b_lo; b < b_hi; ++b) {
+  for (int b = b_lo + tid / lanes; b < b_hi; b += kPlanRowsThreads / lanes) {
     const Req r = request(p, b);
+    const long long start = first[b - b_lo].rows;
+    const int took = first[b - b_lo].take;
     const int take = max(0, r.need - r.held), give = max(0, r.held - r.need);
-    const bool served = r.ok && (take == 0 || took + take <= room);
+    const bool served = r.ok && (take == 0 || (long long)took + take <= room);
     int* table = p.tables + (size_t)b * p.mbps;
-    if (part == 0 && tid == 0) {
+    if (at0 == 0) {
       p.row_starts[b] = (int)min(start, (long long)INT_MAX);
       if (b == p.B - 1) p.row_starts[p.B] = (int)min(start + r.rows, (long long)INT_MAX);
     }
     const auto block = [&](int k) {  // of the sequence's k-th block; -1: none
-      const int e = k < r.held ? __ldg(table + k) : listed(room - 1 - (took + (k - r.held)));
+      const int e = k < r.held ? __ldg(table + k) : listed(room - 1 - ((long long)took + (k - r.held)));
       if (e >= 0 && e < p.num_blocks) return e;
       raise_error(p.err, kErrBounds);
       return -1;
     };
     // blocks given back, those of them that stay on the list
-    for (int k = first; k < give; k += step) {
+    for (int k = at0; k < give; k += step) {
       const int g = give0[b] + k, e = __ldg(table + r.need + k);
       if (e < 0 || e >= p.num_blocks) raise_error(p.err, kErrBounds);
       if (free + (long long)g < room - taken && free + (long long)g < p.num_blocks) p.free_list[free + g] = e;
     }
     if (served)
-      for (int k = first; k < take; k += step) table[r.held + k] = block(r.held + k);
+      for (int k = at0; k < take; k += step) table[r.held + k] = block(r.held + k);
     // rows
     const int rows = (int)min((long long)r.rows, max(0ll, p.N - start));
-    for (int i = first; i < rows; i += step) {
+    for (int i = at0; i < rows; i += step) {
       long long slot = -1;
       if (served) {
         const int k = (r.len + i) / p.bs, e = block(k);
@@ -267,12 +256,10 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
       }
       p.positions[start + i] = r.len + at;
     }
-    start += r.rows;
-    took += take;
   }
   // ---- rows behind the last sequence
-  const long long stride = (long long)gridDim.x * step;
-  for (long long n = total[0] + (long long)blockIdx.x * step + first; n < p.N; n += stride) {
+  const long long threads = (long long)gridDim.x * parts * kPlanRowsThreads;
+  for (long long n = total.rows + ((long long)blockIdx.x * parts + part) * kPlanRowsThreads + tid; n < p.N; n += threads) {
     p.slots[n] = -1;
     p.positions[n] = 0;
     if (p.parents)
@@ -283,23 +270,27 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
 }  // namespace
 
 cudaError_t launch_plan_rows(PlanRows p, cudaStream_t st) {
-  const size_t smem = (size_t)(p.B + 1) * 4;
   int dev = 0;
   cudaGetDevice(&dev);
   static std::atomic<unsigned long long> attr_done{0};  // per device
   if (dev >= 64 || !(attr_done.load(std::memory_order_acquire) >> dev & 1ull)) {
     const cudaError_t e = cudaFuncSetAttribute(plan_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (kPlanRowsMaxB + 1) * 4);
+                                               kPlanRowsMaxB * 5 + 64 * 1024);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
   }
-  // a CTA per sequence, up to eight on each SM; slices of a sequence's rows where that leaves room
-  const int most = 8 * kDenseSms;
-  p.per = (p.B + most - 1) / most;
-  const int gx = (p.B + p.per - 1) / p.per;
+  // a warp for a sequence, up to a CTA where sequences have that many rows (slices of them beyond that); up
+  // to two CTAs an SM, since each scans all lengths
   const long long rows = (long long)p.N / p.B;
-  long long gy = (rows + kPlanRowsThreads - 1) / kPlanRowsThreads;
-  gy = gy < 1 ? 1 : gy > most / gx ? (most / gx < 1 ? 1 : most / gx) : gy;
+  p.lanes = 32;
+  while (p.lanes < kPlanRowsThreads && p.lanes < rows) p.lanes *= 2;
+  const int each = kPlanRowsThreads / p.lanes, most = 2 * kDenseSms;
+  const int groups = (p.B + each - 1) / each;
+  p.per = each * ((groups + most - 1) / most);
+  const int gx = (p.B + p.per - 1) / p.per;
+  const long long slices = (rows + kPlanRowsThreads - 1) / kPlanRowsThreads;
+  const int gy = slices <= 1 ? 1 : slices < most / gx ? (int)slices : most / gx < 1 ? 1 : most / gx;
+  const size_t smem = (size_t)p.per * sizeof(Sums) + (size_t)(p.B + 1) * 4;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)gx, (unsigned)gy);
   cfg.blockDim = dim3(kPlanRowsThreads);
