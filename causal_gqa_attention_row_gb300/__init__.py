@@ -729,18 +729,20 @@ def kv_commit_rows(k_pools, v_pools, block_tables, seq_lens_in, row_starts, path
     if (v_shape[:3] != k_shape[:3] or len(v_shape) != 4 or path.dim() != 2 or path.shape[0] != B or row_starts.numel() != B + 1 or
             seq_lens_in.numel() != B or n_path.numel() != B or seq_lens_out.numel() != B):
         raise ValueError("the pools, the tables, the lengths and the paths do not agree")
-    if any(x.shape != k_shape for x in k_pools) or any(x.shape != v_shape for x in v_pools or ()):
-        raise ValueError("the layers' pools must be alike")
-    dev = torch.cuda.current_device()
+    dev = block_tables.get_device()
 
-    def addresses(pools):
+    def addresses(pools, shape):
         for x in pools:
-            if x.dtype is not dt or x.get_device() != dev or not x.is_contiguous():
-                raise ValueError("pools must share one dtype, be contiguous and live on the current CUDA device")
-        return (ctypes.c_void_p * layers)(*[x.data_ptr() for x in pools])
+            if x.shape != shape or x.dtype is not dt or x.get_device() != dev or not x.is_contiguous():
+                raise ValueError("the layers' pools must be alike, contiguous and on one device")
+        return struct.pack(f"{layers}Q", *[x.data_ptr() for x in pools])
 
+    k_at = addresses(k_pools, k_shape)
+    v_at = None if v_pools is None else addresses(v_pools, v_shape)
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("tensors must live on the current CUDA device")
     _check(load().kv_commit_rows(
-        addresses(k_pools), None if v_pools is None else addresses(v_pools), layers, _at(block_tables, dev, _I32),
+        k_at, v_at, layers, _at(block_tables, dev, _I32),
         _at(seq_lens_in, dev, _I32), _at(row_starts, dev, _I32), _at(path, dev, _I32), _at(n_path, dev, _I32),
         _at(seq_lens_out, dev, _I32), B, path.shape[1], mbps, nb, bs, Hkv, dk, dv, _number(dt),
         _raw_stream(dev) if stream is None else stream.cuda_stream), "kv_commit_rows")
