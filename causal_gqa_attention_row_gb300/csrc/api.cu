@@ -1098,6 +1098,7 @@ gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool
   p.w.bs = block_size;
   p.w.window = arm.window;
   p.w.step_log2 = tc ? 7 : 6;
+  p.w.keys_once = t.n_hchunks == 1 && (max_rows < N ? max_rows : N) <= (t.pair_slots ? 2 : 1) * t.RPT;
   p.w.slots = t.slots;
   p.w.pair_slots = t.pair_slots;
   p.tiles = (int)t.items;

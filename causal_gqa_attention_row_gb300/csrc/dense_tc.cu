@@ -383,7 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!PAGED) {
               if (lane < ncb) tc::tma_load_4d(dst + lane * kBlk, tm, lane * 64, u.key0 + j * kBN, kvh, u.seq, full);
             } else if (lane < per) {
-              tc::tma_load_4d(dst + lane * p.bs * 128 * ncb, tm, 0, 0, 0, (blk * p.Hkv + kvh) * (p.bs / 8), full);
+              // (keys that are read once leave L2 to the partial results: 32 sequences of one row 58.7 us, so 56.3)
+              if (TREE && p.tree.keys_once)
+                tc::tma_load_4d_policy(dst + lane * p.bs * 128 * ncb, tm, 0, 0, 0, (blk * p.Hkv + kvh) * (p.bs / 8), full,
+                                       l2_policy_evict_first());
+              else
+                tc::tma_load_4d(dst + lane * p.bs * 128 * ncb, tm, 0, 0, 0, (blk * p.Hkv + kvh) * (p.bs / 8), full);
             }
             __syncwarp();
             (pair ? pair_sent : kv ? v_sent : k_sent) = (pair ? t_pair : t_all) + 1;

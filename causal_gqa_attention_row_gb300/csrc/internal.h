@@ -214,6 +214,7 @@ struct TreeWork {
   int heads, GH, RPT, R;           // KV heads times head chunks; heads and rows of a tile; rows of a partial result
   int capacity, bs, window;
   int step_log2;                   // keys of a tile
+  int keys_once;                   // no key is read for a second row tile
   int slots, pair_slots;           // pieces of the line of single tiles, and of pairs (0: no pairs)
   TreeRec* rec;                    // of each row tile
   int* line;                       // [0] the row tiles
