@@ -36,7 +36,7 @@ struct TreeCfg {
   static constexpr int kSeq = 16384;  // the line
   static constexpr int kQ = kSeq, kKV = kQ + kTreeRows * DK * 4, kP = kKV + kTreeKeys * kStride * 4;
   static constexpr int kRow = kP + kTreeRows * kPStride * 4;  // pool rows of two tiles, masks, positions
-  static constexpr int kBytes = kRow + 2 * kTreeKeys * 8 + kTreeRows * 8 + kTreeKeys * 4 + kTreeRows * 4;
+  static constexpr int kBytes = kRow + 2 * kTreeKeys * 8 + kTreeRows * 16 + kTreeKeys * 4 + kTreeRows * 4;
   static constexpr int kCtas = kBytes <= 113 * 1024 ? 2 : 1;
   static constexpr int kCh = Elem<ET>::kPerChunk;
   static constexpr int kLoadK = (kTreeKeys * DK / kCh + kTreeThreads - 1) / kTreeThreads;
@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<ET, DK, DV>::kCtas)
   float* skv = reinterpret_cast<float*>(smem + C::kKV);
   float* sp = reinterpret_cast<float*>(smem + C::kP);
   long long* pool_row = reinterpret_cast<long long*>(smem + C::kRow);  // [2][keys], of the KV head; -1: no key
-  uint32_t* masks = reinterpret_cast<uint32_t*>(pool_row + 2 * kTreeKeys);  // [rows][2]
+  long long* q_row = pool_row + 2 * kTreeKeys;  // [rows], of the queries; -1: none
+  uint32_t* masks = reinterpret_cast<uint32_t*>(q_row + kTreeRows);  // [rows][2]
   int* key_pos = reinterpret_cast<int*>(masks + 2 * kTreeRows);
   int* row_pos = key_pos + kTreeKeys;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -115,15 +116,20 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<ET, DK, DV>::kCtas)
     };
     __syncthreads();  // the unit before is done with everything
     places(0);
-    for (int c = tid; c < kTreeRows * DK / CH; c += kTreeThreads) {
+    if (tid >= kTreeThreads - kTreeRows) {
+      const int r = tid - (kTreeThreads - kTreeRows);
+      q_row[r] = r < rows ? (long long)(u.row0 + i0 + r / w.GH) * p.H + head0 + r % w.GH : -1;
+    }
+    __syncthreads();
+    load(p.k, DK, 0);
+    // (a warp's eight rows or none)
+    for (int c = tid; c < (rows + 7) / 8 * 8 * (DK / CH); c += kTreeThreads) {
       const int r = c / (DK / CH), x = c % (DK / CH) * CH;
       float f[CH];
 #pragma unroll
       for (int e = 0; e < CH; ++e) f[e] = 0.f;
-      if (r < rows)
-        Elem<ET>::chunk_to_f32(__ldg(reinterpret_cast<const uint4*>(
-                                   static_cast<const ET*>(p.q) +
-                                   ((size_t)(u.row0 + i0 + r / w.GH) * p.H + head0 + r % w.GH) * DK + x)), f);
+      if (q_row[r] >= 0)
+        Elem<ET>::chunk_to_f32(__ldg(reinterpret_cast<const uint4*>(static_cast<const ET*>(p.q) + q_row[r] * DK + x)), f);
 #pragma unroll
       for (int e = 0; e < CH; e += 4)
         *reinterpret_cast<float4*>(sq + r * DK + x + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
@@ -132,8 +138,6 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<ET, DK, DV>::kCtas)
       const int i = i0 + min(tid, rows - 1) / w.GH;
       row_pos[tid] = u.hist + tree_depth(w, u.row0 + i, i, u.n) - 1;
     }
-    __syncthreads();
-    load(p.k, DK, 0);
     float slope2[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
