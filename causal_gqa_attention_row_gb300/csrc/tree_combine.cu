@@ -161,14 +161,17 @@ __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const __grid
     den = fmaf(f, l, den);
     acc = make_float4(fmaf(f, o.x, acc.x), fmaf(f, o.y, acc.y), fmaf(f, o.z, acc.z), fmaf(f, o.w, acc.w));
   };
-  const auto head_of = [&](int x) { return r0.z * w.GH + x % w.GH; };
+  // x / GH, exact for x and GH up to 128 (a division each took a good third of the kernel's instructions)
+  const uint32_t gh_inverse = 65536u / (uint32_t)w.GH + 1u;
+  const auto over_gh = [&](int x) { return (int)((uint32_t)x * gh_inverse >> 16); };
+  const auto head_of = [&](int x) { return r0.z * w.GH + x - over_gh(x) * w.GH; };
   const auto sink_of = [&](int x) { return p.sinks && x < rows ? __ldg(p.sinks + head_of(x)) * kLog2e : -INFINITY; };
   // row x's output; whether it is not finite
   const auto finish = [&](int x, float den, float4 acc) {
     if (x >= rows) return false;
     const float inv = den != 0.f ? 1.f / den : 0.f;
     const float4 y = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    ET* to = static_cast<ET*>(p.out) + ((size_t)(r0.x + x / w.GH) * p.H + head_of(x)) * dv + 4 * c;
+    ET* to = static_cast<ET*>(p.out) + ((size_t)(r0.x + over_gh(x)) * p.H + head_of(x)) * dv + 4 * c;
     if constexpr (sizeof(ET) == 2) {
       const __nv_bfloat162 a = __floats2bfloat162_rn(y.x, y.y), z = __floats2bfloat162_rn(y.z, y.w);
       *reinterpret_cast<uint2*>(to) =
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const __grid
     for (uint32_t left = again_s[k]; left; left &= left - 1) {  // (the same for all threads)
       const int x = 32 * k + __ffs(left) - 1;
       Row r;
-      r.row = r0.x + x / w.GH;
+      r.row = r0.x + over_gh(x);
       r.row0 = __ldg(w.row_starts + r0.w);
       r.i = r.row - r.row0;
       r.n = __ldg(w.row_starts + r0.w + 1) - r.row0;
