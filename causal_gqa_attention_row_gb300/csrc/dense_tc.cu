@@ -2,7 +2,8 @@
 // (bf16; (d_k, d_v) = (64, 64), (128, 128) or (192, 128), drafted rows (256, 256) too): rows that all see the same
 // keys, as decoder rows against an encoder's states (attn_cross), the decode rows of
 // sequences that share a prefix against that prefix, and a sequence's decode row against
-// its own keys (attn_decode_shared_prefix).
+// its own keys (attn_decode_shared_prefix); and drafted rows against their history and those of
+// one another that a mask names (attn_tree_paged).
 //
 //   out[r] = softmax_{j < n_r}(scale * q_r . k_j) v_j,  n_r the keys of row r
 //
@@ -28,7 +29,11 @@
 // as stages come free, so a unit costs its tiles plus one epilogue, not a launch, a set-up
 // and a first load. The shared prefixes' units are drawn from a ticket counter; those of
 // attn_cross go round by slot: alike but for lengths on the device, which shorten a sequence's
-// last unit and leave those behind it empty.
+// last unit and leave those behind it empty; those of drafted rows follow from a line of all work,
+// which each CTA sums up for itself (tree_part.cuh), and all leave partial results (tree_combine.cu).
+// Where a sequence has two tiles of drafted rows the halves take one each of the same keys, and their K
+// and V stages become one ring: the first half's producer brings K, the second's V, and a stage is free
+// once both halves have done with it.
 //
 // Measured at 32 heads on 8 KV heads of 128, plan and combine included: 64 sequences behind
 // a prefix of 8,192 keys with up to 512 of their own 42 us; 256 sequences behind four prefixes
@@ -38,6 +43,9 @@
 // cap (1,390 W, 1,980 MHz). What bounds them is a half's time from tile to tile, of 1,024 cycles
 // of products: in the last case about 3,200 cycles, S, softmax and PV of a half one after
 // another; in the second a third more, for K and V that come from HBM through one stage each.
+// Drafted rows, with the join: 64 sequences of up to 32 behind up to 8,192 keys 175 us (6.25 TB/s, 0.92 of
+// the copy bandwidth; 160 without the join); 8 sequences of 48 to 64 (two tiles) behind 16,384 to 32,768 keys
+// 182 us (4.4 TB/s, 0.98 PFLOP/s), 1.86 us a tile.
 //
 //   warps 0-3, 4-7   softmax of half 0, 1: thread t owns row t of the tile (TMEM lane t)
 //   warps 8, 11      TMA producer of half 0, 1 (Q once a unit, then K and V tiles; paged:

@@ -8,6 +8,9 @@
 //   the list is a stack: the R blocks given back go onto it, sequence by sequence, entries
 //   ascending; the t-th block taken is the one at free + R - 1 - t
 //
+// Measured in replayed graphs: 256 sequences of one row 5.7 us, 128 trees of up to 64 rows 6.9, 48 prompts of up to
+// 2,048 rows with too few blocks 6.7, 794 trees of seven rows 7.3.
+//
 // What it reads and writes is small (20 bytes a sequence, 12 and more a row), so what bounds it is
 // latency: one launch, and in it one chain of loads (the lengths, the block, the store). So no
 // CTA waits for another: each scans all lengths for itself (a thread takes four
