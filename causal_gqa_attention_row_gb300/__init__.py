@@ -624,7 +624,7 @@ def kv_plan_rows(seq_lens, new_rows, block_tables, blocks_in, blocks_out, free_l
         _at(seq_lens, dev, _I32), _at(new_rows, dev, _I32), _at(block_tables, dev, _I32), _at(blocks_in, dev, _I32),
         _at(blocks_out, dev, _I32), _at(keep_blocks, dev, _I32), _at(free_list, dev, _I32), _at(free_in, dev, _I32),
         _at(free_out, dev, _I32), _at(row_starts, dev, _I32), _at(positions, dev, _I32), _at(slots, dev, _I64),
-        _at(parents, dev, _I32), _at(tree_mask, dev, _I64), words, N, B, mbps, free_list.numel(), block_size,
+        _at(parents, dev, _I32), _at(tree_mask, dev, _I64), words, N, B, mbps, free_list.numel(), int(block_size),
         _raw_stream(dev) if stream is None else stream.cuda_stream), "kv_plan_rows")
 
 
@@ -659,7 +659,7 @@ def kv_append_slots(q, k_new, v_new, q_out, k_pool, v_pool, slots, positions=Non
     _check(load().kv_append_slots(
         _view(q, 3), _view(k_new, 3), _view(v_new, 3), _view(q_out, 3), _at(k_pool, dev, dt), _at(v_pool, dev, dt),
         _at(slots, dev, _I64), _at(positions, dev, _I32), N, nb, bs, H, Hkv, dk, dv, _at(q_weight, dev, dt),
-        _at(k_weight, dev, dt), eps, _ref(rope), _number(dt), _raw_stream(dev) if stream is None else stream.cuda_stream),
+        _at(k_weight, dev, dt), float(eps), _ref(rope), _number(dt), _raw_stream(dev) if stream is None else stream.cuda_stream),
            "kv_append_slots")
     return q_out
 
@@ -707,8 +707,8 @@ def attn_tree_paged(q, k_pool, v_pool, block_tables, position_offset, row_starts
         ws = workspace.numel() * workspace.element_size()
     _check(load().attn_tree_paged(
         _at(q, dev, dt), _at(k_pool, dev, dt), _at(v_pool, dev, dt), _at(block_tables, dev, _I32),
-        _at(position_offset, dev, _I32), _at(row_starts, dev, _I32), _at(tree_mask, dev, _I64), _at(out, dev, dt), N, B, max_rows,
-        words, mbps, nb, bs, H, Hkv, dk, dv, attention_scale, _number(dt), None if workspace is None else workspace.data_ptr(),
+        _at(position_offset, dev, _I32), _at(row_starts, dev, _I32), _at(tree_mask, dev, _I64), _at(out, dev, dt), N, B,
+        int(max_rows), words, mbps, nb, bs, H, Hkv, dk, dv, float(attention_scale), _number(dt), None if workspace is None else workspace.data_ptr(),
         ws, arms, _raw_stream(dev) if stream is None else stream.cuda_stream), "attn_tree_paged")
     return out
 

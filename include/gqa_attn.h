@@ -696,8 +696,8 @@ const char* gqa_status_string(gqa_status status);
  *   - the SIMT attention kernel (decode; SIMT prefill): the first K/V tile of
  *     every CTA;
  *   - the tensor-core prefill: the first K tile of every CTA;
- *   - the tensor-core kernel of attn_cross and attn_decode_shared_prefix: the first K
- *     tile of each of a CTA's halves;
+ *   - the tensor-core kernel of attn_cross, attn_decode_shared_prefix and attn_tree_paged:
+ *     the first K tile of each of a CTA's halves (of both, where they share their tiles);
  *   - the absorbed MLA decode: the first cache tile of the second CTA of every
  *     pair, so the first CTA also gives up waiting for its peer's tile maxima;
  *     both let what they sent each other land before releasing their memory.

@@ -110,6 +110,8 @@ SHAPES = [
     ([3], [2900], 2, 1, 128),                                  # few rows, keys over many CTAs
     ([6, 4], [40, 40], 130, 1, 8),                             # more heads than a tile has rows
     ([2] * 90, [3 * i for i in range(90)], 3, 3, 16),          # many sequences
+    ([80, 150, 20, 0, 65], [900, 333, 50, 7, 0], 8, 2, 16),    # three and five row tiles, pairs and single ones
+    ([700], [200], 2, 1, 32),                                  # eleven mask words
 ]
 
 
@@ -309,11 +311,14 @@ def verify_first(c, out, d, dt):
     check(excess(out[s], o, dt == BF16, dt == BF16, d, 64), 1.0)
 
 
-def test_more_sequences_than_a_launch_takes(gpu_lib):
+@pytest.mark.parametrize("long", [0, 75])
+def test_more_sequences_than_a_launch_takes(gpu_lib, long):
     g = gpu_lib
     B = 2100
     r = np.random.default_rng(0)
-    c = case(r.integers(0, 3, B).tolist(), r.integers(0, 40, B).tolist(), 2, 1, 64, 64, pad=1)
+    rows = r.integers(0, 3, B)
+    rows[::400] = long or 1  # (more than a row tile: pairs in each launch)
+    c = case(rows.tolist(), r.integers(0, 40, B).tolist(), 2, 1, 64, 64, pad=1)
     out = run(g, c, 0.1)
     assert g.attn_get_device_error() == g.OK
     verify(c, 0.1, out)
@@ -372,10 +377,12 @@ def test_rows_of_one_are_the_paged_decode(gpu_lib):
     verify(c, 0.1, out)
 
 
-def test_a_wait_that_runs_out(gpu_lib):
+@pytest.mark.parametrize("rows", [[5, 9], [90, 70]])  # (the second: pairs)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_wait_that_runs_out(gpu_lib, rows, d):
     """The test hook: the first K tile never comes; the call returns, says so, and the next one is right."""
     g = gpu_lib
-    c = case([5, 9], [100, 400], 4, 2, 128, 128)
+    c = case(rows, [100, 400], 8, 2, d, d)
     want = run(g, c, 0.1)
     g.gqa_debug_withhold_first_tile(True)
     try:
