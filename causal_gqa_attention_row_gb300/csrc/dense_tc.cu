@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         lim = u.key1;
         if (TREE) {
           const TreeSeq& s = tree_seq[u.seq];
-          tree_n = __ldg(p.tree.row_starts + u.seq + 1) - s.row0;
+          tree_n = s.n;
           if (ARMS && p.window > 0 && warp_live) {
             const int row = u.i0 + min(r, rows - 1) / p.GH;
             depth = tree_depth(p.tree, row, row - s.row0, tree_n);

@@ -202,10 +202,11 @@ bool prefill_tc_supported(int bf16, int dk, int dv, int bs = 0, int mbps = 0);
 
 // ---- attention without a causal rule on tcgen05 (dense_tc.cu) -----------------
 // How the attention of drafted rows is cut into work (tree_part.cuh).
-constexpr int kTreeSeqs = 640;  // sequences of a launch: their table stays in shared memory
+constexpr int kTreeSeqs = 500;  // sequences of a launch: their table stays in shared memory
 struct alignas(16) TreeRec {    // what the join reads of a row tile
   int row, n, hc, b;            // its first packed row, its drafted rows; KV head and head chunk; sequence
-  int part, parts, stride, hist;  // its partial results: part, part + stride, ..
+  int part, parts, stride, hist;  // its partial results: part, part + stride, ..; the sequence's history
+  int row0, rows, pad[2];         // and its rows
 };
 struct TreeWork {
   const int32_t *row_starts, *offsets;

@@ -257,9 +257,10 @@ __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const __grid
       const int x = 32 * k + __ffs(left) - 1;
       Row r;
       r.row = r0.x + over_gh(x);
-      r.row0 = __ldg(w.row_starts + r0.w);
-      r.i = r.row - r.row0;
-      r.n = __ldg(w.row_starts + r0.w + 1) - r.row0;
+      const int4 r2 = __ldcg(reinterpret_cast<const int4*>(w.rec + blockIdx.x) + 2);
+      r.row0 = r2.x;
+      r.i = r.row - r2.x;
+      r.n = r2.y;
       r.hist = r1.w;
       r.depth = tree_depth(w, r.row, r.i, r.n);
       row_again(p, r0.w, r, head_of(x), reinterpret_cast<float*>(acc_s), md_s);

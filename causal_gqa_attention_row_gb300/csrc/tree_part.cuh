@@ -25,8 +25,9 @@
 namespace gqa {
 
 // A sequence in shared memory; entry B closes the lines. [0] the line of pairs, [1] that of single tiles.
-struct alignas(8) TreeSeq {
-  int cost0[2], item0[2], row0, hist;
+// (The kernels go by what is here: row_starts is read once, whatever happens to it meanwhile.)
+struct alignas(16) TreeSeq {
+  int cost0[2], item0[2], row0, n, hist, pad;
 };
 static_assert(sizeof(TreeSeq) * (kTreeSeqs + 1) + 12 * 16 <= 16384, "the sequences' table and the scan's sums");
 
@@ -57,35 +58,37 @@ __device__ __forceinline__ int tree_slot_of(int C, int S, int x) {
 template <int THREADS>
 __device__ void tree_line(const TreeWork& w, TreeSeq* seq, int cta) {
   constexpr int kWarps = THREADS / 32, kEach = (kTreeSeqs + THREADS - 1) / THREADS;
-  int4* sums = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(seq + kTreeSeqs + 1) + 15) & ~uintptr_t(15));
+  int4* sums = reinterpret_cast<int4*>(seq + kTreeSeqs + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   TreeSeq mine[kEach];
-  int n_of[kEach];
   int4 sum = make_int4(0, 0, 0, 0);  // costs, items
-  bool bad = false;
+  bool bad = false, back = false;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     const int b = tid * kEach + k;
     mine[k] = TreeSeq{};
-    n_of[k] = 0;
     if (b < w.B) {
       const int s0 = __ldg(w.row_starts + b), s1 = __ldg(w.row_starts + b + 1), hist = w.offsets ? __ldg(w.offsets + b) : 0;
       const long long n = (long long)s1 - s0;
       const bool ok = s0 >= 0 && n >= 0 && s1 <= w.N && n <= w.max_rows && hist >= 0 && hist + n <= w.capacity;
       bad |= !ok;
+      back |= n < 0;
       mine[k].row0 = s0;
       mine[k].hist = hist;
-      n_of[k] = ok ? (int)n : 0;
+      mine[k].n = ok ? (int)n : 0;
     }
   }
+  // starts that go back: sequences overlap, and their tiles may be more than there is room for; none is taken
+  back = __syncthreads_or(back);
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
+    if (back) mine[k].n = 0;
     mine[k].cost0[0] = sum.x;
     mine[k].cost0[1] = sum.y;
     mine[k].item0[0] = sum.z;
     mine[k].item0[1] = sum.w;
-    if (n_of[k] > 0) {
-      const TreeShape s = tree_shape(w, n_of[k], mine[k].hist);
+    if (mine[k].n > 0) {
+      const TreeShape s = tree_shape(w, mine[k].n, mine[k].hist);
       const int pairs = w.heads * tree_items(w, s.tiles, 0), singles = w.heads * tree_items(w, s.tiles, 1);
       sum.x += pairs * (s.T + 1);
       sum.y += singles * (s.T + 1);
@@ -119,7 +122,7 @@ __device__ void tree_line(const TreeWork& w, TreeSeq* seq, int cta) {
     if (b < w.B) seq[b] = mine[k];
   }
   if (tid == 0) {
-    seq[w.B] = TreeSeq{{all.x, all.y}, {all.z, all.w}, 0, 0};
+    seq[w.B] = TreeSeq{{all.x, all.y}, {all.z, all.w}, 0, 0, 0, 0};
     if (cta == 0) {
       w.line[0] = 2 * all.z + all.w;  // row tiles
       if (bad) raise_error(w.err, kErrBounds);
@@ -133,11 +136,10 @@ __device__ void tree_line(const TreeWork& w, TreeSeq* seq, int cta) {
 __device__ __forceinline__ void tree_publish(const TreeWork& w, const TreeSeq* seq, int cta, int ctas, int tid, int threads) {
   for (int b = cta; b < w.B; b += ctas) {
     const TreeSeq q = seq[b];
-    const int first = 2 * q.item0[0] + q.item0[1], tiles_all = 2 * seq[b + 1].item0[0] + seq[b + 1].item0[1] - first;
-    if (tiles_all == 0) continue;
-    const int n = __ldg(w.row_starts + b + 1) - q.row0;
+    if (q.n == 0) continue;
+    const int first = 2 * q.item0[0] + q.item0[1], n = q.n;
     const TreeShape s = tree_shape(w, n, q.hist);
-    for (int e = tid; e < tiles_all; e += threads) {
+    for (int e = tid; e < w.heads * s.tiles; e += threads) {
       const int hc = e / s.tiles, tile = e - hc * s.tiles, paired = 2 * tree_items(w, s.tiles, 0);
       const int x = tile >= paired, each = tree_items(w, s.tiles, x);
       const int in = hc * each + (x ? tile - paired : tile >> 1);  // of the sequence's items on line x
@@ -152,9 +154,12 @@ __device__ __forceinline__ void tree_publish(const TreeWork& w, const TreeSeq* s
       r.stride = x ? 1 : 2;
       r.part = x ? 2 * (seq[w.B].item0[0] + w.pair_slots) + q.item0[1] + in + s0 : 2 * (q.item0[0] + in + s0) + (tile & 1);
       r.hist = q.hist;
+      r.row0 = q.row0;
+      r.rows = n;
       int4* to = reinterpret_cast<int4*>(w.rec + first + e);
       to[0] = make_int4(r.row, r.n, r.hc, r.b);
       to[1] = make_int4(r.part, r.parts, r.stride, r.hist);
+      to[2] = make_int4(r.row0, r.rows, 0, 0);
     }
   }
 }
@@ -191,7 +196,7 @@ __device__ __forceinline__ bool tree_next(const TreeWork& w, const TreeSeq* seq,
     u.b = lo;
     u.row0 = q.row0;
     u.hist = q.hist;
-    u.n = __ldg(w.row_starts + lo + 1) - q.row0;
+    u.n = q.n;
     const TreeShape s = tree_shape(w, u.n, q.hist);
     const int r = k.at - q.cost0[x], item = r / (s.T + 1), off = r - item * (s.T + 1);
     const int to = min(s.T + 1, off + k.end - k.at);

@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<ET, DK, DV>::kCtas)
       const int j0 = u.key0 + t * kTreeKeys;
       // some row of the sequence does not see some key of the tile (the window's lower end moves with a row)
       const bool partly = j0 + kTreeKeys > u.hist || (w.window > 0 && j0 < u.hist + u.n - w.window);
+      if (t > 0) load(p.k, DK, t);
       __syncthreads();  // the tile before is done with
       store(DK);
       if (placed && tid < kTreeKeys) {
@@ -173,7 +174,6 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<ET, DK, DV>::kCtas)
             if (key_pos[32 * half + e] <= row_pos[r] - w.window) x &= ~(1u << e);
         masks[tid] = x;
       }
-      load(p.v, DV, t);
       places(t + 1);
       if (partly) __syncthreads();
       if (busy) {
@@ -229,10 +229,10 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<ET, DK, DV>::kCtas)
           }
         }
       }
+      load(p.v, DV, t);
       __syncthreads();  // K is done with
       store(DV);
       __syncthreads();
-      if (t + 1 < n_tiles) load(p.k, DK, t + 1);
       if (busy && tx * 4 < DV) {
         // ---- output
         if (!partly) {

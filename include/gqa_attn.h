@@ -562,7 +562,8 @@ gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa
  *               in a tree. A window hides drafted rows too.
  * A row that sees no key gets zeros; a key that scores -infinity weighs zero. What a row does not see does
  * not reach it, whatever the slot holds, an infinity or NaN included. Sequences with lengths out of range or more
- * rows than max_rows set the device error word, and their rows are left as they are.
+ * rows than max_rows set the device error word, and their rows are left as they are; where row_starts goes back,
+ * so are those of other sequences too (of up to 500 in a row, the sequences of a launch).
  * bf16 with (d_k, d_v) = (64, 64), (128, 128), (192, 128) or (256, 256), block_size a multiple of 8 dividing 128,
  * attention_scale > 0 and no ALiBi slopes runs on the tcgen05 tensor-core kernel (the probabilities rounded to
  * bf16 for the product with V), every other case on a SIMT kernel of fp32 arithmetic. How a sequence's keys are

@@ -282,8 +282,8 @@ def test_bad_sequences(gpu_lib, dt, d, what):
     elif what == "long":
         c["hist"] = [60, c["tables"].shape[1] * 16 - 8, 30]
     elif what == "order":
-        c["starts"] = np.array([1, 5, 3, 19])  # the second goes back: it and the rows that overlap are not compared
-        skip, left = {1, 2}, slice(0, 0)
+        c["starts"] = np.array([1, 5, 3, 19])  # no sequence is taken
+        skip, left = {0, 1, 2}, slice(0, 21)
     elif what == "many":
         max_rows = 8
     elif what == "past":
@@ -296,19 +296,33 @@ def test_bad_sequences(gpu_lib, dt, d, what):
     out = run(g, c, 0.1, ws=workspace(g, good), max_rows=max_rows)
     assert g.attn_get_device_error() == g.ERR_DEVICE_BOUNDS
     assert g.attn_get_device_error() == g.OK
-    if what == "order":
-        c["rows"] = [4, 0, 0]
-        c["hist"], c["starts"] = good["hist"], np.array([1, 5, 5, 5])
-        verify_first(c, out, d, dt)
-    else:
-        verify(good, 0.1, out, tc=dt == BF16, skip=skip)
+    verify(good, 0.1, out, tc=dt == BF16, skip=skip)
     assert (out[left] == 9.0).all()
 
 
-def verify_first(c, out, d, dt):
-    s = slice(1, 5)
-    o = S.attend(c["q"][s].double().cpu().numpy(), rows_of(c, c["k"], 0), rows_of(c, c["v"], 0), 60, c["seen"][:4], 0.1)
-    check(excess(out[s], o, dt == BF16, dt == BF16, d, 64), 1.0)
+@pytest.mark.parametrize("dt,d", PATHS)
+def test_starts_that_go_back_and_forth(gpu_lib, dt, d):
+    """Overlapping sequences, whose tiles would be more than the workspace has room for: nothing is written
+    behind it."""
+    g = gpu_lib
+    c = case([100], [40], 4, 1, d, d, dt=dt)
+    B, H = 40, 4
+    starts = i32([0 if b % 2 == 0 else 100 for b in range(B + 1)])
+    tables = c["tables"].expand(B, -1).contiguous()
+    need = g.attn_tree_paged_workspace_bytes(100, B, 100, tables.shape[1] * 16, H, 1, d, d, dt)
+    ws = torch.full((need + (1 << 22),), 77, dtype=torch.uint8, device=DEV)
+    out = torch.full((100, H, d), 9.0, dtype=dt, device=DEV)
+    g.attn_tree_paged(c["q"], c["k"], c["v"], tables, i32([40] * B), starts, c["mask"], out, 0.1, 100, ws[:need])
+    assert g.attn_get_device_error() == g.ERR_DEVICE_BOUNDS
+    assert (out == 9.0).all() and (ws[need:] == 77).all()
+
+
+def test_no_offsets_are_zeros(gpu_lib):
+    g = gpu_lib
+    c = case([9, 30], [0, 0], 4, 2, 128, 128)
+    out = torch.empty(39, 4, 128, dtype=BF16, device=DEV)
+    g.attn_tree_paged(c["q"], c["k"], c["v"], c["tables"], None, i32(c["starts"]), c["mask"], out, 0.1, 30, workspace(g, c))
+    assert torch.equal(out, run(g, c, 0.1))
 
 
 @pytest.mark.parametrize("long", [0, 75])
