@@ -984,11 +984,11 @@ gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa
 namespace {
 
 // How a call's rows are tiled, on the tensor cores or on the SIMT kernel, and its workspace: the number of row
-// tiles, their records, the partial results.
+// tiles, their records and marks, the partial results.
 struct TreeLayout {
   int GH, RPT, R, n_hchunks, heads, slots, pair_slots;
   long long items;  // row tiles of all heads, at most, of a launch
-  size_t rec, partial, bytes;
+  size_t rec, odd, partial, bytes;
 };
 
 bool tree_layout(int N, int B, int max_rows, int max_len, int H, int Hkv, int d_k, int d_v, int bf16, bool tc,
@@ -1027,6 +1027,7 @@ bool tree_layout(int N, int B, int max_rows, int max_len, int H, int Hkv, int d_
     return a;
   };
   t->rec = take((size_t)t->items * sizeof(gqa::TreeRec));
+  t->odd = take((size_t)t->items * 4);
   t->partial = take(parts * gqa::dense_part_floats(t->R, d_v) * 4);
   t->bytes = at;
   return true;
@@ -1103,6 +1104,8 @@ gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool
   p.w.pair_slots = t.pair_slots;
   p.tiles = (int)t.items;
   p.w.rec = reinterpret_cast<gqa::TreeRec*>(ws + t.rec);
+  p.w.odd = reinterpret_cast<uint8_t*>(ws + t.odd);
+  p.w.whole = tc && !arm.sinks;  // (a sink joins with the parts)
   p.w.line = reinterpret_cast<int*>(ws);
   p.w.err = err;
   p.q = q;

@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (some) {
               const int i0 = t.tile * p.RPT, part = (int)(dense_part_floats(p.own_rows, DV) / 4);
-              next_u = {t.row0 + i0, min(p.RPT, t.n - i0), t.hc * p.GH, t.b, t.key0, t.key1, t.index * part, tree_line_no == 0};
+              next_u = {t.row0 + i0, min(p.RPT, t.n - i0), t.hc * p.GH, t.b, t.key0, t.key1,
+                          t.index < 0 ? t.index : t.index * part, tree_line_no == 0};
             }
           } else if (next_x < n_units) {
             if (PAGED) {
@@ -787,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (a NaN among a row's scores makes its l NaN, and has to reach the output)
       const bool some = l_run != 0.f;
       const int at = u.part;
-      if (PAGED || at >= 0) {
+      if (TREE ? at >= 0 : PAGED || at >= 0) {
         if (warp_live) {
           const int rows = u.n_i * p.GH, R = TREE || (PAGED && u.batch_or_own) ? p.own_rows : kBM;
           float* part = p.partial + (size_t)at * 4;
@@ -811,6 +812,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             part[(size_t)R * DV + R + r] = l_run;
           }
         }
+      } else if (TREE) {
+        // all keys of the row: its output, and for the join whether it holds a value that is not finite (a
+        // row's 16 bytes are on a line of their own; 40% of the row tiles of 64 sequences of up to 32 rows)
+        bool odd = false;
+        if (warp_live) {
+          const int rows = u.n_i * p.GH, row = min(r, rows - 1), i = row / p.GH;
+          __nv_bfloat16* to = p.out + ((size_t)(u.i0 + i) * p.H + u.head0 + row - i * p.GH) * DV;
+          const float inv = some ? 1.f / l_run : 0.f;
+          float z = 0.f;
+#pragma unroll 1
+          for (int cc = 0; cc < DV / 32; ++cc) {
+            uint32_t o[32];
+            tc::tmem_ld_32x32b_x32(tO + cc * 32, o);
+            tc::tmem_ld_wait();
+            if (r < rows) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                uint32_t w4[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                  const float x0 = __uint_as_float(o[t * 8 + 2 * v]) * inv, x1 = __uint_as_float(o[t * 8 + 2 * v + 1]) * inv;
+                  w4[v] = some ? pack_bf16(x0, x1) : 0u;
+                  if (some) z = fmaf(x0, 0.f, fmaf(x1, 0.f, z));  // (an infinity or NaN times zero is NaN)
+                }
+                *reinterpret_cast<uint4*>(to + cc * 32 + t * 8) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              }
+            }
+            __syncwarp();
+          }
+          odd = !(z == 0.f);
+        }
+        odd = __any_sync(0xffffffffu, odd);
+        if (lane == 0) p.tree.odd[4 * (size_t)~at + quarter] = odd;
       } else {
         // 64 columns at a time through shared memory (the output map's 128-byte swizzle) and
         // out by TMA: stored from the registers, each row's 16 bytes on a line of its own, a

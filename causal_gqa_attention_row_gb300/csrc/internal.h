@@ -205,7 +205,7 @@ bool prefill_tc_supported(int bf16, int dk, int dv, int bs = 0, int mbps = 0);
 constexpr int kTreeSeqs = 500;  // sequences of a launch: their table stays in shared memory
 struct alignas(16) TreeRec {    // what the join reads of a row tile
   int row, n, hc, b;            // its first packed row, its drafted rows; KV head and head chunk; sequence
-  int part, parts, stride, hist;  // its partial results: part, part + stride, ..; the sequence's history
+  int part, parts, stride, hist;  // its partial results: part, part + stride, .. (0: written whole); the sequence's history
   int row0, rows, pad[2];         // and its rows
 };
 struct TreeWork {
@@ -216,8 +216,10 @@ struct TreeWork {
   int capacity, bs, window;
   int step_log2;                   // keys of a tile
   int keys_once;                   // no key is read for a second row tile
+  int whole;                       // a unit of all of an item's keys writes its rows' outputs itself
   int slots, pair_slots;           // pieces of the line of single tiles, and of pairs (0: no pairs)
   TreeRec* rec;                    // of each row tile
+  uint8_t* odd;                    // [row tiles][4]: of those written whole, a quarter's rows hold a value that is not finite
   int* line;                       // [0] the row tiles
   unsigned* err;
 };

@@ -132,6 +132,10 @@ __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const __grid
   __shared__ float4 acc_s[CHECK ? 2 * kJoinThreads : kJoinThreads];  // (row_again: eight rows of up to 256 columns)
   __shared__ float2 md_s[kJoinThreads];
   __shared__ uint32_t again_s[4];  // rows of the tile (at most 128) to be worked out again
+  if (CHECK) {
+    if (threadIdx.x < 4) again_s[threadIdx.x] = 0;
+    __syncthreads();
+  }
   grid_dep_wait();
   const TreeWork& w = p.w;
   const int dv = p.dv, rows_here = 1024 / dv / shares;  // powers of two, as dv is
@@ -142,6 +146,12 @@ __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const __grid
   const int4 r1 = __ldcg(reinterpret_cast<const int4*>(w.rec + blockIdx.x) + 1);
   if ((int)blockIdx.x >= tiles) return;  // as many row tiles as there may be are launched
   const int rows = r0.y * w.GH, total = r1.y;
+  if (total == 0) {  // written whole
+    const uint32_t odd = CHECK && blockIdx.y == 0 ? __ldcg(reinterpret_cast<const uint32_t*>(w.odd) + blockIdx.x) : 0;
+    if (odd == 0) return;
+    if (CHECK && tid < 4 && (odd >> 8 * tid & 0xff) && rows > 32 * tid)
+      again_s[tid] = rows - 32 * tid >= 32 ? ~0u : (1u << (rows - 32 * tid)) - 1u;
+  }
   const size_t part = dense_part_floats(w.R, dv), next = part * r1.z;
   const float* parts = p.partial + part * r1.x;
   // part s of row x: its maximum, sum and this thread's columns
@@ -182,17 +192,13 @@ __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const __grid
     }
     return CHECK && !(finite4(y) && finite4(acc));
   };
-  if (CHECK) {
-    if (tid < 4) again_s[tid] = 0;
-    __syncthreads();
-  }
   const auto mark = [&](int x, bool again) {
     if (CHECK && again) atomicOr(&again_s[x >> 5], 1u << (x & 31));
   };
   const int step = (int)gridDim.y * rows_here;
   if (shares == 1 && total <= 2) {
 #pragma unroll 1
-    for (int x0 = (int)blockIdx.y * rows_here; x0 < rows; x0 += 2 * step) {
+    for (int x0 = (int)blockIdx.y * rows_here; x0 < rows && total > 0; x0 += 2 * step) {
       float m[2][2], l[2][2];
       float4 o[2][2];
 #pragma unroll
@@ -212,7 +218,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_combine_kernel(const __grid
     }
   }
 #pragma unroll 1
-  for (int x0 = (int)blockIdx.y * rows_here; x0 < rows && !(shares == 1 && total <= 2); x0 += step) {
+  for (int x0 = (int)blockIdx.y * rows_here; x0 < rows && total > 0 && !(shares == 1 && total <= 2); x0 += step) {
     const int x = x0 + rr;
     const float z2 = sink_of(x);
     float M = share == 0 ? z2 : -INFINITY, den = M != -INFINITY ? 1.f : 0.f;

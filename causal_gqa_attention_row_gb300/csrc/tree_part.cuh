@@ -10,7 +10,7 @@
 // one is needed: a CTA sums up the lengths for itself (the planner of the shared prefixes, a
 // launch of its own, takes 8 us). From one unit to the next in a walk the item or the slot moves
 // on by one, so item + slot numbers the units without a gap that matters, and the place of a
-// unit's partial result follows from it.
+// unit's partial result follows from it. A unit that has all of an item's tiles writes the rows' outputs.
 //
 // There are two lines. Where a sequence has two row tiles or more (of the same heads), pairs of them lie on the
 // first, cut for the CTAs: the halves of a CTA take a tile each of the same keys at the same time, so
@@ -150,7 +150,7 @@ __device__ __forceinline__ void tree_publish(const TreeWork& w, const TreeSeq* s
       r.n = min(w.RPT, n - tile * w.RPT);
       r.hc = hc;
       r.b = b;
-      r.parts = s1 - s0 + 1;
+      r.parts = w.whole && s0 == s1 ? 0 : s1 - s0 + 1;
       r.stride = x ? 1 : 2;
       r.part = x ? 2 * (seq[w.B].item0[0] + w.pair_slots) + q.item0[1] + in + s0 : 2 * (q.item0[0] + in + s0) + (tile & 1);
       r.hist = q.hist;
@@ -182,7 +182,7 @@ __device__ __forceinline__ TreeWalk tree_walk(const TreeWork& w, const TreeSeq* 
 // The next unit of a walk along line x; false at its end. half: the tile of a pair that is wanted.
 struct TreeUnit {
   int b, hc, tile, row0, n, hist;  // hc: KV head and head chunk; the sequence's rows row0 .. row0 + n - 1
-  int key0, key1, index;
+  int key0, key1, index;  // index: of its partial result; below 0: it has all of the item's keys and is ~ the row tile
 };
 __device__ __forceinline__ bool tree_next(const TreeWork& w, const TreeSeq* seq, int x, int half, TreeWalk& k, TreeUnit& u) {
   while (k.at < k.end) {
@@ -209,6 +209,7 @@ __device__ __forceinline__ bool tree_next(const TreeWork& w, const TreeSeq* seq,
     u.key1 = min(s.key0 + ((to - 1) << w.step_log2), q.hist + u.n);
     const int at = q.item0[x] + item + k.slot;
     u.index = x ? 2 * (seq[w.B].item0[0] + w.pair_slots) + at : 2 * at + half;
+    if (w.whole && off <= 1 && to == s.T + 1) u.index = ~(2 * q.item0[0] + q.item0[1] + u.hc * s.tiles + u.tile);
     return true;
   }
   return false;

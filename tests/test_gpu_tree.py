@@ -257,6 +257,32 @@ def test_what_a_row_does_not_see_does_not_reach_it(gpu_lib, dt, d, of, what):
 
 
 @pytest.mark.parametrize("dt,d", PATHS)
+@pytest.mark.parametrize("window", [0, 20])
+def test_the_same_where_a_unit_has_all_keys_of_its_rows(gpu_lib, dt, d, window):
+    """More row tiles than the GPU takes at a time, so that most are written without a join."""
+    g = gpu_lib
+    r = np.random.default_rng(d)
+    rows, hist = r.integers(1, 13, 200).tolist(), r.integers(0, 60, 200).tolist()
+    c = case(rows, hist, 8, 4, d, d, dt=dt, seed=7)
+    verify(c, 0.1, run(g, c, 0.1, window=window), tc=dt == BF16, window=window)
+    bad = {b: int(r.integers(0, rows[b])) for b in range(0, 200, 7)}
+    for b, j in bad.items():
+        at = hist[b] + j
+        c["v"][int(c["tables"][b, at // 16]), 2, at % 16, 3] = (float("nan"), float("inf"), -float("inf"))[b % 3]
+    out = run(g, c, 0.1, window=window).double()
+    assert g.attn_get_device_error() == g.OK
+    worst = 0.0
+    for b, n in enumerate(rows):
+        s = slice(int(c["starts"][b]), int(c["starts"][b + 1]))
+        o = S.attend(c["q"][s].double().cpu().numpy(), rows_of(c, c["k"], b), rows_of(c, c["v"], b), hist[b], c["seen"][s], 0.1, window=window)
+        assert (np.isfinite(o[0]) == torch.isfinite(out[s]).cpu().numpy()).all()
+        free = [i for i in range(n) if b not in bad or bad[b] not in c["seen"][s.start + i]]
+        if free:
+            worst = max(worst, excess(out[s][free], tuple(x[free] for x in o), dt == BF16, dt == BF16, d, hist[b] + n))
+    check(worst, 1.0)
+
+
+@pytest.mark.parametrize("dt,d", PATHS)
 def test_scores_of_minus_infinity(gpu_lib, dt, d):
     """Keys that score -infinity weigh zero; a row of such keys alone gets zeros."""
     g = gpu_lib
