@@ -290,10 +290,14 @@ cudaError_t launch_tree_combine(const TreeParams& p, int bf16, cudaStream_t st) 
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
   }
-  // few rows: fewer of a CTA, by more shares of their parts; many: a CTA goes through more of its tile's
+  // Few rows: fewer of a CTA, by more shares of their parts, while a share has four parts; many: a CTA goes
+  // through more of its tile's. (One sequence of one row, 14 heads on 2 of 64, 32,000 keys: with one share 33 us, with
+  // two 24, with eight 19; four sequences of 600 keys, five parts a row: with one share 10.8, with eight 11.4.)
+  const int keys = p.w.capacity >> p.w.step_log2, cut = (p.w.slots + p.tiles) / (p.tiles > 0 ? p.tiles : 1);
+  const int parts = (keys < cut ? keys : cut) + 1;  // of a row, about, at most
   int rows_here = 1024 / p.dv, shares = 1;
   const auto blocks_of = [&](int rows) { return (long long)p.tiles * ((p.w.R + rows - 1) / rows); };
-  while (rows_here > 1 && shares < 8 && blocks_of(rows_here / 2) <= 2 * kDenseSms) {
+  while (rows_here > 1 && shares < 8 && 4 * shares < parts && blocks_of(rows_here / 2) <= 2 * kDenseSms) {
     rows_here /= 2;
     shares *= 2;
   }
