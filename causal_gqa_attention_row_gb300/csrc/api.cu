@@ -1041,8 +1041,7 @@ size_t attn_tree_paged_workspace_bytes(int N, int B, int max_rows, int max_len, 
   if (bf16 < 0 || N <= 0 || B <= 0 || max_rows <= 0 || max_len <= 0 || !heads_ok(H, Hkv) || !width_ok(d_k) ||
       !width_ok(d_v))
     return 0;
-  // a call with ALiBi slopes, say, runs on the SIMT kernel; fewer rows of a sequence may make larger
-  // tiles of more heads' rows, never more of them
+  // (a block size that the tensor cores do not take, or a scale below zero, runs on the SIMT kernel)
   size_t most = 0;
   for (int tc = 0; tc < 2; ++tc) {
     TreeLayout t;
@@ -1073,7 +1072,9 @@ gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool
   bool arms_on;
   const gqa_status sa = apply_arms(arm, arms, &arms_on);
   if (sa != GQA_OK) return sa;
-  const bool tc = gqa::tree_tc_supported(bf16, d_k, d_v, block_size) && attention_scale > 0.f && !arm.alibi;
+  // (tensor cores and SIMT kernel: 4 sequences of 4-8 rows behind up to 600 keys, 14 heads on 2 of 64, 11.7 and 14.5 us;
+  // 32 of one row behind up to 4,096, 32 heads on 8 of 128, 53 and 253; 64 of up to 32 rows 162 and 2,238)
+  const bool tc = gqa::tree_tc_supported(bf16, d_k, d_v, block_size) && attention_scale > 0.f;
   const int capacity = max_blocks_per_seq * block_size;
   TreeLayout t;
   if (!tree_layout(N, B, max_rows, capacity, H, Hkv, d_k, d_v, bf16, tc, &t)) return GQA_ERR_UNSUPPORTED;
@@ -1155,8 +1156,9 @@ gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool
       d.window = arm.window;
       d.cap_out = arm.softcap2;
       d.cap_in = arm.softcap2 > 0.f ? d.qscale / arm.softcap2 : 0.f;
+      d.alibi = arm.alibi;
       d.tree = p.w;
-      e = gqa::launch_dense_tc(q, k_pool, v_pool, d, 1, d_k, d_v, arm.window > 0 || arm.softcap2 > 0.f, st);
+      e = gqa::launch_dense_tc(q, k_pool, v_pool, d, 1, d_k, d_v, arm.window > 0 || arm.softcap2 > 0.f || arm.alibi, st);
     } else {
       e = gqa::launch_tree_rows(p, bf16, st);
     }

@@ -589,9 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (TREE) {
           const TreeSeq& s = tree_seq[u.seq];
           tree_n = s.n;
-          if (ARMS && p.window > 0 && warp_live) {
+          if (ARMS && (p.window > 0 || p.alibi) && warp_live) {
             const int row = u.i0 + min(r, rows - 1) / p.GH;
             depth = tree_depth(p.tree, row, row - s.row0, tree_n);
+            pos = s.hist + depth - 1;
             lo_key = min(first_visible_key(s.hist + depth - 1, p.window), s.hist);  // (drafted rows: by their masks)
           }
         } else if (ARMS) {  // a row is a sequence of its own length; its position is its last key's
@@ -681,6 +682,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 sv[c][e] = __float_as_uint(fmaf(alibi2, (float)(c * 32 + e), __uint_as_float(sv[c][e])));
+            if (TREE && drafted) {  // (a drafted row stands at its depth, not at its place: a lane for each 32nd column)
+              const TreeSeq* s = tree_seq + u.seq;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int j = j0 + 32 * c + lane - s->hist;
+                const int off = j >= 0 && j < tree_n ? tree_depth(p.tree, s->row0 + j, j, tree_n) - 1 - j : 0;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  sv[c][e] = __float_as_uint(fmaf(alibi2, (float)__shfl_sync(0xffffffffu, off, e), __uint_as_float(sv[c][e])));
+              }
+            }
           }
         }
         // keys that some row of the warp does not see weigh zero for it

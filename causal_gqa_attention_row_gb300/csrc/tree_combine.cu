@@ -96,6 +96,10 @@ __device__ __noinline__ void row_again(const TreeParams& p, int b, const Row& r,
     for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     s *= p.qscale;
     if (p.softcap2 > 0.f) s = p.softcap2 * (1.f - 2.f / (exp2_of(s * (2.8853900817779268f / p.softcap2)) + 1.f));
+    if (p.alibi) {
+      const int j = key - r.hist, at_key = j < 0 ? key : r.hist + tree_depth(w, r.row0 + j, j, r.n) - 1;
+      s = fmaf(__ldg(p.alibi + h) * kLog2e, (float)(at_key - (r.hist + r.depth - 1)), s);
+    }
     const float mn = fmaxf(m, s), c = mn == -INFINITY ? 0.f : mn;
     const float f = exp2_of(m - c), x = exp2_of(s - c);
     m = mn;

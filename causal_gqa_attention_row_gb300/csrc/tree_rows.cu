@@ -1,5 +1,5 @@
 // tree_rows.cu -- attention of drafted rows (attn_tree_paged) where the tensor cores do not take the
-// call: fp32, other head widths, other block sizes, ALiBi slopes.
+// call: fp32, other head widths, other block sizes, a scale that is not positive.
 //
 //   out[r] = softmax over the history and the drafted rows that r sees of scale * q_r . k_j, times v_j
 //

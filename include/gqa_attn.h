@@ -565,8 +565,8 @@ gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa
  * rows than max_rows set the device error word, and their rows are left as they are; where row_starts goes back,
  * so are those of other sequences too (of up to 500 in a row, the sequences of a launch).
  * bf16 with (d_k, d_v) = (64, 64), (128, 128), (192, 128) or (256, 256), block_size a multiple of 8 dividing 128,
- * attention_scale > 0 and no ALiBi slopes runs on the tcgen05 tensor-core kernel (the probabilities rounded to
- * bf16 for the product with V), every other case on a SIMT kernel of fp32 arithmetic. How a sequence's keys are
+ * and attention_scale > 0 runs on the tcgen05 tensor-core kernel (the probabilities rounded to bf16 for the
+ * product with V), every other case on a SIMT kernel of fp32 arithmetic. How a sequence's keys are
  * split depends on the batch, so the last bits of its results do too; repeated calls give the same bits.
  * workspace: at least attn_tree_paged_workspace_bytes(..) bytes, 16-byte aligned, always needed; calls
  * whose kernels may overlap must not share one. The size does for smaller N, B, max_rows and max_len too.

@@ -205,7 +205,7 @@ def test_arms(gpu_lib, dt, d, arms):
                 c["tables"][b, :max(0, h - a["window"] + 1) // c["bs"]] = -1
         out = run(g, c, 0.11, **a)
         assert g.attn_get_device_error() == g.OK
-        verify_arms(c, 0.11, out, dt == BF16 and "alibi_slopes" not in a, a)
+        verify_arms(c, 0.11, out, dt == BF16, a)
 
 
 def verify_arms(c, scale, out, tc, a):
@@ -254,6 +254,28 @@ def test_what_a_row_does_not_see_does_not_reach_it(gpu_lib, dt, d, of, what):
     out = run(g, c, 0.1, window=50).double()
     o = S.attend(c["q"].double().cpu().numpy(), rows_of(c, c["k"], 0), rows_of(c, c["v"], 0), 200, c["seen"], 0.1, window=50)
     check(excess(out[5:], tuple(x[5:] for x in o), dt == BF16, dt == BF16, d, 230), 1.0)
+
+
+@pytest.mark.parametrize("dt,d", PATHS)
+def test_what_a_row_does_not_see_with_every_arm(gpu_lib, dt, d):
+    """The rows worked out again have the arms too."""
+    g = gpu_lib
+    H = 4
+    a = dict(window=90, softcap=20.0, sinks=torch.linspace(-1, 3, H, device=DEV),
+             alibi_slopes=torch.tensor([2.0 ** -(h + 2) for h in range(H)], device=DEV))
+    c = case([30, 12], [100, 270], H, 2, d, d, dt=dt, seed=5)
+    for b, j in ((0, 4), (1, 7)):
+        at = c["hist"][b] + j
+        c["v"][int(c["tables"][b, at // 16]), :, at % 16, 3] = float("nan")
+    out = run(g, c, 0.1, **a).double()
+    kw = dict(window=90, softcap=20.0, sinks=a["sinks"].double().cpu().numpy(), slopes=a["alibi_slopes"].double().cpu().numpy())
+    worst = 0.0
+    for b, j in ((0, 4), (1, 7)):
+        s = slice(int(c["starts"][b]), int(c["starts"][b + 1]))
+        o = S.attend(c["q"][s].double().cpu().numpy(), rows_of(c, c["k"], b), rows_of(c, c["v"], b), c["hist"][b], c["seen"][s], 0.1, **kw)
+        free = [i for i in range(c["rows"][b]) if j not in c["seen"][s.start + i]]
+        worst = max(worst, excess(out[s][free], tuple(x[free] for x in o), dt == BF16, dt == BF16, d, c["hist"][b] + c["rows"][b], 20.0))
+    check(worst, 1.0)
 
 
 @pytest.mark.parametrize("dt,d", PATHS)
