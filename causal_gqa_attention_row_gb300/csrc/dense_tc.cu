@@ -30,7 +30,8 @@
 // and a first load. The shared prefixes' units are drawn from a ticket counter; those of
 // attn_cross go round by slot: alike but for lengths on the device, which shorten a sequence's
 // last unit and leave those behind it empty; those of drafted rows follow from a line of all work,
-// which each CTA sums up for itself (tree_part.cuh), and all leave partial results (tree_combine.cu).
+// which each CTA sums up for itself (tree_part.cuh); they leave partial results (tree_combine.cu) but for those
+// that have all keys of their rows.
 // Where a sequence has two tiles of drafted rows the halves take one each of the same keys, and their K
 // and V stages become one ring: the first half's producer brings K, the second's V, and a stage is free
 // once both halves have done with it.
@@ -43,7 +44,7 @@
 // cap (1,390 W, 1,980 MHz). What bounds them is a half's time from tile to tile, of 1,024 cycles
 // of products: in the last case about 3,200 cycles, S, softmax and PV of a half one after
 // another; in the second a third more, for K and V that come from HBM through one stage each.
-// Drafted rows, with the join: 64 sequences of up to 32 behind up to 8,192 keys 175 us (6.25 TB/s, 0.92 of
+// Drafted rows, with the join: 64 sequences of up to 32 behind up to 8,192 keys 172 us (6.4 TB/s, 0.94 of
 // the copy bandwidth; 160 without the join); 8 sequences of 48 to 64 (two tiles) behind 16,384 to 32,768 keys
 // 182 us (4.4 TB/s, 0.98 PFLOP/s), 1.86 us a tile.
 //
