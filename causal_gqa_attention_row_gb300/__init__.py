@@ -576,6 +576,7 @@ def kv_append_paged_rows(q, k_new, v_new, q_out, k_pool, v_pool, block_tables, r
 # object for each pointer, kv_plan_rows took 12 us of a Grace core).
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_device = torch._C._cuda_getDevice  # torch.cuda.current_device without its look at the set-up, which the tensors show
 
 
 def _at(t, dev, dtype):
@@ -619,7 +620,7 @@ def kv_plan_rows(seq_lens, new_rows, block_tables, blocks_in, blocks_out, free_l
             (keep_blocks is not None and keep_blocks.numel() != B) or row_starts.numel() != B + 1 or slots.numel() != N or
             free_in.numel() < 1 or free_out.numel() != 2):
         raise ValueError("the lengths, the blocks, row_starts, positions, slots and the list's counts do not agree")
-    dev = torch.cuda.current_device()
+    dev = _device()
     _check(load().kv_plan_rows(
         _at(seq_lens, dev, _I32), _at(new_rows, dev, _I32), _at(block_tables, dev, _I32), _at(blocks_in, dev, _I32),
         _at(blocks_out, dev, _I32), _at(keep_blocks, dev, _I32), _at(free_list, dev, _I32), _at(free_in, dev, _I32),
@@ -648,14 +649,15 @@ def kv_append_slots(q, k_new, v_new, q_out, k_pool, v_pool, slots, positions=Non
         raise ValueError("slots and positions must be [N]")
     if (q_weight is not None and q_weight.shape != (dk,)) or (k_weight is not None and k_weight.shape != (dk,)):
         raise ValueError(f"a norm weight must be [{dk}]")
-    dev = torch.cuda.current_device()
+    dev = _device()
     dt = k_new.dtype
-    for t in (q, k_new, v_new, q_out):
-        if t is not None and (t.dtype is not dt or t.get_device() != dev):
-            raise (TypeError("tensors must share one dtype") if t.dtype is not dt else
-                   ValueError("tensors must live on the current CUDA device"))
-    if rope is not None:
-        _here(rope.table)
+    for t in (k_new, v_new) if q is None else (q, k_new, v_new, q_out):
+        if t.dtype is not dt:
+            raise TypeError("tensors must share one dtype")
+        if t.get_device() != dev:
+            raise ValueError("tensors must live on the current CUDA device")
+    if rope is not None and rope.table.get_device() != dev:
+        raise ValueError("tensors must live on the current CUDA device")
     _check(load().kv_append_slots(
         _view(q, 3), _view(k_new, 3), _view(v_new, 3), _view(q_out, 3), _at(k_pool, dev, dt), _at(v_pool, dev, dt),
         _at(slots, dev, _I64), _at(positions, dev, _I32), N, nb, bs, H, Hkv, dk, dv, _at(q_weight, dev, dt),
@@ -693,7 +695,7 @@ def attn_tree_paged(q, k_pool, v_pool, block_tables, position_offset, row_starts
     if (k_pool.shape != (nb, Hkv, bs, dk) or out.shape != (N, H, dv) or row_starts.numel() != B + 1 or
             (position_offset is not None and position_offset.numel() != B)):
         raise ValueError("q, the pools, the tables, the lengths, row_starts and out do not agree")
-    dev = torch.cuda.current_device()
+    dev = _device()
     arms = None
     if window or softcap or sinks is not None or alibi_slopes is not None:
         _here(sinks, alibi_slopes)
@@ -715,16 +717,21 @@ def attn_tree_paged(q, k_pool, v_pool, block_tables, position_offset, row_starts
 
 def kv_commit_rows(k_pools, v_pools, block_tables, seq_lens_in, row_starts, path, n_path, seq_lens_out, stream=None):
     """Moves row seq_lens_in[b] + path[b][j] to row seq_lens_in[b] + j, j < n_path[b], in every layer's pools
-    (k_pools, v_pools: a tensor [num_blocks, Hkv, bs, d] each layer; v_pools None: keys alone) and sets
+    (k_pools, v_pools: a tensor [num_blocks, Hkv, bs, d] each layer, or one of all layers [layers, num_blocks, ..],
+    which is looked at once: 28 layers 16 us a call instead of 32; v_pools None: keys alone) and sets
     seq_lens_out[b] = seq_lens_in[b] + n_path[b] (may be the same tensor). path int32 [B, max_path], ascending
     indices among the row_starts[b + 1] - row_starts[b] drafted rows; n_path int32 [B]."""
     layers = len(k_pools)
     B, mbps = block_tables.shape
     if not layers or (v_pools is not None and len(v_pools) != layers):
         raise ValueError("a pool of keys, and with values one of those, for each layer")
-    k_shape, dt = k_pools[0].shape, k_pools[0].dtype
+
+    def shape_of(pools):
+        return pools.shape[1:] if isinstance(pools, torch.Tensor) else pools[0].shape
+
+    k_shape, dt = shape_of(k_pools), k_pools.dtype if isinstance(k_pools, torch.Tensor) else k_pools[0].dtype
     nb, Hkv, bs, dk = k_shape
-    v_shape = k_shape if v_pools is None else v_pools[0].shape
+    v_shape = k_shape if v_pools is None else shape_of(v_pools)
     dv = 0 if v_pools is None else v_shape[3]
     if (v_shape[:3] != k_shape[:3] or len(v_shape) != 4 or path.dim() != 2 or path.shape[0] != B or row_starts.numel() != B + 1 or
             seq_lens_in.numel() != B or n_path.numel() != B or seq_lens_out.numel() != B):
@@ -732,6 +739,9 @@ def kv_commit_rows(k_pools, v_pools, block_tables, seq_lens_in, row_starts, path
     dev = block_tables.get_device()
 
     def addresses(pools, shape):
+        if isinstance(pools, torch.Tensor):
+            at, step = _at(pools, dev, dt), pools.stride(0) * pools.element_size()
+            return struct.pack(f"{layers}Q", *range(at, at + layers * step, step))
         for x in pools:
             if x.shape != shape or x.dtype is not dt or x.get_device() != dev or not x.is_contiguous():
                 raise ValueError("the layers' pools must be alike, contiguous and on one device")
@@ -739,7 +749,7 @@ def kv_commit_rows(k_pools, v_pools, block_tables, seq_lens_in, row_starts, path
 
     k_at = addresses(k_pools, k_shape)
     v_at = None if v_pools is None else addresses(v_pools, v_shape)
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _device():
         raise ValueError("tensors must live on the current CUDA device")
     _check(load().kv_commit_rows(
         k_at, v_at, layers, _at(block_tables, dev, _I32),

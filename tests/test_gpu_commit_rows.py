@@ -84,6 +84,19 @@ def test_overlapping_moves(gpu_lib):
         np.testing.assert_array_equal(x.double().cpu().numpy(), y)
 
 
+def test_one_tensor_of_all_layers(gpu_lib):
+    g = gpu_lib
+    c = case(5, 3, 20, 2, 64, 32, 16, torch.bfloat16, seed=4)
+    want = [wanted(c, x) for x in c["k"] + c["v"]]
+    c["k"], c["v"] = torch.stack(c["k"]), torch.stack(c["v"])
+    run(g, c)
+    assert g.attn_get_device_error() == g.OK
+    for x, y in zip([*c["k"], *c["v"]], want):
+        np.testing.assert_array_equal(x.double().cpu().numpy(), y)
+    with pytest.raises(ValueError):  # layers that do not lie one behind the other
+        g.kv_commit_rows(c["k"][::2], None, i32(c["tables"]), i32(c["lens"]), i32(c["starts"]), i32(c["path"]), i32([0] * 5), i32([0] * 5))
+
+
 @pytest.mark.parametrize("same", [False, True])
 @pytest.mark.parametrize("what", ["order", "twice", "past", "below", "count", "length", "capacity", "entry", "starts"])
 def test_bad_paths(gpu_lib, what, same):
