@@ -77,13 +77,13 @@ def commit(pool, table, length, path):
 
 def attend(q, k, v, hist, seen, scale, window=0, softcap=0.0, sinks=None, slopes=None):
     """q [n, H, dk] of one sequence's drafted rows, k [Hkv, hist + n, dk], v [.., dv]; seen[i]: the drafted rows
-    that row i sees. A drafted row stands at position hist + (rows that it sees) - 1. Keys that a row does not see
+    that row i sees. A drafted row stands at position hist + (rows that it sees, at least 1) - 1. Keys that a row does not see
     take no part, whatever they hold. Returns the output, sum_j w_j |v_j| and the largest scale * sum |q_i k_ji|."""
     n, H, _ = q.shape
     dv = v.shape[2]
     out, size, reach = np.zeros((n, H, dv)), np.zeros((n, H, dv)), np.zeros((n, H, 1))
     G = H // k.shape[0]
-    at = [hist + len(s) - 1 for s in seen]
+    at = [hist + max(len(s), 1) - 1 for s in seen]
     for i in range(n):
         keys = [(j, j) for j in range(hist)] + [(hist + j, at[j]) for j in sorted(seen[i])]
         if window > 0:

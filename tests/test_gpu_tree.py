@@ -181,6 +181,8 @@ def test_masks(gpu_lib, dt, d):
     out = run(g, c, 0.1)
     verify(c, 0.1, out, tc=dt == BF16)
     assert (out[70] == 0).all() and (out[72] == 0).all()  # no history, no bit
+    for window in (1, 4, 40):  # (a row that sees no drafted row stands where the first one does)
+        verify(c, 0.1, run(g, c, 0.1, window=window), tc=dt == BF16, window=window)
     assert g.attn_get_device_error() == g.OK
 
 
