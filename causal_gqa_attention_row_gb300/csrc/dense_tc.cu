@@ -46,7 +46,7 @@
 // another; in the second a third more, for K and V that come from HBM through one stage each.
 // Drafted rows, with the join: 64 sequences of up to 32 behind up to 8,192 keys 172 us (6.4 TB/s, 0.94 of
 // the copy bandwidth; 160 without the join); 8 sequences of 48 to 64 (two tiles) behind 16,384 to 32,768 keys
-// 182 us (4.4 TB/s, 0.98 PFLOP/s), 1.86 us a tile.
+// 182 us (4.4 TB/s, 0.98 PFLOP/s), 1.80 us a tile.
 //
 //   warps 0-3, 4-7   softmax of half 0, 1: thread t owns row t of the tile (TMEM lane t)
 //   warps 8, 11      TMA producer of half 0, 1 (Q once a unit, then K and V tiles; paged:
@@ -583,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float alibi2 = 0.f;
       bool warp_live;
       int depth = 0, tree_n = 0;  // drafted rows: those that this row sees, and the sequence's
+      int plain_end = 0;          // where they begin
       {
         const int rows = u.n_i * p.GH;  // rows of the tile in use
         warp_live = quarter * 32 < rows;
@@ -590,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (TREE) {
           const TreeSeq& s = tree_seq[u.seq];
           tree_n = s.n;
+          plain_end = s.hist;
           if (ARMS && (p.window > 0 || p.alibi) && warp_live) {
             const int row = u.i0 + min(r, rows - 1) / p.GH;
             depth = tree_depth(p.tree, row, row - s.row0, tree_n);
@@ -614,9 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool drafted = false;           // some of the tile's keys are
         uint4 seen = make_uint4(~0u, ~0u, ~0u, ~0u);
         if (TREE) {
-          const TreeSeq* s = tree_seq + u.seq;
-          drafted = j0 + kBN > s->hist;
-          if (drafted && lim != INT_MAX) seen = tree_mask_of<ARMS>(p, s, u.i0 + r / p.GH, tree_n, j0, depth);
+          drafted = j0 + kBN > plain_end;
+          if (drafted && lim != INT_MAX) seen = tree_mask_of<ARMS>(p, tree_seq + u.seq, u.i0 + r / p.GH, tree_n, j0, depth);
         }
         if (!warp_wait_tc(&hb.s_full, t_all & 1, bars, p.err)) {
           alive = false;

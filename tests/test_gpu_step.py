@@ -9,6 +9,7 @@ from dense_bound import excess
 from margins import check
 from oracle import rows as R
 from oracle import step as S
+from test_gpu_qk_rows import excess as rows_excess
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -117,12 +118,13 @@ def test_steps(gpu_lib, dt, H, Hkv, d, captured):
             for x in range(layers):
                 if n == 0:
                     continue
-                # the rows as they lie in the cache (their rounding is test_gpu_append_slots.py's)
+                # the rows as they lie in the cache
                 blk, row = p.slots[s] // bs, p.slots[s] % bs
                 kc = p.k[x][blk, :, row].double().cpu().numpy()
                 vc = p.v[x][blk, :, row].double().cpu().numpy()
-                want = R.rotate(p.kn[x][s].double().cpu().numpy(), at, freqs, "half")[0]
-                assert np.abs(kc - want).max() <= 0.03 if dt == torch.bfloat16 else np.abs(kc - want).max() <= 1e-4
+                want, size = R.rotate(p.kn[x][s].double().cpu().numpy(), at, freqs, "half")
+                check(rows_excess(p.k[x][blk, :, row], want, size, dt, at), 1.0)
+                assert torch.equal(p.v[x][blk, :, row], p.vn[x][s])
                 k = np.concatenate([rows[b][x][0], kc]).transpose(1, 0, 2)
                 v = np.concatenate([rows[b][x][1], vc]).transpose(1, 0, 2)
                 o = S.attend(p.q_rot[x][s].double().cpu().numpy(), k, v, hist, seen[s], 0.1)
