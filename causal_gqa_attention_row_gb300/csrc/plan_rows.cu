@@ -8,8 +8,8 @@
 //   the list is a stack: the R blocks given back go onto it, sequence by sequence, entries
 //   ascending; the t-th block taken is the one at free + R - 1 - t
 //
-// Measured in replayed graphs: 256 sequences of one row 5.7 us, 128 trees of up to 64 rows 6.9, 48 prompts of up to
-// 2,048 rows with too few blocks 6.7, 794 trees of seven rows 7.3.
+// Measured in replayed graphs: 256 sequences of one row 5.0 us, 128 trees of up to 64 rows 5.9, 48 prompts of up to
+// 2,048 rows with too few blocks 6.0, 794 trees of seven rows 7.3.
 //
 // What it reads and writes is small (20 bytes a sequence, 12 and more a row), so what bounds it is
 // latency: one launch, and in it one chain of loads (the lengths, the block, the store). So no
@@ -158,8 +158,8 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
   __syncthreads();
   // ---- blocks that are taken: all that are wanted, or as many as the sequences served take
   int taken = (int)min((long long)total.take, room);
-  const bool keeper = p.write_state && blockIdx.x == 0 && blockIdx.y == 0;  // writes what the next step starts from
-  if (total.take > room || keeper) {
+  const bool state_only = !p.write_rows;  // (one CTA)
+  if (total.take > room || state_only) {
     int before = 0, most = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += kRound) {
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
         v.take += take[k];
         const bool served = take[k] == 0 || v.take <= room;
         if (served && take[k]) most = v.take;
-        if (keeper && b + k < p.B) p.held_out[b + k] = served ? need[k] : held[k];
+        if (state_only && b + k < p.B) p.held_out[b + k] = served ? need[k] : held[k];
       }
       before += sum.take;
     }
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
   }
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     if (__syncthreads_or(bad) && tid == 0 && p.report) raise_error(p.err, kErrBounds);
-    if (keeper && tid == 0) {  // (every thread has read the count)
+    if (p.write_state && tid == 0) {  // (every thread has read the count)
       p.free_out[0] = (int)min(room - taken, (long long)p.num_blocks);
       p.free_out[1] = total.take - taken;
     }
@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
     const bool served = r.ok && (take == 0 || (long long)took + take <= room);
     int* table = p.tables + (size_t)b * p.mbps;
     if (at0 == 0) {
+      if (p.write_state) p.held_out[b] = served ? r.need : r.held;
       p.row_starts[b] = (int)min(start, (long long)INT_MAX);
       if (b == p.B - 1) p.row_starts[p.B] = (int)min(start + r.rows, (long long)INT_MAX);
     }
