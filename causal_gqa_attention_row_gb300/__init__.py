@@ -575,8 +575,10 @@ def kv_append_paged_rows(q, k_new, v_new, q_out, k_pool, v_pool, block_tables, r
 # the GPU: their arguments are looked at once each, and go as plain numbers (with the helpers above, which build an
 # object for each pointer, kv_plan_rows took 12 us of a Grace core).
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_device = torch._C._cuda_getDevice  # torch.cuda.current_device without its look at the set-up, which the tensors show
+# (absent from a build of PyTorch without CUDA, where the package can still be imported)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# torch.cuda.current_device without its look at the set-up, which the tensors show
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _at(t, dev, dtype):
