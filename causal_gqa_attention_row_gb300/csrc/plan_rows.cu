@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
       if (e < 0 || e >= p.num_blocks) raise_error(p.err, kErrBounds);
       if (free + (long long)g < room - taken && free + (long long)g < p.num_blocks) p.free_list[free + g] = e;
     }
-    if (served)
-      for (int k = at0; k < take; k += step) table[r.held + k] = block(r.held + k);
+    // (what a sequence that is not served wanted: -1, not a block of before that another has by now)
+    for (int k = at0; k < take; k += step) table[r.held + k] = served ? block(r.held + k) : -1;
     // rows
     const int rows = (int)min((long long)r.rows, max(0ll, p.N - start));
     for (int i = at0; i < rows; i += step) {

@@ -506,10 +506,10 @@ gqa_status kv_append_paged_rows(const gqa_heads* q, const gqa_heads* k_new, cons
  * Sequence b needs max(ceil((seq_lens[b] + new_rows[b]) / block_size), keep_blocks[b]) blocks. Blocks
  * past that go back onto the stack (sequence by sequence, entries ascending), then those that are
  * missing are taken off it, in the order of the sequences, until one cannot be served: it and later
- * ones that need blocks get none, keep what they have, and their rows have no slot. A finished request
- * (seq_lens 0, new_rows 0) gives its blocks back. Entries behind blocks_out[b] and stack places behind
- * free_out[0] hold whatever they held, so that the same call again (with arrays of its own for
- * blocks_out and free_out) gives the same.
+ * ones that need blocks get none, keep what they have, and their rows have no slot; the entries that they
+ * wanted are -1. A finished request (seq_lens 0, new_rows 0) gives its blocks back. Other entries
+ * behind blocks_out[b] and stack places behind free_out[0] hold whatever they held, so that the same call again
+ * (with arrays of its own for blocks_out and free_out) gives the same.
  *   row_starts   int32 [B + 1]: the prefix sums of new_rows
  *   positions    int32 [N]: seq_lens[b] + i for row i of sequence b; with parents, + its depth
  *   slots        int64 [N]: block * block_size + row in the block; -1 for a row without one

@@ -9,12 +9,16 @@ import math
 import numpy as np
 
 
-def plan(lens, new, tables, held, free_list, free, bs, num_blocks, N, keep=None):
+def plan(lens, new, tables, held, free_list, free, bs, num_blocks, N, keep=None, bad=()):
     """Returns (tables, held, free_list, free, missing, row_starts, positions, slots); lists and arrays are copied.
-    What a stack place or table entry held stays where nothing is written."""
+    What a stack place or table entry held stays where nothing is written; entries that a sequence wanted and did not
+    get are -1. Sequences `bad` have numbers out of range:
+    their blocks stay and their rows have no slot."""
     B, mbps = tables.shape
     tables, stack = tables.copy(), list(free_list[:free])
     need = [max(-(-(lens[b] + new[b]) // bs), 0 if keep is None else keep[b]) for b in range(B)]
+    for b in bad:
+        need[b] = held[b]
     for b in range(B):
         for k in range(need[b], held[b]):
             stack.append(tables[b, k])
@@ -25,6 +29,7 @@ def plan(lens, new, tables, held, free_list, free, bs, num_blocks, N, keep=None)
         if take and wanted > room:
             short.add(b)
             missing += take
+            tables[b, held[b]:need[b]] = -1
             continue
         for k in range(held[b], held[b] + take):
             tables[b, k] = stack[room - 1 - taken]
@@ -32,13 +37,13 @@ def plan(lens, new, tables, held, free_list, free, bs, num_blocks, N, keep=None)
     left = room - taken
     out_list = np.array(free_list).copy()
     out_list[free:left] = stack[free:left]
-    starts = np.concatenate([[0], np.cumsum(new)])
+    starts = np.concatenate([[0], np.cumsum(np.maximum(new, 0))])
     positions, slots = np.zeros(N, np.int64), np.full(N, -1, np.int64)
     for b in range(B):
-        for i in range(new[b]):
+        for i in range(min(new[b], N - starts[b])):
             at = lens[b] + i
             positions[starts[b] + i] = at
-            if b not in short:
+            if b not in short and b not in bad:
                 slots[starts[b] + i] = int(tables[b, at // bs]) * bs + at % bs
     held_out = [held[b] if b in short else need[b] for b in range(B)]
     return tables, np.array(held_out), out_list, left, missing, starts, positions, slots
