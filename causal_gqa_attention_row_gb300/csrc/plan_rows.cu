@@ -8,15 +8,14 @@
 //   the list is a stack: the R blocks given back go onto it, sequence by sequence, entries
 //   ascending; the t-th block taken is the one at free + R - 1 - t
 //
-// Measured in replayed graphs: 256 sequences of one row 5.0 us, 128 trees of up to 64 rows 5.9, 48 prompts of up to
-// 2,048 rows with too few blocks 6.0, 794 trees of seven rows 7.3.
+// Measured in replayed graphs: 256 sequences of one row 4.9 us, 128 trees of up to 64 rows 6.1, 48 prompts of up to
+// 2,048 rows with too few blocks 6.1, 794 trees of seven rows 7.0.
 //
 // What it reads and writes is small (20 bytes a sequence, 12 and more a row), so what bounds it is
 // latency: one launch, and in it one chain of loads (the lengths, the block, the store). So no
-// CTA waits for another: each scans all lengths for itself (a thread takes four
-// sequences, 1024 of them a round) and then writes what is its sequences' own, a warp or
-// more for each (a CTA for each sequence had 794 of them of seven rows scan all lengths 794 times:
-// 11 to 13 us). A block that is
+// CTA waits for another: each scans all lengths for itself (and looks at all entries that are given
+// back, below) and then writes what is its sequences' own, a warp or more for each (a CTA for each
+// sequence had 794 of them of seven rows scan all lengths 794 times: 11 to 13 us). A block that is
 // given back and taken in one call is not read from the list, where another CTA would be
 // writing it, but found at its place in the table that gives it back, by a search over the
 // prefix sums of give_b, which stay in shared memory. The list below `free` is only read, above
@@ -33,15 +32,15 @@ namespace gqa {
 namespace {
 
 constexpr int kPlanRowsThreads = 256;
-constexpr int kPer = 4;                             // sequences of a thread in a round
-constexpr int kRound = kPlanRowsThreads * kPer;
+constexpr int kMany = 16, kLongs = 1024;            // of entries given back (below)
 
 // What sequence b brings.
 struct Req {
   int len, rows, held, need;  // rows: those that count for the starts; need: held where nothing moves
   bool ok;                    // its numbers are in range
 };
-__device__ __forceinline__ Req request(const PlanRows& p, int b) {
+// out: a bit each for sequences that are out of range by what they give back (NULL: there are none).
+__device__ __forceinline__ Req request(const PlanRows& p, int b, const uint32_t* out) {
   Req r;
   r.len = __ldg(p.lens + b);
   const int n = __ldg(p.new_rows + b);
@@ -50,7 +49,7 @@ __device__ __forceinline__ Req request(const PlanRows& p, int b) {
   const long long want = (long long)r.len + n;
   r.rows = n > 0 && n <= p.N ? n : 0;
   r.ok = r.len >= 0 && n >= 0 && n <= p.N && want <= (long long)p.mbps * p.bs && r.held >= 0 && r.held <= p.mbps &&
-         keep >= 0 && keep <= r.held;
+         keep >= 0 && keep <= r.held && !(out && out[b >> 5] >> (b & 31) & 1u);
   r.need = r.ok ? max((int)((want + p.bs - 1) / p.bs), keep) : r.held;
   return r;
 }
@@ -110,52 +109,121 @@ __device__ __forceinline__ int walk_up(const PlanRows& p, long long start, int i
   return depth;
 }
 
+// A bit each for the sequences that give back an entry that is no block.
+__device__ __noinline__ void look_for_them(const PlanRows& p, uint32_t* out) {
+  for (int i = threadIdx.x; i < (p.B + 31) / 32; i += kPlanRowsThreads) {
+    uint32_t bits = 0;
+    for (int b = 32 * i; b < min(p.B, 32 * i + 32); ++b) {
+      const Req r = request(p, b, nullptr);
+      bool none = false;
+      for (int k = r.need; k < r.held; ++k)
+        none |= (unsigned)__ldg(p.tables + (size_t)b * p.mbps + k) >= (unsigned)p.num_blocks;
+      bits |= (uint32_t)none << (b & 31);
+    }
+    out[i] = bits;
+  }
+}
+
+// PER: sequences of a thread in a round of the scans. One where that takes a round or two (256 sequences of one row
+// 4.9 us, with four 6.0), four where it would take more (1,024 of them 7.3 us, with one 8.9).
+template <int PER>
 __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanRows p) {
+  constexpr int kPer = PER, kRound = kPlanRowsThreads * kPer, kFew = PER == 1 ? 8 : 4;
   __shared__ Sums sums[kPlanRowsThreads / 32];
-  __shared__ int taken_s;
+  __shared__ int taken_s, n_longs;
+  __shared__ int2 longs[kLongs];  // sequences that give back more than kFew: where in the tables, how many
   extern __shared__ __align__(16) unsigned char dyn[];
   Sums* first = reinterpret_cast<Sums*>(dyn);       // before each of this CTA's sequences
   int* give0 = reinterpret_cast<int*>(first + p.per);  // [B + 1]
+  uint32_t* out_s = reinterpret_cast<uint32_t*>(give0 + p.B + 1);
+  if (threadIdx.x == 0) n_longs = 0;
+  __syncthreads();
   // launched as a programmatic dependent: the lengths may come from the kernel before this one
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x;
   const int b_lo = (int)min((long long)blockIdx.x * p.per, (long long)p.B), b_hi = min(p.B, b_lo + p.per);
   const int free_raw = __ldg(p.free_in), free = min(max(free_raw, 0), p.num_blocks);
-  // ---- all lengths
-  Sums total = {0, 0, 0};  // (blocks wanted, whether served or not)
+  // ---- all lengths, and all entries that are given back: one that is no block must not come onto the list, so its
+  // sequence keeps all, and where the others' blocks lie on the list hangs on that. The thread that has the length of
+  // a sequence that gives back a few reads them behind the scan; of those that give back more a half warp each does. If one
+  // turns out to be no block, its sequences are looked for and everything is summed up without them. (128 requests of
+  // 256 that are over and give back 16,000 entries: 7.5 us, 5.0 without a look at them.)
+  const uint32_t* out = nullptr;
+  Sums total;  // (blocks wanted, whether served or not)
   bool bad = free_raw != free;
+  const auto block_entry = [&](int e) { return (unsigned)e < (unsigned)p.num_blocks; };
 #pragma unroll 1
-  for (int b0 = 0; b0 < p.B; b0 += kRound) {
-    const int b = b0 + tid * kPer;
-    Sums of[kPer], v = {0, 0, 0}, sum;
+  while (true) {
+    total = Sums{0, 0, 0};
+    bool found = false;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += kRound) {
+      const int b = b0 + tid * kPer;
+      Sums of[kPer], v = {0, 0, 0}, sum;
+      unsigned back[kPer][kFew];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      of[k] = Sums{0, 0, 0};
-      if (b + k < p.B) {
-        const Req r = request(p, b + k);
-        bad |= !r.ok;
-        of[k] = Sums{r.rows, max(0, r.need - r.held), max(0, r.held - r.need)};
+      for (int k = 0; k < kPer; ++k) {
+        of[k] = Sums{0, 0, 0};
+#pragma unroll
+        for (int x = 0; x < kFew; ++x) back[k][x] = 0;
+        if (b + k < p.B) {
+          const Req r = request(p, b + k, out);
+          bad |= !r.ok;
+          of[k] = Sums{r.rows, max(0, r.need - r.held), max(0, r.held - r.need)};
+          const int at = (b + k) * p.mbps + r.need, give = of[k].give;
+#pragma unroll
+          for (int x = 0; x < kFew; ++x)
+            if (x < give) back[k][x] = (unsigned)__ldg(p.tables + at + x);
+          if (give > kFew && !out) {
+            const int to = atomicAdd(&n_longs, 1);
+            if (to < kLongs) longs[to] = make_int2(at + kFew, give - kFew);
+            else
+              for (int x = kFew; x < give; ++x) found |= !block_entry(__ldg(p.tables + at + x));
+          }
+        }
+        v = Sums{v.rows + of[k].rows, v.take + of[k].take, v.give + of[k].give};
       }
-      v = Sums{v.rows + of[k].rows, v.take + of[k].take, v.give + of[k].give};
-    }
-    scan(v, sum, sums);
-    v = Sums{v.rows + total.rows, v.take + total.take, v.give + total.give};
+      scan(v, sum, sums);
+      v = Sums{v.rows + total.rows, v.take + total.take, v.give + total.give};
+      unsigned most = 0;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (b + k < p.B) give0[b + k] = v.give;
-      if (b + k >= b_lo && b + k < b_hi) first[b + k - b_lo] = v;
-      v = Sums{v.rows + of[k].rows, v.take + of[k].take, v.give + of[k].give};
+      for (int k = 0; k < kPer; ++k) {
+        if (b + k < p.B) give0[b + k] = v.give;
+        if (b + k >= b_lo && b + k < b_hi) first[b + k - b_lo] = v;
+        v = Sums{v.rows + of[k].rows, v.take + of[k].take, v.give + of[k].give};
+#pragma unroll
+        for (int x = 0; x < kFew; ++x) most = max(most, back[k][x]);
+      }
+      found |= most >= (unsigned)p.num_blocks;
+      total = Sums{total.rows + sum.rows, total.take + sum.take, total.give + sum.give};
     }
-    total = Sums{total.rows + sum.rows, total.take + sum.take, total.give + sum.give};
-  }
-  if (tid == 0) {
-    give0[p.B] = total.give;
-    taken_s = 0;
+    if (tid == 0) {
+      give0[p.B] = total.give;
+      taken_s = 0;
+    }
+    if (!out) {  // (the scan ends with a barrier: they are all noted)
+#pragma unroll 1
+      for (int i = tid / 16; i < min(n_longs, kLongs); i += kPlanRowsThreads / 16) {
+        const int2 l = longs[i];
+#pragma unroll 1
+        for (int k = tid % 16; k < l.y; k += 16 * kMany) {
+          unsigned e[kMany], most = 0;
+#pragma unroll
+          for (int x = 0; x < kMany; ++x) e[x] = k + 16 * x < l.y ? (unsigned)__ldg(p.tables + l.x + k + 16 * x) : 0;
+#pragma unroll
+          for (int x = 0; x < kMany; ++x) most = max(most, e[x]);
+          found |= most >= (unsigned)p.num_blocks;
+        }
+      }
+    }
+    if (!__syncthreads_or(found) || out) break;
+    look_for_them(p, out_s);
+    out = out_s;
+    __syncthreads();
   }
   const long long room = (long long)free + total.give;  // blocks that can be taken
   bad |= room > p.num_blocks || total.rows > p.N;
-  __syncthreads();
   // ---- blocks that are taken: all that are wanted, or as many as the sequences served take
   int taken = (int)min((long long)total.take, room);
   const bool state_only = !p.write_rows;  // (one CTA)
@@ -170,7 +238,7 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
       for (int k = 0; k < kPer; ++k) {
         take[k] = need[k] = held[k] = 0;
         if (b + k < p.B) {
-          const Req r = request(p, b + k);
+          const Req r = request(p, b + k, out);
           need[k] = r.need;
           held[k] = r.held;
           take[k] = max(0, r.need - r.held);
@@ -214,12 +282,12 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
       if (give0[mid] <= g) lo = mid;
       else hi = mid;
     }
-    const Req r = request(p, lo);
+    const Req r = request(p, lo, out);
     return __ldg(p.tables + (size_t)lo * p.mbps + r.need + (g - give0[lo]));
   };
 #pragma unroll 1
   for (int b = b_lo + tid / lanes; b < b_hi; b += kPlanRowsThreads / lanes) {
-    const Req r = request(p, b);
+    const Req r = request(p, b, out);
     const long long start = first[b - b_lo].rows;
     const int took = first[b - b_lo].take;
     const int take = max(0, r.need - r.held), give = max(0, r.held - r.need);
@@ -239,7 +307,6 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
     // blocks given back, those of them that stay on the list
     for (int k = at0; k < give; k += step) {
       const int g = give0[b] + k, e = __ldg(table + r.need + k);
-      if (e < 0 || e >= p.num_blocks) raise_error(p.err, kErrBounds);
       if (free + (long long)g < room - taken && free + (long long)g < p.num_blocks) p.free_list[free + g] = e;
     }
     // (what a sequence that is not served wanted: -1, not a block of before that another has by now)
@@ -277,10 +344,13 @@ cudaError_t launch_plan_rows(PlanRows p, cudaStream_t st) {
   int dev = 0;
   cudaGetDevice(&dev);
   static std::atomic<unsigned long long> attr_done{0};  // per device
+  const auto kernel = p.B <= 2 * kPlanRowsThreads ? plan_rows_kernel<1> : plan_rows_kernel<4>;
   if (dev >= 64 || !(attr_done.load(std::memory_order_acquire) >> dev & 1ull)) {
-    const cudaError_t e = cudaFuncSetAttribute(plan_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kPlanRowsMaxB * 5 + 64 * 1024);
-    if (e != cudaSuccess) return e;
+    for (const auto k : {plan_rows_kernel<1>, plan_rows_kernel<4>}) {
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kPlanRowsMaxB * 5 + 64 * 1024);
+      if (e != cudaSuccess) return e;
+    }
     if (dev < 64) attr_done.fetch_or(1ull << dev, std::memory_order_release);
   }
   // a warp for a sequence, up to a CTA where sequences have that many rows (slices of them beyond that); up
@@ -294,7 +364,7 @@ cudaError_t launch_plan_rows(PlanRows p, cudaStream_t st) {
   const int gx = (p.B + p.per - 1) / p.per;
   const long long slices = (rows + kPlanRowsThreads - 1) / kPlanRowsThreads;
   const int gy = slices <= 1 ? 1 : slices < most / gx ? (int)slices : most / gx < 1 ? 1 : most / gx;
-  const size_t smem = (size_t)p.per * sizeof(Sums) + (size_t)(p.B + 1) * 4;
+  const size_t smem = (size_t)p.per * sizeof(Sums) + (size_t)(p.B + 1) * 4 + (size_t)(p.B + 31) / 32 * 4;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)gx, (unsigned)gy);
   cfg.blockDim = dim3(kPlanRowsThreads);
@@ -309,13 +379,13 @@ cudaError_t launch_plan_rows(PlanRows p, cudaStream_t st) {
   p.write_rows = 1;
   p.write_state = !same;
   p.report = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_rows_kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess || !same) return e;
   p.write_rows = 0;
   p.write_state = 1;
   p.report = 0;
   cfg.gridDim = dim3(1);
-  return cudaLaunchKernelEx(&cfg, plan_rows_kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace gqa

@@ -1,10 +1,12 @@
-"""The index arrays of a step that cannot serve a sequence (GPU): every output of every sequence against the plain plan;
-whole numbers, equal."""
+"""The index arrays of a step that cannot serve a sequence, or whose numbers are out of range (GPU): the sequence that
+has them keeps its blocks and its rows have no slot; every output of every sequence against the plain plan; whole
+numbers, equal."""
 import numpy as np
 import pytest
+import torch
 
 from oracle import step as S
-from test_gpu_plan_rows import run
+from test_gpu_plan_rows import case, run
 
 pytestmark = pytest.mark.gpu
 
@@ -39,6 +41,87 @@ def verify(c, got, bad, parents=None, words=1):
         np.testing.assert_array_equal(x, y)
 
 
+def flagged(g):
+    assert g.attn_get_device_error() == g.ERR_DEVICE_BOUNDS
+    assert g.attn_get_device_error() == g.OK
+
+
+@pytest.mark.parametrize("same", [False, True])
+@pytest.mark.parametrize("entry", [-1, 60, 1 << 30])
+@pytest.mark.parametrize("at", [3, 5, 8])
+def test_an_entry_given_back_that_is_no_block(gpu_lib, at, entry, same):
+    """(a request behind a window, say, whose first entries are gone)"""
+    g, c = gpu_lib, small()
+    c["tables"][2, at] = entry
+    got, _ = run(g, c, same=same)
+    flagged(g)
+    verify(c, got, [2])
+
+
+@pytest.mark.parametrize("same", [False, True])
+def test_a_finished_request_with_entries_that_are_gone(gpu_lib, same):
+    g, c = gpu_lib, small()
+    c["tables"][3, :4] = -1
+    c["tables"][1, 8] = c["nb"]
+    got, _ = run(g, c, same=same)
+    flagged(g)
+    verify(c, got, [1, 3])
+
+
+@pytest.mark.parametrize("B,finished", [(257, 0.3), (1500, 0.6), (4000, 0.2)])
+def test_many_sequences_with_such_entries(gpu_lib, B, finished):
+    """More rounds than one of lengths and of entries, blocks wanting."""
+    g = gpu_lib
+    c = case(B, 500, 20, 16, seed=B, finished=finished, room=0.8, pad=5)
+    r = np.random.default_rng(1)
+    need = -(-(c["lens"] + c["new"]) // c["bs"])
+    giving = np.flatnonzero(need < c["held"])
+    bad = sorted(r.choice(giving, 9, replace=False).tolist()) + [int(giving[-1])]
+    for b in bad:
+        c["tables"][b, r.integers(need[b], c["held"][b])] = r.choice([-1, c["nb"], -(1 << 31)])
+    got, _ = run(g, c)
+    flagged(g)
+    verify(c, got, sorted(set(bad)))
+
+
+def test_a_parent_that_does_not_precede_its_row(gpu_lib):
+    """It counts as hanging on the history, and those below it go by that."""
+    g, c = gpu_lib, small()
+    par = np.full(c["N"], -1)
+    start = int(c["new"][:5].sum())
+    par[start + 1:start + 40] = np.arange(39)
+    for up in (7, 9, 39, -2, 1 << 30):
+        given, meant = par.copy(), par.copy()
+        given[start + 7], meant[start + 7] = up, -1
+        got, _ = run(g, c, given, 1)
+        flagged(g)
+        verify(c, got, [], meant)
+
+
+@pytest.mark.parametrize("same", [False, True])
+@pytest.mark.parametrize("what", ["length", "rows", "many", "capacity", "held", "keep"])
+def test_the_others_are_as_ever(gpu_lib, what, same):
+    g, c = gpu_lib, small()
+    c["keep"] = np.array([0, 8, 0, 2, 0, 1, 0])
+    if what == "length":
+        c["lens"][2] = -1
+    elif what == "rows":
+        c["new"][2] = -3
+    elif what == "many":  # more than N by itself: counts as none
+        c["new"][2] = 1 << 30
+    elif what == "capacity":
+        c["lens"][2] = 12 * 16 - 2
+    elif what == "held":
+        c["held"][2] = 13
+    else:
+        c["keep"][2] = 10
+    got, _ = run(g, c, same=same)
+    flagged(g)
+    if what == "many":
+        c["new"][2] = 0
+    verify(c, got, [2])
+
+
 @pytest.mark.parametrize("same", [False, True])
 def test_a_sequence_that_cannot_be_served_has_no_entries_behind_its_own(gpu_lib, same):
     """What it wanted and did not get is -1 in its row of the table, not a block of before that others hold by now."""
@@ -52,3 +135,25 @@ def test_a_sequence_that_cannot_be_served_has_no_entries_behind_its_own(gpu_lib,
     assert g.attn_get_device_error() == g.OK
     assert got[3][1] > 0 and (got[0][4, 4:11] == -1).all() and got[0][4, 11] != -1
     verify(c, got, [])
+
+
+def test_refused_and_captured(gpu_lib):
+    """The same in a graph, replayed on other numbers: good ones, then bad ones again."""
+    g, c = gpu_lib, small()
+    first, (args, kw) = run(g, c)
+    verify(c, first, [])
+    assert g.attn_get_device_error() == g.OK
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.kv_plan_rows(*args, **kw)
+    outs = (args[2], args[4], args[5], args[7], args[8], args[9], args[10])
+    for bad in ([2], [], [2]):
+        c = small()
+        if bad:
+            c["tables"][2, 4] = -1
+        args[2].copy_(torch.tensor(c["tables"]))
+        args[5].copy_(torch.tensor(c["free_list"]))
+        graph.replay()
+        torch.cuda.synchronize()
+        verify(c, [x.cpu().numpy() for x in outs] + [None], bad)
+        assert g.attn_get_device_error() == (g.ERR_DEVICE_BOUNDS if bad else g.OK)
