@@ -36,10 +36,10 @@ constexpr int kMany = 16, kLongs = 1024;            // of entries given back (be
 
 // What sequence b brings.
 struct Req {
-  int len, rows, held, need;  // rows: those that count for the starts; need: held where nothing moves
+  int len, rows, held, need;  // need: held where nothing moves
   bool ok;                    // its numbers are in range
 };
-// out: a bit each for sequences that are out of range by what they give back (NULL: there are none).
+// out: a bit each for sequences that are out of range by other numbers (NULL: there are none).
 __device__ __forceinline__ Req request(const PlanRows& p, int b, const uint32_t* out) {
   Req r;
   r.len = __ldg(p.lens + b);
@@ -47,7 +47,7 @@ __device__ __forceinline__ Req request(const PlanRows& p, int b, const uint32_t*
   r.held = p.held_in[b];  // (may be the array that the state is written to)
   const int keep = p.keep ? __ldg(p.keep + b) : 0;
   const long long want = (long long)r.len + n;
-  r.rows = n > 0 && n <= p.N ? n : 0;
+  r.rows = max(n, 0);
   r.ok = r.len >= 0 && n >= 0 && n <= p.N && want <= (long long)p.mbps * p.bs && r.held >= 0 && r.held <= p.mbps &&
          keep >= 0 && keep <= r.held && !(out && out[b >> 5] >> (b & 31) & 1u);
   r.need = r.ok ? max((int)((want + p.bs - 1) / p.bs), keep) : r.held;
@@ -109,13 +109,13 @@ __device__ __forceinline__ int walk_up(const PlanRows& p, long long start, int i
   return depth;
 }
 
-// A bit each for the sequences that give back an entry that is no block.
-__device__ __noinline__ void look_for_them(const PlanRows& p, uint32_t* out) {
+// A bit each for the sequences that give back an entry that is no block, and for those with rows from `cut` on.
+__device__ __noinline__ void look_for_them(const PlanRows& p, int cut, uint32_t* out) {
   for (int i = threadIdx.x; i < (p.B + 31) / 32; i += kPlanRowsThreads) {
     uint32_t bits = 0;
     for (int b = 32 * i; b < min(p.B, 32 * i + 32); ++b) {
       const Req r = request(p, b, nullptr);
-      bool none = false;
+      bool none = b >= cut && r.rows > 0;
       for (int k = r.need; k < r.held; ++k)
         none |= (unsigned)__ldg(p.tables + (size_t)b * p.mbps + k) >= (unsigned)p.num_blocks;
       bits |= (uint32_t)none << (b & 31);
@@ -130,13 +130,16 @@ template <int PER>
 __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanRows p) {
   constexpr int kPer = PER, kRound = kPlanRowsThreads * kPer, kFew = PER == 1 ? 8 : 4;
   __shared__ Sums sums[kPlanRowsThreads / 32];
-  __shared__ int taken_s, n_longs;
+  __shared__ int taken_s, n_longs, cut_s;
   __shared__ int2 longs[kLongs];  // sequences that give back more than kFew: where in the tables, how many
   extern __shared__ __align__(16) unsigned char dyn[];
   Sums* first = reinterpret_cast<Sums*>(dyn);       // before each of this CTA's sequences
   int* give0 = reinterpret_cast<int*>(first + p.per);  // [B + 1]
   uint32_t* out_s = reinterpret_cast<uint32_t*>(give0 + p.B + 1);
-  if (threadIdx.x == 0) n_longs = 0;
+  if (threadIdx.x == 0) {
+    n_longs = 0;
+    cut_s = INT_MAX;
+  }
   __syncthreads();
   // launched as a programmatic dependent: the lengths may come from the kernel before this one
   grid_dep_wait();
@@ -147,8 +150,8 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
   // ---- all lengths, and all entries that are given back: one that is no block must not come onto the list, so its
   // sequence keeps all, and where the others' blocks lie on the list hangs on that. The thread that has the length of
   // a sequence that gives back a few reads them behind the scan; of those that give back more a half warp each does. If one
-  // turns out to be no block, its sequences are looked for and everything is summed up without them. (128 requests of
-  // 256 that are over and give back 16,000 entries: 7.5 us, 5.0 without a look at them.)
+  // turns out to be no block, or the rows are more than N, such sequences are looked for and everything is summed up
+  // without them. (128 requests of 256 that are over and give back 16,000 entries: 7.5 us, 5.0 without a look at them.)
   const uint32_t* out = nullptr;
   Sums total;  // (blocks wanted, whether served or not)
   bool bad = free_raw != free;
@@ -191,6 +194,7 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
       for (int k = 0; k < kPer; ++k) {
         if (b + k < p.B) give0[b + k] = v.give;
         if (b + k >= b_lo && b + k < b_hi) first[b + k - b_lo] = v;
+        if (of[k].rows > 0 && v.rows + of[k].rows > p.N) atomicMin(&cut_s, b + k);
         v = Sums{v.rows + of[k].rows, v.take + of[k].take, v.give + of[k].give};
 #pragma unroll
         for (int x = 0; x < kFew; ++x) most = max(most, back[k][x]);
@@ -217,8 +221,8 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
         }
       }
     }
-    if (!__syncthreads_or(found) || out) break;
-    look_for_them(p, out_s);
+    if (!__syncthreads_or(found || total.rows > p.N) || out) break;
+    look_for_them(p, cut_s, out_s);
     out = out_s;
     __syncthreads();
   }

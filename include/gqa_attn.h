@@ -510,19 +510,23 @@ gqa_status kv_append_paged_rows(const gqa_heads* q, const gqa_heads* k_new, cons
  * wanted are -1. A finished request (seq_lens 0, new_rows 0) gives its blocks back. Other entries
  * behind blocks_out[b] and stack places behind free_out[0] hold whatever they held, so that the same call again
  * (with arrays of its own for blocks_out and free_out) gives the same.
- *   row_starts   int32 [B + 1]: the prefix sums of new_rows
+ *   row_starts   int32 [B + 1]: the prefix sums of new_rows (a count below 0: none)
  *   positions    int32 [N]: seq_lens[b] + i for row i of sequence b; with parents, + its depth
  *   slots        int64 [N]: block * block_size + row in the block; -1 for a row without one
  *   parents      int32 [N] or NULL: each packed row's parent in its tree, -1 .. its own index - 1
  *   tree_mask    uint64 [N, mask_words] (with parents): bit j of row i: row j of the sequence is
  *                row i or an ancestor of it
  * Rows behind the last sequence get position 0, slot -1 and an empty mask. Numbers out of range set the device error
- * word. A length or count below 0, more rows than N or than a table row or a mask can name, blocks_in or keep_blocks
- * out of range, an entry among those given back that is no block: such a sequence keeps its blocks and its rows have no
- * slot (a request that is over, of a cache whose blocks in front of a window are gone, goes once the entries that it
- * still has are at the front of its row). An entry that is no block where rows would lie, or one taken off the list
- * (-1 in the table then): those rows have no slot. A parent that does not precede its row: the row counts as hanging on
- * the history. More blocks free than there are: as many as there are. B is at most 16384, B * max_blocks_per_seq at most INT_MAX;
+ * word:
+ *   - a length or count below 0, rows past the first N, more of them than a table row or a mask can name, blocks_in or
+ *     keep_blocks out of range, an entry among those given back that is no block: the sequence keeps its blocks and its
+ *     rows have no slot (a request that is over, of a cache whose blocks in front of a window are gone, goes once
+ *     the entries that it still has are at the front of its row);
+ *   - an entry that is no block where rows would lie, or one taken off the list (-1 in the table then): those rows have
+ *     no slot;
+ *   - a parent that does not precede its row: the row counts as hanging on the history;
+ *   - more blocks free than there are: as many as there are.
+ * B is at most 16384, B * max_blocks_per_seq at most INT_MAX;
  * B = 0 does nothing. No workspace.
  */
 gqa_status kv_plan_rows(const int32_t* seq_lens, const int32_t* new_rows, int32_t* block_tables,

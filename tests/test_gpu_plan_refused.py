@@ -68,9 +68,9 @@ def test_a_finished_request_with_entries_that_are_gone(gpu_lib, same):
     verify(c, got, [1, 3])
 
 
-@pytest.mark.parametrize("B,finished", [(257, 0.3), (1500, 0.6), (4000, 0.2)])
+@pytest.mark.parametrize("B,finished", [(257, 0.3), (1500, 0.6), (4000, 0.2), (3000, 0.8)])
 def test_many_sequences_with_such_entries(gpu_lib, B, finished):
-    """More rounds than one of lengths and of entries, blocks wanting."""
+    """More rounds than one of lengths and of entries, more sequences that give back many than are noted, blocks wanting."""
     g = gpu_lib
     c = case(B, 500, 20, 16, seed=B, finished=finished, room=0.8, pad=5)
     r = np.random.default_rng(1)
@@ -82,6 +82,19 @@ def test_many_sequences_with_such_entries(gpu_lib, B, finished):
     got, _ = run(g, c)
     flagged(g)
     verify(c, got, sorted(set(bad)))
+
+
+@pytest.mark.parametrize("same", [False, True])
+@pytest.mark.parametrize("less", [1, 2, 21, 63])
+def test_more_rows_than_there_is_room_for(gpu_lib, less, same):
+    """The sequence that does not fit, and those behind it that have rows."""
+    g, c = gpu_lib, small()
+    total = int(c["new"].sum())
+    c["N"] = total - less
+    end = np.cumsum(c["new"])
+    got, _ = run(g, c, same=same)
+    flagged(g)
+    verify(c, got, [b for b in range(7) if c["new"][b] and end[b] > c["N"]])
 
 
 def test_a_parent_that_does_not_precede_its_row(gpu_lib):
@@ -107,7 +120,7 @@ def test_the_others_are_as_ever(gpu_lib, what, same):
         c["lens"][2] = -1
     elif what == "rows":
         c["new"][2] = -3
-    elif what == "many":  # more than N by itself: counts as none
+    elif what == "many":  # more than N by itself: no row behind it is in range
         c["new"][2] = 1 << 30
     elif what == "capacity":
         c["lens"][2] = 12 * 16 - 2
@@ -117,9 +130,7 @@ def test_the_others_are_as_ever(gpu_lib, what, same):
         c["keep"][2] = 10
     got, _ = run(g, c, same=same)
     flagged(g)
-    if what == "many":
-        c["new"][2] = 0
-    verify(c, got, [2])
+    verify(c, got, [2, 4, 5, 6] if what == "many" else [2])
 
 
 @pytest.mark.parametrize("same", [False, True])
