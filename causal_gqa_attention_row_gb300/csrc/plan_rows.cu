@@ -49,7 +49,7 @@ __device__ __forceinline__ Req request(const PlanRows& p, int b, const uint32_t*
   const long long want = (long long)r.len + n;
   r.rows = max(n, 0);
   r.ok = r.len >= 0 && n >= 0 && n <= p.N && want <= (long long)p.mbps * p.bs && r.held >= 0 && r.held <= p.mbps &&
-         keep >= 0 && keep <= r.held && !(out && out[b >> 5] >> (b & 31) & 1u);
+         keep >= 0 && keep <= r.held && (!p.parents || n <= 64ll * p.words) && !(out && out[b >> 5] >> (b & 31) & 1u);
   r.need = r.ok ? max((int)((want + p.bs - 1) / p.bs), keep) : r.held;
   return r;
 }
@@ -325,10 +325,7 @@ __global__ void __launch_bounds__(kPlanRowsThreads) plan_rows_kernel(const PlanR
       }
       p.slots[start + i] = slot;
       int at = i;
-      if (p.parents) {
-        if (i >= 64 * p.words) raise_error(p.err, kErrBounds);
-        at = walk_up(p, start, i);
-      }
+      if (p.parents) at = walk_up(p, start, i);
       p.positions[start + i] = r.len + at;
     }
   }

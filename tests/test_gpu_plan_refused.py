@@ -97,6 +97,22 @@ def test_more_rows_than_there_is_room_for(gpu_lib, less, same):
     verify(c, got, [b for b in range(7) if c["new"][b] and end[b] > c["N"]])
 
 
+@pytest.mark.parametrize("same", [False, True])
+def test_more_rows_than_a_mask_can_name(gpu_lib, same):
+    g, c = gpu_lib, small()
+    c["new"][2] = 70
+    c["N"] = int(c["new"].sum()) + 1
+    par = np.full(c["N"], -1)
+    at = 0
+    r = np.random.default_rng(2)
+    for n in c["new"]:
+        par[at + 1:at + n] = [r.integers(0, i) for i in range(1, n)]
+        at += n
+    got, _ = run(g, c, par, 1, same=same)
+    flagged(g)
+    verify(c, got, [2], par)
+
+
 def test_a_parent_that_does_not_precede_its_row(gpu_lib):
     """It counts as hanging on the history, and those below it go by that."""
     g, c = gpu_lib, small()
