@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<ET, DK, DV>::kCtas)
         if (t < n_tiles && key < u.key1) {
           const int e = __ldg(p.tables + (size_t)u.b * p.mbps + key / w.bs);
           if (e >= 0 && e < p.num_blocks) at = ((long long)e * p.Hkv + kvh) * w.bs + key % w.bs;
-          else raise_error(w.err, kErrBounds);
+          else if (e >= 0 || key < u.hist) raise_error(w.err, kErrBounds);  // (below 0 behind it: no block was to be had)
         }
         pool_row[(t & 1) * kTreeKeys + tid] = at;
       }

@@ -488,6 +488,8 @@ gqa_status kv_append_paged_rows(const gqa_heads* q, const gqa_heads* k_new, cons
  * itself. kv_plan_rows makes the step's index arrays (the blocks too), kv_append_slots writes the
  * rows, attn_tree_paged is their attention, and kv_commit_rows keeps those of the path that was
  * accepted. A step of plain rows (one each, or chunks of prompts) is the case without parents.
+ * Where blocks are wanting the step runs all the same: the rows of a sequence that is not served have no slots and are
+ * not written, its outputs mean nothing, it must have no path, and the next step may bring its rows again.
  * The rows of all sequences lie packed, as for kv_append_paged_rows; `position_offset` and
  * `seq_lens` below are the rows present before the step's.
  */
@@ -570,6 +572,8 @@ gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa
  * not reach it, whatever the slot holds, an infinity or NaN included. Sequences with lengths out of range or more
  * rows than max_rows set the device error word, and their rows are left as they are; where row_starts goes back,
  * so are those of other sequences too (of up to 500 in a row, the sequences of a launch).
+ * A table entry that is no block sets it too, and the outputs of its sequence mean nothing. Below 0 and behind the
+ * history (kv_plan_rows leaves such to a sequence that it could not serve) it sets nothing, but they mean nothing either.
  * bf16 with (d_k, d_v) = (64, 64), (128, 128), (192, 128) or (256, 256), block_size a multiple of 8 dividing 128,
  * and attention_scale > 0 runs on the tcgen05 tensor-core kernel (the probabilities rounded to bf16 for the
  * product with V), every other case on a SIMT kernel of fp32 arithmetic. How a sequence's keys are
@@ -603,7 +607,8 @@ size_t attn_tree_paged_workspace_bytes(int N, int B, int max_rows, int max_len, 
  *   seq_lens_in int32 [B], seq_lens_out int32 [B] (may be the same array, at the cost of a second launch)
  * A path that does not ascend or leaves the drafted rows, a length out of range, or a table entry that
  * is no block leaves the sequence as it is (seq_lens_out[b] = seq_lens_in[b]) and sets the device error
- * word. Two sequences must not name one block for the rows that move. d_k and d_v multiples of 8, at
+ * word. A sequence whose rows have no slots, since kv_plan_rows could not serve it, has nothing to keep: n_path 0.
+ * Two sequences must not name one block for the rows that move. d_k and d_v multiples of 8, at
  * most 1024. No workspace.
  */
 gqa_status kv_commit_rows(void* const* k_pools, void* const* v_pools, int n_layers, const int32_t* block_tables,
