@@ -578,8 +578,9 @@ gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa
  * and attention_scale > 0 runs on the tcgen05 tensor-core kernel (the probabilities rounded to bf16 for the
  * product with V), every other case on a SIMT kernel of fp32 arithmetic. How a sequence's keys are
  * split depends on the batch, so the last bits of its results do too; repeated calls give the same bits.
- * workspace: at least attn_tree_paged_workspace_bytes(..) bytes, 16-byte aligned, always needed; calls
- * whose kernels may overlap must not share one. The size does for smaller N, B, max_rows and max_len too.
+ * workspace: at least attn_tree_paged_workspace_bytes(N, B, max_rows, max_blocks_per_seq * block_size, ..) bytes,
+ * 16-byte aligned, always needed; calls whose kernels may overlap must not share one. The size does for smaller N, B,
+ * max_rows and max_len too.
  * H / GH * (N / RPT + B) * (max_blocks_per_seq * block_size / 64 + 3), with GH * RPT = 64 to 128 heads times
  * rows, is at most INT_MAX.
  */
@@ -588,8 +589,8 @@ gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool
                            void* out, int N, int B, int max_rows, int mask_words, int max_blocks_per_seq, int num_blocks,
                            int block_size, int H, int Hkv, int d_k, int d_v, float attention_scale, gqa_dtype dt,
                            void* workspace, size_t workspace_bytes, const gqa_arms* arms, void* stream);
-/* For up to N rows of B sequences, max_rows of one, and max_len keys (history and drafted rows) of one; 0 for
- * arguments that attn_tree_paged refuses. Host only; launches nothing. */
+/* For up to N rows of B sequences, max_rows of one, and table rows that name up to max_len rows of the cache, however
+ * many of them a sequence has; 0 for arguments that attn_tree_paged refuses. Host only; launches nothing. */
 size_t attn_tree_paged_workspace_bytes(int N, int B, int max_rows, int max_len, int H, int Hkv, int d_k, int d_v,
                                        gqa_dtype dt);
 
