@@ -568,8 +568,9 @@ gqa_status kv_append_slots(const gqa_heads* q, const gqa_heads* k_new, const gqa
  *   arms        as for attn_decode_paged_ex, or NULL. A drafted row's position, by which the window and the
  *               ALiBi slopes go, is position_offset[b] + (drafted rows that it sees, at least 1) - 1: its depth
  *               in a tree. A window hides drafted rows too.
- * A row that sees no key gets zeros; a key that scores -infinity weighs zero. What a row does not see does
- * not reach it, whatever the slot holds, an infinity or NaN included. Sequences with lengths out of range or more
+ * A row that sees no key gets zeros; a key that scores -infinity weighs zero, but a value that a row sees has to be
+ * finite even so: an infinity or NaN in it may reach the row's output in that column, whatever the key weighs. What a
+ * row does not see does not reach it, whatever the slot holds, an infinity or NaN included. Sequences with lengths out of range or more
  * rows than max_rows set the device error word, and their rows are left as they are; where row_starts goes back,
  * so are those of other sequences too (of up to 500 in a row, the sequences of a launch).
  * A table entry that is no block sets it too, and the outputs of its sequence mean nothing. Below 0 and behind the

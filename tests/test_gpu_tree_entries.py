@@ -1,8 +1,12 @@
-"""Attention of drafted rows (GPU) over tables with entries that are no blocks."""
+"""Attention of drafted rows (GPU) over tables with entries that are no blocks, and over keys that score -infinity; the
+tolerance is dense_bound.py's."""
 import pytest
 import torch
 
-from test_gpu_tree import BF16, F32, PATHS, case, run, verify
+from dense_bound import excess
+from margins import check
+from oracle import step as S
+from test_gpu_tree import BF16, DEV, F32, PATHS, case, rows_of, run, verify
 
 pytestmark = pytest.mark.gpu
 WIDE = (192, 128)
@@ -26,3 +30,32 @@ def test_drafted_rows_without_blocks(gpu_lib, dt, dims):
         out = run(g, c, 0.1)
         assert g.attn_get_device_error() == (g.ERR_DEVICE_BOUNDS if error else g.OK)
         assert torch.equal(out[end[1]:], want[end[1]:])
+
+
+@pytest.mark.parametrize("dt,dims", KINDS, ids=str)
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_values_of_keys_that_score_minus_infinity(gpu_lib, dt, dims, what):
+    """Such a key weighs zero. What its value holds may reach a row that sees it, in that column alone; the other rows
+    and columns are as without it."""
+    g = gpu_lib
+    rows, hist = [30, 12], [100, 290]
+    for b, j in ((0, 7), (0, 104), (1, 200), (1, 295)):
+        c = case(rows, hist, 4, 2, *dims, dt=dt, seed=5)
+        c["q"][:, :, 0] = 1.0
+        at = int(c["tables"][b, j // 16]), slice(None), j % 16
+        c["k"][at][:, 0] = -float("inf")
+        c["v"][at][:, 3] = what
+        out = run(g, c, 0.1).double()
+        assert g.attn_get_device_error() == g.OK
+        c["v"][at][:, 3] = 0.0
+        worst = 0.0
+        for x, n in enumerate(rows):
+            s = slice(int(c["starts"][x]), int(c["starts"][x + 1]))
+            o = S.attend(c["q"][s].double().cpu().numpy(), rows_of(c, c["k"], x), rows_of(c, c["v"], x), hist[x], c["seen"][s], 0.1)
+            sees = [i for i in range(n) if x == b and (j < hist[x] or j - hist[x] in c["seen"][s.start + i])]
+            got = out[s].clone()
+            for i in sees:
+                col = got[i, :, 3]
+                got[i, :, 3] = torch.where(torch.isfinite(col), col, torch.tensor(o[0][i, :, 3], device=DEV))
+            worst = max(worst, excess(got, o, dt == BF16, dt == BF16, dims[0], hist[x] + n))
+        check(worst, 1.0)
