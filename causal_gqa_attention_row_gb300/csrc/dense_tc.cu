@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           }
-          odd = !(z == 0.f);
+          odd = !(z == 0.f) && l_run * 0.f == 0.f;  // (a NaN of the row's own scores is meant)
         }
         odd = __any_sync(0xffffffffu, odd);
         if (lane == 0) p.tree.odd[4 * (size_t)~at + quarter] = odd;

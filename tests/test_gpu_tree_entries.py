@@ -59,3 +59,25 @@ def test_values_of_keys_that_score_minus_infinity(gpu_lib, dt, dims, what):
                 got[i, :, 3] = torch.where(torch.isfinite(col), col, torch.tensor(o[0][i, :, 3], device=DEV))
             worst = max(worst, excess(got, o, dt == BF16, dt == BF16, dims[0], hist[x] + n))
         check(worst, 1.0)
+
+
+@pytest.mark.parametrize("dt,dims", KINDS, ids=str)
+@pytest.mark.parametrize("many", [False, True])
+def test_a_sequence_without_numbers(gpu_lib, dt, dims, many):
+    """Queries, keys and values of a sequence's drafted rows, or its queries and drafted values, are NaN: its rows are
+    NaN throughout, the others to the bit as they were. many: more row tiles than the GPU takes at a time."""
+    g = gpu_lib
+    rows, hist = ([30, 12, 9], [100, 290, 40]) if not many else ([5, 12, 9] * 70, [20, 60, 0] * 70)
+    c = case(rows, hist, 4, 2, *dims, dt=dt, seed=8)
+    want = run(g, c, 0.1)
+    verify(c, 0.1, want, tc=dt == BF16)
+    s, at = slice(int(c["starts"][1]), int(c["starts"][2])), hist[1] + torch.arange(rows[1], device=DEV)
+    where = c["tables"][1].long()[at // c["bs"]], slice(None), at % c["bs"]
+    c["q"][s] = float("nan")
+    c["v"][where] = float("nan")
+    for of in ("v", "k"):
+        c[of][where] = float("nan")
+        out = run(g, c, 0.1)
+        assert g.attn_get_device_error() == g.OK
+        assert torch.isnan(out[s]).all()
+        assert torch.equal(out[:s.start], want[:s.start]) and torch.equal(out[s.stop:], want[s.stop:])
