@@ -111,16 +111,14 @@ __device__ __forceinline__ int walk_up(const PlanRows& p, long long start, int i
 
 // A bit each for the sequences that give back an entry that is no block, and for those with rows from `cut` on.
 __device__ __noinline__ void look_for_them(const PlanRows& p, int cut, uint32_t* out) {
-  for (int i = threadIdx.x; i < (p.B + 31) / 32; i += kPlanRowsThreads) {
-    uint32_t bits = 0;
-    for (int b = 32 * i; b < min(p.B, 32 * i + 32); ++b) {
-      const Req r = request(p, b, nullptr);
-      bool none = b >= cut && r.rows > 0;
-      for (int k = r.need; k < r.held; ++k)
-        none |= (unsigned)__ldg(p.tables + (size_t)b * p.mbps + k) >= (unsigned)p.num_blocks;
-      bits |= (uint32_t)none << (b & 31);
-    }
-    out[i] = bits;
+  for (int i = threadIdx.x; i < (p.B + 31) / 32; i += kPlanRowsThreads) out[i] = 0;
+  __syncthreads();
+  for (int b = threadIdx.x / 16; b < p.B; b += kPlanRowsThreads / 16) {
+    const Req r = request(p, b, nullptr);
+    bool none = b >= cut && r.rows > 0;
+    for (int k = r.need + (int)threadIdx.x % 16; k < r.held; k += 16)
+      none |= (unsigned)__ldg(p.tables + (size_t)b * p.mbps + k) >= (unsigned)p.num_blocks;
+    if (none) atomicOr(out + b / 32, 1u << (b & 31));
   }
 }
 

@@ -164,6 +164,30 @@ def test_a_sequence_that_cannot_be_served_has_no_entries_behind_its_own(gpu_lib,
     verify(c, got, [])
 
 
+@pytest.mark.parametrize("same", [False, True])
+@pytest.mark.parametrize("what", ["list", "rows"])
+def test_rows_whose_block_is_none(gpu_lib, what, same):
+    """A place of the list that holds no block, or an entry in use where rows would lie: just those rows have no slot."""
+    g, c = gpu_lib, small(held=np.array([2, 7, 3, 0, 4, 1, 3]), free=6)
+    c["free_list"][:6] = [x for x in range(c["nb"]) if x not in c["tables"]][:6]
+    nb = c["nb"]
+    if what == "list":
+        c["free_list"][4] = nb  # sequence 4 takes it for the first of its two
+    else:
+        c["tables"][6, 2] = nb
+    got, _ = run(g, c, same=same)
+    flagged(g)
+    tables, held, flist, left, missing, starts, pos, slots = S.plan(c["lens"], c["new"], c["tables"], c["held"], c["free_list"],
+                                                                    c["free"], c["bs"], nb, c["N"])
+    assert (slots >= nb * c["bs"]).sum() == (16 if what == "list" else 2)
+    slots[slots >= nb * c["bs"]] = -1
+    if what == "list":
+        assert tables[4, 4] == nb
+        tables[4, 4] = -1
+    for x, y in zip(got, (tables, held, flist, [left, missing], starts, pos, slots)):
+        np.testing.assert_array_equal(x, y)
+
+
 def test_refused_and_captured(gpu_lib):
     """The same in a graph, replayed on other numbers: good ones, then bad ones again."""
     g, c = gpu_lib, small()
