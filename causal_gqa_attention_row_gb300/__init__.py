@@ -608,7 +608,8 @@ def kv_plan_rows(seq_lens, new_rows, block_tables, blocks_in, blocks_out, free_l
     after (keep_blocks of them never given back), free_out int32 [2] the blocks free afterwards and those that
     were wanting. Writes row_starts int32 [B + 1], positions int32 [N] and slots int64 [N] (-1: none). With
     parents int32 [N] (-1: the history) positions go by depth, and tree_mask int64 [N, words] gets each row's
-    bits for itself and its ancestors. blocks_out and free_out may be blocks_in and free_in."""
+    bits for itself and its ancestors. A sequence for which there are too few blocks keeps what it has, its rows have no
+    slot and the entries that it wanted are -1. blocks_out and free_out may be blocks_in and free_in."""
     B, mbps = block_tables.shape
     N = positions.shape[0]
     words = 0
@@ -685,7 +686,8 @@ def attn_tree_paged(q, k_pool, v_pool, block_tables, position_offset, row_starts
     max_rows each) of q [N, H, dk] are sequence b's, lie in its cache behind position_offset[b] rows of history (int32
     [B] or None), and see that history and the drafted rows whose bits tree_mask int64 [N, words] sets (None: a chain,
     row i sees rows 0 .. i). pools [num_blocks, Hkv, bs, d]; block_tables int32 [B, mbps]; out [N, H, dv]; workspace from
-    tree_workspace; window / softcap / sinks / alibi_slopes: the arms (`gqa_arms`)."""
+    tree_workspace; window / softcap / sinks / alibi_slopes: the arms (`gqa_arms`). Rows of a sequence that kv_plan_rows
+    could not serve get outputs that mean nothing."""
     N, H, dk = q.shape
     nb, Hkv, bs, dv = v_pool.shape
     B, mbps = block_tables.shape
@@ -720,9 +722,10 @@ def attn_tree_paged(q, k_pool, v_pool, block_tables, position_offset, row_starts
 def kv_commit_rows(k_pools, v_pools, block_tables, seq_lens_in, row_starts, path, n_path, seq_lens_out, stream=None):
     """Moves row seq_lens_in[b] + path[b][j] to row seq_lens_in[b] + j, j < n_path[b], in every layer's pools
     (k_pools, v_pools: a tensor [num_blocks, Hkv, bs, d] each layer, or one of all layers [layers, num_blocks, ..],
-    which is looked at once: 28 layers 16 us a call instead of 32; v_pools None: keys alone) and sets
+    which is looked at once: 28 layers 14 us a call instead of 30; v_pools None: keys alone) and sets
     seq_lens_out[b] = seq_lens_in[b] + n_path[b] (may be the same tensor). path int32 [B, max_path], ascending
-    indices among the row_starts[b + 1] - row_starts[b] drafted rows; n_path int32 [B]."""
+    indices among the row_starts[b + 1] - row_starts[b] drafted rows; n_path int32 [B] (0 for a sequence whose rows have
+    no slots)."""
     layers = len(k_pools)
     B, mbps = block_tables.shape
     if not layers or (v_pools is not None and len(v_pools) != layers):

@@ -1072,8 +1072,8 @@ gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool
   bool arms_on;
   const gqa_status sa = apply_arms(arm, arms, &arms_on);
   if (sa != GQA_OK) return sa;
-  // (tensor cores and SIMT kernel: 4 sequences of 4-8 rows behind up to 600 keys, 14 heads on 2 of 64, 11.7 and 14.5 us;
-  // 32 of one row behind up to 4,096, 32 heads on 8 of 128, 53 and 253; 64 of up to 32 rows 162 and 2,238)
+  // (tensor cores and SIMT kernel: 4 sequences of 4-8 rows behind up to 600 keys, 14 heads on 2 of 64, 10.9 and 13.2 us;
+  // 32 of one row behind up to 4,096, 32 heads on 8 of 128, 56 and 250; 64 of up to 32 rows 172 and 2,211)
   const bool tc = gqa::tree_tc_supported(bf16, d_k, d_v, block_size) && attention_scale > 0.f;
   const int capacity = max_blocks_per_seq * block_size;
   TreeLayout t;
@@ -1116,7 +1116,6 @@ gqa_status attn_tree_paged(const void* q, const void* k_pool, const void* v_pool
   p.partial = reinterpret_cast<float*>(ws + t.partial);
   p.H = H;
   p.G = H / Hkv;
-  p.n_hchunks = t.n_hchunks;
   p.Hkv = Hkv;
   p.mbps = max_blocks_per_seq;
   p.num_blocks = num_blocks;

@@ -1143,7 +1143,7 @@ cudaError_t launch_dense_tc(const void* q, const void* k, const void* v, const D
     if (!make_map(&tk, k, dk, p.S_kv, p.Hkv, n_b, kBN, 1)) return cudaErrorInvalidValue;
     if (!make_map(&tv, v, dv, p.S_kv, p.Hkv, n_b, kBN, 1)) return cudaErrorInvalidValue;
   }
-  if (tree) to = tq;  // (nor this: the join writes the output)
+  if (tree) to = tq;  // (nor this: rows of drafted tiles leave from registers, or by the join)
   else if (!make_map(&to, p.out, dv, p.H, p.n_i, n_b, p.GH, p.RPT)) return cudaErrorInvalidValue;
   if (dk == 64) return launch_w<64, 64>(tq, tq1, tk, tv, to, p, arms, st);
   if (dk == 128) return launch_w<128, 128>(tq, tq1, tk, tv, to, p, arms, st);

@@ -341,7 +341,7 @@ struct TreeParams {
   void* out;                       // [N, H, d_v]
   const int32_t* tables;
   float* partial;
-  int H, G, n_hchunks, Hkv, mbps, num_blocks, dk, dv;
+  int H, G, Hkv, mbps, num_blocks, dk, dv;
   float qscale;                    // attention_scale * log2(e)
   float softcap2;                  // softcap * log2(e), 0: none
   const float *sinks, *alibi;

@@ -8,17 +8,18 @@
 // (16 bytes of four queries and four keys a step, packed products), its half warp owns those four rows,
 // so the row maximum and the probabilities stay within it, then 4 rows x d_v / 16 columns of the
 // output in registers. K and V share one tile in shared memory, which leaves room for two CTAs an SM (one
-// beyond 128 columns); each is on its way in registers while the other is worked on. Eight rows are a
-// warp's, and warps without rows only load.
+// beyond 128 columns); each is requested once the other has been worked on, so its way through memory stands open
+// (held in registers meanwhile, they left too few: 16 sequences of one row, 32 heads on 8 of 128, behind 4,000 keys 311 us,
+// so 272). Eight rows are a warp's, and warps without rows only load.
 //
 // A row's masked keys weigh nothing whatever they hold: their scores are set to -infinity, and
 // in a tile that some row does not see whole a key of weight zero is left out of the second product, since
-// 0 * NaN would not be 0.
+// 0 * NaN would not be 0. (In the other tiles the value of a key that scores -infinity counts, as 0 * v.)
 //
 // Where rows are many the fp32 rate bounds it, 4 d flops a row and key: tiles of 64 rows by 64 keys read 12 KB of
 // shared memory a 16-byte step for 64 x 64 x 4 products, so issue and shared memory are about even. Where they
 // are few it is the latency of the one warp that has them. Measured (fp32): 6 sequences of 3 to 24 rows, 8 heads
-// on 2 of 64, up to 1,500 keys 22.4 us; 8 of up to 21 rows behind 5,338 keys of 2 heads of 128 116 us (10 TFLOP/s).
+// on 2 of 64, up to 1,500 keys 21.6 us.
 
 #include <atomic>
 
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<ET, DK, DV>::kCtas)
               }
           }
         } else {
-const int some = min(kTreeKeys, u.key1 - j0);  // (the last tile's keys)
+          const int some = min(kTreeKeys, u.key1 - j0);  // (the last tile's keys)
 #pragma unroll 1
           for (int k = 0; k < some; k += 4) {
             float4 pr[4];
